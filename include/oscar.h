@@ -82,7 +82,8 @@ enum {
   OSCAR_DEV_BAD_PAGE = 1,     /* block table entry out of [0, num_pages) on a needed page */
   OSCAR_DEV_TIMEOUT = 2,      /* a bounded barrier wait gave up */
   OSCAR_DEV_BAD_LEN = 4,      /* seq_len / start_pos outside [0, max_pages*page_size] */
-  OSCAR_DEV_BAD_SLOT = 8      /* req_slot outside [0, max_requests) */
+  OSCAR_DEV_BAD_SLOT = 8,     /* req_slot outside [0, max_requests) */
+  OSCAR_DEV_BAD_VALUE = 16    /* an infinity or NaN among the K or V values of a quantised 8-bit page */
 };
 
 typedef struct {
@@ -398,6 +399,147 @@ oscar_status oscar_bf16_decode_attn(oscar_ctx* ctx, int32_t layer, const void* b
                                     int32_t bt_stride, const int32_t* seq_lens, int32_t batch, int32_t max_seq,
                                     void* workspace, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------- 8-bit cache
+ * A paged cache at 8 bits beside the INT2 one, for layers or models that need more
+ * than 2 bits (no rotation, no clip threshold), with its own attention calls.  It
+ * shares the context's page allocator and block tables: page id p addresses block p
+ * of the 8-bit pool as it does in the INT2 pool.
+ *
+ * Tokens.  Page j of a request holds tokens j*P .. j*P + P-1.  A page is quantised
+ * when its last token arrives; the n % P tokens of the page that is not complete yet
+ * are BF16 rows in the tail slab.  So what the cache holds at length n does not
+ * depend on how the tokens arrived (one prompt, chunks or single tokens).  F32 rows
+ * are rounded to BF16 on entry.
+ *
+ * 8-bit pool: [num_layers][num_pages][n_kv_heads][block], one (layer, page, kv head)
+ * block of oscar_kv8_block_bytes bytes being
+ *     K codes [P][d] | V codes [P][d] | K scale, V scale (float32), 8 unused bytes |
+ *     K lo [d] | K hi [d] | unused bytes up to a multiple of 128
+ * Token rows are d bytes in channel order, but the 16-byte chunks of each 128-byte
+ * line of a code section are stored at place (chunk ^ turn), with turn = 4 (t & 1)
+ * for K at d = 128, 0 for K at d = 64, and 2 ((t >> 1) & 3) for V, t being the chunk's
+ * token in the page.
+ *   OSCAR_KV8_INT8: byte = code + 128, code in [-127, 127], M = 127.  A uniform step
+ *     per block: the closer format for values of even size.
+ *   OSCAR_KV8_E4M3: byte = the 8-bit floating-point number (4 exponent, 3 mantissa
+ *     bits), M = 448.  A relative step: for channels that differ much in size.
+ * With m = max |x| over the block's finite values: scale = m / M (float32), code =
+ * x M / m rounded to nearest even, dequantised value = code * scale.  A block with
+ * m < 2^-100 is stored as zeros with scale 0.  An infinity saturates, a NaN is stored
+ * as 0, and both set OSCAR_DEV_BAD_VALUE.  lo and hi are the smallest and largest K
+ * code of each channel over the page's tokens (-0 as +0), for oscar_kv8_select_pages.
+ *
+ * Tail slab: [num_layers][max_requests][n_kv_heads][2 (K,V)][P][d] bf16, token t at
+ * row t mod P.
+ *
+ * Row arguments (K, V, q) have heads x d adjacent elements per token and a stride in
+ * elements between tokens (a slice of a wider projection needs no copy; 0: adjacent
+ * tokens); the address and the stride in bytes must be multiples of 16.  Every kernel call must be made
+ * with the device current on which the buffers were bound (else OSCAR_ERR_INVALID),
+ * takes at most 65535 requests (else OSCAR_ERR_UNSUPPORTED), needs no allocation and
+ * can be captured into a graph.  Requests of one call have distinct req_slots and
+ * write distinct pages. */
+enum { OSCAR_KV8_INT8 = 0, OSCAR_KV8_E4M3 = 1 };
+
+/* Bytes of the 8-bit pool / tail slab / one block for a configuration (sink, recent
+ * and group_size do not matter to them); 0 if the configuration is invalid. */
+size_t oscar_kv8_pool_bytes(const oscar_config* cfg);
+size_t oscar_kv8_tail_bytes(const oscar_config* cfg);
+size_t oscar_kv8_block_bytes(const oscar_config* cfg);
+
+/* Pages a request of length n needs mapped in the 8-bit cache: n / P, its complete
+ * pages.  -1 for an invalid configuration or a negative length. */
+int32_t oscar_kv8_pages_needed(const oscar_config* cfg, int32_t seq_len);
+
+/* Bind an 8-bit cache (caller-owned device buffers of the sizes above, 16-byte
+ * aligned) to a context, which may be one created without INT2 buffers.  Once per
+ * context; the context keeps both pointers until oscar_destroy.  Allocates the 4-byte
+ * status word if the context has none. */
+oscar_status oscar_kv8_bind(oscar_ctx* ctx, int32_t format, void* pool, void* tail);
+
+/* Varlen write (prefill or extend) of tokens [start_pos[b], start_pos[b]+len_b) of each
+ * request b; cu_seqlens, start_pos, req_slot, block_table and total_tokens as for
+ * oscar_write_kv.  K, V: [total_tokens][n_kv_heads][d] in dtype, tokens k_stride and
+ * v_stride elements apart.  The cache must hold exactly start_pos[b] tokens of request b
+ * (its tail rows are read).  Every page that the chunk completes must be mapped (else
+ * OSCAR_DEV_BAD_PAGE and that page is not stored). */
+oscar_status oscar_kv8_write(oscar_ctx* ctx, int32_t layer, const void* K, int64_t k_stride, const void* V,
+                             int64_t v_stride, int32_t dtype, const int32_t* cu_seqlens, const int32_t* start_pos,
+                             int32_t batch, int32_t total_tokens, const int32_t* block_table, int32_t bt_stride,
+                             const int32_t* req_slot, void* stream);
+
+/* One token per request: K_new, V_new [batch][n_kv_heads][d] become token
+ * seq_lens_before[b], row seq_lens_before[b] mod P of the tail; a request whose page it
+ * completes has that page quantised (and needs it mapped).  Same cache contents as
+ * oscar_kv8_write of the same tokens. */
+oscar_status oscar_kv8_append(oscar_ctx* ctx, int32_t layer, const void* K_new, int64_t k_stride, const void* V_new,
+                              int64_t v_stride, int32_t dtype, const int32_t* seq_lens_before, int32_t batch,
+                              const int32_t* block_table, int32_t bt_stride, const int32_t* req_slot, void* stream);
+
+/* Decode attention over the 8-bit cache: o = softmax(q K^T / sqrt(d)) V over the
+ * seq_lens[b] / P complete pages and the seq_lens[b] mod P tail rows.  q: [batch]
+ * [n_q_heads][d], requests q_stride elements apart; out: [batch][n_q_heads][d] adjacent,
+ * 16-byte aligned; the other arguments as for oscar_decode_attn.  A request of length 0
+ * (or of a bad length) gets zeros; a page that is not mapped is left out and sets
+ * OSCAR_DEV_BAD_PAGE. */
+oscar_status oscar_kv8_decode_workspace_size(const oscar_config* cfg, int32_t batch, int32_t max_seq, size_t* bytes);
+oscar_status oscar_kv8_decode_attn(oscar_ctx* ctx, int32_t layer, const void* q, int64_t q_stride, int32_t q_dtype,
+                                   void* out, int32_t out_dtype, const int32_t* block_table, int32_t bt_stride,
+                                   const int32_t* seq_lens, const int32_t* req_slot, int32_t batch, int32_t max_seq,
+                                   void* workspace, size_t ws_bytes, void* stream);
+
+/* Select the pages that sparse decode reads.  For a page p of a kv head,
+ *     U_p = scale_p sum_c (a_c hi_pc - b_c lo_pc),
+ *     a_c = sum_h max(q_hc, 0),  b_c = sum_h max(-q_hc, 0)  over the heads h that share it,
+ * is the sum over those heads of an upper bound of q_h . k over the page's keys.
+ * page_idx [batch][n_kv_heads][n_select] receives logical page indexes in ascending
+ * order, -1 after the last: the first keep_first and the last keep_last complete pages
+ * of the request, then those of the largest U_p, the lowest index first among equal
+ * ones; every complete page when there are no more than n_select.  1 <= n_select,
+ * keep_first + keep_last <= n_select.  The order is that of U_p in float64 (a page whose
+ * U_p is NaN, or that is not mapped, comes last; the latter sets OSCAR_DEV_BAD_PAGE).  The list may
+ * serve several calls (later tokens, other layers) as long as its pages are complete. */
+oscar_status oscar_kv8_select_workspace_size(const oscar_config* cfg, int32_t batch, int32_t max_seq, size_t* bytes);
+oscar_status oscar_kv8_select_pages(oscar_ctx* ctx, int32_t layer, const void* q, int64_t q_stride, int32_t q_dtype,
+                                    const int32_t* block_table, int32_t bt_stride, const int32_t* seq_lens,
+                                    int32_t batch, int32_t max_seq, int32_t keep_first, int32_t keep_last,
+                                    int32_t n_select, int32_t* page_idx, void* workspace, size_t ws_bytes,
+                                    void* stream);
+
+/* oscar_kv8_decode_attn over the listed pages of each (request, kv head) and the tail
+ * rows.  page_idx [batch][n_kv_heads][n_select] (device): complete pages of the request,
+ * strictly ascending, negative entries after the last.  An entry that is out of order,
+ * given twice or not a complete page sets OSCAR_DEV_BAD_PAGE and is left out, or counts
+ * again where it is not next to its like: check the status before using the output. */
+oscar_status oscar_kv8_sparse_workspace_size(const oscar_config* cfg, int32_t batch, int32_t n_select, size_t* bytes);
+oscar_status oscar_kv8_sparse_decode_attn(oscar_ctx* ctx, int32_t layer, const void* q, int64_t q_stride,
+                                          int32_t q_dtype, void* out, int32_t out_dtype, const int32_t* page_idx,
+                                          int32_t n_select, const int32_t* block_table, int32_t bt_stride,
+                                          const int32_t* seq_lens, const int32_t* req_slot, int32_t batch,
+                                          void* workspace, size_t ws_bytes, void* stream);
+
+/* Fork n_dst requests off request src at its current length n in the 8-bit cache (parallel
+ * sampling, beams, a shared prompt).  Host arrays: src_bt (n / P entries are read), dst_slots
+ * [n_dst] (distinct, not src_slot), dst_bt [n_dst][max_pages_per_req] (written; unused entries
+ * -1).  The n / P complete pages are shared (each refcount + n_dst); the n mod P tail rows are
+ * copied to every destination slot, in every layer, by one kernel on stream.  On an error
+ * nothing is forked.  Without a bound cache only the host part is done.  The allocator changes
+ * at the call, so the call is not for graph capture. */
+oscar_status oscar_kv8_fork(oscar_ctx* ctx, const int32_t* src_bt, int32_t n, int32_t src_slot,
+                            const int32_t* dst_slots, int32_t n_dst, int32_t* dst_bt, void* stream);
+
+/* Move the allocated pages down to ids [0, live), live = pages in use, so that the rest of
+ * the pools holds nothing: every allocated page with an id >= live moves to a free id below,
+ * in every layer of the INT2 pool and of the bound 8-bit pool.  block_table [rows][bt_stride]
+ * (device int32, adjacent rows; rows = 0 for none) is rewritten to the new ids; out_map [num_pages]
+ * (host) gives every page's new id (-1 for a free one) for block tables on the host, and
+ * *out_live receives live.  Refcounts move with their pages, and fresh pages are handed out from
+ * live upwards.  The copies and the rewriting run on stream; every block table that maps a moved
+ * page must be rewritten before its next use, and work on other streams that reads those pages
+ * must be ordered around the call.  Not for graph capture (the allocator changes at the call). */
+oscar_status oscar_compact_pages(oscar_ctx* ctx, int32_t* block_table, int32_t rows, int32_t bt_stride,
+                                 int32_t* out_map, int32_t* out_live, void* stream);
+
 /* Self-test of the device-side failure path (no counterpart in the OSCAR
  * paper).  Every kernel bounds its mbarrier waits and, when one runs out, sets
  * OSCAR_DEV_TIMEOUT in the status word instead of trapping, so the context
@@ -431,7 +573,8 @@ oscar_status oscar_set_decode_form(oscar_ctx* ctx, int32_t form);
  * oscar_kernel_time returns the summed milliseconds and launch count since the
  * last reset (synchronises the recorded events).  Names: "decode_splitk",
  * "decode_combine", "q_rotate", "step_prep", "append", "evict", "write", "bf16_prepare",
- * "bf16_decode", "bf16_combine", "extend", "selftest".  Launches
+ * "bf16_decode", "bf16_combine", "extend", "selftest", "kv8_write", "kv8_append", "kv8_decode",
+ * "kv8_combine", "kv8_select", "kv8_fork", "copy_pages", "remap_table".  Launches
  * recorded into a CUDA graph get external event-record nodes: replay the graph
  * once, then read; the events return to the library when read, so a graph
  * captured with timing on is replayed at most once.  With timing on, the decode

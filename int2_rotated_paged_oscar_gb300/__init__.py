@@ -21,7 +21,8 @@ LIB_PATH = os.path.join(_HERE, "liboscar.so")
 OK, ERR_INVALID, ERR_OOM, ERR_CUDA, ERR_DEVICE, ERR_UNSUPPORTED = 0, -1, -2, -3, -4, -5
 DTYPE_F32, DTYPE_BF16 = 0, 1
 DECODE_AUTO, DECODE_THREE_KERNELS, DECODE_ONE_LAUNCH = 0, 1, 2
-DEV_BAD_PAGE, DEV_TIMEOUT, DEV_BAD_LEN, DEV_BAD_SLOT = 1, 2, 4, 8
+DEV_BAD_PAGE, DEV_TIMEOUT, DEV_BAD_LEN, DEV_BAD_SLOT, DEV_BAD_VALUE = 1, 2, 4, 8, 16
+KV8_INT8, KV8_E4M3 = 0, 1
 
 
 class OscarError(RuntimeError):
@@ -51,6 +52,8 @@ _c_i32p = ctypes.POINTER(ctypes.c_int32)
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
 _f32 = ctypes.c_float
+_i64 = ctypes.c_int64
+_szp = ctypes.POINTER(ctypes.c_size_t)
 _cfgp = ctypes.POINTER(oscar_config)
 
 # name -> (restype, argtypes); every entry point declared in include/oscar.h
@@ -92,6 +95,24 @@ _SIGS = {
     "oscar_bf16_decode_workspace_size": (_i32, [_cfgp, _i32, _i32, ctypes.POINTER(ctypes.c_size_t)]),
     "oscar_bf16_decode_attn": (_i32, [_vp, _i32, _vp, _vp, _i32, _vp, _i32, _vp, _i32, _vp, _i32, _i32, _vp,
                                       ctypes.c_size_t, _vp]),
+    "oscar_kv8_pool_bytes": (ctypes.c_size_t, [_cfgp]),
+    "oscar_kv8_tail_bytes": (ctypes.c_size_t, [_cfgp]),
+    "oscar_kv8_block_bytes": (ctypes.c_size_t, [_cfgp]),
+    "oscar_kv8_pages_needed": (_i32, [_cfgp, _i32]),
+    "oscar_kv8_bind": (_i32, [_vp, _i32, _vp, _vp]),
+    "oscar_kv8_write": (_i32, [_vp, _i32, _vp, _i64, _vp, _i64, _i32, _vp, _vp, _i32, _i32, _vp, _i32, _vp, _vp]),
+    "oscar_kv8_append": (_i32, [_vp, _i32, _vp, _i64, _vp, _i64, _i32, _vp, _i32, _vp, _i32, _vp, _vp]),
+    "oscar_kv8_decode_workspace_size": (_i32, [_cfgp, _i32, _i32, _szp]),
+    "oscar_kv8_decode_attn": (_i32, [_vp, _i32, _vp, _i64, _i32, _vp, _i32, _vp, _i32, _vp, _vp, _i32, _i32, _vp,
+                                     ctypes.c_size_t, _vp]),
+    "oscar_kv8_select_workspace_size": (_i32, [_cfgp, _i32, _i32, _szp]),
+    "oscar_kv8_select_pages": (_i32, [_vp, _i32, _vp, _i64, _i32, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _vp,
+                                      _vp, ctypes.c_size_t, _vp]),
+    "oscar_kv8_sparse_workspace_size": (_i32, [_cfgp, _i32, _i32, _szp]),
+    "oscar_kv8_sparse_decode_attn": (_i32, [_vp, _i32, _vp, _i64, _i32, _vp, _i32, _vp, _i32, _vp, _i32, _vp, _vp,
+                                            _i32, _vp, ctypes.c_size_t, _vp]),
+    "oscar_kv8_fork": (_i32, [_vp, _vp, _i32, _i32, _vp, _i32, _vp, _vp]),
+    "oscar_compact_pages": (_i32, [_vp, _vp, _i32, _i32, _vp, _c_i32p, _vp]),
     "oscar_selftest_wait_timeout": (_i32, [_vp, _i32, _vp]),
     "oscar_check_status": (_i32, [_vp, _vp, _c_i32p]),
     "oscar_set_decode_form": (_i32, [_vp, _i32]),
@@ -102,6 +123,7 @@ _SIGS = {
 }
 
 _lib: Optional[ctypes.CDLL] = None
+_configs: dict = {}   # context -> its configuration
 
 
 def load() -> ctypes.CDLL:
@@ -168,10 +190,12 @@ def oscar_page_block_bytes(cfg: oscar_config) -> int:
 def oscar_create(cfg: oscar_config, int2_pool=None, window_slab=None) -> int:
     out = ctypes.c_void_p()
     _check(load().oscar_create(ctypes.byref(cfg), ptr(int2_pool), ptr(window_slab), ctypes.byref(out)))
+    _configs[out.value] = oscar_config.from_buffer_copy(cfg)
     return out.value
 
 
 def oscar_destroy(ctx: int) -> None:
+    _configs.pop(ctx, None)
     _check(load().oscar_destroy(ctx))
 
 
@@ -321,6 +345,177 @@ def oscar_bf16_decode_attn(ctx, layer, bf16_pool, q, q_dtype, out, out_dtype, bl
     _check(load().oscar_bf16_decode_attn(ctx, layer, ptr(bf16_pool), ptr(q), q_dtype, ptr(out), out_dtype,
                                          ptr(block_table), bt_stride, ptr(seq_lens), batch, max_seq, ptr(workspace),
                                          ws_bytes, stream_ptr(stream)))
+
+
+# ------------------------------------------------------------------ 8-bit cache
+# These wrappers also check what the C ABI cannot see of a torch tensor: its device, element type, layout and size.
+# A plain integer is passed on as an address, unchecked (rows then lie next to one another).
+_DTYPE_NAMES = {DTYPE_F32: "torch.float32", DTYPE_BF16: "torch.bfloat16"}
+
+
+def _dense(x, name: str, count: int = 0, dtype: str = "torch.int32") -> Optional[int]:
+    """Address of a dense CUDA tensor of at least ``count`` elements of one type (dtype "": count bytes of any type)."""
+    if x is None or isinstance(x, int):
+        return x
+    have = x.numel() if dtype else x.numel() * x.element_size()
+    if not x.is_cuda or not x.is_contiguous() or have < count or (dtype and str(x.dtype) != dtype):
+        raise OscarError(ERR_INVALID, f"{name} must be a contiguous CUDA tensor of at least {count} "
+                                      f"{dtype or 'bytes'}, not {x.dtype} {tuple(x.shape)} on {x.device} with strides "
+                                      f"{tuple(x.stride())}")
+    return x.data_ptr()
+
+
+def _rows(x, name: str, dtype: int, tokens: int, heads: int, d: int):
+    """(address, elements between tokens) of [tokens][heads][d] rows; the tokens may lie further apart than their rows
+    are long."""
+    if x is None or isinstance(x, int):
+        return x, 0
+    want, shape = _DTYPE_NAMES.get(dtype, ""), tuple(x.shape)
+    if not x.is_cuda or (want and str(x.dtype) != want) or len(shape) != 3 or shape[0] < tokens or shape[1:] != (heads, d):
+        raise OscarError(ERR_INVALID, f"{name} must be a [{tokens}][{heads}][{d}] CUDA tensor of {want}, not {x.dtype} "
+                                      f"{shape} on {x.device}")
+    t, h, c = x.stride()
+    if c != 1 or (heads > 1 and h != d):
+        raise OscarError(ERR_INVALID, f"the heads and channels of {name} must be adjacent, not strided {(t, h, c)}")
+    return x.data_ptr(), t if shape[0] > 1 else 0
+
+
+def _config(ctx) -> oscar_config:
+    cfg = _configs.get(ctx)
+    if cfg is None:
+        raise OscarError(ERR_INVALID, "not a context of oscar_create")
+    return cfg
+
+
+def oscar_kv8_pool_bytes(cfg: oscar_config) -> int:
+    return load().oscar_kv8_pool_bytes(ctypes.byref(cfg))
+
+
+def oscar_kv8_tail_bytes(cfg: oscar_config) -> int:
+    return load().oscar_kv8_tail_bytes(ctypes.byref(cfg))
+
+
+def oscar_kv8_block_bytes(cfg: oscar_config) -> int:
+    return load().oscar_kv8_block_bytes(ctypes.byref(cfg))
+
+
+def oscar_kv8_pages_needed(cfg: oscar_config, seq_len: int) -> int:
+    return load().oscar_kv8_pages_needed(ctypes.byref(cfg), seq_len)
+
+
+def oscar_kv8_bind(ctx: int, fmt: int, pool, tail) -> None:
+    """Bind an 8-bit cache: device buffers of oscar_kv8_pool_bytes and oscar_kv8_tail_bytes (any element type)."""
+    cfg = _config(ctx)
+    _check(load().oscar_kv8_bind(ctx, fmt, _dense(pool, "pool", oscar_kv8_pool_bytes(cfg), ""),
+                                 _dense(tail, "tail", oscar_kv8_tail_bytes(cfg), "")))
+
+
+def oscar_kv8_write(ctx, layer, K, V, dtype, cu_seqlens, start_pos, batch, total_tokens, block_table, bt_stride,
+                    req_slot, stream=None) -> None:
+    cfg = _config(ctx)
+    k, ks = _rows(K, "K", dtype, total_tokens, cfg.n_kv_heads, cfg.head_dim)
+    v, vs = _rows(V, "V", dtype, total_tokens, cfg.n_kv_heads, cfg.head_dim)
+    _check(load().oscar_kv8_write(ctx, layer, k, ks, v, vs, dtype, _dense(cu_seqlens, "cu_seqlens", batch + 1),
+                                  _dense(start_pos, "start_pos", batch), batch, total_tokens,
+                                  _dense(block_table, "block_table", batch * bt_stride), bt_stride,
+                                  _dense(req_slot, "req_slot", batch), stream_ptr(stream)))
+
+
+def oscar_kv8_append(ctx, layer, K_new, V_new, dtype, seq_lens_before, batch, block_table, bt_stride, req_slot,
+                     stream=None) -> None:
+    cfg = _config(ctx)
+    k, ks = _rows(K_new, "K_new", dtype, batch, cfg.n_kv_heads, cfg.head_dim)
+    v, vs = _rows(V_new, "V_new", dtype, batch, cfg.n_kv_heads, cfg.head_dim)
+    _check(load().oscar_kv8_append(ctx, layer, k, ks, v, vs, dtype, _dense(seq_lens_before, "seq_lens_before", batch),
+                                   batch, _dense(block_table, "block_table", batch * bt_stride), bt_stride,
+                                   _dense(req_slot, "req_slot", batch), stream_ptr(stream)))
+
+
+def _size(fn, cfg, a: int, b: int) -> int:
+    out = ctypes.c_size_t()
+    _check(fn(ctypes.byref(cfg), a, b, ctypes.byref(out)))
+    return out.value
+
+
+def oscar_kv8_decode_workspace_size(cfg: oscar_config, batch: int, max_seq: int) -> int:
+    return _size(load().oscar_kv8_decode_workspace_size, cfg, batch, max_seq)
+
+
+def oscar_kv8_select_workspace_size(cfg: oscar_config, batch: int, max_seq: int) -> int:
+    return _size(load().oscar_kv8_select_workspace_size, cfg, batch, max_seq)
+
+
+def oscar_kv8_sparse_workspace_size(cfg: oscar_config, batch: int, n_select: int) -> int:
+    return _size(load().oscar_kv8_sparse_workspace_size, cfg, batch, n_select)
+
+
+def oscar_kv8_decode_attn(ctx, layer, q, q_dtype, out, out_dtype, block_table, bt_stride, seq_lens, req_slot, batch,
+                          max_seq, workspace, ws_bytes, stream=None) -> None:
+    cfg = _config(ctx)
+    hq, d = cfg.n_q_heads, cfg.head_dim
+    qp, qs = _rows(q, "q", q_dtype, batch, hq, d)
+    _check(load().oscar_kv8_decode_attn(ctx, layer, qp, qs, q_dtype,
+                                        _dense(out, "out", batch * hq * d, _DTYPE_NAMES.get(out_dtype, "")), out_dtype,
+                                        _dense(block_table, "block_table", batch * bt_stride), bt_stride,
+                                        _dense(seq_lens, "seq_lens", batch), _dense(req_slot, "req_slot", batch), batch,
+                                        max_seq, _dense(workspace, "workspace", ws_bytes, ""), ws_bytes,
+                                        stream_ptr(stream)))
+
+
+def oscar_kv8_select_pages(ctx, layer, q, q_dtype, block_table, bt_stride, seq_lens, batch, max_seq, keep_first,
+                           keep_last, n_select, page_idx, workspace, ws_bytes, stream=None) -> None:
+    cfg = _config(ctx)
+    qp, qs = _rows(q, "q", q_dtype, batch, cfg.n_q_heads, cfg.head_dim)
+    _check(load().oscar_kv8_select_pages(ctx, layer, qp, qs, q_dtype,
+                                         _dense(block_table, "block_table", batch * bt_stride), bt_stride,
+                                         _dense(seq_lens, "seq_lens", batch), batch, max_seq, keep_first, keep_last,
+                                         n_select, _dense(page_idx, "page_idx", batch * cfg.n_kv_heads * n_select),
+                                         _dense(workspace, "workspace", ws_bytes, ""), ws_bytes, stream_ptr(stream)))
+
+
+def oscar_kv8_sparse_decode_attn(ctx, layer, q, q_dtype, out, out_dtype, page_idx, n_select, block_table, bt_stride,
+                                 seq_lens, req_slot, batch, workspace, ws_bytes, stream=None) -> None:
+    cfg = _config(ctx)
+    hq, d = cfg.n_q_heads, cfg.head_dim
+    qp, qs = _rows(q, "q", q_dtype, batch, hq, d)
+    _check(load().oscar_kv8_sparse_decode_attn(ctx, layer, qp, qs, q_dtype,
+                                               _dense(out, "out", batch * hq * d, _DTYPE_NAMES.get(out_dtype, "")),
+                                               out_dtype,
+                                               _dense(page_idx, "page_idx", batch * cfg.n_kv_heads * n_select), n_select,
+                                               _dense(block_table, "block_table", batch * bt_stride), bt_stride,
+                                               _dense(seq_lens, "seq_lens", batch), _dense(req_slot, "req_slot", batch),
+                                               batch, _dense(workspace, "workspace", ws_bytes, ""), ws_bytes,
+                                               stream_ptr(stream)))
+
+
+def oscar_kv8_fork(ctx: int, src_bt: Sequence[int], n: int, src_slot: int, dst_slots: Sequence[int], max_pages: int,
+                   stream=None):
+    """The block tables of the forks, int32 [len(dst_slots)][max_pages]; max_pages is the configuration's
+    max_pages_per_req.  A host-only context takes stream=0."""
+    import numpy as np
+    if max_pages != _config(ctx).max_pages_per_req:
+        raise OscarError(ERR_INVALID, f"max_pages {max_pages} is not the configuration's max_pages_per_req")
+    src = np.full(max_pages, -1, np.int32)
+    mapped = np.asarray(src_bt, np.int32)[:max_pages]
+    src[:len(mapped)] = mapped
+    slots = np.ascontiguousarray(dst_slots, np.int32)
+    dst = np.empty((len(slots), max_pages), np.int32)
+    _check(load().oscar_kv8_fork(ctx, src.ctypes.data, n, src_slot, slots.ctypes.data, len(slots), dst.ctypes.data,
+                                 stream_ptr(stream) if stream != 0 else None))
+    return dst
+
+
+def oscar_compact_pages(ctx: int, block_table, rows: int, bt_stride: int, num_pages: int, stream=None):
+    """Compact the context's pages; returns (map, live): map int32 [num_pages] holds every page's new id, -1 for a free
+    page.  num_pages is the configuration's.  block_table may be None (rows = 0); a host-only context takes stream=0."""
+    import numpy as np
+    if num_pages != _config(ctx).num_pages:
+        raise OscarError(ERR_INVALID, f"num_pages {num_pages} is not the configuration's")
+    table = np.empty(num_pages, np.int32)
+    live = ctypes.c_int32()
+    _check(load().oscar_compact_pages(ctx, _dense(block_table, "block_table", rows * bt_stride), rows, bt_stride,
+                                      table.ctypes.data, ctypes.byref(live), stream_ptr(stream) if stream != 0 else None))
+    return table, live.value
 
 
 def oscar_selftest_wait_timeout(ctx, limit_us: int, stream=None) -> None:

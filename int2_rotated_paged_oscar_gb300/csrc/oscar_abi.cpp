@@ -18,17 +18,25 @@
 #include <string>
 #include <vector>
 
-#include "../../include/oscar.h"
-#include "oscar_internal.h"
+#include "oscar_ctx.h"
 
+using oscar::check_layer;
+using oscar::check_workspace;
+using oscar::cuda_fail;
 using oscar::DecodeArgs;
 using oscar::DecodeWs;
+using oscar::fail;
 using oscar::Geom;
+using oscar::LaunchScope;
+using oscar::validate;
 using oscar::WriteArgs;
+using Timing = oscar_timing;
 
 namespace {
-
 thread_local std::string g_last_error;
+}  // namespace
+
+namespace oscar {
 
 oscar_status fail(oscar_status code, const char* fmt, ...) {
   char buf[512];
@@ -44,38 +52,7 @@ oscar_status cuda_fail(int err, const char* what) {
   return fail(OSCAR_ERR_CUDA, "%s: %s", what, cudaGetErrorString(static_cast<cudaError_t>(err)));
 }
 
-struct Timing {
-  std::vector<std::pair<cudaEvent_t, cudaEvent_t>> pending;
-  double ms = 0.0;
-  int launches = 0;
-};
-
-}  // namespace
-
-struct oscar_ctx {
-  Geom g{};
-  uint8_t* pool = nullptr;
-  uint16_t* slab = nullptr;
-  int* d_status = nullptr;
-  int* d_tickets = nullptr;  // one-launch decode counters [max_requests][n_kv_heads], zero between launches
-  std::mutex mu;
-  std::vector<int32_t> refcount;
-  std::vector<int32_t> free_stack;  // top = back
-  long long alloc_fail_after = -1;  // fault injection (OSCAR_FAULT_ALLOC_FAIL_AFTER)
-  long long allocs_done = 0;
-  bool timing = false;
-  std::map<std::string, Timing> timers;
-  std::vector<cudaEvent_t> event_pool;
-  long long launches = 0;
-  // per layer: operand exponents of the history's scales and zeros in the
-  // decode MMAs (kNoOperandExp until a clip threshold is known for the layer)
-  std::vector<int> opexp_K, opexp_V;
-  int decode_form = OSCAR_DECODE_AUTO;
-};
-
-namespace {
-
-bool is_pow2_in(int v, std::initializer_list<int> allowed) {
+static bool is_pow2_in(int v, std::initializer_list<int> allowed) {
   for (int a : allowed)
     if (v == a) return true;
   return false;
@@ -130,32 +107,20 @@ cudaEvent_t take_event(oscar_ctx* ctx) {
   return e;
 }
 
-struct LaunchScope {
-  oscar_ctx* ctx;
-  const char* name;
-  cudaStream_t s;
-  cudaEvent_t a = nullptr, b = nullptr;
-  // Inside stream capture the two records become external event-record nodes
-  // of the graph, so one replay of the graph times the kernel on the device.
-  unsigned flags = cudaEventRecordDefault;
-  LaunchScope(oscar_ctx* c, const char* n, void* stream) : ctx(c), name(n), s(static_cast<cudaStream_t>(stream)) {
-    if (ctx->timing) {
-      cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-      if (cudaStreamIsCapturing(s, &cs) == cudaSuccess && cs == cudaStreamCaptureStatusActive)
-        flags = cudaEventRecordExternal;
-      a = take_event(ctx);
-      b = take_event(ctx);
-      if (a) cudaEventRecordWithFlags(a, s, flags);
-    }
-  }
-  void done(int err) {
-    if (err == 0) ctx->launches++;
-    if (ctx->timing && a && b) {
-      cudaEventRecordWithFlags(b, s, flags);
-      ctx->timers[name].pending.push_back({a, b});
-    }
-  }
-};
+oscar_status check_layer(const oscar_ctx* ctx, int32_t layer) {
+  if (layer < 0 || layer >= ctx->g.L) return fail(OSCAR_ERR_INVALID, "layer %d out of [0, %d)", layer, ctx->g.L);
+  return OSCAR_OK;
+}
+
+oscar_status check_workspace(const void* workspace) {
+  if (!workspace) return fail(OSCAR_ERR_INVALID, "null tensor argument");
+  if (reinterpret_cast<uintptr_t>(workspace) & 255) return fail(OSCAR_ERR_INVALID, "workspace must be 256-byte aligned");
+  return OSCAR_OK;
+}
+
+}  // namespace oscar
+
+namespace {
 
 oscar_status need_device(oscar_ctx* ctx) {
   if (!ctx) return fail(OSCAR_ERR_INVALID, "context is null");
@@ -168,11 +133,6 @@ oscar_status need_device(oscar_ctx* ctx) {
 oscar_status check_r_align(const float* R_K, const float* R_V) {
   if ((reinterpret_cast<uintptr_t>(R_K) | reinterpret_cast<uintptr_t>(R_V)) & 15)
     return fail(OSCAR_ERR_INVALID, "R_K and R_V must be 16-byte aligned");
-  return OSCAR_OK;
-}
-
-oscar_status check_layer(const oscar_ctx* ctx, int32_t layer) {
-  if (layer < 0 || layer >= ctx->g.L) return fail(OSCAR_ERR_INVALID, "layer %d out of [0, %d)", layer, ctx->g.L);
   return OSCAR_OK;
 }
 
@@ -363,7 +323,8 @@ oscar_status oscar_create(const oscar_config* cfg, void* int2_pool, void* window
   if (const char* f = std::getenv("OSCAR_FAULT_ALLOC_FAIL_AFTER")) ctx->alloc_fail_after = std::atoll(f);
   if (int2_pool) {
     const size_t tickets = (size_t)g.max_req * g.Hkv * sizeof(int);
-    cudaError_t e = cudaMalloc(&ctx->d_status, sizeof(int));
+    cudaError_t e = cudaGetDevice(&ctx->device);
+    if (e == cudaSuccess) e = cudaMalloc(&ctx->d_status, sizeof(int));
     if (e == cudaSuccess) e = cudaMemset(ctx->d_status, 0, sizeof(int));
     if (e == cudaSuccess) e = cudaMalloc(&ctx->d_tickets, tickets);
     if (e == cudaSuccess) e = cudaMemset(ctx->d_tickets, 0, tickets);
@@ -705,12 +666,6 @@ static oscar_status layer_operand_exps(oscar_ctx* ctx, int32_t layer, int* ek, i
   if (*ek == oscar::kNoOperandExp || *ev == oscar::kNoOperandExp)
     return fail(OSCAR_ERR_INVALID,
                 "no clip threshold known for layer %d: write to it or call oscar_set_layer_clip first", layer);
-  return OSCAR_OK;
-}
-
-static oscar_status check_workspace(const void* workspace) {
-  if (!workspace) return fail(OSCAR_ERR_INVALID, "null tensor argument");
-  if (reinterpret_cast<uintptr_t>(workspace) & 255) return fail(OSCAR_ERR_INVALID, "workspace must be 256-byte aligned");
   return OSCAR_OK;
 }
 
@@ -1087,8 +1042,8 @@ oscar_status oscar_bf16_decode_attn(oscar_ctx* ctx, int32_t layer, const void* b
 
 // ---------------------------------------------------------------- status, tracing
 oscar_status oscar_check_status(oscar_ctx* ctx, void* stream, int32_t* out_bits) {
-  oscar_status st = need_device(ctx);
-  if (st != OSCAR_OK) return st;
+  if (!ctx) return fail(OSCAR_ERR_INVALID, "context is null");
+  if (!ctx->d_status) return fail(OSCAR_ERR_INVALID, "context was created without device buffers");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return cuda_fail(e, "stream synchronize");
@@ -1099,9 +1054,10 @@ oscar_status oscar_check_status(oscar_ctx* ctx, void* stream, int32_t* out_bits)
   if (bits) {
     cudaMemset(ctx->d_status, 0, sizeof(int));
     // a launch that failed may have left the one-launch decode counters mid-count
-    cudaMemset(ctx->d_tickets, 0, (size_t)ctx->g.max_req * ctx->g.Hkv * sizeof(int));
-    return fail(OSCAR_ERR_DEVICE, "device status 0x%x (%s%s%s)", bits, (bits & oscar::kDevBadPage) ? "bad page " : "",
-                (bits & oscar::kDevTimeout) ? "wait timeout " : "", (bits & oscar::kDevBadLen) ? "bad length " : "");
+    if (ctx->d_tickets) cudaMemset(ctx->d_tickets, 0, (size_t)ctx->g.max_req * ctx->g.Hkv * sizeof(int));
+    return fail(OSCAR_ERR_DEVICE, "device status 0x%x (%s%s%s%s)", bits, (bits & oscar::kDevBadPage) ? "bad page " : "",
+                (bits & oscar::kDevTimeout) ? "wait timeout " : "", (bits & oscar::kDevBadLen) ? "bad length " : "",
+                (bits & oscar::kDevBadValue) ? "non-finite value " : "");
   }
   return OSCAR_OK;
 }

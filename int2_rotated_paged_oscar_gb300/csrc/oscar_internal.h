@@ -15,6 +15,7 @@ constexpr int kDevBadPage = 1;
 constexpr int kDevTimeout = 2;
 constexpr int kDevBadLen = 4;
 constexpr int kDevBadSlot = 8;
+constexpr int kDevBadValue = 16;
 constexpr unsigned long long kWaitLimitNs = 200ull * 1000ull * 1000ull;  // 200 ms per barrier wait
 
 // Size of the file-scope scratch used by the allocation-free decode entry point.
