@@ -25,6 +25,31 @@ __device__ __forceinline__ float kv8_value(uint32_t b) {
   return __half2float(__half(h));
 }
 
+// Two neighbouring code bytes of a word as an f16 pair: bytes 0, 1 (HALF = 0) or 2, 3 (HALF = 1).
+// Both are exact.  INT8: the byte under the exponent of 1024 is 1024 + byte; less 1152 that is
+// byte - 128.  E4M3: the hardware's conversion.
+template <int FMT, int HALF>
+__device__ __forceinline__ uint32_t kv8_pair(uint32_t w) {
+  if constexpr (FMT == kKv8Int8) {
+    const uint32_t x = prmt(w, 0x64646464u, HALF ? 0x4342u : 0x4140u);
+    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&x), __half2half2(__ushort_as_half(0x6480)));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  } else {
+    uint32_t r;
+    const uint16_t b = (uint16_t)(HALF ? w >> 16 : w);
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(b));
+    return r;
+  }
+}
+
+// Transpose of an 8 x 8 matrix of 16-bit elements held as an MMA fragment (lane: row lane / 4,
+// columns 2 (lane % 4) and the next).
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
 // x / m * M rounded to a code.  x M is exact (x and M have 8 and at most 7 significant bits),
 // and a quotient of two numbers that short lies no nearer to a code border than float32's
 // rounding unless it is on it, so the one rounding of the division loses nothing.
