@@ -166,8 +166,11 @@ def stream_ptr(stream=None) -> Optional[int]:
 
 
 def _i32_array(seq: Sequence[int]):
-    arr = (ctypes.c_int32 * len(seq))(*[int(v) for v in seq])
-    return arr
+    n = len(seq)
+    if n > 16:   # long lists of pages: numpy's conversion
+        import numpy as np
+        return (ctypes.c_int32 * n).from_buffer(np.array(seq, dtype=np.int32))
+    return (ctypes.c_int32 * n)(*[int(v) for v in seq])
 
 
 # ------------------------------------------------------------------ thin wrappers (same names as the C ABI)
@@ -202,7 +205,7 @@ def oscar_destroy(ctx: int) -> None:
 def oscar_alloc_pages(ctx: int, n: int):
     arr = (ctypes.c_int32 * max(n, 1))()
     _check(load().oscar_alloc_pages(ctx, n, arr))
-    return [arr[i] for i in range(n)]
+    return arr[:n]
 
 
 def oscar_ref_pages(ctx: int, ids: Sequence[int]) -> None:
@@ -350,19 +353,30 @@ def oscar_bf16_decode_attn(ctx, layer, bf16_pool, q, q_dtype, out, out_dtype, bl
 # ------------------------------------------------------------------ 8-bit cache
 # These wrappers also check what the C ABI cannot see of a torch tensor: its device, element type, layout and size.
 # A plain integer is passed on as an address, unchecked (rows then lie next to one another).
-_DTYPE_NAMES = {DTYPE_F32: "torch.float32", DTYPE_BF16: "torch.bfloat16"}
+_torch_types: dict = {}
 
 
-def _dense(x, name: str, count: int = 0, dtype: str = "torch.int32") -> Optional[int]:
-    """Address of a dense CUDA tensor of at least ``count`` elements of one type (dtype "": count bytes of any type)."""
+def _types() -> dict:
+    """Element types by name and by DTYPE_* code (torch is imported on the first tensor argument)."""
+    if not _torch_types:
+        import torch
+        _torch_types.update({"i32": torch.int32, DTYPE_F32: torch.float32, DTYPE_BF16: torch.bfloat16})
+    return _torch_types
+
+
+def _dense(x, name: str, count: int = 0, dtype="i32") -> Optional[int]:
+    """Address of a dense CUDA tensor of at least ``count`` elements of one type (dtype None: count bytes of any type)."""
     if x is None or isinstance(x, int):
         return x
-    have = x.numel() if dtype else x.numel() * x.element_size()
-    if not x.is_cuda or not x.is_contiguous() or have < count or (dtype and str(x.dtype) != dtype):
-        raise OscarError(ERR_INVALID, f"{name} must be a contiguous CUDA tensor of at least {count} "
-                                      f"{dtype or 'bytes'}, not {x.dtype} {tuple(x.shape)} on {x.device} with strides "
-                                      f"{tuple(x.stride())}")
-    return x.data_ptr()
+    if x.is_cuda and x.is_contiguous():
+        if dtype is None:
+            if x.numel() * x.element_size() >= count:
+                return x.data_ptr()
+        elif x.numel() >= count and x.dtype is (_torch_types or _types()).get(dtype, x.dtype):
+            return x.data_ptr()
+    raise OscarError(ERR_INVALID, f"{name} must be a contiguous CUDA tensor of at least {count} "
+                                  f"{'bytes' if dtype is None else _types().get(dtype, 'elements')}, not {x.dtype} "
+                                  f"{tuple(x.shape)} on {x.device} with strides {tuple(x.stride())}")
 
 
 def _rows(x, name: str, dtype: int, tokens: int, heads: int, d: int):
@@ -370,10 +384,11 @@ def _rows(x, name: str, dtype: int, tokens: int, heads: int, d: int):
     are long."""
     if x is None or isinstance(x, int):
         return x, 0
-    want, shape = _DTYPE_NAMES.get(dtype, ""), tuple(x.shape)
-    if not x.is_cuda or (want and str(x.dtype) != want) or len(shape) != 3 or shape[0] < tokens or shape[1:] != (heads, d):
-        raise OscarError(ERR_INVALID, f"{name} must be a [{tokens}][{heads}][{d}] CUDA tensor of {want}, not {x.dtype} "
-                                      f"{shape} on {x.device}")
+    shape = x.shape
+    if not x.is_cuda or x.dtype is not (_torch_types or _types()).get(dtype, x.dtype) or len(shape) != 3 \
+            or shape[0] < tokens or shape[1] != heads or shape[2] != d:
+        raise OscarError(ERR_INVALID, f"{name} must be a [{tokens}][{heads}][{d}] CUDA tensor of {_types().get(dtype)}, "
+                                      f"not {x.dtype} {tuple(shape)} on {x.device}")
     t, h, c = x.stride()
     if c != 1 or (heads > 1 and h != d):
         raise OscarError(ERR_INVALID, f"the heads and channels of {name} must be adjacent, not strided {(t, h, c)}")
@@ -406,8 +421,8 @@ def oscar_kv8_pages_needed(cfg: oscar_config, seq_len: int) -> int:
 def oscar_kv8_bind(ctx: int, fmt: int, pool, tail) -> None:
     """Bind an 8-bit cache: device buffers of oscar_kv8_pool_bytes and oscar_kv8_tail_bytes (any element type)."""
     cfg = _config(ctx)
-    _check(load().oscar_kv8_bind(ctx, fmt, _dense(pool, "pool", oscar_kv8_pool_bytes(cfg), ""),
-                                 _dense(tail, "tail", oscar_kv8_tail_bytes(cfg), "")))
+    _check(load().oscar_kv8_bind(ctx, fmt, _dense(pool, "pool", oscar_kv8_pool_bytes(cfg), None),
+                                 _dense(tail, "tail", oscar_kv8_tail_bytes(cfg), None)))
 
 
 def oscar_kv8_write(ctx, layer, K, V, dtype, cu_seqlens, start_pos, batch, total_tokens, block_table, bt_stride,
@@ -455,10 +470,10 @@ def oscar_kv8_decode_attn(ctx, layer, q, q_dtype, out, out_dtype, block_table, b
     hq, d = cfg.n_q_heads, cfg.head_dim
     qp, qs = _rows(q, "q", q_dtype, batch, hq, d)
     _check(load().oscar_kv8_decode_attn(ctx, layer, qp, qs, q_dtype,
-                                        _dense(out, "out", batch * hq * d, _DTYPE_NAMES.get(out_dtype, "")), out_dtype,
+                                        _dense(out, "out", batch * hq * d, out_dtype), out_dtype,
                                         _dense(block_table, "block_table", batch * bt_stride), bt_stride,
                                         _dense(seq_lens, "seq_lens", batch), _dense(req_slot, "req_slot", batch), batch,
-                                        max_seq, _dense(workspace, "workspace", ws_bytes, ""), ws_bytes,
+                                        max_seq, _dense(workspace, "workspace", ws_bytes, None), ws_bytes,
                                         stream_ptr(stream)))
 
 
@@ -470,7 +485,7 @@ def oscar_kv8_select_pages(ctx, layer, q, q_dtype, block_table, bt_stride, seq_l
                                          _dense(block_table, "block_table", batch * bt_stride), bt_stride,
                                          _dense(seq_lens, "seq_lens", batch), batch, max_seq, keep_first, keep_last,
                                          n_select, _dense(page_idx, "page_idx", batch * cfg.n_kv_heads * n_select),
-                                         _dense(workspace, "workspace", ws_bytes, ""), ws_bytes, stream_ptr(stream)))
+                                         _dense(workspace, "workspace", ws_bytes, None), ws_bytes, stream_ptr(stream)))
 
 
 def oscar_kv8_sparse_decode_attn(ctx, layer, q, q_dtype, out, out_dtype, page_idx, n_select, block_table, bt_stride,
@@ -479,12 +494,12 @@ def oscar_kv8_sparse_decode_attn(ctx, layer, q, q_dtype, out, out_dtype, page_id
     hq, d = cfg.n_q_heads, cfg.head_dim
     qp, qs = _rows(q, "q", q_dtype, batch, hq, d)
     _check(load().oscar_kv8_sparse_decode_attn(ctx, layer, qp, qs, q_dtype,
-                                               _dense(out, "out", batch * hq * d, _DTYPE_NAMES.get(out_dtype, "")),
+                                               _dense(out, "out", batch * hq * d, out_dtype),
                                                out_dtype,
                                                _dense(page_idx, "page_idx", batch * cfg.n_kv_heads * n_select), n_select,
                                                _dense(block_table, "block_table", batch * bt_stride), bt_stride,
                                                _dense(seq_lens, "seq_lens", batch), _dense(req_slot, "req_slot", batch),
-                                               batch, _dense(workspace, "workspace", ws_bytes, ""), ws_bytes,
+                                               batch, _dense(workspace, "workspace", ws_bytes, None), ws_bytes,
                                                stream_ptr(stream)))
 
 

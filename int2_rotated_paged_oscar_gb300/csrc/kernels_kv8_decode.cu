@@ -491,6 +491,7 @@ __global__ void __launch_bounds__(128) kv8_combine_kernel(const __grid_constant_
   const Geom& g = a.g;
   const int head = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
+  pdl_launch_dependents();
   const int n = a.seq_lens[b], slot = a.req_slot[b];
   const bool ok = length_ok(a, n);
   const int have = !ok ? 0 : a.page_idx ? a.n_select : n / g.P;

@@ -91,7 +91,7 @@ oscar_status write_rows(oscar_ctx* ctx, int32_t layer, const void* K, int64_t k_
   a.tail = ctx->kv8_tail;
   a.status = ctx->d_status;
   LaunchScope ls(ctx, name, stream);
-  const int e = oscar::launch_kv8_write(a, stream);
+  const int e = oscar::launch_kv8_write(a, stream, !ctx->timing);
   ls.done(e);
   if (e) return cuda_fail(e, "8-bit write launch");
   return OSCAR_OK;
@@ -297,7 +297,7 @@ oscar_status oscar_kv8_select_pages(oscar_ctx* ctx, int32_t layer, const void* q
   a.ws = static_cast<uint8_t*>(workspace);
   a.max_pages = max_seq / ctx->g.P;
   LaunchScope ls(ctx, "kv8_select", stream);
-  const int e = oscar::launch_kv8_select(a, stream);
+  const int e = oscar::launch_kv8_select(a, stream, !ctx->timing);
   ls.done(e);
   if (e) return cuda_fail(e, "page selection launch");
   return OSCAR_OK;

@@ -114,10 +114,10 @@ struct ForkSlots {
 Kv8DecodeWs kv8_plan(const Geom& g, int batch, long long max_pages);
 size_t kv8_select_ws_bytes(const Geom& g, int batch, int max_seq);
 
-int launch_kv8_write(const Kv8WriteArgs& a, void* stream);
+int launch_kv8_write(const Kv8WriteArgs& a, void* stream, bool pdl);
 int launch_kv8_decode(const Kv8DecodeArgs& a, void* stream, bool pdl);
 int launch_kv8_combine(const Kv8DecodeArgs& a, void* stream, bool pdl);
-int launch_kv8_select(const Kv8SelectArgs& a, void* stream);
+int launch_kv8_select(const Kv8SelectArgs& a, void* stream, bool pdl);
 // rows [0, n_rows) of the src slot's tail to every dst slot, in every layer
 int launch_kv8_fork_tail(const Geom& g, uint16_t* tail, int src, const ForkSlots& dst, int n_rows, void* stream);
 // pool: [layers][num_pages][page_bytes]; page src[i] to page dst[i] in every layer

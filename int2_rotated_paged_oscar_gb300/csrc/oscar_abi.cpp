@@ -8,6 +8,7 @@
 // message.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -384,18 +385,27 @@ oscar_status oscar_ref_pages(oscar_ctx* ctx, const int32_t* ids, int32_t n) {
 oscar_status oscar_unref_pages(oscar_ctx* ctx, const int32_t* ids, int32_t n) {
   if (!ctx || (n > 0 && !ids) || n < 0) return fail(OSCAR_ERR_INVALID, "bad arguments to oscar_unref_pages");
   std::lock_guard<std::mutex> lk(ctx->mu);
-  std::map<int32_t, int> dec;
-  for (int i = 0; i < n; ++i) {
-    if (ids[i] < 0 || ids[i] >= ctx->g.num_pages) return fail(OSCAR_ERR_INVALID, "page %d out of range", ids[i]);
-    dec[ids[i]]++;
+  // one reference at a time, all given back if one of them cannot be taken
+  int32_t done = 0;
+  for (; done < n; ++done) {
+    if (ids[done] < 0 || ids[done] >= ctx->g.num_pages || ctx->refcount[ids[done]] <= 0) break;
+    ctx->refcount[ids[done]]--;
   }
-  for (auto& kv : dec)
-    if (ctx->refcount[kv.first] < kv.second)
-      return fail(OSCAR_ERR_INVALID, "page %d released more often than referenced", kv.first);
-  for (auto& kv : dec) {
-    ctx->refcount[kv.first] -= kv.second;
-    if (ctx->refcount[kv.first] == 0) ctx->free_stack.push_back(kv.first);
+  if (done < n) {
+    const int32_t id = ids[done];
+    while (done > 0) ctx->refcount[ids[--done]]++;
+    if (id < 0 || id >= ctx->g.num_pages) return fail(OSCAR_ERR_INVALID, "page %d out of range", id);
+    return fail(OSCAR_ERR_INVALID, "page %d released more often than referenced", id);
   }
+  // freed pages return in ascending order, each once
+  const size_t first = ctx->free_stack.size();
+  for (int i = 0; i < n; ++i)
+    if (ctx->refcount[ids[i]] == 0) {
+      ctx->refcount[ids[i]] = -1;
+      ctx->free_stack.push_back(ids[i]);
+    }
+  for (size_t i = first; i < ctx->free_stack.size(); ++i) ctx->refcount[ctx->free_stack[i]] = 0;
+  std::sort(ctx->free_stack.begin() + first, ctx->free_stack.end());
   return OSCAR_OK;
 }
 
