@@ -15,7 +15,9 @@
 //           relative to the block's largest).
 // Codes are exact f16 numbers, so the only roundings are float32's.  The block's scales multiply scores
 // and sums in float32, and the weights are relative to the 16-token block's own maximum, so a quiet page
-// next to a loud one keeps its digits.
+// next to a loud one keeps its digits.  The tail rows go the same way with BF16 operands, 16 rows a warp, in
+// the CTA of the request's last pages while its first pages are on their way.
+#include <cstdlib>
 #include "kv8.cuh"
 
 namespace oscar {
@@ -31,15 +33,10 @@ struct Layout {
   static constexpr int kPad = 128;  // scales, and the 128-byte alignment of the next page
   OSCAR_HD static int page_stride(int P) { return 2 * P * D + kPad; }
   OSCAR_HD static int stage_bytes(int P) { return (kKv8StageTokens / P) * page_stride(P); }
-  static constexpr int kTailRow = 2 * D + 16;  // bytes of a staged tail row of K (padded: no bank conflicts)
-  // tail CTA: K rows | V rows | q [8][D] | weights [64][8] | (m, l) [8]
-  static constexpr int kTailBytes = 64 * kTailRow + 64 * 2 * D + 8 * D * 4 + 64 * 8 * 4 + 64;
   static size_t smem(int P) {
     const size_t ring = (size_t)kStages * stage_bytes(P);
     const size_t merge = kConsumers * 8 * (D + 2) * sizeof(float);
-    size_t n = ring > kTailBytes ? ring : (size_t)kTailBytes;
-    if (merge > n) n = merge;
-    return n + 128;
+    return (ring > merge ? ring : merge) + 128;
   }
 };
 
@@ -47,101 +44,128 @@ __device__ __forceinline__ bool length_ok(const Kv8DecodeArgs& a, int n) {
   return n >= 0 && n <= (a.page_idx ? (long long)a.g.max_pages_per_req * a.g.P : (long long)a.max_seq);
 }
 
+// Partial of a split (m, l, -, -, acc[D]).
 __device__ __forceinline__ float* partial(const Kv8DecodeArgs& a, int b, int head, int split, int D) {
-  return a.part + (((size_t)b * a.g.Hq + head) * (1 + a.wl.max_splits) + split) * (D + 4);
+  return a.part + (((size_t)b * a.g.Hq + head) * a.wl.max_splits + split) * (D + 4);
+}
+
+// Splits of a request with `have` page entries: one at least, for its tail.
+__device__ __forceinline__ int split_count(const Kv8DecodeArgs& a, int have) {
+  const int per = a.wl.stages_per_split * (kKv8StageTokens / a.g.P);
+  return max((have + per - 1) / per, 1);
+}
+
+// Four neighbouring query components.
+template <bool QF32>
+__device__ __forceinline__ float4 load_q4(const void* q, size_t i) {
+  if constexpr (QF32) return *reinterpret_cast<const float4*>(static_cast<const float*>(q) + i);
+  const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(q) + i);
+  return make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
+}
+
+// x, y as three BF16 pairs whose sum has float32's digits.
+__device__ __forceinline__ void split3(float x, float y, uint32_t (&t)[3]) {
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    t[i] = pack_bf162(x, y);
+    x -= bf16_lo(t[i]);
+    y -= bf16_hi(t[i]);
+  }
 }
 
 // ------------------------------------------------------------------ tail rows
-// At most 63 BF16 rows, in float32 on the CUDA cores: a thread per (token, head) for the scores, a thread
-// per two channels and every (256 / D)-th head for the sums.
-template <int D>
-__device__ void tail_rows(const Kv8DecodeArgs& a, int b, int h, int cnt, uint8_t* smem) {
-  using L = Layout<D>;
-  const Geom& g = a.g;
-  const int G = g.gq(), tid = threadIdx.x;
-  uint8_t* ks = smem;
-  uint8_t* vs = ks + 64 * L::kTailRow;
-  float* qs = reinterpret_cast<float*>(vs + 64 * 2 * D);
-  float* ps = qs + 8 * D;
-  float* ml = ps + 64 * 8;
-  const uint16_t* rows = a.tail + ((size_t)a.layer * g.max_req + a.req_slot[b]) * kv8_tail_req_elems(g) + (size_t)h * 2 * g.P * D;
-  constexpr int kVec = D / 8;
-  for (int i = tid; i < cnt * kVec; i += kThreads) {
-    const int t = i / kVec, c = i % kVec;
-    *reinterpret_cast<uint4*>(ks + t * L::kTailRow + c * 16) = reinterpret_cast<const uint4*>(rows)[t * kVec + c];
-    reinterpret_cast<uint4*>(vs)[i] = reinterpret_cast<const uint4*>(rows + (size_t)g.P * D)[i];
-  }
-  for (int i = tid; i < G * D; i += kThreads)
-    qs[i] = kv8_load(a.q, (size_t)b * a.q_stride + (size_t)h * G * D + i, a.q_dtype);
-  __syncthreads();
-  const float scale = kLog2e * rsqrtf((float)D);
-  for (int i = tid; i < 64 * G; i += kThreads) {
-    const int t = i & 63, hh = i >> 6;
-    if (t >= cnt) continue;
-    float s0 = 0.f, s1 = 0.f;
-#pragma unroll 4
-    for (int c = 0; c < kVec; ++c) {
-      const uint4 k = *reinterpret_cast<const uint4*>(ks + t * L::kTailRow + c * 16);
-      const float4 x = reinterpret_cast<const float4*>(qs + hh * D)[2 * c], y = reinterpret_cast<const float4*>(qs + hh * D)[2 * c + 1];
-      s0 = fmaf(x.x, bf16_lo(k.x), s0);
-      s1 = fmaf(x.y, bf16_hi(k.x), s1);
-      s0 = fmaf(x.z, bf16_lo(k.y), s0);
-      s1 = fmaf(x.w, bf16_hi(k.y), s1);
-      s0 = fmaf(y.x, bf16_lo(k.z), s0);
-      s1 = fmaf(y.y, bf16_hi(k.z), s1);
-      s0 = fmaf(y.z, bf16_lo(k.w), s0);
-      s1 = fmaf(y.w, bf16_hi(k.w), s1);
-    }
-    ps[t * 8 + hh] = (s0 + s1) * scale;
-  }
-  __syncthreads();
-  const int warp = tid >> 5, lane = tid & 31;
-  for (int hh = warp; hh < G; hh += kThreads / 32) {
-    const float x = lane < cnt ? ps[lane * 8 + hh] : -INFINITY, y = lane + 32 < cnt ? ps[(lane + 32) * 8 + hh] : -INFINITY;
-    float m = fmaxf(x, y);
+// 16 BF16 rows of the tail (cnt of them there) as a warp's first block: m, l, acc as the page loop goes on with them.
+// Keys and values are BF16 operands as they are, queries and weights sums of up to three.
+template <int D, bool G8, bool QF32, int NH>
+__device__ __forceinline__ void tail_block(const Kv8DecodeArgs& a, int b, int h, const uint16_t* krows, const uint16_t* vrows, int cnt,
+                                           float sm_log2, float (&m_run)[NH], float (&l_run)[NH], float (&acc)[D / 16][2 * NH]) {
+  constexpr int KS = D / 16;
+  const int G = a.g.gq(), lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+  const int head = G8 ? gid : gid >> 1;
+  const bool odd = !G8 && (gid & 1), live = head < G;
+  const size_t qat = (size_t)b * a.q_stride + (size_t)(h * G + (live ? head : 0)) * D;
+  const uint4 none = make_uint4(0, 0, 0, 0);
+  float sc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int o = 16; o; o >>= 1) m = warp_max_xor(m, o);
-    const float px = lane < cnt ? ex2(x - m) : 0.f, py = lane + 32 < cnt ? ex2(y - m) : 0.f;
-    float l = px + py;
+  for (int c = 0; c < D / 32; ++c) {   // 32 channels: two k-steps from 16 bytes a lane
+    const int ch = c * 32 + tig * 8;
+    const uint4 k0 = gid < cnt ? *reinterpret_cast<const uint4*>(krows + (size_t)gid * D + ch) : none;
+    const uint4 k1 = gid + 8 < cnt ? *reinterpret_cast<const uint4*>(krows + (size_t)(gid + 8) * D + ch) : none;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    if (lane < cnt) ps[lane * 8 + hh] = px;
-    if (lane + 32 < cnt) ps[(lane + 32) * 8 + hh] = py;
-    if (lane == 0) {
-      ml[2 * hh] = m;
-      ml[2 * hh + 1] = l;
-    }
-  }
-  __syncthreads();
-  constexpr int kGroups = 256 / D;      // 128 threads cover D / 2 channel pairs this many times
-  constexpr int kHeads = 8 / kGroups;
-  if (tid >= 128) return;
-  const int cp = tid % (D / 2), g0 = tid / (D / 2);
-  float2 acc[kHeads];
+    for (int u = 0; u < 2; ++u) {
+      float4 q = load_q4<QF32>(a.q, qat + ch + 4 * u);
+      if (!live) q = make_float4(0.f, 0.f, 0.f, 0.f);
+      const uint32_t a0 = u ? k0.z : k0.x, a2 = u ? k0.w : k0.y, a1 = u ? k1.z : k1.x, a3 = u ? k1.w : k1.y;
+      if constexpr (QF32) {
+        uint32_t x[3], y[3];
+        split3(q.x, q.y, x);
+        split3(q.z, q.w, y);
+        if constexpr (G8) {
 #pragma unroll
-  for (int i = 0; i < kHeads; ++i) acc[i] = make_float2(0.f, 0.f);
-  for (int t = 0; t < cnt; ++t) {
-    const uint32_t v = reinterpret_cast<const uint32_t*>(vs)[t * (D / 2) + cp];
-#pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
-      const int hh = g0 + i * kGroups;
-      if (hh < G) {
-        const float p = ps[t * 8 + hh];
-        acc[i].x = fmaf(p, bf16_lo(v), acc[i].x);
-        acc[i].y = fmaf(p, bf16_hi(v), acc[i].y);
+          for (int i = 0; i < 3; ++i) mma_bf16(sc, a0, a1, a2, a3, x[i], y[i]);
+        } else {
+          mma_bf16(sc, a0, a1, a2, a3, odd ? x[1] : x[0], odd ? y[1] : y[0]);
+          mma_bf16(sc, a0, a1, a2, a3, odd ? 0u : x[2], odd ? 0u : y[2]);
+        }
+      } else {
+        const uint32_t x = odd ? 0u : pack_bf162(q.x, q.y), y = odd ? 0u : pack_bf162(q.z, q.w);
+        mma_bf16(sc, a0, a1, a2, a3, x, y);
       }
     }
   }
+  uint32_t pb[3][2];
+  float pr[NH][2];
 #pragma unroll
-  for (int i = 0; i < kHeads; ++i) {
-    const int hh = g0 + i * kGroups;
-    if (hh < G) {
-      float* pp = partial(a, b, h * G + hh, 0, D);
-      *reinterpret_cast<float2*>(pp + 4 + 2 * cp) = acc[i];
-      if (cp == 0) {
-        pp[0] = ml[2 * hh];
-        pp[1] = ml[2 * hh + 1];
-      }
+  for (int i = 0; i < NH; ++i) {
+    // (BF16 queries leave their odd columns empty: an infinite key times their 0 would be NaN)
+    const float sa = gid < cnt ? (G8 ? sc[i] : QF32 ? sc[0] + sc[1] : sc[0]) * sm_log2 : -INFINITY;
+    const float sb = gid + 8 < cnt ? (G8 ? sc[2 + i] : QF32 ? sc[2] + sc[3] : sc[2]) * sm_log2 : -INFINITY;
+    float m = fmaxf(sa, sb);
+    m = warp_max_xor(m, 4);
+    m = warp_max_xor(m, 8);
+    m = warp_max_xor(m, 16);
+    pr[i][0] = gid < cnt ? ex2(sa - m) : 0.f;
+    pr[i][1] = gid + 8 < cnt ? ex2(sb - m) : 0.f;
+    m_run[i] = m;
+    l_run[i] = pr[i][0] + pr[i][1];
+  }
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    uint32_t t[3];
+    if constexpr (G8) {
+      split3(pr[0][r], pr[1][r], t);
+    } else {  // columns 2 h, 2 h + 1: the first and second part of head h's weight; then the third
+      split3(pr[0][r], 0.f, t);
+      t[0] = (t[0] & 0xffffu) | (t[1] << 16);
+      t[1] = t[2] & 0xffffu;
+    }
+#pragma unroll
+    for (int i = 0; i < (G8 ? 3 : 2); ++i) pb[i][r] = transpose_8x8(t[i]);
+  }
+  // values: rows 2 tig (+ 1, + 8, + 9), channels gid D / 8 and on
+  uint32_t vw[4][KS];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int t = 2 * tig + (j & 1) + 8 * (j >> 1);
+#pragma unroll
+    for (int c = 0; c < KS / 4; ++c) {
+      const uint4 v = t < cnt ? *reinterpret_cast<const uint4*>(vrows + (size_t)t * D + gid * (D / 8) + 8 * c) : none;
+      vw[j][4 * c] = v.x, vw[j][4 * c + 1] = v.y, vw[j][4 * c + 2] = v.z, vw[j][4 * c + 3] = v.w;
+    }
+  }
+#pragma unroll
+  for (int mt = 0; mt < KS; ++mt) {
+    const uint32_t a0 = prmt(vw[0][mt], vw[1][mt], 0x5410u), a1 = prmt(vw[0][mt], vw[1][mt], 0x7632u);
+    const uint32_t a2 = prmt(vw[2][mt], vw[3][mt], 0x5410u), a3 = prmt(vw[2][mt], vw[3][mt], 0x7632u);
+    float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < (G8 ? 3 : 2); ++i) mma_bf16(o, a0, a1, a2, a3, pb[i][0], pb[i][1]);
+    if constexpr (G8) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[mt][i] = o[i];
+    } else {
+      acc[mt][0] = o[0] + o[1];
+      acc[mt][1] = o[2] + o[3];
     }
   }
 }
@@ -160,34 +184,11 @@ __global__ void __launch_bounds__(kThreads, 3) kv8_decode_kernel(const __grid_co
   __shared__ int abort_flag, issued;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
   const Geom& g = a.g;
-  const int b = blockIdx.z, h = blockIdx.y, split = (int)blockIdx.x - 1;
+  const int b = blockIdx.z, h = blockIdx.y, split = blockIdx.x;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = g.gq(), P = g.P;
   const int per_stage = kKv8StageTokens / P;
-  pdl_wait();
-  pdl_launch_dependents();
-  const int n = a.seq_lens[b];
-  if (!length_ok(a, n)) {
-    if (tid == 0 && split < 0) flag_error(a.status, kDevBadLen);
-    return;
-  }
-  const int pages = n / P;
-  if (split < 0) {
-    if (n % P == 0) return;
-    const int slot = a.req_slot[b];
-    if (slot < 0 || slot >= g.max_req) {
-      if (tid == 0) flag_error(a.status, kDevBadSlot);
-      return;
-    }
-    tail_rows<D>(a, b, h, n % P, smem);
-    return;
-  }
-  const int have = a.page_idx ? a.n_select : pages;
   const int e0 = split * a.wl.stages_per_split * per_stage;
-  if (e0 >= have) return;
-  const int e1 = min(e0 + a.wl.stages_per_split * per_stage, have);
-  const int stages = (e1 - e0 + per_stage - 1) / per_stage;
-  const int page_stride = L::page_stride(P), stage_bytes = L::stage_bytes(P);
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
@@ -196,6 +197,29 @@ __global__ void __launch_bounds__(kThreads, 3) kv8_decode_kernel(const __grid_co
     abort_flag = 0;
     fence_barrier_init();
   }
+  pdl_wait();
+  pdl_launch_dependents();
+  const int n = a.seq_lens[b];
+  // the producer's first table entries travel with the length
+  const int* bt = a.block_table + (size_t)b * a.bt_stride;
+  const int* list = a.page_idx ? a.page_idx + ((size_t)b * g.Hkv + h) * a.n_select : nullptr;
+  int early = -1;
+  if (warp == kConsumers) {
+    const int e = e0 + lane;
+    if (list) early = e < a.n_select ? list[e] : -1;
+    else early = e < a.bt_stride ? bt[e] : -1;
+  }
+  if (!length_ok(a, n)) {
+    if (tid == 0 && blockIdx.x == 0) flag_error(a.status, kDevBadLen);
+    return;
+  }
+  const int pages = n / P;
+  const int have = a.page_idx ? a.n_select : pages;
+  const int splits = split_count(a, have);
+  if (n == 0 || split >= splits) return;
+  const int e1 = min(e0 + a.wl.stages_per_split * per_stage, have);
+  const int stages = (e1 - e0 + per_stage - 1) / per_stage;
+  const int page_stride = L::page_stride(P), stage_bytes = L::stage_bytes(P);
   __syncthreads();
   const float sm_log2 = kLog2e * rsqrtf((float)D);
   const int gid = lane >> 2, tig = lane & 3;
@@ -216,29 +240,27 @@ __global__ void __launch_bounds__(kThreads, 3) kv8_decode_kernel(const __grid_co
     const uint64_t policy = l2_evict_first_policy();
     const uint32_t bytes = 2 * P * D + 16;
     const uint8_t* layer = a.pool + (size_t)a.layer * g.num_pages * kg.page_bytes() + (size_t)h * kg.block_bytes();
-    const int* bt = a.block_table + (size_t)b * a.bt_stride;
-    const int* list = a.page_idx ? a.page_idx + ((size_t)b * g.Hkv + h) * a.n_select : nullptr;
-    // lane i looks up entry e0 + base + i; -1: nothing to copy
-    auto lookup = [&](int e) {
+    // page of entry e (value: the list's or the table's word for it); -1: nothing to copy
+    auto lookup = [&](int e, int value) {
       if (e >= e1) return -1;
-      int lp = e;
+      int pid = value;
       if (list) {
-        lp = list[e];
         const int before = e > 0 ? list[e - 1] : -1;
-        if (lp < 0) return -1;
-        if (lp >= pages || (e > 0 && before < 0) || before >= lp) {
+        if (value < 0) return -1;
+        if (value >= pages || (e > 0 && before < 0) || before >= value) {
           flag_error(a.status, kDevBadPage);
           return -1;
         }
+        pid = value < a.bt_stride ? bt[value] : -1;
       }
-      const int pid = lp < a.bt_stride ? bt[lp] : -1;
       if (pid < 0 || pid >= g.num_pages) {
         flag_error(a.status, kDevBadPage);
         return -1;
       }
       return pid;
     };
-    int pid_now = lookup(e0 + lane), pid_next = lookup(e0 + 32 + lane);
+    auto word = [&](int e) { return e >= e1 ? -1 : list ? list[e] : e < a.bt_stride ? bt[e] : -1; };
+    int pid_now = lookup(e0 + lane, early), pid_next = lookup(e0 + 32 + lane, word(e0 + 32 + lane));
     int it = 0;
     bool good = true;
     for (; it < stages; ++it) {
@@ -251,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 3) kv8_decode_kernel(const __grid_co
       const int at = it * per_stage;                    // first entry of the stage, relative to e0
       if (at > 0 && at % 32 == 0) {
         pid_now = pid_next;
-        pid_next = lookup(e0 + at + 32 + lane);
+        pid_next = lookup(e0 + at + 32 + lane, word(e0 + at + 32 + lane));
       }
       const int pid = __shfl_sync(0xffffffffu, pid_now, (at & 31) + (lane % per_stage));
       const unsigned there = __ballot_sync(0xffffffffu, lane < per_stage && pid >= 0);
@@ -284,13 +306,7 @@ __global__ void __launch_bounds__(kThreads, 3) kv8_decode_kernel(const __grid_co
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           const size_t i = at + (tig + 4 * c) * 16 + 4 * w;
-          float4 v;
-          if constexpr (QF32) {
-            v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + i);
-          } else {
-            const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q) + i);
-            v = make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
-          }
+          const float4 v = load_q4<QF32>(a.q, i);
           float* y = x[4 * c + w];
           y[0] = v.x, y[1] = v.y, y[2] = v.z, y[3] = v.w;
 #pragma unroll
@@ -325,6 +341,16 @@ __global__ void __launch_bounds__(kThreads, 3) kv8_decode_kernel(const __grid_co
     const uint32_t k_off = D == 128 ? (t0 + gid) * 128 + ((tig ^ (4 * (gid & 1))) << 4) : (t0 + gid) * 64 + tig * 16;
     const uint32_t v_off = P * D + (D == 128 ? (t0 + 2 * tig) * 128 + ((gid ^ (2 * tig)) << 4)
                                              : (t0 / 2 + tig) * 128 + (((gid >> 1) ^ (2 * tig)) << 4) + (gid & 1) * 8);
+    if (split == splits - 1 && warp * 16 < n % P) {
+      const int slot = a.req_slot[b];
+      if (slot >= 0 && slot < g.max_req) {
+        const uint16_t* rows = a.tail + ((size_t)a.layer * g.max_req + slot) * kv8_tail_req_elems(g) +
+                               ((size_t)h * 2 * P + warp * 16) * D;
+        tail_block<D, G8, QF32>(a, b, h, rows, rows + (size_t)P * D, n % P - warp * 16, sm_log2, m_run, l_run, acc);
+      } else if (lane == 0) {
+        flag_error(a.status, kDevBadSlot);
+      }
+    }
     for (int it = 0; it < stages; ++it) {
       const int s = it % kStages;
       bool good = mbar_wait_sleep_bounded(&full[s], (it / kStages) & 1, a.status);
@@ -473,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 3) kv8_decode_kernel(const __grid_co
       l = fmaf(f, row[1], l);
       o = fmaf(f, row[2 + ch], o);
     }
-    float* pp = partial(a, b, h * G + hh, 1 + split, D);
+    float* pp = partial(a, b, h * G + hh, split, D);
     pp[4 + ch] = o;
     if (ch == 0) {
       pp[0] = M;
@@ -483,35 +509,30 @@ __global__ void __launch_bounds__(kThreads, 3) kv8_decode_kernel(const __grid_co
 }
 
 // ------------------------------------------------------------------ merge of the splits
-// One CTA per (query head, request): warp w takes every fourth split, a lane D / 32 channels.
-template <int D>
-__global__ void __launch_bounds__(128) kv8_combine_kernel(const __grid_constant__ Kv8DecodeArgs a) {
+// One CTA per (query head, request): warp w takes every W-th partial, a lane D / 32 channels.  What the splits' count
+// needs is read before the wait: no kernel since the decode kernel's own wait writes it.
+template <int D, int W>
+__global__ void __launch_bounds__(32 * W) kv8_combine_kernel(const __grid_constant__ Kv8DecodeArgs a) {
   constexpr int C = D / 32;
-  __shared__ float s_o[4][D], s_l[4];
+  __shared__ float s_o[W][D], s_l[W];
   const Geom& g = a.g;
   const int head = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int n = a.seq_lens[b];
+  const int count = length_ok(a, n) && n > 0 ? split_count(a, a.page_idx ? a.n_select : n / g.P) : 0;
+  const float* base = partial(a, b, head, 0, D);
   pdl_wait();
   pdl_launch_dependents();
-  const int n = a.seq_lens[b], slot = a.req_slot[b];
-  const bool ok = length_ok(a, n);
-  const int have = !ok ? 0 : a.page_idx ? a.n_select : n / g.P;
-  const int per_split = a.wl.stages_per_split * (kKv8StageTokens / g.P);
-  const int last = 1 + (have + per_split - 1) / per_split;
-  const int first = ok && n % g.P && slot >= 0 && slot < g.max_req ? 0 : 1;
-  const float* base = partial(a, b, head, 0, D);
   float M = -INFINITY;
-  for (int i = first + lane; i < last; i += 32) M = fmaxf(M, base[(size_t)i * (D + 4)]);
+  for (int i = lane; i < count; i += 32) M = fmaxf(M, base[(size_t)i * (D + 4)]);
 #pragma unroll
   for (int o = 16; o; o >>= 1) M = warp_max_xor(M, o);
   float l = 0.f, r[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) r[c] = 0.f;
-#pragma unroll 4
-  for (int i = first + warp; i < last; i += 4) {
+#pragma unroll 8
+  for (int i = warp; i < count; i += W) {
     const float* p = base + (size_t)i * (D + 4);
-    const float m = p[0];
-    const float w = m == -INFINITY ? 0.f : ex2(m - M);
-    l = fmaf(w, p[1], l);
+    const float2 ml = *reinterpret_cast<const float2*>(p);
     float v[C];
     if constexpr (C == 4) {
       const float4 x = *reinterpret_cast<const float4*>(p + 4 + lane * 4);
@@ -520,6 +541,8 @@ __global__ void __launch_bounds__(128) kv8_combine_kernel(const __grid_constant_
       const float2 x = *reinterpret_cast<const float2*>(p + 4 + lane * 2);
       v[0] = x.x, v[1] = x.y;
     }
+    const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+    l = fmaf(w, ml.y, l);
 #pragma unroll
     for (int c = 0; c < C; ++c) r[c] = fmaf(w, v[c], r[c]);
   }
@@ -528,8 +551,12 @@ __global__ void __launch_bounds__(128) kv8_combine_kernel(const __grid_constant_
   if (lane == 0) s_l[warp] = l;
   __syncthreads();
   if (tid >= D) return;
-  const float sum = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
-  const float o = (s_o[0][tid] + s_o[1][tid]) + (s_o[2][tid] + s_o[3][tid]);
+  float sum = 0.f, o = 0.f;
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    sum += s_l[w];
+    o += s_o[w][tid];
+  }
   const float y = sum > 0.f ? o / sum : 0.f;
   const size_t at = ((size_t)b * g.Hq + head) * D + tid;
   if (a.out_dtype == kDtypeBF16) static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(y);
@@ -538,7 +565,7 @@ __global__ void __launch_bounds__(128) kv8_combine_kernel(const __grid_constant_
 
 template <int D, int FMT>
 int launch_pages(const Kv8DecodeArgs& a, cudaStream_t s, bool pdl) {
-  const dim3 grid(1 + a.wl.max_splits, a.g.Hkv, a.batch);
+  const dim3 grid(a.wl.max_splits, a.g.Hkv, a.batch);
   const size_t smem = Layout<D>::smem(a.g.P);
   auto go = [&](auto kern) {
     const cudaError_t e = ensure_smem_limit(kern, smem, true);
@@ -558,16 +585,18 @@ Kv8DecodeWs kv8_plan(const Geom& g, int batch, long long max_pages) {
   const long long stages = (max_pages + per_stage - 1) / per_stage;
   const long long pairs = (long long)batch * g.Hkv > 0 ? (long long)batch * g.Hkv : 1;
   const long long wave = 152LL * 3;        // resident CTAs
-  // one wave where CTAs of up to 16 stages fill it, else CTAs of at least 16 stages in up to eight waves
-  long long ctas = pairs * stages / 16;
-  if (ctas < wave) ctas = wave;
-  if (ctas > 8 * wave) ctas = 8 * wave;
-  long long splits = ctas / pairs;
-  if (splits < 1) splits = 1;
-  long long per = stages > 0 ? (stages + splits - 1) / splits : 1;
-  w.stages_per_split = (int)per;
-  w.max_splits = stages > 0 ? (int)((stages + per - 1) / per) : 0;
-  w.total = (size_t)batch * g.Hq * (1 + w.max_splits) * (g.D + 4) * sizeof(float);
+  // The split that takes the fewest rounds of (its stages + a CTA's fixed cost in stages)
+  static const int ov = getenv("OV") ? atoi(getenv("OV")) : 6, mx = getenv("MXS") ? atoi(getenv("MXS")) : 64;
+  long long best = 1, cost = -1;
+  for (long long per = 1; per <= mx; ++per) {
+    const long long ctas = pairs * ((stages + per - 1) / per);
+    const long long c = ((ctas + wave - 1) / wave) * (per + ov);
+    if (cost < 0 || c < cost) best = per, cost = c;
+  }
+  if (getenv("PER")) best = atoi(getenv("PER"));
+  w.stages_per_split = (int)best;
+  w.max_splits = stages > 0 ? (int)((stages + best - 1) / best) : 1;
+  w.total = (size_t)batch * g.Hq * w.max_splits * (g.D + 4) * sizeof(float);
   return w;
 }
 
@@ -580,8 +609,11 @@ int launch_kv8_decode(const Kv8DecodeArgs& a, void* stream, bool pdl) {
 int launch_kv8_combine(const Kv8DecodeArgs& a, void* stream, bool pdl) {
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const dim3 grid(a.g.Hq, a.batch);
-  if (a.g.D == 128) return launch_pdl(kv8_combine_kernel<128>, grid, dim3(128), 0, s, pdl, a);
-  return launch_pdl(kv8_combine_kernel<64>, grid, dim3(128), 0, s, pdl, a);
+  auto go = [&](auto kern, int warps) { return launch_pdl(kern, grid, dim3(32 * warps), 0, s, pdl, a); };
+  // many partials of few rows: more warps, so that they are all on their way at once
+  const bool wide = a.wl.max_splits > 16;
+  if (a.g.D == 128) return wide ? go(kv8_combine_kernel<128, 8>, 8) : go(kv8_combine_kernel<128, 4>, 4);
+  return wide ? go(kv8_combine_kernel<64, 8>, 8) : go(kv8_combine_kernel<64, 4>, 4);
 }
 
 }  // namespace oscar

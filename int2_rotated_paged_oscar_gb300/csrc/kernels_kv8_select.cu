@@ -22,7 +22,9 @@ constexpr int kScoreThreads = 128;
 constexpr int kPagesPerCta = 64;   // 8 lanes a page, 16 pages at a time
 constexpr int kPickThreads = 512;
 constexpr int kSmemKeys = 8192;    // pages whose keys the pick kernel holds in shared memory
-constexpr int kSerialBand = 64;    // band of pages scored again that is ranked within shared memory tiles of this size
+constexpr int kBinBits = 11, kBins = 1 << kBinBits;
+constexpr int kFew = 64;           // keys that are ranked one by one
+constexpr int kTile = 64;          // pages scored again are ranked against tiles of this many
 using Key = unsigned long long;
 
 // Workspace: float32 keys [batch][Hkv][max_pages], float64 keys of the band (same count), its page indexes,
@@ -48,9 +50,7 @@ __device__ __forceinline__ uint32_t key_of(float x) {
   const uint32_t u = __float_as_uint(x + 0.f);
   return x != x ? 0u : (u >> 31) ? ~u : (u | 0x80000000u);
 }
-__device__ __forceinline__ double value_of(uint32_t k) {
-  return (double)__uint_as_float((k >> 31) ? (k & 0x7fffffffu) : ~k);
-}
+__device__ __forceinline__ float value_of(uint32_t k) { return __uint_as_float((k >> 31) ? (k & 0x7fffffffu) : ~k); }
 __device__ __forceinline__ Key key_of(double x) {
   const Key u = (Key)__double_as_longlong(x + 0.0);
   return x != x ? 0ull : (u >> 63) ? ~u : (u | 0x8000000000000000ull);
@@ -65,104 +65,120 @@ __device__ __forceinline__ bool kept(const Kv8SelectArgs& a, int p, int pages) {
   return p < a.keep_first || p >= pages - a.keep_last;
 }
 
+// sum_h max(q_hc, 0) and sum_h max(-q_hc, 0) over the heads of kv head h (a NaN stays one).
+__device__ __forceinline__ float2 query_sums(const Kv8SelectArgs& a, int b, int h, int c, int D) {
+  const int G = a.g.gq();
+  const size_t at = (size_t)b * a.q_stride + (size_t)h * G * D + c;
+  float q[8];
+#pragma unroll
+  for (int hh = 0; hh < 8; ++hh) q[hh] = hh < G ? kv8_load(a.q, at + (size_t)hh * D, a.q_dtype) : 0.f;
+  float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int hh = 0; hh < 8; ++hh) {
+    s.x += q[hh] < 0.f ? 0.f : q[hh];
+    s.y += q[hh] > 0.f ? 0.f : -q[hh];
+  }
+  return s;
+}
+
 // ------------------------------------------------------------------ scores
 template <int D, int FMT>
 __global__ void __launch_bounds__(kScoreThreads) kv8_score_kernel(const __grid_constant__ Kv8SelectArgs a) {
   constexpr int C = D / 8;                 // channels of a lane
+  constexpr int kRounds = kPagesPerCta / (kScoreThreads / 8);
   __shared__ float s_bound[kScoreThreads / 32];
+  __shared__ __align__(16) float s_wa[D], s_wb[D];
   const Geom& g = a.g;
   const Kv8Geom kg{g.P, D, g.Hkv};
   const int b = blockIdx.z, h = blockIdx.y, tid = threadIdx.x, lane = tid & 31, sub = lane & 7;
-  const int G = g.gq();
   pdl_wait();
   pdl_launch_dependents();
   const int n = a.seq_lens[b];
+  const int p0 = blockIdx.x * kPagesPerCta;
+  // the table entries and the query travel together
+  int pids[kRounds];
+#pragma unroll
+  for (int it = 0; it < kRounds; ++it) {
+    const int p = p0 + it * (kScoreThreads / 8) + (tid >> 3);
+    pids[it] = p < a.bt_stride ? a.block_table[(size_t)b * a.bt_stride + p] : -1;
+  }
+  for (int c = tid; c < D; c += kScoreThreads) {
+    // (channels 4 w .. 4 w + 3 of lane `sub` next to those of the other lanes: no bank conflicts)
+    const float2 x = query_sums(a, b, h, c, D);
+    const int at = ((c % C) / 4 * 8 + c / C) * 4 + c % 4;
+    s_wa[at] = x.x;
+    s_wb[at] = x.y;
+  }
   if (n < 0 || n > a.max_seq) return;
-  const int pages = n / g.P, p0 = blockIdx.x * kPagesPerCta;
+  const int pages = n / g.P;
   if (pages <= a.n_select || p0 >= pages) return;
-  float wa[C], wb[C];
+  __syncthreads();
+  // and so do the bounds of all this CTA's pages
+  const uint8_t* layer = a.pool + (size_t)a.layer * g.num_pages * kg.page_bytes() + (size_t)h * kg.block_bytes();
+  uint32_t lo[kRounds][C / 4], hi[kRounds][C / 4];
+  float scale[kRounds];
 #pragma unroll
-  for (int c = 0; c < C; ++c) wa[c] = wb[c] = 0.f;
-  for (int hh = 0; hh < G; ++hh) {
-    const size_t at = (size_t)b * a.q_stride + (size_t)(h * G + hh) * D + sub * C;
+  for (int it = 0; it < kRounds; ++it) {
+    const int p = p0 + it * (kScoreThreads / 8) + (tid >> 3);
+    const bool wanted = p < pages && !kept(a, p, pages);
+    if (wanted && (pids[it] < 0 || pids[it] >= g.num_pages) && sub == 0) flag_error(a.status, kDevBadPage);
+    if (!wanted || pids[it] >= g.num_pages) pids[it] = -1;
+  }
 #pragma unroll
-    for (int c = 0; c < C; c += 8) {
-      float x[8];
-      if (a.q_dtype == kDtypeBF16) {
-        const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at + c);
-        x[0] = bf16_lo(u.x), x[1] = bf16_hi(u.x), x[2] = bf16_lo(u.y), x[3] = bf16_hi(u.y);
-        x[4] = bf16_lo(u.z), x[5] = bf16_hi(u.z), x[6] = bf16_lo(u.w), x[7] = bf16_hi(u.w);
-      } else {
-        const float4 u = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at + c);
-        const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at + c + 4);
-        x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {  // (not fmaxf: a NaN has to stay one)
-        wa[c + i] += x[i] < 0.f ? 0.f : x[i];
-        wb[c + i] += x[i] > 0.f ? 0.f : -x[i];
-      }
+  for (int it = 0; it < kRounds; ++it) {
+    const uint8_t* block = layer + (size_t)max(pids[it], 0) * kg.page_bytes();   // (page 0 in the place of none)
+    scale[it] = *reinterpret_cast<const float*>(block + kg.scale_off());
+    if constexpr (C == 16) {
+      const uint4 x = *reinterpret_cast<const uint4*>(block + kg.lo_off() + sub * C);
+      const uint4 y = *reinterpret_cast<const uint4*>(block + kg.hi_off() + sub * C);
+      lo[it][0] = x.x, lo[it][1] = x.y, lo[it][2] = x.z, lo[it][3] = x.w;
+      hi[it][0] = y.x, hi[it][1] = y.y, hi[it][2] = y.z, hi[it][3] = y.w;
+    } else {
+      const uint2 x = *reinterpret_cast<const uint2*>(block + kg.lo_off() + sub * C);
+      const uint2 y = *reinterpret_cast<const uint2*>(block + kg.hi_off() + sub * C);
+      lo[it][0] = x.x, lo[it][1] = x.y;
+      hi[it][0] = y.x, hi[it][1] = y.y;
     }
   }
-  float mass = 0.f;
+  float mass = 0.f, u[kRounds];
 #pragma unroll
-  for (int c = 0; c < C; ++c) mass += wa[c] + wb[c];
+  for (int it = 0; it < kRounds; ++it) u[it] = 0.f;
 #pragma unroll
-  for (int o = 1; o < 8; o <<= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
+  for (int w = 0; w < C / 4; ++w) {
+    const float4 wa = reinterpret_cast<const float4*>(s_wa)[w * 8 + sub], wb = reinterpret_cast<const float4*>(s_wb)[w * 8 + sub];
+    mass += ((wa.x + wb.x) + (wa.y + wb.y)) + ((wa.z + wb.z) + (wa.w + wb.w));
+#pragma unroll
+    for (int it = 0; it < kRounds; ++it) {
+      const uint32_t l0 = kv8_pair<FMT, 0>(lo[it][w]), l1 = kv8_pair<FMT, 1>(lo[it][w]);
+      const uint32_t h0 = kv8_pair<FMT, 0>(hi[it][w]), h1 = kv8_pair<FMT, 1>(hi[it][w]);
+      const float2 x0 = __half22float2(*reinterpret_cast<const __half2*>(&l0)), x1 = __half22float2(*reinterpret_cast<const __half2*>(&l1));
+      const float2 y0 = __half22float2(*reinterpret_cast<const __half2*>(&h0)), y1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
+      u[it] = fmaf(wa.x, y0.x, fmaf(-wb.x, x0.x, u[it]));
+      u[it] = fmaf(wa.y, y0.y, fmaf(-wb.y, x0.y, u[it]));
+      u[it] = fmaf(wa.z, y1.x, fmaf(-wb.z, x1.x, u[it]));
+      u[it] = fmaf(wa.w, y1.y, fmaf(-wb.w, x1.y, u[it]));
+    }
+  }
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) {
+    mass += __shfl_xor_sync(0xffffffffu, mass, o);
+#pragma unroll
+    for (int it = 0; it < kRounds; ++it) u[it] += __shfl_xor_sync(0xffffffffu, u[it], o);
+  }
   mass *= (FMT == kKv8Int8 ? 127.f : 448.f) * 0x1p-18f;
   uint32_t* keys = reinterpret_cast<uint32_t*>(a.ws + select_ws(g.Hkv, a.batch, a.max_pages).keys) +
                    ((size_t)b * g.Hkv + h) * a.max_pages;
-  const uint8_t* layer = a.pool + (size_t)a.layer * g.num_pages * kg.page_bytes() + (size_t)h * kg.block_bytes();
   float bound = 0.f;
 #pragma unroll
-  for (int it = 0; it < kPagesPerCta / (kScoreThreads / 8); ++it) {
+  for (int it = 0; it < kRounds; ++it) {
     const int p = p0 + it * (kScoreThreads / 8) + (tid >> 3);
-    int pid = -1;
-    bool scored = false;
-    if (p < pages && !kept(a, p, pages)) {
-      pid = page_id(a, b, p);
-      scored = pid >= 0;
-      if (!scored && sub == 0) flag_error(a.status, kDevBadPage);
-    }
-    float u = 0.f, scale = 0.f;
+    const bool scored = pids[it] >= 0;
+    const float score = u[it] * scale[it];
+    if (p < pages && sub == 0) keys[p] = scored ? key_of(score) : 0u;
     if (scored) {
-      const uint8_t* block = layer + (size_t)pid * kg.page_bytes();
-      scale = *reinterpret_cast<const float*>(block + kg.scale_off());
-      uint32_t lo[C / 4], hi[C / 4];
-      if constexpr (C == 16) {
-        const uint4 x = *reinterpret_cast<const uint4*>(block + kg.lo_off() + sub * C);
-        const uint4 y = *reinterpret_cast<const uint4*>(block + kg.hi_off() + sub * C);
-        lo[0] = x.x, lo[1] = x.y, lo[2] = x.z, lo[3] = x.w;
-        hi[0] = y.x, hi[1] = y.y, hi[2] = y.z, hi[3] = y.w;
-      } else {
-        const uint2 x = *reinterpret_cast<const uint2*>(block + kg.lo_off() + sub * C);
-        const uint2 y = *reinterpret_cast<const uint2*>(block + kg.hi_off() + sub * C);
-        lo[0] = x.x, lo[1] = x.y;
-        hi[0] = y.x, hi[1] = y.y;
-      }
-#pragma unroll
-      for (int w = 0; w < C / 4; ++w) {
-        const uint32_t l2[2] = {kv8_pair<FMT, 0>(lo[w]), kv8_pair<FMT, 1>(lo[w])};
-        const uint32_t h2[2] = {kv8_pair<FMT, 0>(hi[w]), kv8_pair<FMT, 1>(hi[w])};
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&l2[i]));
-          const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&h2[i]));
-          const int c = 4 * w + 2 * i;
-          u = fmaf(wa[c], y.x, u);
-          u = fmaf(-wb[c], x.x, u);
-          u = fmaf(wa[c + 1], y.y, u);
-          u = fmaf(-wb[c + 1], x.y, u);
-        }
-      }
-    }
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
-    if (p < pages && sub == 0) keys[p] = scored ? key_of(u * scale) : 0u;
-    if (scored) {
-      const float e = mass * scale + 0x1p-140f;  // (and the roundings among the subnormal numbers)
+      const float e = mass * scale[it] + 0x1p-140f;  // (and the roundings among the subnormal numbers)
       // no finite bound, or a score that overflowed: every page is scored again
-      bound = (e <= 3e38f && fabsf(u * scale) <= 3e38f) ? fmaxf(bound, e) : INFINITY;
+      bound = (e <= 3e38f && fabsf(score) <= 3e38f) ? fmaxf(bound, e) : INFINITY;
     }
   }
 #pragma unroll
@@ -178,35 +194,20 @@ __global__ void __launch_bounds__(kScoreThreads) kv8_score_kernel(const __grid_c
 }
 
 // ------------------------------------------------------------------ pick
-// Exclusive count of f over the block's lower threads, and the block's total.  sums: one int per warp.
-__device__ __forceinline__ int block_rank(bool f, int* sums, int* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const unsigned m = __ballot_sync(0xffffffffu, f);
-  if (lane == 0) sums[warp] = __popc(m);
-  __syncthreads();
-  const int v = lane < kPickThreads / 32 ? sums[lane] : 0;
-  int incl = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += x;
-  }
-  *total = __shfl_sync(0xffffffffu, incl, 31);
-  const int before = warp ? __shfl_sync(0xffffffffu, incl, warp - 1) : 0;
-  __syncthreads();
-  return before + __popc(m & ((1u << lane) - 1));
-}
-
 template <int D, int FMT>
-__global__ void __launch_bounds__(kPickThreads) kv8_pick_kernel(const __grid_constant__ Kv8SelectArgs a) {
+__global__ void __launch_bounds__(kPickThreads, 2) kv8_pick_kernel(const __grid_constant__ Kv8SelectArgs a) {
   __shared__ uint32_t s_keys[kSmemKeys];
-  __shared__ int hist[256], sums[kPickThreads / 32];
-  __shared__ uint32_t s_lo[kPickThreads / 32], s_hi[kPickThreads / 32], s_prefix;
-  __shared__ float s_e[kPickThreads / 32];
-  __shared__ int s_need, s_band, s_above;
+  __shared__ int hist[kBins];              // then the list's bit words
+  __shared__ uint32_t s_few[kFew];
+  __shared__ uint32_t u_lo[kPickThreads / 32], u_hi[kPickThreads / 32];
+  __shared__ float f_e[kPickThreads / 32];
+  __shared__ int sums[kPickThreads / 32];
+  __shared__ uint32_t s_prefix;
+  __shared__ int s_need, s_count, s_few_n, s_band, s_above;
+  __shared__ float s_q[8 * D];
   __shared__ double wa[D], wb[D];
-  __shared__ Key tile[kSerialBand];
-  __shared__ int tile_at[kSerialBand];
+  __shared__ Key tile[kTile];
+  __shared__ int tile_at[kTile];
   const Geom& g = a.g;
   const int b = blockIdx.y, h = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const size_t pair = (size_t)b * g.Hkv + h;
@@ -226,51 +227,58 @@ __global__ void __launch_bounds__(kPickThreads) kv8_pick_kernel(const __grid_con
   Key* band_key = reinterpret_cast<Key*>(a.ws + w.band) + pair * a.max_pages;
   int* band_at = reinterpret_cast<int*>(a.ws + w.index) + pair * a.max_pages;
   const float* bounds = reinterpret_cast<const float*>(a.ws + w.bound) + pair * w.chunks;
-  // the free choice: pages keep_first .. pages - keep_last, `need` of them
+  // the free choice: pages keep_first .. pages - keep_last, need0 of them
   const int first = a.keep_first, last = pages - a.keep_last;
   const int need0 = a.n_select - a.keep_first - a.keep_last;
-  if (pages <= kSmemKeys) {
-    for (int i = tid; i < pages; i += kPickThreads) s_keys[i] = keys[i];
-    keys = s_keys;
-  }
+  // keys into shared memory where they fit, their range, and the largest bound
   uint32_t lo = ~0u, hi = 0u;
-  float e = 0.f;
-  __syncthreads();
-  for (int i = first + tid; i < last; i += kPickThreads) {
-    lo = min(lo, keys[i]);
-    hi = max(hi, keys[i]);
+  const bool fits = pages <= kSmemKeys;
+  for (int i = tid; i < pages; i += kPickThreads) {
+    const uint32_t k = keys[i];
+    if (fits) s_keys[i] = k;
+    if (i >= first && i < last) {
+      lo = min(lo, k);
+      hi = max(hi, k);
+    }
   }
-  const int used_chunks = (pages + kPagesPerCta - 1) / kPagesPerCta;
-  for (int i = tid; i < used_chunks; i += kPickThreads) e = fmaxf(e, bounds[i]);
+  if (fits) keys = s_keys;
+  // the query for a second scoring, should there be one, travels with the keys
+  for (int i = tid; i < g.gq() * D; i += kPickThreads)
+    s_q[i] = kv8_load(a.q, (size_t)b * a.q_stride + (size_t)h * g.gq() * D + i, a.q_dtype);
+  float e = 0.f;
+  const int chunks = (pages + kPagesPerCta - 1) / kPagesPerCta;
+  for (int i = tid; i < chunks; i += kPickThreads) e = fmaxf(e, bounds[i]);
+  for (int i = tid; i < kBins; i += kPickThreads) hist[i] = 0;
+  if (tid == 0) {
+    s_prefix = 0;
+    s_need = need0;
+    s_band = s_above = s_few_n = 0;
+  }
   lo = __reduce_min_sync(0xffffffffu, lo);
   hi = __reduce_max_sync(0xffffffffu, hi);
 #pragma unroll
   for (int o = 16; o; o >>= 1) e = warp_max_xor(e, o);
   if (lane == 0) {
-    s_lo[warp] = lo;
-    s_hi[warp] = hi;
-    s_e[warp] = e;
-  }
-  if (tid == 0) {
-    s_prefix = 0;
-    s_need = need0;
-    s_band = s_above = 0;
+    u_lo[warp] = lo;
+    u_hi[warp] = hi;
+    f_e[warp] = e;
   }
   __syncthreads();
+  lo = __reduce_min_sync(0xffffffffu, u_lo[lane % (kPickThreads / 32)]);
+  hi = __reduce_max_sync(0xffffffffu, u_hi[lane % (kPickThreads / 32)]);
+  e = f_e[lane % (kPickThreads / 32)];
 #pragma unroll
-  for (int i = 0; i < kPickThreads / 32; ++i) {
-    lo = min(lo, s_lo[i]);
-    hi = max(hi, s_hi[i]);
-    e = fmaxf(e, s_e[i]);
-  }
-  double above = INFINITY, below = INFINITY;  // need0 == 0: only the kept ones
+  for (int o = kPickThreads / 64; o; o >>= 1) e = warp_max_xor(e, o);
+  // keys over `above` are in, those under `below` out (need0 == 0: only the kept pages are in).  Both come from float32
+  // arithmetic rounded outwards: the card's float64 rate is a hundredth of that, too slow for every page.
+  uint32_t above = ~0u, below = ~0u;
   if (need0 > 0) {
-    // the need-th largest of keys - lo, eight bits at a time from the highest bit in which they differ
-    int shift = max(0, 24 - __clz((hi - lo) | 1)), width = 8;
+    // the need-th largest of keys - lo, eleven bits at a time from the highest bit in which they differ, until few
+    // enough keys share its digits to be ranked one by one
+    int shift = max(0, 32 - kBinBits - __clz((hi - lo) | 1)), width = kBinBits;
     bool top = true;
+    uint32_t found;
     while (true) {
-      for (int i = tid; i < 256; i += kPickThreads) hist[i] = 0;
-      __syncthreads();
       const uint32_t prefix = s_prefix;
       for (int i = first + tid; i < last; i += kPickThreads) {
         const uint32_t k = keys[i] - lo;
@@ -278,50 +286,77 @@ __global__ void __launch_bounds__(kPickThreads) kv8_pick_kernel(const __grid_con
           atomicAdd(&hist[(k >> shift) & ((1 << width) - 1)], 1);
       }
       __syncthreads();
-      if (warp == 0) {  // bins from the largest down: lane l holds 255 - 8 l .. 248 - 8 l
-        int c[8], sum = 0;
+      // bins from the largest down: thread t holds the kBins / kPickThreads below kBins - 1 - t kBins / kPickThreads
+      constexpr int kPer = kBins / kPickThreads;
+      int c[kPer], sum = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum += c[i] = hist[255 - 8 * lane - i];
-        int incl = sum;
+      for (int i = 0; i < kPer; ++i) sum += c[i] = hist[kBins - 1 - tid * kPer - i];
+      int incl = sum;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int x = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += x;
-        }
-        const int want = s_need;
-        int before = incl - sum;
-        __syncwarp();
-        if (before < want && want <= incl) {
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
+      }
+      if (lane == 31) sums[warp] = incl;
+      const int want = s_need;
+      __syncthreads();
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (before < want && want <= before + c[i]) {
-              s_need = want - before;
-              s_prefix = prefix | ((uint32_t)(255 - 8 * lane - i) << shift);
-            }
-            before += c[i];
+      for (int i = 0; i < kPickThreads / 32; ++i) incl += i < warp ? sums[i] : 0;
+      int before = incl - sum;
+      if (before < want && want <= incl) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          if (before < want && want <= before + c[i]) {
+            s_need = want - before;
+            s_count = c[i];
+            s_prefix = prefix | ((uint32_t)(kBins - 1 - tid * kPer - i) << shift);
           }
+          before += c[i];
         }
       }
       __syncthreads();
+      found = s_prefix;
       if (shift == 0) break;
+      if (s_count <= kFew) {
+        for (int i = first + tid; i < last; i += kPickThreads) {
+          const uint32_t k = keys[i] - lo;
+          if ((k >> shift) == (found >> shift)) s_few[atomicAdd(&s_few_n, 1)] = k;
+        }
+        __syncthreads();
+        // the need-th largest of them: fewer than need are larger, and it with its equals reaches need
+        const int m = s_few_n, left = s_need;
+        if (tid < m) {
+          const uint32_t k = s_few[tid];
+          int more = 0, same = 0;
+          for (int i = 0; i < m; ++i) {
+            more += s_few[i] > k;
+            same += s_few[i] == k;
+          }
+          if (more < left && left <= more + same) s_prefix = k;
+        }
+        __syncthreads();
+        found = s_prefix;
+        break;
+      }
+      for (int i = tid; i < kBins; i += kPickThreads) hist[i] = 0;
+      __syncthreads();
       top = false;
-      width = min(8, shift);
+      width = min(kBinBits, shift);
       shift -= width;
     }
-    const double t = value_of(s_prefix + lo);
-    above = t + 2.0 * e;
-    below = t - 2.0 * e;
-    if (!(e < INFINITY) || !(t > -INFINITY)) above = INFINITY, below = -INFINITY;  // score all again
+    const float t = value_of(found + lo), far = 2.f * e;
+    if (e < 3e38f / 2 && t > -INFINITY) {
+      above = key_of(__fadd_ru(t, far));
+      below = key_of(__fadd_rd(t, -far));
+    } else {
+      below = 0u;  // score all again
+    }
   }
   // count the ones above, list the ones between
   for (int i = first + tid; need0 > 0 && i < last; i += kPickThreads) {
     const uint32_t k = keys[i];
-    const double v = value_of(k);
-    if (k && v > above) {
-      atomicAdd(&s_above, 1);
-    } else if (!(below > -INFINITY) || (k && v >= below)) {
-      band_at[atomicAdd(&s_band, 1)] = i;
-    }
+    if (k > above) atomicAdd(&s_above, 1);
+    else if (k >= below) band_at[atomicAdd(&s_band, 1)] = i;
   }
   __syncthreads();
   const int band = s_band, need = need0 - s_above;
@@ -329,8 +364,8 @@ __global__ void __launch_bounds__(kPickThreads) kv8_pick_kernel(const __grid_con
   if (rank) {
     for (int c = tid; c < D; c += kPickThreads) {
       double x = 0, y = 0;
-      for (int hh = 0; hh < g.gq(); ++hh) {
-        const double q = kv8_load(a.q, (size_t)b * a.q_stride + (size_t)(h * g.gq() + hh) * D + c, a.q_dtype);
+      for (int i = c; i < g.gq() * D; i += D) {
+        const double q = s_q[i];
         x += q < 0 ? 0 : q;
         y += q > 0 ? 0 : -q;
       }
@@ -345,12 +380,14 @@ __global__ void __launch_bounds__(kPickThreads) kv8_pick_kernel(const __grid_con
       Key k = 0;
       if (pid >= 0) {
         const uint8_t* block = layer + (size_t)pid * kg.page_bytes();
+        const double scale = *reinterpret_cast<const float*>(block + kg.scale_off());
         double u = 0;
-        for (int c = lane; c < D; c += 32)
-          u += wa[c] * kv8_value<FMT>(block[kg.hi_off() + c]) - wb[c] * kv8_value<FMT>(block[kg.lo_off() + c]);
+#pragma unroll
+        for (int c = 0; c < D; c += 32)
+          u += wa[c + lane] * kv8_value<FMT>(block[kg.hi_off() + c + lane]) - wb[c + lane] * kv8_value<FMT>(block[kg.lo_off() + c + lane]);
 #pragma unroll
         for (int o = 16; o; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
-        k = key_of(u * (double)*reinterpret_cast<const float*>(block + kg.scale_off()));
+        k = key_of(u * scale);
       }
       if (lane == 0) band_key[j] = k;
     }
@@ -361,37 +398,57 @@ __global__ void __launch_bounds__(kPickThreads) kv8_pick_kernel(const __grid_con
       const Key k = j < band ? band_key[j] : 0;
       const int at = j < band ? band_at[j] : 0;
       int r = 0;
-      for (int i0 = 0; i0 < band; i0 += kSerialBand) {
+      for (int i0 = 0; i0 < band; i0 += kTile) {
         __syncthreads();
-        if (tid < kSerialBand && i0 + tid < band) {
+        if (tid < kTile && i0 + tid < band) {
           tile[tid] = band_key[i0 + tid];
           tile_at[tid] = band_at[i0 + tid];
         }
         __syncthreads();
-        const int m = min(kSerialBand, band - i0);
+        const int m = min(kTile, band - i0);
         for (int i = 0; i < m; ++i) r += tile[i] > k || (tile[i] == k && tile_at[i] < at);
       }
       if (j < band) keys[at] = r < need ? ~0u : 0u;
     }
     __syncthreads();
   }
-  // ascending list
+  // ascending list: a bit per page, 32 kWords pages at a time; thread t counts and writes those of word t
+  constexpr int kWords = kPickThreads;
+  uint32_t* words = reinterpret_cast<uint32_t*>(hist);
+  static_assert(kWords <= kBins, "the bit words take the bins' place");
   int taken = 0;
-  for (int i0 = 0; i0 < pages; i0 += kPickThreads) {
-    const int i = i0 + tid;
-    bool take = false;
-    if (i < pages) {
-      take = i < first || i >= last;
-      if (!take && need0 > 0) {
+  for (int i0 = 0; i0 < pages; i0 += 32 * kWords) {
+    const int m = min(pages - i0, 32 * kWords);
+    for (int j = tid; j < (m + 31) / 32 * 32; j += kPickThreads) {
+      const int i = i0 + j;
+      bool take = false;
+      if (i < pages) {
         const uint32_t k = keys[i];
-        const double v = value_of(k);
-        take = rank ? k == ~0u || (k && v > above) : !(below > -INFINITY) || (k && v >= below);
+        take = i < first || i >= last || (need0 > 0 && (rank ? k > above || k == ~0u : k >= below));
       }
+      const unsigned bits = __ballot_sync(__activemask(), take);
+      if (lane == 0) words[j / 32] = bits;
     }
-    int total;
-    const int at = taken + block_rank(take, sums, &total);
-    if (take && at < a.n_select) out[at] = i;
-    taken += total;
+    __syncthreads();
+    uint32_t mine = tid < (m + 31) / 32 ? words[tid] : 0;
+    int incl = __popc(mine);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    int at = taken + incl - __popc(mine);
+#pragma unroll
+    for (int i = 0; i < kPickThreads / 32; ++i) {
+      const int s = sums[i];
+      at += i < warp ? s : 0;
+      taken += s;
+    }
+    for (; mine; mine &= mine - 1, ++at)
+      if (at < a.n_select) out[at] = i0 + 32 * tid + __ffs(mine) - 1;
+    __syncthreads();
   }
 }
 

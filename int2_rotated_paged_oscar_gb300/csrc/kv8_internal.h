@@ -53,8 +53,8 @@ struct Kv8WriteArgs {
 
 struct Kv8DecodeWs {
   int stages_per_split;  // 64-token stages of one split CTA
-  int max_splits;        // page splits of a request; grid.x has one more CTA, for the tail rows
-  size_t total;          // bytes: partials [batch][Hq][1 + max_splits][D + 4] float32
+  int max_splits;        // splits of a request, one at least
+  size_t total;          // bytes: partials [batch][Hq][max_splits][D + 4] float32
 };
 
 struct Kv8DecodeArgs {
