@@ -55,14 +55,6 @@ __device__ __forceinline__ int split_count(const Kv8DecodeArgs& a, int have) {
   return max((have + per - 1) / per, 1);
 }
 
-// Four neighbouring query components.
-template <bool QF32>
-__device__ __forceinline__ float4 load_q4(const void* q, size_t i) {
-  if constexpr (QF32) return *reinterpret_cast<const float4*>(static_cast<const float*>(q) + i);
-  const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(q) + i);
-  return make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
-}
-
 // x, y as three BF16 pairs whose sum has float32's digits.
 __device__ __forceinline__ void split3(float x, float y, uint32_t (&t)[3]) {
 #pragma unroll
@@ -93,7 +85,7 @@ __device__ __forceinline__ void tail_block(const Kv8DecodeArgs& a, int b, int h,
     const uint4 k1 = gid + 8 < cnt ? *reinterpret_cast<const uint4*>(krows + (size_t)(gid + 8) * D + ch) : none;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      float4 q = load_q4<QF32>(a.q, qat + ch + 4 * u);
+      float4 q = kv8_load4<QF32>(a.q, qat + ch + 4 * u);
       if (!live) q = make_float4(0.f, 0.f, 0.f, 0.f);
       const uint32_t a0 = u ? k0.z : k0.x, a2 = u ? k0.w : k0.y, a1 = u ? k1.z : k1.x, a3 = u ? k1.w : k1.y;
       if constexpr (QF32) {
@@ -306,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 3) kv8_decode_kernel(const __grid_co
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           const size_t i = at + (tig + 4 * c) * 16 + 4 * w;
-          const float4 v = load_q4<QF32>(a.q, i);
+          const float4 v = kv8_load4<QF32>(a.q, i);
           float* y = x[4 * c + w];
           y[0] = v.x, y[1] = v.y, y[2] = v.z, y[3] = v.w;
 #pragma unroll

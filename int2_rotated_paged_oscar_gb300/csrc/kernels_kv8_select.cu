@@ -6,29 +6,40 @@
 // index.  It reads 2 d + 4 bytes per page and kv head, 1 / P of what dense attention reads, so latency
 // decides: a score kernel over all pages and a pick kernel per (request, kv head).
 //
-// The order is float64's, the scores are float32's.  A float32 score is off by at most
-//   E_p = 2^-18 M scale_p sum_c (a_c + b_c),   M the largest code:
-// its terms add up to at most E_p 2^18, and it takes fewer than 64 roundings of half a step (2^-24) each:
-// 7 in a sum over 8 heads, one in a product, 3 + 32 in the sum of a lane and of its page, one in the scale.
+// A score is a product of a page's 2 d codes (exact f16 numbers) with one vector per (request, kv head), taken on the
+// tensor cores: 16 pages a warp, the vector as f16 high and low halves in two columns (on the CUDA cores, 8 lanes a page,
+// conversions and multiply-adds took 13 us where this takes 8, at 32 requests of 16K to 32K tokens).
+//
+// The order is float64's, the scores are float32's.  One is off by at most
+//   E_p = 2^-14 A_p,   A_p = scale_p sum_c (a_c |hi_pc| + b_c |lo_pc|):
+// the sums over 8 heads take 7 roundings of half a step (2^-24), the halves leave out 2^-22 of a weight, the scale takes 2
+// roundings, and each of the 2 d / 16 <= 16 matrix instructions adds 17 numbers and loses less than a step (2^-23) of the
+// largest for each: 7 + 4 + 2 + 16 x 17 x 2 = 557 half steps, where 2^-14 is 1024; A_p itself comes from the same
+// instructions on the magnitudes, off by as little.
 // With E the largest E_p and t the n-th largest float32 score, the n-th largest exact score lies within E of
 // t; so a page above t + 2 E is in, one below t - 2 E is out, and only the ones between, mostly the n-th
-// alone, are scored again in float64 and ranked.
+// alone, are scored again to about 48 bits and ranked.
 #include "kv8.cuh"
 
 namespace oscar {
 namespace {
 
-constexpr int kScoreThreads = 128;
-constexpr int kPagesPerCta = 64;   // 8 lanes a page, 16 pages at a time
-constexpr int kPickThreads = 512;
-constexpr int kSmemKeys = 8192;    // pages whose keys the pick kernel holds in shared memory
-constexpr int kBinBits = 11, kBins = 1 << kBinBits;
+constexpr int kScoreWarps = 4;
+constexpr int kChunk = 16;         // pages that a warp scores
+// The pick kernel's threads, its digits' bits, and how many pages' keys it holds in shared memory.  Up to 1024 pages a
+// small block takes less time than a large one spends in its barriers and empty bins (see launch_select).
+template <bool SMALL>
+struct Pick {
+  static constexpr int kThreads = SMALL ? 128 : 512;
+  static constexpr int kBits = SMALL ? 8 : 11;
+  static constexpr int kKeys = SMALL ? 1024 : 8192;
+};
 constexpr int kFew = 64;           // keys that are ranked one by one
 constexpr int kTile = 64;          // pages scored again are ranked against tiles of this many
 using Key = unsigned long long;
 
-// Workspace: float32 keys [batch][Hkv][max_pages], float64 keys of the band (same count), its page indexes,
-// and the largest E_p of each score CTA [batch][Hkv][chunks].
+// Workspace: float32 keys [batch][Hkv][max_pages], 64-bit keys of the band (same count), its page indexes,
+// and the largest E_p of each chunk [batch][Hkv][chunks].
 struct SelectWs {
   size_t keys, band, index, bound, total;
   int chunks;
@@ -36,7 +47,7 @@ struct SelectWs {
 __host__ __device__ inline SelectWs select_ws(int Hkv, int batch, int max_pages) {
   SelectWs w;
   const size_t n = (size_t)batch * Hkv * max_pages;
-  w.chunks = (max_pages + kPagesPerCta - 1) / kPagesPerCta;
+  w.chunks = (max_pages + kChunk - 1) / kChunk;
   w.band = 0;
   w.keys = n * sizeof(Key);
   w.index = w.keys + n * sizeof(uint32_t);
@@ -65,137 +76,147 @@ __device__ __forceinline__ bool kept(const Kv8SelectArgs& a, int p, int pages) {
   return p < a.keep_first || p >= pages - a.keep_last;
 }
 
-// sum_h max(q_hc, 0) and sum_h max(-q_hc, 0) over the heads of kv head h (a NaN stays one).
-__device__ __forceinline__ float2 query_sums(const Kv8SelectArgs& a, int b, int h, int c, int D) {
-  const int G = a.g.gq();
-  const size_t at = (size_t)b * a.q_stride + (size_t)h * G * D + c;
-  float q[8];
-#pragma unroll
-  for (int hh = 0; hh < 8; ++hh) q[hh] = hh < G ? kv8_load(a.q, at + (size_t)hh * D, a.q_dtype) : 0.f;
-  float2 s = make_float2(0.f, 0.f);
-#pragma unroll
-  for (int hh = 0; hh < 8; ++hh) {
-    s.x += q[hh] < 0.f ? 0.f : q[hh];
-    s.y += q[hh] > 0.f ? 0.f : -q[hh];
-  }
-  return s;
+// 2^e and its inverse with big 2^e in [2^14, 2^15).
+__device__ __forceinline__ void power_of_two(float big, float* up, float* down) {
+  const int k = min(max((int)(__float_as_uint(big) >> 23) - 127, -100), 127);
+  *up = __uint_as_float((uint32_t)(127 + 14 - k) << 23);
+  *down = __uint_as_float((uint32_t)(127 - 14 + k) << 23);
 }
 
+// A sum of float32 numbers kept as hi + lo, about 48 bits: the second scoring.  (Its float64 form took three times as
+// long: the card's float64 rate is a hundredth of float32's.)  The additions are Knuth's exact two-number sum.
+struct Sum2 {
+  float hi, lo;
+  __device__ __forceinline__ void add(float x) {
+    const float s = hi + x, t = s - hi;
+    lo += (hi - (s - t)) + (x - t);
+    hi = s;
+  }
+  // code (8 significant bits) times the weight w + v
+  __device__ __forceinline__ void add_product(float code, float w, float v) {
+    const float p = __fmul_rn(code, w);
+    add(p);
+    lo = fmaf(code, v, lo + fmaf(code, w, -p));
+  }
+};
+
 // ------------------------------------------------------------------ scores
-template <int D, int FMT>
-__global__ void __launch_bounds__(kScoreThreads) kv8_score_kernel(const __grid_constant__ Kv8SelectArgs a) {
-  constexpr int C = D / 8;                 // channels of a lane
-  constexpr int kRounds = kPagesPerCta / (kScoreThreads / 8);
-  __shared__ float s_bound[kScoreThreads / 32];
-  __shared__ __align__(16) float s_wa[D], s_wb[D];
+// A warp scores 16 pages of one kv head.  Neighbouring warps take the kv heads of the same pages, whose bounds lie in the
+// same few megabytes: fewer address translations than with 64 pages of one head a CTA.
+template <int D, int FMT, bool QF32>
+__global__ void __launch_bounds__(32 * kScoreWarps) kv8_score_kernel(const __grid_constant__ Kv8SelectArgs a) {
+  constexpr int KS = D / 16, NC = D / 64;  // k-steps of a section (hi or lo), 16-byte chunks of it that a lane holds
+  __shared__ __align__(16) __half s_w[kScoreWarps][2][2][D];  // [hi, lo section][high, low half][channel]
   const Geom& g = a.g;
   const Kv8Geom kg{g.P, D, g.Hkv};
-  const int b = blockIdx.z, h = blockIdx.y, tid = threadIdx.x, lane = tid & 31, sub = lane & 7;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, tig = lane & 3;
+  const int b = blockIdx.y, unit = blockIdx.x * kScoreWarps + warp, h = unit % g.Hkv, chunk = unit / g.Hkv;
+  const int G = g.gq();
   pdl_wait();
   pdl_launch_dependents();
   const int n = a.seq_lens[b];
-  const int p0 = blockIdx.x * kPagesPerCta;
-  // the table entries and the query travel together
-  int pids[kRounds];
+  const int p0 = chunk * kChunk;
+  // the table entries of this lane's two pages and the query travel together
+  int pid[2];
 #pragma unroll
-  for (int it = 0; it < kRounds; ++it) {
-    const int p = p0 + it * (kScoreThreads / 8) + (tid >> 3);
-    pids[it] = p < a.bt_stride ? a.block_table[(size_t)b * a.bt_stride + p] : -1;
+  for (int r = 0; r < 2; ++r) {
+    const int p = p0 + gid + 8 * r;
+    pid[r] = p < a.bt_stride ? a.block_table[(size_t)b * a.bt_stride + p] : -1;
   }
-  for (int c = tid; c < D; c += kScoreThreads) {
-    // (channels 4 w .. 4 w + 3 of lane `sub` next to those of the other lanes: no bank conflicts)
-    const float2 x = query_sums(a, b, h, c, D);
-    const int at = ((c % C) / 4 * 8 + c / C) * 4 + c % 4;
-    s_wa[at] = x.x;
-    s_wb[at] = x.y;
-  }
+  float4 q[8];                             // channels 4 lane .. 4 lane + 3 (lanes of D = 64: the lower half)
+  const int qc = 4 * lane % D;
+#pragma unroll
+  for (int hh = 0; hh < 8; ++hh)
+    if (hh < G) q[hh] = kv8_load4<QF32>(a.q, (size_t)b * a.q_stride + (size_t)(h * G + hh) * D + qc);
   if (n < 0 || n > a.max_seq) return;
   const int pages = n / g.P;
   if (pages <= a.n_select || p0 >= pages) return;
-  __syncthreads();
-  // and so do the bounds of all this CTA's pages
   const uint8_t* layer = a.pool + (size_t)a.layer * g.num_pages * kg.page_bytes() + (size_t)h * kg.block_bytes();
-  uint32_t lo[kRounds][C / 4], hi[kRounds][C / 4];
-  float scale[kRounds];
+  uint4 code[2][2][NC];                    // [hi, lo][page][chunk tig + 4 c]
+  float scale[2];
 #pragma unroll
-  for (int it = 0; it < kRounds; ++it) {
-    const int p = p0 + it * (kScoreThreads / 8) + (tid >> 3);
+  for (int r = 0; r < 2; ++r) {
+    const int p = p0 + gid + 8 * r;
     const bool wanted = p < pages && !kept(a, p, pages);
-    if (wanted && (pids[it] < 0 || pids[it] >= g.num_pages) && sub == 0) flag_error(a.status, kDevBadPage);
-    if (!wanted || pids[it] >= g.num_pages) pids[it] = -1;
-  }
+    if (wanted && (pid[r] < 0 || pid[r] >= g.num_pages) && tig == 0) flag_error(a.status, kDevBadPage);
+    if (!wanted || pid[r] >= g.num_pages) pid[r] = -1;
+    const uint8_t* block = layer + (size_t)max(pid[r], 0) * kg.page_bytes();   // (page 0 in the place of none)
+    scale[r] = *reinterpret_cast<const float*>(block + kg.scale_off());
 #pragma unroll
-  for (int it = 0; it < kRounds; ++it) {
-    const uint8_t* block = layer + (size_t)max(pids[it], 0) * kg.page_bytes();   // (page 0 in the place of none)
-    scale[it] = *reinterpret_cast<const float*>(block + kg.scale_off());
-    if constexpr (C == 16) {
-      const uint4 x = *reinterpret_cast<const uint4*>(block + kg.lo_off() + sub * C);
-      const uint4 y = *reinterpret_cast<const uint4*>(block + kg.hi_off() + sub * C);
-      lo[it][0] = x.x, lo[it][1] = x.y, lo[it][2] = x.z, lo[it][3] = x.w;
-      hi[it][0] = y.x, hi[it][1] = y.y, hi[it][2] = y.z, hi[it][3] = y.w;
-    } else {
-      const uint2 x = *reinterpret_cast<const uint2*>(block + kg.lo_off() + sub * C);
-      const uint2 y = *reinterpret_cast<const uint2*>(block + kg.hi_off() + sub * C);
-      lo[it][0] = x.x, lo[it][1] = x.y;
-      hi[it][0] = y.x, hi[it][1] = y.y;
+    for (int c = 0; c < NC; ++c) {
+      code[0][r][c] = *reinterpret_cast<const uint4*>(block + kg.hi_off() + (tig + 4 * c) * 16);
+      code[1][r][c] = *reinterpret_cast<const uint4*>(block + kg.lo_off() + (tig + 4 * c) * 16);
     }
   }
-  float mass = 0.f, u[kRounds];
+  // a = sum_h max(q_h, 0) and -b = -sum_h max(-q_h, 0) as f16 halves, the largest component brought to 2^14
+  float4 pos = make_float4(0.f, 0.f, 0.f, 0.f), neg = pos;
 #pragma unroll
-  for (int it = 0; it < kRounds; ++it) u[it] = 0.f;
+  for (int hh = 0; hh < 8; ++hh)
+    if (hh < G) {
+      pos.x += fmaxf(q[hh].x, 0.f), pos.y += fmaxf(q[hh].y, 0.f), pos.z += fmaxf(q[hh].z, 0.f), pos.w += fmaxf(q[hh].w, 0.f);
+      neg.x += fminf(q[hh].x, 0.f), neg.y += fminf(q[hh].y, 0.f), neg.z += fminf(q[hh].z, 0.f), neg.w += fminf(q[hh].w, 0.f);
+    }
+  float big = fmaxf(fmaxf(fmaxf(pos.x, pos.y), fmaxf(pos.z, pos.w)), -fminf(fminf(neg.x, neg.y), fminf(neg.z, neg.w)));
 #pragma unroll
-  for (int w = 0; w < C / 4; ++w) {
-    const float4 wa = reinterpret_cast<const float4*>(s_wa)[w * 8 + sub], wb = reinterpret_cast<const float4*>(s_wb)[w * 8 + sub];
-    mass += ((wa.x + wb.x) + (wa.y + wb.y)) + ((wa.z + wb.z) + (wa.w + wb.w));
+  for (int o = 16; o; o >>= 1) big = warp_max_xor(big, o);
+  float up, down;
+  power_of_two(big, &up, &down);
+  if (4 * lane < D) {
 #pragma unroll
-    for (int it = 0; it < kRounds; ++it) {
-      const uint32_t l0 = kv8_pair<FMT, 0>(lo[it][w]), l1 = kv8_pair<FMT, 1>(lo[it][w]);
-      const uint32_t h0 = kv8_pair<FMT, 0>(hi[it][w]), h1 = kv8_pair<FMT, 1>(hi[it][w]);
-      const float2 x0 = __half22float2(*reinterpret_cast<const __half2*>(&l0)), x1 = __half22float2(*reinterpret_cast<const __half2*>(&l1));
-      const float2 y0 = __half22float2(*reinterpret_cast<const __half2*>(&h0)), y1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
-      u[it] = fmaf(wa.x, y0.x, fmaf(-wb.x, x0.x, u[it]));
-      u[it] = fmaf(wa.y, y0.y, fmaf(-wb.y, x0.y, u[it]));
-      u[it] = fmaf(wa.z, y1.x, fmaf(-wb.z, x1.x, u[it]));
-      u[it] = fmaf(wa.w, y1.y, fmaf(-wb.w, x1.y, u[it]));
+    for (int sect = 0; sect < 2; ++sect) {
+      const float4 x = sect ? neg : pos;
+      const uint2 hi = make_uint2(pack_half2(x.x * up, x.y * up), pack_half2(x.z * up, x.w * up));
+      const float2 h0 = __half22float2(*reinterpret_cast<const __half2*>(&hi.x)), h1 = __half22float2(*reinterpret_cast<const __half2*>(&hi.y));
+      *reinterpret_cast<uint2*>(&s_w[warp][sect][0][qc]) = hi;
+      *reinterpret_cast<uint2*>(&s_w[warp][sect][1][qc]) =
+          make_uint2(pack_half2(x.x * up - h0.x, x.y * up - h0.y), pack_half2(x.z * up - h1.x, x.w * up - h1.y));
     }
   }
+  __syncwarp();
+  // columns 0 and 1: high and low halves; sc: scores, sa: sums of magnitudes
+  float sc[4] = {0.f, 0.f, 0.f, 0.f}, sa[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int o = 1; o < 8; o <<= 1) {
-    mass += __shfl_xor_sync(0xffffffffu, mass, o);
+  for (int sect = 0; sect < 2; ++sect)
 #pragma unroll
-    for (int it = 0; it < kRounds; ++it) u[it] += __shfl_xor_sync(0xffffffffu, u[it], o);
-  }
-  mass *= (FMT == kKv8Int8 ? 127.f : 448.f) * 0x1p-18f;
-  uint32_t* keys = reinterpret_cast<uint32_t*>(a.ws + select_ws(g.Hkv, a.batch, a.max_pages).keys) +
-                   ((size_t)b * g.Hkv + h) * a.max_pages;
+    for (int kk = 0; kk < KS; ++kk) {
+      const int c = kk / 4, w = kk % 4;
+      uint2 bw = make_uint2(0u, 0u);
+      if (gid < 2) bw = *reinterpret_cast<const uint2*>(&s_w[warp][sect][gid][(tig + 4 * c) * 16 + 4 * w]);
+      uint32_t x[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const uint4 v = code[sect][r][c];
+        x[r] = w == 0 ? v.x : w == 1 ? v.y : w == 2 ? v.z : v.w;
+      }
+      const uint32_t a0 = kv8_pair<FMT, 0>(x[0]), a1 = kv8_pair<FMT, 0>(x[1]), a2 = kv8_pair<FMT, 1>(x[0]), a3 = kv8_pair<FMT, 1>(x[1]);
+      constexpr uint32_t kAbs = 0x7fff7fffu;
+      mma_f16(sc, a0, a1, a2, a3, bw.x, bw.y);
+      mma_f16(sa, a0 & kAbs, a1 & kAbs, a2 & kAbs, a3 & kAbs, bw.x & kAbs, bw.y & kAbs);
+    }
+  const SelectWs w = select_ws(g.Hkv, a.batch, a.max_pages);
+  const size_t pair = (size_t)b * g.Hkv + h;
+  uint32_t* keys = reinterpret_cast<uint32_t*>(a.ws + w.keys) + pair * a.max_pages;
   float bound = 0.f;
 #pragma unroll
-  for (int it = 0; it < kRounds; ++it) {
-    const int p = p0 + it * (kScoreThreads / 8) + (tid >> 3);
-    const bool scored = pids[it] >= 0;
-    const float score = u[it] * scale[it];
-    if (p < pages && sub == 0) keys[p] = scored ? key_of(score) : 0u;
-    if (scored) {
-      const float e = mass * scale[it] + 0x1p-140f;  // (and the roundings among the subnormal numbers)
-      // no finite bound, or a score that overflowed: every page is scored again
-      bound = (e <= 3e38f && fabsf(score) <= 3e38f) ? fmaxf(bound, e) : INFINITY;
-    }
+  for (int r = 0; r < 2; ++r) {
+    const int p = p0 + gid + 8 * r;
+    const float f = scale[r] * down;
+    const float score = (sc[2 * r] + sc[2 * r + 1]) * f;
+    const float e = (sa[2 * r] + sa[2 * r + 1]) * f * 0x1p-14f + 0x1p-140f;   // (and the roundings among the subnormal numbers)
+    if (tig == 0 && p < pages) keys[p] = pid[r] >= 0 ? key_of(score) : 0u;
+    // no finite bound, or a score that overflowed: every page is scored again
+    if (tig == 0 && pid[r] >= 0) bound = (e <= 3e38f && fabsf(score) <= 3e38f) ? fmaxf(bound, e) : INFINITY;
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) bound = warp_max_xor(bound, o);
-  if (lane == 0) s_bound[tid >> 5] = bound;
-  __syncthreads();
-  if (tid == 0) {
-    const SelectWs w = select_ws(g.Hkv, a.batch, a.max_pages);
-    float m = 0.f;
-    for (int i = 0; i < kScoreThreads / 32; ++i) m = fmaxf(m, s_bound[i]);
-    reinterpret_cast<float*>(a.ws + w.bound)[((size_t)b * g.Hkv + h) * w.chunks + blockIdx.x] = m;
-  }
+  if (lane == 0) reinterpret_cast<float*>(a.ws + w.bound)[pair * w.chunks + chunk] = bound;
 }
 
 // ------------------------------------------------------------------ pick
-template <int D, int FMT>
-__global__ void __launch_bounds__(kPickThreads, 2) kv8_pick_kernel(const __grid_constant__ Kv8SelectArgs a) {
+template <int D, int FMT, bool SMALL>
+__global__ void __launch_bounds__(Pick<SMALL>::kThreads, 2) kv8_pick_kernel(const __grid_constant__ Kv8SelectArgs a) {
+  constexpr int kPickThreads = Pick<SMALL>::kThreads, kSmemKeys = Pick<SMALL>::kKeys;
+  constexpr int kBinBits = Pick<SMALL>::kBits, kBins = 1 << kBinBits;
   __shared__ uint32_t s_keys[kSmemKeys];
   __shared__ int hist[kBins];              // then the list's bit words
   __shared__ uint32_t s_few[kFew];
@@ -205,7 +226,8 @@ __global__ void __launch_bounds__(kPickThreads, 2) kv8_pick_kernel(const __grid_
   __shared__ uint32_t s_prefix;
   __shared__ int s_need, s_count, s_few_n, s_band, s_above;
   __shared__ float s_q[8 * D];
-  __shared__ double wa[D], wb[D];
+  __shared__ __align__(16) float w_hi[2][D], w_lo[2][D];   // [a, b]: the weights of a second scoring as two numbers
+  __shared__ float s_big[kPickThreads / 32];
   __shared__ Key tile[kTile];
   __shared__ int tile_at[kTile];
   const Geom& g = a.g;
@@ -246,7 +268,7 @@ __global__ void __launch_bounds__(kPickThreads, 2) kv8_pick_kernel(const __grid_
   for (int i = tid; i < g.gq() * D; i += kPickThreads)
     s_q[i] = kv8_load(a.q, (size_t)b * a.q_stride + (size_t)h * g.gq() * D + i, a.q_dtype);
   float e = 0.f;
-  const int chunks = (pages + kPagesPerCta - 1) / kPagesPerCta;
+  const int chunks = (pages + kChunk - 1) / kChunk;
   for (int i = tid; i < chunks; i += kPickThreads) e = fmaxf(e, bounds[i]);
   for (int i = tid; i < kBins; i += kPickThreads) hist[i] = 0;
   if (tid == 0) {
@@ -362,34 +384,56 @@ __global__ void __launch_bounds__(kPickThreads, 2) kv8_pick_kernel(const __grid_
   const int band = s_band, need = need0 - s_above;
   const bool rank = band > need;  // else the whole band is in
   if (rank) {
+    float big = 0.f;
+    for (int i = tid; i < g.gq() * D; i += kPickThreads) big = fmaxf(big, fabsf(s_q[i]));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) big = warp_max_xor(big, o);
+    if (lane == 0) s_big[warp] = big;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPickThreads / 32; ++i) big = fmaxf(big, s_big[i]);
+    float up, down;
+    power_of_two(big, &up, &down);
     for (int c = tid; c < D; c += kPickThreads) {
-      double x = 0, y = 0;
+      Sum2 x{0.f, 0.f}, y{0.f, 0.f};
       for (int i = c; i < g.gq() * D; i += D) {
-        const double q = s_q[i];
-        x += q < 0 ? 0 : q;
-        y += q > 0 ? 0 : -q;
+        const float q = s_q[i] * up;
+        x.add(fmaxf(q, 0.f));
+        y.add(fmaxf(-q, 0.f));
       }
-      wa[c] = x;
-      wb[c] = y;
+      w_hi[0][c] = x.hi, w_lo[0][c] = x.lo;
+      w_hi[1][c] = y.hi, w_lo[1][c] = y.lo;
     }
     __syncthreads();
+    // eight lanes a page
+    constexpr int C = D / 8;
     const Kv8Geom kg{g.P, D, g.Hkv};
     const uint8_t* layer = a.pool + (size_t)a.layer * g.num_pages * kg.page_bytes() + (size_t)h * kg.block_bytes();
-    for (int j = warp; j < band; j += kPickThreads / 32) {
-      const int pid = page_id(a, b, band_at[j]);
-      Key k = 0;
-      if (pid >= 0) {
-        const uint8_t* block = layer + (size_t)pid * kg.page_bytes();
-        const double scale = *reinterpret_cast<const float*>(block + kg.scale_off());
-        double u = 0;
+    for (int j0 = 0; j0 < band; j0 += kPickThreads / 8) {
+      const int j = j0 + (tid >> 3), sub = tid & 7;
+      const int pid = j < band ? page_id(a, b, band_at[j]) : -1;
+      const uint8_t* block = layer + (size_t)max(pid, 0) * kg.page_bytes();
+      const float scale = *reinterpret_cast<const float*>(block + kg.scale_off());
+      Sum2 u{0.f, 0.f};
 #pragma unroll
-        for (int c = 0; c < D; c += 32)
-          u += wa[c + lane] * kv8_value<FMT>(block[kg.hi_off() + c + lane]) - wb[c + lane] * kv8_value<FMT>(block[kg.lo_off() + c + lane]);
+      for (int i = 0; i < C / 4; ++i) {
+        const uint32_t hw = *reinterpret_cast<const uint32_t*>(block + kg.hi_off() + sub * C + 4 * i);
+        const uint32_t lw = *reinterpret_cast<const uint32_t*>(block + kg.lo_off() + sub * C + 4 * i);
 #pragma unroll
-        for (int o = 16; o; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
-        k = key_of(u * scale);
+        for (int k = 0; k < 4; ++k) {
+          const int c = sub * C + 4 * i + k;
+          u.add_product(kv8_value<FMT>((hw >> (8 * k)) & 255u), w_hi[0][c], w_lo[0][c]);
+          u.add_product(-kv8_value<FMT>((lw >> (8 * k)) & 255u), w_hi[1][c], w_lo[1][c]);
+        }
       }
-      if (lane == 0) band_key[j] = k;
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) {
+        const float x = __shfl_xor_sync(0xffffffffu, u.hi, o), y = __shfl_xor_sync(0xffffffffu, u.lo, o);
+        u.add(x);
+        u.lo += y;
+      }
+      // (the power of two is the same for every page)
+      if (sub == 0 && j < band) band_key[j] = pid >= 0 ? key_of(((double)u.hi + (double)u.lo) * scale) : 0ull;
     }
     __syncthreads();
     // rank of each: those with a larger key, or an equal one and a lower index
@@ -455,11 +499,16 @@ __global__ void __launch_bounds__(kPickThreads, 2) kv8_pick_kernel(const __grid_
 template <int D, int FMT>
 int launch_select(const Kv8SelectArgs& a, cudaStream_t s, bool pdl) {
   if (a.max_pages > a.n_select) {
-    const dim3 grid((a.max_pages + kPagesPerCta - 1) / kPagesPerCta, a.g.Hkv, a.batch);
-    const int e = launch_pdl(kv8_score_kernel<D, FMT>, grid, dim3(kScoreThreads), 0, s, pdl, a);
+    const long long units = (long long)((a.max_pages + kChunk - 1) / kChunk) * a.g.Hkv;
+    const dim3 grid((unsigned)((units + kScoreWarps - 1) / kScoreWarps), a.batch);
+    const int e = a.q_dtype == kDtypeF32 ? launch_pdl(kv8_score_kernel<D, FMT, true>, grid, dim3(32 * kScoreWarps), 0, s, pdl, a)
+                                         : launch_pdl(kv8_score_kernel<D, FMT, false>, grid, dim3(32 * kScoreWarps), 0, s, pdl, a);
     if (e) return e;
   }
-  return launch_pdl(kv8_pick_kernel<D, FMT>, dim3(a.g.Hkv, a.batch), dim3(kPickThreads), 0, s, pdl, a);
+  const dim3 grid(a.g.Hkv, a.batch);
+  if (a.max_pages <= Pick<true>::kKeys)
+    return launch_pdl(kv8_pick_kernel<D, FMT, true>, grid, dim3(Pick<true>::kThreads), 0, s, pdl, a);
+  return launch_pdl(kv8_pick_kernel<D, FMT, false>, grid, dim3(Pick<false>::kThreads), 0, s, pdl, a);
 }
 
 }  // namespace

@@ -50,6 +50,14 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
   return r;
 }
 
+// Four neighbouring query components.
+template <bool QF32>
+__device__ __forceinline__ float4 kv8_load4(const void* q, size_t i) {
+  if constexpr (QF32) return *reinterpret_cast<const float4*>(static_cast<const float*>(q) + i);
+  const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(q) + i);
+  return make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
+}
+
 __device__ __forceinline__ float kv8_load(const void* p, size_t i, int dtype) {
   if (dtype == kDtypeBF16) return __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16);
   return static_cast<const float*>(p)[i];
