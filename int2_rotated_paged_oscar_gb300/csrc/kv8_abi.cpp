@@ -1,5 +1,5 @@
 // C ABI of the 8-bit paged cache and of the page moves (see include/oscar.h).
-#include <cmath>
+#include <algorithm>
 #include <new>
 #include <vector>
 
@@ -361,12 +361,10 @@ oscar_status oscar_kv8_fork(oscar_ctx* ctx, const int32_t* src_bt, int32_t n, in
   }
   int err = 0;
   if (ctx->kv8_pool && rows > 0) {
-    oscar::ForkSlots d;
-    for (int at = 0; at < n_dst && !err; at += oscar::kForkSlots) {
-      d.n = n_dst - at < oscar::kForkSlots ? n_dst - at : oscar::kForkSlots;
-      for (int i = 0; i < d.n; ++i) d.dst[i] = dst_slots[at + i];
+    for (int at = 0; at < n_dst && !err; at += oscar::kMostPairs) {
       LaunchScope ls(ctx, "kv8_fork", stream);
-      err = oscar::launch_kv8_fork_tail(g, ctx->kv8_tail, src_slot, d, rows, stream);
+      err = oscar::launch_kv8_fork_tail(g, ctx->kv8_tail, src_slot, dst_slots + at, std::min(n_dst - at, oscar::kMostPairs), rows,
+                                        stream);
       ls.done(err);
     }
   }
@@ -406,19 +404,17 @@ oscar_status oscar_compact_pages(oscar_ctx* ctx, int32_t* block_table, int32_t r
     stack.reserve(g.num_pages);
     for (int i = g.num_pages - 1; i >= live; --i) stack.push_back(i);  // lowest id first
     // every copy before any table entry changes: after a failed launch the old pages still hold
-    oscar::PagePairs p;
+    const int moves = (int)src.size();
     for (int pass = 0; pass < 3 && device; ++pass) {
       if (pass == 0 ? !ctx->pool : pass == 1 ? !ctx->kv8_pool : rows == 0) continue;
-      for (size_t at = 0; at < src.size(); at += oscar::kPagePairs) {
-        p.n = (int)(src.size() - at < (size_t)oscar::kPagePairs ? src.size() - at : (size_t)oscar::kPagePairs);
-        for (int i = 0; i < p.n; ++i) {
-          p.src[i] = src[at + i];
-          p.dst[i] = dst[at + i];
-        }
+      for (int at = 0; at < moves; at += oscar::kMostPairs) {
+        const int n = std::min(moves - at, oscar::kMostPairs);
+        const int *from = src.data() + at, *to = dst.data() + at;
         LaunchScope ls(ctx, pass < 2 ? "copy_pages" : "remap_table", stream);
-        const int e = pass == 0   ? oscar::launch_copy_pages(ctx->pool, g.L, g.num_pages, g.Hkv * g.block_bytes(), p, stream)
-                      : pass == 1 ? oscar::launch_copy_pages(ctx->kv8_pool, g.L, g.num_pages, oscar::kv8_geom(g).page_bytes(), p, stream)
-                                  : oscar::launch_remap_table(block_table, rows, bt_stride, bt_stride, p, stream);
+        const int e =
+            pass == 0   ? oscar::launch_copy_pages(ctx->pool, g.L, g.num_pages, g.Hkv * g.block_bytes(), from, to, n, stream)
+            : pass == 1 ? oscar::launch_copy_pages(ctx->kv8_pool, g.L, g.num_pages, oscar::kv8_geom(g).page_bytes(), from, to, n, stream)
+                        : oscar::launch_remap_table(block_table, rows, bt_stride, from, to, n, stream);
         ls.done(e);
         if (e) return cuda_fail(e, "page move launch");
       }

@@ -97,18 +97,15 @@ struct Kv8SelectArgs {
   int max_pages;                 // max_seq / P
 };
 
-// Pages of a host-side list handed to a kernel by value (the list needs no device buffer and
-// no copy, so the call can be captured); a call with more pairs launches once per kPagePairs.
-constexpr int kPagePairs = 1000;
-struct PagePairs {
+// Host-side lists that a kernel takes by value: they need no device buffer and no copy.  A call with
+// more entries launches once per list of kMostPairs; a short list goes in a short argument, which
+// takes the host less time to hand over.
+constexpr int kMostPairs = 1000, kFewPairs = 60;
+template <int N>
+struct IntPairs {
   int n;
-  int src[kPagePairs];  // ascending
-  int dst[kPagePairs];
-};
-constexpr int kForkSlots = 1000;
-struct ForkSlots {
-  int n;
-  int dst[kForkSlots];
+  int src[N];  // ascending
+  int dst[N];
 };
 
 Kv8DecodeWs kv8_plan(const Geom& g, int batch, long long max_pages);
@@ -118,11 +115,12 @@ int launch_kv8_write(const Kv8WriteArgs& a, void* stream, bool pdl);
 int launch_kv8_decode(const Kv8DecodeArgs& a, void* stream, bool pdl);
 int launch_kv8_combine(const Kv8DecodeArgs& a, void* stream, bool pdl);
 int launch_kv8_select(const Kv8SelectArgs& a, void* stream, bool pdl);
-// rows [0, n_rows) of the src slot's tail to every dst slot, in every layer
-int launch_kv8_fork_tail(const Geom& g, uint16_t* tail, int src, const ForkSlots& dst, int n_rows, void* stream);
-// pool: [layers][num_pages][page_bytes]; page src[i] to page dst[i] in every layer
-int launch_copy_pages(uint8_t* pool, int layers, int num_pages, size_t page_bytes, const PagePairs& p, void* stream);
-// block-table entries equal to src[i] become dst[i]
-int launch_remap_table(int* table, int rows, int cols, int stride, const PagePairs& p, void* stream);
+// rows [0, n_rows) of the src slot's tail to every dst slot (n <= kMostPairs of them), in every layer
+int launch_kv8_fork_tail(const Geom& g, uint16_t* tail, int src, const int* dst, int n, int n_rows, void* stream);
+// pool: [layers][num_pages][page_bytes]; page src[i] to page dst[i] in every layer (n <= kMostPairs)
+int launch_copy_pages(uint8_t* pool, int layers, int num_pages, size_t page_bytes, const int* src, const int* dst, int n,
+                      void* stream);
+// block-table entries equal to src[i] (ascending) become dst[i] (n <= kMostPairs)
+int launch_remap_table(int* table, int rows, int cols, const int* src, const int* dst, int n, void* stream);
 
 }  // namespace oscar
