@@ -437,8 +437,10 @@ oscar_status oscar_bf16_decode_attn(oscar_ctx* ctx, int32_t layer, const void* b
  * tokens); the address and the stride in bytes must be multiples of 16.  Every kernel call must be made
  * with the device current on which the buffers were bound (else OSCAR_ERR_INVALID),
  * takes at most 65535 requests (else OSCAR_ERR_UNSUPPORTED), needs no allocation and
- * can be captured into a graph.  Requests of one call have distinct req_slots and
- * write distinct pages. */
+ * can be captured into a graph (after one such call outside a capture).  Requests of one
+ * call have distinct req_slots and write distinct pages.  Workspaces are scratch of the
+ * one call, 256-byte aligned, with no initialisation; calls whose kernels may run at the
+ * same time need a workspace each. */
 enum { OSCAR_KV8_INT8 = 0, OSCAR_KV8_E4M3 = 1 };
 
 /* Bytes of the 8-bit pool / tail slab / one block for a configuration (sink, recent
@@ -471,7 +473,8 @@ oscar_status oscar_kv8_write(oscar_ctx* ctx, int32_t layer, const void* K, int64
 /* One token per request: K_new, V_new [batch][n_kv_heads][d] become token
  * seq_lens_before[b], row seq_lens_before[b] mod P of the tail; a request whose page it
  * completes has that page quantised (and needs it mapped).  Same cache contents as
- * oscar_kv8_write of the same tokens. */
+ * oscar_kv8_write of the same tokens.  seq_lens_before[b] = -1 skips request b (a padded
+ * batch); its length in the attention calls is then 0. */
 oscar_status oscar_kv8_append(oscar_ctx* ctx, int32_t layer, const void* K_new, int64_t k_stride, const void* V_new,
                               int64_t v_stride, int32_t dtype, const int32_t* seq_lens_before, int32_t batch,
                               const int32_t* block_table, int32_t bt_stride, const int32_t* req_slot, void* stream);

@@ -27,8 +27,9 @@ __device__ __forceinline__ int request(const Kv8WriteArgs& a, int b, int* start,
   const Geom& g = a.g;
   *start = a.start_pos[b];
   *row0 = a.cu_seqlens ? a.cu_seqlens[b] : b;
-  const long long l = a.cu_seqlens ? (long long)a.cu_seqlens[b + 1] - *row0 : 1;
+  const long long l = a.cu_seqlens ? (long long)a.cu_seqlens[b + 1] - *row0 : (*start == -1 ? 0 : 1);
   const int slot = a.req_slot[b];
+  if (l == 0) return 0;
   if (*start < 0 || *row0 < 0 || l < 0 || *row0 + l > a.total_tokens || *start + l > (long long)g.max_pages_per_req * g.P) {
     flag_error(a.status, kDevBadLen);
     return 0;
@@ -38,7 +39,7 @@ __device__ __forceinline__ int request(const Kv8WriteArgs& a, int b, int* start,
     return 0;
   }
   *len = (int)l;
-  return l > 0 ? max((*start + *len) / g.P - *start / g.P, 1) : 0;
+  return max((*start + *len) / g.P - *start / g.P, 1);
 }
 
 // The j-th item of a request.  A request whose chunk completes c pages has max(c, 1) items: item j quantises its j-th
@@ -56,32 +57,27 @@ __device__ __forceinline__ Item item_of(const Kv8WriteArgs& a, int b, int j, int
   return it;
 }
 
-// One warp finds the item of a CTA: a scan over the requests' item counts.
-__device__ bool find_item(const Kv8WriteArgs& a, int item, Item* out) {
-  const int lane = threadIdx.x & 31;
-  int base = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += 32) {
-    int start = 0, len = 0, row0 = 0;
-    const int cnt = b0 + lane < a.batch ? request(a, b0 + lane, &start, &len, &row0) : 0;
-    int incl = cnt;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    const int total = __shfl_sync(0xffffffffu, incl, 31);
-    if (item < base + total) {
-      const int l = __ffs(__ballot_sync(0xffffffffu, base + incl > item)) - 1;
-      const int j = item - base - __shfl_sync(0xffffffffu, incl - cnt, l);
-      start = __shfl_sync(0xffffffffu, start, l);
-      len = __shfl_sync(0xffffffffu, len, l);
-      row0 = __shfl_sync(0xffffffffu, row0, l);
-      *out = item_of(a, b0 + l, j, start, len, row0);
-      return true;
-    }
-    base += total;
+// One warp finds the item of CTA x.  A request of len rows completes at most len / P + 1 pages, so request b has the CTAs
+// from cu[b] / P + b on, as many as it can need (the rest end at once), and a 32-way search over that bound finds b.
+// CTA x also checks request x: one that no CTA works on is reported all the same.
+__device__ bool find_item(const Kv8WriteArgs& a, int x, Item* out) {
+  const int lane = threadIdx.x & 31, P = a.g.P;
+  int start, len, row0;
+  if (x < a.batch) (void)request(a, x, &start, &len, &row0);
+  int b = 0, n = a.batch;
+  while (n > 1) {
+    const int step = (n + 31) / 32, at = b + lane * step;
+    const bool below = lane * step < n && a.cu_seqlens[at] / P + at <= x;
+    const unsigned hit = __ballot_sync(0xffffffffu, below);
+    if (hit == 0) return false;
+    const int l = 31 - __clz(hit);
+    b += l * step;
+    n = min(step, n - l * step);
   }
-  return false;
+  const int j = x - (a.cu_seqlens[b] / P + b);
+  if (j < 0 || j >= request(a, b, &start, &len, &row0)) return false;
+  *out = item_of(a, b, j, start, len, row0);
+  return true;
 }
 
 // x M / m, correctly rounded, from x (2^e M) and m 2^e in [2, 4): with r the correctly rounded reciprocal of the latter,

@@ -97,6 +97,14 @@ oscar_status write_rows(oscar_ctx* ctx, int32_t layer, const void* K, int64_t k_
   return OSCAR_OK;
 }
 
+constexpr int kMaxSelect = 1 << 24;
+
+oscar_status check_select(int32_t n_select) {
+  if (n_select < 1) return fail(OSCAR_ERR_INVALID, "n_select %d is below 1", n_select);
+  if (n_select > kMaxSelect) return fail(OSCAR_ERR_UNSUPPORTED, "n_select %d exceeds %d", n_select, kMaxSelect);
+  return OSCAR_OK;
+}
+
 // What the two attention calls and the selection have in common.
 oscar_status check_query(oscar_ctx* ctx, int32_t layer, const void* q, int64_t* q_stride, int32_t q_dtype,
                          const int32_t* block_table, int32_t bt_stride, const int32_t* seq_lens, int32_t batch) {
@@ -268,9 +276,10 @@ oscar_status oscar_kv8_select_pages(oscar_ctx* ctx, int32_t layer, const void* q
   oscar_status st = check_query(ctx, layer, q, &q_stride, q_dtype, block_table, bt_stride, seq_lens, batch);
   if (st != OSCAR_OK) return st;
   if ((st = check_max_seq(ctx, max_seq)) != OSCAR_OK) return st;
-  if (n_select < 1 || keep_first < 0 || keep_last < 0 || (long long)keep_first + keep_last > n_select)
-    return fail(OSCAR_ERR_INVALID, "n_select %d, keep_first %d, keep_last %d: 1 <= n_select, keep_first + keep_last <= n_select",
-                n_select, keep_first, keep_last);
+  if ((st = check_select(n_select)) != OSCAR_OK) return st;
+  if (keep_first < 0 || keep_last < 0 || (long long)keep_first + keep_last > n_select)
+    return fail(OSCAR_ERR_INVALID, "keep_first %d and keep_last %d: neither below 0, together at most n_select (%d)", keep_first,
+                keep_last, n_select);
   if (batch == 0) return OSCAR_OK;
   if (!page_idx) return fail(OSCAR_ERR_INVALID, "null tensor argument");
   if ((st = check_workspace(workspace)) != OSCAR_OK) return st;
@@ -307,7 +316,9 @@ oscar_status oscar_kv8_sparse_workspace_size(const oscar_config* cfg, int32_t ba
   Geom g;
   const oscar_status st = validate(cfg, &g);
   if (st != OSCAR_OK) return st;
-  if (!bytes || batch < 0 || n_select < 1) return fail(OSCAR_ERR_INVALID, "bad arguments to workspace size");
+  if (!bytes || batch < 0) return fail(OSCAR_ERR_INVALID, "bad arguments to workspace size");
+  const oscar_status ok = check_select(n_select);
+  if (ok != OSCAR_OK) return ok;
   *bytes = oscar::kv8_plan(g, batch, n_select).total;
   return OSCAR_OK;
 }
@@ -319,8 +330,7 @@ oscar_status oscar_kv8_sparse_decode_attn(oscar_ctx* ctx, int32_t layer, const v
                                           void* stream) {
   oscar_status st = check_query(ctx, layer, q, &q_stride, q_dtype, block_table, bt_stride, seq_lens, batch);
   if (st != OSCAR_OK) return st;
-  if (n_select < 1) return fail(OSCAR_ERR_INVALID, "n_select %d is below 1", n_select);
-  if (batch == 0) return OSCAR_OK;
+  if ((st = check_select(n_select)) != OSCAR_OK || batch == 0) return st;
   if (!page_idx) return fail(OSCAR_ERR_INVALID, "null tensor argument");
   return attend(ctx, layer, q, q_stride, q_dtype, out, out_dtype, page_idx, n_select, block_table, bt_stride, seq_lens,
                 req_slot, batch, 0, workspace, ws_bytes, stream);

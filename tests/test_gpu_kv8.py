@@ -203,7 +203,7 @@ def test_refusals(osc):
                        (5, 3), (6, None), (7, 0), (8, None), (9, None), (10, -1), (10, 65536), (11, -1), (11, 12 * 16 + 1),
                        (12, None), (12, ws[1:]), (13, 64), (13, 1 << 21)],
             "select": [(1, 2), (2, None), (3, 9), (4, None), (5, 0), (6, None), (7, -1), (8, -1), (8, 193), (9, -1), (10, -1),
-                       (9, 3), (11, 0), (11, 1), (12, None), (12, idx[:3]), (13, None), (14, 8)],
+                       (9, 3), (11, 0), (11, 1), (11, 1 << 25), (12, None), (12, idx[:3]), (13, None), (14, 8)],
             "sparse": [(1, 2), (2, None), (3, 9), (4, None), (5, 4), (6, None), (6, idx[:, :, :2].contiguous()), (7, 0), (8, None),
                        (9, 0), (10, None), (11, None), (12, -1), (13, None), (14, 64)],
         }
@@ -275,6 +275,46 @@ def test_appends_leave_what_a_write_leaves(osc, fmt, P, d, dtype):
         for b in range(B):
             at = (whole.layer, slots[b], slice(None), slice(None), slice(end[b] % P))
             assert torch.equal(r.tail[at], whole.tail[at])
+
+
+def test_write_shuffled_rows_of_a_thousand_requests(osc):
+    """More requests than one probe of the search covers twice over, many of them empty, rows with a gap before the first."""
+    rng = np.random.default_rng(6)
+    B, P = 1100, 16
+    lens = [int(x) for x in rng.integers(0, 30, B) * (rng.random(B) < 0.7)]
+    starts = [0] * B
+    with Rig(osc, O.INT8, P, 64, heads=1, slots=B, per_req=2, pages=sum(n // P for n in lens) + 1) as r:
+        bt, slots = tables(rng, B, 2, r.cfg.num_pages, [n // P for n in lens]), rng.permutation(B)
+        cu = 5 + np.concatenate([[0], np.cumsum(lens)])
+        K, V = (acts(rng, (int(cu[-1]) + 3, 1, 64)) for _ in range(2))
+        osc.oscar_kv8_write(r.ctx, r.layer, r.rows(K, 1), r.rows(V, 1), 1, dev(cu), dev(starts), B, len(K), dev(bt), 2, dev(slots))
+        for b in range(B):
+            r.ref.write(bt[b], slots[b], 0, bf16(K[cu[b]:cu[b + 1]]), bf16(V[cu[b]:cu[b + 1]]))
+        r.same()
+        assert r.status() == 0
+
+
+def test_padded_batch(osc):
+    """Padding in a batch: appends of length -1 and writes of no rows are skipped whatever their slot says."""
+    rng = np.random.default_rng(7)
+    P, d = 16, 64
+    with Rig(osc, O.E4M3, P, d) as r:
+        bt = tables(rng, 4, 12, 48, [2, 0, 2, 0])
+        lens, slots = [20, 0, 31, 0], [1, -1, 3, 99]
+        K, V = ([acts(rng, (n, 2, d)) for n in lens] for _ in range(2))
+        r.write(K, V, 1, lens, [0, -5, 0, 1 << 30], bt, slots, ref=False)
+        k, v = acts(rng, (4, 2, d)), acts(rng, (4, 2, d))
+        osc.oscar_kv8_append(r.ctx, r.layer, r.rows(k, 1), r.rows(v, 1), 1, dev([20, -1, 31, -1]), 4, dev(bt), 12, dev(slots))
+        for b in (0, 2):
+            r.ref.write(bt[b], slots[b], 0, bf16(K[b]), bf16(V[b]))
+            r.ref.write(bt[b], slots[b], lens[b], bf16(k[b:b + 1]), bf16(v[b:b + 1]), append=True)
+        assert r.status() == 0
+        r.same()
+        q = acts(rng, (4, 4, d), False)
+        out = r.decode(q, 1, 0, bt, [21, 0, 32, 0], slots)
+        assert torch.all(out[[1, 3]] == 0) and r.status() == 0
+        for b in (0, 2):
+            r.check(out[b:b + 1], q[b:b + 1], 1, 0, bt[b:b + 1], [[21, 0, 32, 0][b]], [slots[b]])
 
 
 @pytest.mark.parametrize("fmt", [O.INT8, O.E4M3])

@@ -113,6 +113,9 @@ def test_workspace_sizes(osc):
             f(_cfg(osc, page_size=8), 1, 10)
     with pytest.raises(osc.OscarError):
         osc.oscar_kv8_sparse_workspace_size(c, 1, 0)
+    with pytest.raises(osc.OscarError) as e:
+        osc.oscar_kv8_sparse_workspace_size(c, 1, (1 << 24) + 1)
+    assert e.value.status == osc.ERR_UNSUPPORTED
     assert osc.oscar_kv8_decode_workspace_size(c, 3, 100) >= 3 * 8 * 68 * 4
     assert osc.oscar_kv8_decode_workspace_size(c, 0, 100) >= 0
 
