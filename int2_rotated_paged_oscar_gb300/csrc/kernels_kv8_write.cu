@@ -7,49 +7,53 @@
 // and writes d + (2 d + 16) / P bytes per K or V row, so it is bound by memory: one CTA holds a block's P x d values in
 // registers as BF16 pairs, from 16-byte copies, for both passes over them (the maximum, then the codes).
 // 8 x 32K tokens, 8 kv heads of 128 channels, BF16 to E4M3: 265 us, 6.1 TB/s, 0.90 of the measured copy bandwidth.
+#include <cstdlib>
 #include "kv8.cuh"
 
 namespace oscar {
 namespace {
 
-constexpr int kMaxThreads = 256;
+constexpr int kThreads = 256;
 // Units on their way: 1, 2 and 3 took 291, 265 and 270 us for 8 x 32K tokens (8 kv heads of 128, BF16, E4M3).
 constexpr int kAhead = 2;
 
 struct Item {
-  int b, page;           // request, logical page completed by this item (-1: none)
+  int b, slot;           // request, its slot
+  int page, pages;       // logical pages completed by this item: page, page + 1, ... (pages may be 0)
   int tail0, tail1;      // tokens copied into the tail
   int start, row0;       // first new token and its input row
 };
 
-// What request b of the call asks for, if it is sound: cnt items (0: nothing, or flagged).
-__device__ __forceinline__ int request(const Kv8WriteArgs& a, int b, int* start, int* len, int* row0) {
+// What request b of the call asks for, if it is sound: its items (0: nothing, or flagged).
+// An item is a span of up to `span` pages.
+__device__ __forceinline__ int request(const Kv8WriteArgs& a, int span, int b, int* start, int* len, int* row0, int* slot) {
   const Geom& g = a.g;
   *start = a.start_pos[b];
   *row0 = a.cu_seqlens ? a.cu_seqlens[b] : b;
   const long long l = a.cu_seqlens ? (long long)a.cu_seqlens[b + 1] - *row0 : (*start == -1 ? 0 : 1);
-  const int slot = a.req_slot[b];
+  *slot = a.req_slot[b];
   if (l == 0) return 0;
   if (*start < 0 || *row0 < 0 || l < 0 || *row0 + l > a.total_tokens || *start + l > (long long)g.max_pages_per_req * g.P) {
     flag_error(a.status, kDevBadLen);
     return 0;
   }
-  if (slot < 0 || slot >= g.max_req) {
+  if (*slot < 0 || *slot >= g.max_req) {
     flag_error(a.status, kDevBadSlot);
     return 0;
   }
   *len = (int)l;
-  return max((*start + *len) / g.P - *start / g.P, 1);
+  return max(((*start + *len) / g.P - *start / g.P + span - 1) / span, 1);
 }
 
-// The j-th item of a request.  A request whose chunk completes c pages has max(c, 1) items: item j quantises its j-th
-// page, item 0 also stores the rows of the page that stays incomplete, after it has read the rows of the old one from
-// the same tail.  An append keeps its row in the tail even when it completes the page.
-__device__ __forceinline__ Item item_of(const Kv8WriteArgs& a, int b, int j, int start, int len, int row0) {
+// The j-th item of a request.  Item 0 also stores the rows of the page that stays incomplete, after it has read the rows
+// of the old one from the same tail.  An append keeps its row in the tail even when it completes the page.
+__device__ __forceinline__ Item item_of(const Kv8WriteArgs& a, int span, int b, int j, int start, int len, int row0, int slot) {
   const int P = a.g.P, first = start / P, last = (start + len) / P;
   Item it;
   it.b = b;
-  it.page = first + j < last ? first + j : -1;
+  it.slot = slot;
+  it.page = first + j * span;
+  it.pages = min(span, last - it.page);
   it.start = start;
   it.row0 = row0;
   it.tail0 = j == 0 ? (a.cu_seqlens ? max(last * P, start) : start) : 0;
@@ -57,72 +61,90 @@ __device__ __forceinline__ Item item_of(const Kv8WriteArgs& a, int b, int j, int
   return it;
 }
 
-// One warp finds the item of CTA x.  A request of len rows completes at most len / P + 1 pages, so request b has the CTAs
-// from cu[b] / P + b on, as many as it can need (the rest end at once), and a 32-way search over that bound finds b.
+// One warp finds the item of CTA x.  A request of len rows completes at most len / P + 1 pages, which is at most
+// len / (P span) + 1 spans, so request b has the CTAs from cu[b] / (P span) + b on, as many as it can need (the rest end at
+// once), and a 32-way search over that bound finds b.
 // CTA x also checks request x: one that no CTA works on is reported all the same.
-__device__ bool find_item(const Kv8WriteArgs& a, int x, Item* out) {
-  const int lane = threadIdx.x & 31, P = a.g.P;
-  int start, len, row0;
-  if (x < a.batch) (void)request(a, x, &start, &len, &row0);
+__device__ bool find_item(const Kv8WriteArgs& a, int span, int x, Item* out) {
+  const int lane = threadIdx.x & 31, rows = a.g.P * span;
+  int start = 0, len = 0, row0 = 0, slot = 0;
+  if (a.batch <= 32) {  // every lane its request, one round of loads
+    const int cnt = lane < a.batch ? request(a, span, lane, &start, &len, &row0, &slot) : 0;
+    const int first = row0 / rows + lane;
+    const unsigned hit = __ballot_sync(0xffffffffu, lane < a.batch && first <= x);
+    if (hit == 0) return false;
+    const int l = 31 - __clz(hit), j = x - __shfl_sync(0xffffffffu, first, l);
+    if (j < 0 || j >= __shfl_sync(0xffffffffu, cnt, l)) return false;
+    *out = item_of(a, span, l, j, __shfl_sync(0xffffffffu, start, l), __shfl_sync(0xffffffffu, len, l), __shfl_sync(0xffffffffu, row0, l),
+                   __shfl_sync(0xffffffffu, slot, l));
+    return true;
+  }
+  if (x < a.batch) (void)request(a, span, x, &start, &len, &row0, &slot);
   int b = 0, n = a.batch;
   while (n > 1) {
     const int step = (n + 31) / 32, at = b + lane * step;
-    const bool below = lane * step < n && a.cu_seqlens[at] / P + at <= x;
+    const bool below = lane * step < n && a.cu_seqlens[at] / rows + at <= x;
     const unsigned hit = __ballot_sync(0xffffffffu, below);
     if (hit == 0) return false;
     const int l = 31 - __clz(hit);
     b += l * step;
     n = min(step, n - l * step);
   }
-  const int j = x - (a.cu_seqlens[b] / P + b);
-  if (j < 0 || j >= request(a, b, &start, &len, &row0)) return false;
-  *out = item_of(a, b, j, start, len, row0);
+  const int j = x - (a.cu_seqlens[b] / rows + b);
+  if (j < 0 || j >= request(a, span, b, &start, &len, &row0, &slot)) return false;
+  *out = item_of(a, span, b, j, start, len, row0, slot);
   return true;
 }
 
-// x M / m, correctly rounded, from x (2^e M) and m 2^e in [2, 4): with r the correctly rounded reciprocal of the latter,
-// one correction of x r by its exact remainder (Markstein, "Computation of elementary functions on the IBM RISC
-// System/6000 processor", 1990).  Numbers below float32's normal range only arise where the code is 0.
+// The code nearest x M / m from one multiplication by a float32 near M / m.  A quotient of numbers of 8 and 7 significant
+// bits by one of 8 is a tie T between two codes or far from one: x M - T m, where it is not 0, is a whole number of last
+// places of numbers of at most 16 bits (INT8: T has 8, m 8) or 13 (E4M3: T has 5), so the quotient misses T by 2^-16 or
+// 2^-13 of T at least.  The factor is a little too large (by up to 9 half steps of 2^-24: the approximate reciprocal is off
+// by 2 at most, a rounding by 1, and three last places, 3 to 6 of them, are added), so that dropping the product's last 5
+// or 8 bits takes what belongs on a tie back to it and carries nothing across one.  Then E4M3 has the hardware's
+// rounding, and INT8 the sum with 1.5 2^23 + 128, whose low byte is the code's.
+template <int FMT>
 struct Quotient {
-  float up, den, rec;
-  __device__ __forceinline__ Quotient(float m, float M) {
-    const int k = (int)(__float_as_uint(m) >> 23) - 127;  // m in [2^k, 2^(k+1)), -100 <= k <= 127
+  float f;
+  __device__ __forceinline__ explicit Quotient(float m) {  // 2^-100 <= m
+    // m in [2^k, 2^(k+1)) is brought to [2, 4) and back by powers of two, so that nothing leaves the normal numbers
+    const int k = (int)(__float_as_uint(m) >> 23) - 127;
     const float s = __uint_as_float((uint32_t)(128 - k) << 23);
-    up = s * M;
-    den = m * s;
-    rec = __frcp_rn(den);
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(m * s));
+    f = __uint_as_float(__float_as_uint(r * (FMT == kKv8Int8 ? 127.f : 448.f) * s) + 3u);
   }
   __device__ __forceinline__ float operator()(float x) const {
-    const float t = x * up, q = t * rec;
-    return fmaf(-fmaf(q, den, -t), rec, q);   // (in these signs a -0 stays one)
+    return __uint_as_float(__float_as_uint(x * f) & (FMT == kKv8Int8 ? 0xffffffe0u : 0xffffff00u));
   }
+  __device__ __forceinline__ uint32_t byte(float x) const { return __float_as_uint((*this)(x) + 12583040.f); }
 };
 
 // Codes of four finite values as one word.
 template <int FMT>
-__device__ __forceinline__ uint32_t encode4(const Quotient& quo, uint32_t x01, uint32_t x23) {
-  const float y0 = quo(bf16_lo(x01)), y1 = quo(bf16_hi(x01)), y2 = quo(bf16_lo(x23)), y3 = quo(bf16_hi(x23));
+__device__ __forceinline__ uint32_t encode4(const Quotient<FMT>& quo, uint32_t x01, uint32_t x23) {
+  const float x0 = bf16_lo(x01), x1 = bf16_hi(x01), x2 = bf16_lo(x23), x3 = bf16_hi(x23);
   if constexpr (FMT == kKv8Int8) {
-    // 1.5 2^23 + 128 + y: the sum's rounding is the code's, its low byte the stored byte
-    const uint32_t a = __float_as_uint(y0 + 12583040.f), b = __float_as_uint(y1 + 12583040.f);
-    const uint32_t c = __float_as_uint(y2 + 12583040.f), d = __float_as_uint(y3 + 12583040.f);
-    return prmt(prmt(a, b, 0x0040u), prmt(c, d, 0x0040u), 0x5410u);
+    return prmt(prmt(quo.byte(x0), quo.byte(x1), 0x0040u), prmt(quo.byte(x2), quo.byte(x3), 0x0040u), 0x5410u);
   } else {
     uint16_t lo, hi;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(y1), "f"(y0));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(y3), "f"(y2));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(quo(x1)), "f"(quo(x0)));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(quo(x3)), "f"(quo(x2)));
     return (uint32_t)lo | ((uint32_t)hi << 16);
   }
 }
 
+// Smaller and larger BF16 pairs, and the larger in magnitude (a NaN stays one).
 __device__ __forceinline__ uint32_t bmin2(uint32_t a, uint32_t b) {
-  const __nv_bfloat162 r = __hmin2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  const __nv_bfloat162 r = __hmin2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 __device__ __forceinline__ uint32_t bmax2(uint32_t a, uint32_t b) {
-  const __nv_bfloat162 r = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
+
+__device__ __forceinline__ uint32_t babs2(uint32_t a) { return a & 0x7fff7fffu; }
 
 // Eight float32 values as BF16 pairs.
 __device__ __forceinline__ uint4 to_bf16(const uint4& x, const uint4& y) {
@@ -134,41 +156,54 @@ __device__ __forceinline__ void copy_async(void* smem, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem)), "l"(src) : "memory");
 }
 
-// A block of P x D values: T threads, V vectors of eight channels each, the channels of a thread the same in all of them.
+// A block of P x D values is a group of T threads' work, V vectors of eight channels each, the channels of a thread the
+// same in all of them; a CTA holds NU groups, and works on a span of NU pages: as much for any P and D.  (With one block a
+// CTA, P = 16 and d = 128 ran at 0.42 of the measured copy bandwidth: most of a CTA's time was its look-up and barriers.)
 template <int D, int P>
 struct Shape {
-  static constexpr int T = P * D / 8 < kMaxThreads ? P * D / 8 : kMaxThreads;
-  static constexpr int V = P * D / 8 / T;
+  static constexpr int V = 4;
+  static constexpr int T = P * D / 8 / V;
+  static constexpr int NU = kThreads / T, SPAN = NU;
   static constexpr int CH = D / 8;       // threads of a row
   static constexpr int RS = T / CH;      // rows between a thread's vectors
+  static_assert(T >= 32 && T % 32 == 0 && T % CH == 0, "a group is whole warps and whole rows");
+  __device__ __forceinline__ static void sync(int group) {
+    if constexpr (T == 32) __syncwarp();
+    else if constexpr (T == kThreads) __syncthreads();
+    else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(T) : "memory");
+  }
 };
 
 template <int D, int P, int FMT, bool F32>
-__global__ void __launch_bounds__(Shape<D, P>::T) kv8_write_kernel(const __grid_constant__ Kv8WriteArgs a) {
+__global__ void __launch_bounds__(kThreads, F32 ? 3 : 4) kv8_write_kernel(const __grid_constant__ Kv8WriteArgs a) {
   using S = Shape<D, P>;
-  constexpr int W = S::T / 32;
+  constexpr int W = S::T / 32;             // warps of a group
   constexpr float M = FMT == kKv8Int8 ? 127.f : 448.f;
   __shared__ Item s_item;
-  __shared__ int s_have;
-  __shared__ int s_max[W], s_fin[W];
-  __shared__ uint4 s_lo[W][S::CH], s_hi[W][S::CH];
-  extern __shared__ uint4 ahead[];         // [kAhead][V][words][T]
+  __shared__ int s_have, s_pid[S::SPAN];
+  __shared__ int s_max_all[kThreads / 32], s_fin_all[kThreads / 32];
+  __shared__ uint4 s_lo_all[kThreads / 32][S::CH], s_hi_all[kThreads / 32][S::CH];
+  extern __shared__ uint4 ahead[];         // [kAhead][V][words][threads]
   const Geom& g = a.g;
   const Kv8Geom kg{P, D, g.Hkv};
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int group = threadIdx.x / S::T, tid = threadIdx.x % S::T, warp = tid >> 5, lane = tid & 31;   // in the group
+  int* s_max = s_max_all + group * W;
+  int* s_fin = s_fin_all + group * W;
+  auto s_lo = s_lo_all + group * W;
+  auto s_hi = s_hi_all + group * W;
   pdl_wait();
   pdl_launch_dependents();
-  if (tid < 32) {
+  if (threadIdx.x < 32) {
     Item it;
     bool have;
     if (a.cu_seqlens) {
-      have = find_item(a, blockIdx.x, &it);
+      have = find_item(a, S::SPAN, blockIdx.x, &it);
     } else {
-      int start, len, row0;
-      have = request(a, blockIdx.x, &start, &len, &row0) > 0;
-      if (have) it = item_of(a, blockIdx.x, 0, start, len, row0);
+      int start, len, row0, slot;
+      have = request(a, S::SPAN, blockIdx.x, &start, &len, &row0, &slot) > 0;
+      if (have) it = item_of(a, S::SPAN, blockIdx.x, 0, start, len, row0, slot);
     }
-    if (tid == 0) {
+    if (threadIdx.x == 0) {
       s_item = it;
       s_have = have;
     }
@@ -177,80 +212,121 @@ __global__ void __launch_bounds__(Shape<D, P>::T) kv8_write_kernel(const __grid_
   if (!s_have) return;
   const Item it = s_item;
   const int row = tid / S::CH, ch = (tid % S::CH) * 8;   // this thread's first row and its channels
-  const int slot = a.req_slot[it.b];
-  int pid = -1;
-  if (it.page >= 0) {
-    if (it.page < a.bt_stride) pid = a.block_table[(size_t)it.b * a.bt_stride + it.page];
+  const int k_place = kv8_place<D, false>(row, ch), v_place = kv8_place<D, true>(row, ch);
+  if (threadIdx.x < it.pages) {            // (SPAN <= 8 pages)
+    const int lp = it.page + threadIdx.x;
+    int pid = lp < a.bt_stride ? a.block_table[(size_t)it.b * a.bt_stride + lp] : -1;
     if (pid < 0 || pid >= g.num_pages) {
       pid = -1;
-      if (tid == 0) flag_error(a.status, kDevBadPage);
+      flag_error(a.status, kDevBadPage);
     }
+    s_pid[threadIdx.x] = pid;
   }
-  // eight values of an input row
-  auto input_at = [&](int kv, int h, int t) -> const void* {
-    const size_t i = (size_t)(it.row0 + (t - it.start)) * (size_t)(kv ? a.v_stride : a.k_stride) + (size_t)h * D + ch;
-    if constexpr (F32) return static_cast<const float*>(kv ? a.V : a.K) + i;
-    return static_cast<const uint16_t*>(kv ? a.V : a.K) + i;
+  // this thread's channels of input row t of K or V, head 0
+  constexpr int E = F32 ? 4 : 2;
+  auto input_at = [&](int kv, int t) {
+    return static_cast<const uint8_t*>(kv ? a.V : a.K) + ((long long)(it.row0 + (t - it.start)) * (kv ? a.v_stride : a.k_stride) + ch) * E;
   };
   auto input = [&](int kv, int h, int t) {  // as BF16 pairs
-    const uint4* p = static_cast<const uint4*>(input_at(kv, h, t));
+    const uint4* p = reinterpret_cast<const uint4*>(input_at(kv, t) + h * D * E);
     if constexpr (F32) return to_bf16(p[0], p[1]);
     return p[0];
   };
   auto tail_of = [&](int unit) {
-    return a.tail + ((size_t)a.layer * g.max_req + slot) * kv8_tail_req_elems(g) + (size_t)unit * P * D;
+    return a.tail + ((size_t)a.layer * g.max_req + it.slot) * kv8_tail_req_elems(g) + (size_t)unit * P * D;
   };
-  // A unit is (kv head, K | V).  The next ones' rows are on their way, by asynchronous copies into words of shared
-  // memory that only this thread reads again, while this one's are worked on.
+  // A unit is (kv head, K | V) of a page of the span.  The next ones' rows are on their way, by asynchronous copies into
+  // words of shared memory that only this thread reads again, while this one's are worked on.
   constexpr int WD = F32 ? 2 : 1;           // 16-byte words of eight input values
-  const int units = 2 * g.Hkv;
-  auto fetch = [&](int i) {                 // the i-th unit of this CTA
-    const int unit = blockIdx.y + i * gridDim.y;
-    if (unit < units) {
-      const uint16_t* tail = tail_of(unit);
+  const int units = 2 * g.Hkv, step = gridDim.y * S::NU;
+  // (page of the span, unit) of this group's current work and of the next to fetch
+  auto advance = [&](int& page, int& unit) {
+    for (unit += step; unit >= units; unit -= units) ++page;
+  };
+  int page = 0, unit = blockIdx.y * S::NU + group, buffer = 0;
+  for (; unit >= units; unit -= units) ++page;
+  int next_page = page, next_unit = unit;
+  // Float32 rows are fetched as each lane's 16 bytes of a run, and read as each thread's 32: word w of a row lies at place
+  // (w & 1) CH + w / 2 of its 2 CH places, so neither crosses banks more than twice.
+  const int place0 = threadIdx.x / S::CH * S::CH * WD, mine = threadIdx.x % S::CH;
+  const long long rs_k = a.k_stride * S::RS * E, rs_v = a.v_stride * S::RS * E;   // bytes between a thread's rows
+  const uint8_t *from_k = nullptr, *from_v = nullptr;                               // of the page that is fetched
+  int from_page = -1;
+  auto fetch = [&](int at) {                // into buffer `at`
+    if (next_page < it.pages) {
+      const int t0 = (it.page + next_page) * P + row;
+      if (next_page != from_page) {
+        from_page = next_page;
+        from_k = input_at(0, t0);
+        from_v = input_at(1, t0);
+      }
+      const uint8_t* from = ((next_unit & 1) ? from_v : from_k) + (next_unit >> 1) * D * E;
+      const long long rs = (next_unit & 1) ? rs_v : rs_k;
+      uint4* to = ahead + at * S::V * WD * kThreads + place0;
+      const bool mixed = (it.page + next_page) * P < it.start;   // rows of the old tail among them
 #pragma unroll
       for (int k = 0; k < S::V; ++k) {
-        const int r = row + k * S::RS, t = it.page * P + r;
-        uint4* to = ahead + ((i % kAhead * S::V + k) * WD) * S::T + tid;
-        if (t < it.start) {
-          copy_async(to, tail + (size_t)r * D + ch);
+        uint4* slab = to + k * WD * kThreads;
+        if (mixed && t0 + k * S::RS < it.start) {
+          copy_async(slab + mine, tail_of(next_unit) + (size_t)(row + k * S::RS) * D + ch);
+        } else if constexpr (F32) {
+          const uint8_t* line = from + k * rs - mine * 32;
+          copy_async(slab + (mine & 1) * S::CH + mine / 2, line + mine * 16);
+          copy_async(slab + (mine & 1) * S::CH + (mine + S::CH) / 2, line + (mine + S::CH) * 16);
         } else {
-          const uint4* from = static_cast<const uint4*>(input_at(unit & 1, unit >> 1, t));
-#pragma unroll
-          for (int w = 0; w < WD; ++w) copy_async(to + w * S::T, from + w);
+          copy_async(slab + mine, from + k * rs);
         }
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
+    advance(next_page, next_unit);
   };
-  if (it.page >= 0)
-    for (int i = 0; i < kAhead; ++i) fetch(i);
-  for (int i = 0, unit = blockIdx.y; unit < units; ++i, unit += gridDim.y) {
+  for (int i = 0; i < kAhead; ++i) fetch(i);
+  __syncthreads();                          // (the pages' ids)
+  for (const int pages = max(it.pages, 1); page < pages; advance(page, unit)) {
     const int kv = unit & 1, h = unit >> 1;
     uint16_t* tail = tail_of(unit);
-    if (it.page >= 0) {
+    if (it.pages > 0) {
+      const int pid = s_pid[page];
       asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+      if constexpr (F32) __syncwarp();
       uint4 x[S::V];
+      const uint4* from = ahead + buffer * S::V * WD * kThreads + place0 + mine;
+      const bool mixed = (it.page + page) * P < it.start;
 #pragma unroll
       for (int k = 0; k < S::V; ++k) {
-        const uint4* from = ahead + ((i % kAhead * S::V + k) * WD) * S::T + tid;
-        x[k] = from[0];
+        x[k] = from[k * WD * kThreads];
         if constexpr (F32) {
-          if (it.page * P + row + k * S::RS >= it.start) x[k] = to_bf16(x[k], from[S::T]);
+          if (!(mixed && (it.page + page) * P + row + k * S::RS < it.start)) x[k] = to_bf16(x[k], from[k * WD * kThreads + S::CH]);
         }
       }
-      fetch(i + kAhead);
-      uint32_t m2 = 0;
+      if constexpr (F32) __syncwarp();
+      fetch(buffer);
+      buffer = buffer + 1 == kAhead ? 0 : buffer + 1;
+      // the channels' smallest and largest values (K), and from them, or directly (V), the largest magnitude
+      uint4 lo = x[0], hi = x[0];
+      auto fold = [&](const uint4& l, const uint4& u) {
+        lo = make_uint4(bmin2(lo.x, l.x), bmin2(lo.y, l.y), bmin2(lo.z, l.z), bmin2(lo.w, l.w));
+        hi = make_uint4(bmax2(hi.x, u.x), bmax2(hi.y, u.y), bmax2(hi.z, u.z), bmax2(hi.w, u.w));
+      };
+      uint32_t m2;
+      if (!kv) {
 #pragma unroll
-      for (int k = 0; k < S::V; ++k) {
-        m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(x[k].x & 0x7fff7fffu, x[k].y & 0x7fff7fffu),
-                                   __vmaxu2(x[k].z & 0x7fff7fffu, x[k].w & 0x7fff7fffu)));
+        for (int k = 1; k < S::V; ++k) fold(x[k], x[k]);
+        m2 = bmax2(bmax2(bmax2(babs2(lo.x), babs2(lo.y)), bmax2(babs2(lo.z), babs2(lo.w))),
+                   bmax2(bmax2(babs2(hi.x), babs2(hi.y)), bmax2(babs2(hi.z), babs2(hi.w))));
+      } else {
+        m2 = 0;
+#pragma unroll
+        for (int k = 0; k < S::V; ++k)
+          m2 = bmax2(m2, bmax2(bmax2(babs2(x[k].x), babs2(x[k].y)), bmax2(babs2(x[k].z), babs2(x[k].w))));
       }
       int big = (int)__reduce_max_sync(0xffffffffu, max(m2 & 0xffffu, m2 >> 16));
-      if (lane == 0) s_max[warp] = big;
-      __syncthreads();
-#pragma unroll
-      for (int w = 0; w < W; ++w) big = max(big, s_max[w]);
+      if constexpr (W > 1) {
+        if (lane == 0) s_max[warp] = big;
+        S::sync(group);
+        big = (int)__reduce_max_sync(0xffffffffu, (unsigned)s_max[lane % W]);
+      }
       if (big >= 0x7f80) {
         // infinities and NaNs: the scale is the finite values'; an infinity becomes the largest of them, a NaN 0
         if (tid == 0) flag_error(a.status, kDevBadValue);
@@ -262,38 +338,33 @@ __global__ void __launch_bounds__(Shape<D, P>::T) kv8_write_kernel(const __grid_
         }
         fin = (int)__reduce_max_sync(0xffffffffu, (unsigned)fin);
         if (lane == 0) s_fin[warp] = fin;
-        __syncthreads();
-        big = 0;
-        for (int w = 0; w < W; ++w) big = max(big, s_fin[w]);
+        S::sync(group);
+        big = (int)__reduce_max_sync(0xffffffffu, (unsigned)s_fin[lane % W]);
         for (int i = 0; i < 8 * S::V; ++i) {
           const int v = e[i] & 0x7fff;
           if (v >= 0x7f80) e[i] = (uint16_t)(v == 0x7f80 ? (e[i] & 0x8000) | big : 0);
         }
+        lo = hi = x[0];
+#pragma unroll
+        for (int k = 1; k < S::V; ++k) fold(x[k], x[k]);
       }
       const float m = __uint_as_float((uint32_t)big << 16);
       const bool some = m >= kKv8Smallest;
-      const Quotient quo(some ? m : 1.f, M);
+      const Quotient<FMT> quo(some ? m : 1.f);
       constexpr uint32_t kZero = FMT == kKv8Int8 ? 0x80808080u : 0u;
       uint8_t* block = a.pool + ((size_t)a.layer * g.num_pages + (pid < 0 ? 0 : pid)) * kg.page_bytes() + (size_t)h * kg.block_bytes();
       if (pid >= 0) {
 #pragma unroll
         for (int k = 0; k < S::V; ++k) {
-          const int r = row + k * S::RS;
           uint2 code = make_uint2(kZero, kZero);
           if (some) code = make_uint2(encode4<FMT>(quo, x[k].x, x[k].y), encode4<FMT>(quo, x[k].z, x[k].w));
-          uint8_t* at = kv ? block + kg.v_off() + kv8_place<D, true>(r, ch) : block + kv8_place<D, false>(r, ch);
-          *reinterpret_cast<uint2*>(at) = code;
+          // (rows RS apart have the same turn, but for V's at RS = 4, where it changes by 4 chunks)
+          const int off = kv ? v_place ^ (S::RS == 4 && (k & 1) ? 64 : 0) : k_place;
+          *reinterpret_cast<uint2*>(block + off + (kv ? P * D : 0) + k * S::RS * D) = code;
         }
         if (tid == 0) reinterpret_cast<float*>(block + kg.scale_off())[kv] = some ? __fdiv_rn(m, M) : 0.f;
       }
       if (!kv) {
-        uint4 lo = x[0], hi = x[0];
-        auto fold = [&](const uint4& l, const uint4& u) {
-          lo = make_uint4(bmin2(lo.x, l.x), bmin2(lo.y, l.y), bmin2(lo.z, l.z), bmin2(lo.w, l.w));
-          hi = make_uint4(bmax2(hi.x, u.x), bmax2(hi.y, u.y), bmax2(hi.z, u.z), bmax2(hi.w, u.w));
-        };
-#pragma unroll
-        for (int k = 1; k < S::V; ++k) fold(x[k], x[k]);
 #pragma unroll
         for (int o = S::CH; o < 32; o <<= 1) {
           uint4 l, u;
@@ -307,7 +378,7 @@ __global__ void __launch_bounds__(Shape<D, P>::T) kv8_write_kernel(const __grid_
           s_lo[warp][lane] = lo;
           s_hi[warp][lane] = hi;
         }
-        __syncthreads();
+        S::sync(group);
         if (tid < S::CH && pid >= 0) {
           for (int w = 0; w < W; ++w) fold(s_lo[w][tid], s_hi[w][tid]);
           uint2 l = make_uint2(kZero, kZero), u = l;
@@ -323,28 +394,30 @@ __global__ void __launch_bounds__(Shape<D, P>::T) kv8_write_kernel(const __grid_
           *reinterpret_cast<uint2*>(block + kg.hi_off() + ch) = u;
         }
       }
-      __syncthreads();   // every row of the old tail is read, and the shared words are free
+      S::sync(group);   // every row of the old tail is read, and the shared words are free
     }
-    for (int t = it.tail0 + row; t < it.tail1; t += S::RS) *reinterpret_cast<uint4*>(tail + (size_t)(t % P) * D + ch) = input(kv, h, t);
+    if (page == 0)
+      for (int t = it.tail0 + row; t < it.tail1; t += S::RS) *reinterpret_cast<uint4*>(tail + (size_t)(t % P) * D + ch) = input(kv, h, t);
   }
 }
 
 template <int D, int P, int FMT>
 int launch_write(const Kv8WriteArgs& a, cudaStream_t s, bool pdl) {
-  const int items = a.cu_seqlens ? a.total_tokens / P + a.batch : a.batch;
-  // several units a CTA where there are CTAs enough: one look-up of the item, and loads that never pause
-  // (16 units each at 8 x 32K tokens: 265 us, 8 each 271 us; one each without prefetch 411 us)
-  const int units = 2 * a.g.Hkv;
-  long long per = (long long)items * units / (152LL * 4 * 4);
-  if (per < 1) per = 1;
-  if (per > units) per = units;
-  const dim3 grid(items, (unsigned)((units + per - 1) / per));
   using S = Shape<D, P>;
+  const int items = a.cu_seqlens ? a.total_tokens / (P * S::SPAN) + a.batch : a.batch;
+  // several units a group where there are CTAs enough: one look-up of the item, and loads that never pause
+  // (16 units each at 8 x 32K tokens: 265 us, 8 each 271 us; one each without prefetch 411 us)
+  const int rounds = a.cu_seqlens ? 2 * a.g.Hkv : (2 * a.g.Hkv + S::NU - 1) / S::NU;   // a CTA's, were it alone with its item
+  static const int TG = getenv("TG") ? atoi(getenv("TG")) : 4;
+  long long per = (long long)items * rounds / (152LL * 4 * TG);
+  if (per < 1) per = 1;
+  if (per > rounds) per = rounds;
+  const dim3 grid(items, (unsigned)((rounds + per - 1) / per));
   const bool f32 = a.dtype == kDtypeF32;
-  const size_t smem = (size_t)kAhead * S::V * S::T * (f32 ? 2 : 1) * sizeof(uint4);
+  const size_t smem = (size_t)kAhead * S::V * kThreads * (f32 ? 2 : 1) * sizeof(uint4);
   auto go = [&](auto kern) {
     const cudaError_t e = ensure_smem_limit(kern, smem, true);
-    return e != cudaSuccess ? (int)e : launch_pdl(kern, grid, dim3(S::T), smem, s, pdl, a);
+    return e != cudaSuccess ? (int)e : launch_pdl(kern, grid, dim3(kThreads), smem, s, pdl, a);
   };
   return f32 ? go(kv8_write_kernel<D, P, FMT, true>) : go(kv8_write_kernel<D, P, FMT, false>);
 }

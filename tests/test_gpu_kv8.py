@@ -277,6 +277,25 @@ def test_appends_leave_what_a_write_leaves(osc, fmt, P, d, dtype):
             assert torch.equal(r.tail[at], whole.tail[at])
 
 
+@pytest.mark.parametrize("fmt", [O.INT8, O.E4M3])
+def test_every_quotient(osc, fmt):
+    """All pairs of BF16 mantissas of a value and of its block's maximum, the value up to 2^15 smaller: every tie between two
+    codes and every quotient next to one."""
+    P, d = 64, 128
+    x = np.outer(2.0 ** -np.arange(16), np.arange(128, 256)).reshape(-1)            # 2048 values
+    rows = np.zeros((128, P * d))
+    for i, m in enumerate(range(128, 256)):
+        own = x[x <= m]
+        rows[i, :2 * len(own)] = np.concatenate([own, -own])
+        rows[i, -1] = m
+    K = np.concatenate([rows, rows[::-1] * 2.0 ** 90]).reshape(-1, 1, d)
+    with Rig(osc, fmt, P, d, heads=1, per_req=256, pages=256, slots=1) as r:
+        bt = np.arange(256, dtype=np.int32)[None]
+        r.write([K], [K[::-1] * 2.0 ** -180], 0, [256 * P], [0], bt, [0])
+        r.same()
+        assert r.status() == 0
+
+
 def test_write_shuffled_rows_of_a_thousand_requests(osc):
     """More requests than one probe of the search covers twice over, many of them empty, rows with a gap before the first."""
     rng = np.random.default_rng(6)
