@@ -6,17 +6,14 @@
 // Rounding is monotone, so lo and hi are the codes of a channel's smallest and largest x.  It reads 2 d (or 4 d) bytes
 // and writes d + (2 d + 16) / P bytes per K or V row, so it is bound by memory: one CTA holds a block's P x d values in
 // registers as BF16 pairs, from 16-byte copies, for both passes over them (the maximum, then the codes).
-// 8 x 32K tokens, 8 kv heads of 128 channels, BF16 to E4M3: 265 us, 6.1 TB/s, 0.90 of the measured copy bandwidth.
-#include <cstdlib>
+// 8 x 32K tokens, 8 kv heads of 128 channels, BF16 to E4M3: 250 us, 6.5 TB/s, 0.95 of the measured copy bandwidth; float32
+// rows come to 0.6 of it.
 #include "kv8.cuh"
 
 namespace oscar {
 namespace {
 
 constexpr int kThreads = 256;
-// Units on their way: 1, 2 and 3 took 291, 265 and 270 us for 8 x 32K tokens (8 kv heads of 128, BF16, E4M3).
-constexpr int kAhead = 2;
-
 struct Item {
   int b, slot;           // request, its slot
   int page, pages;       // logical pages completed by this item: page, page + 1, ... (pages may be 0)
@@ -158,10 +155,12 @@ __device__ __forceinline__ void copy_async(void* smem, const void* src) {
 
 // A block of P x D values is a group of T threads' work, V vectors of eight channels each, the channels of a thread the
 // same in all of them; a CTA holds NU groups, and works on a span of NU pages: as much for any P and D.  (With one block a
-// CTA, P = 16 and d = 128 ran at 0.42 of the measured copy bandwidth: most of a CTA's time was its look-up and barriers.)
+// CTA, P = 16 and d = 128 ran at 0.42 of the measured copy bandwidth instead of 0.85: most of a CTA's time was its look-up
+// and barriers.  Four vectors a thread instead of eight, and two units ahead, took 265 us at 8 x 32K tokens instead of 250:
+// what a unit costs beside its elements counts, the kernel issues instructions 0.65 of its cycles.)
 template <int D, int P>
 struct Shape {
-  static constexpr int V = 4;
+  static constexpr int V = P * D >= 2048 ? 8 : 4;
   static constexpr int T = P * D / 8 / V;
   static constexpr int NU = kThreads / T, SPAN = NU;
   static constexpr int CH = D / 8;       // threads of a row
@@ -175,7 +174,7 @@ struct Shape {
 };
 
 template <int D, int P, int FMT, bool F32>
-__global__ void __launch_bounds__(kThreads, F32 ? 3 : 4) kv8_write_kernel(const __grid_constant__ Kv8WriteArgs a) {
+__global__ void __launch_bounds__(kThreads, F32 ? 2 : 3) kv8_write_kernel(const __grid_constant__ Kv8WriteArgs a) {
   using S = Shape<D, P>;
   constexpr int W = S::T / 32;             // warps of a group
   constexpr float M = FMT == kKv8Int8 ? 127.f : 448.f;
@@ -183,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, F32 ? 3 : 4) kv8_write_kernel(const 
   __shared__ int s_have, s_pid[S::SPAN];
   __shared__ int s_max_all[kThreads / 32], s_fin_all[kThreads / 32];
   __shared__ uint4 s_lo_all[kThreads / 32][S::CH], s_hi_all[kThreads / 32][S::CH];
-  extern __shared__ uint4 ahead[];         // [kAhead][V][words][threads]
+  extern __shared__ uint4 ahead[];         // [V][words][threads]
   const Geom& g = a.g;
   const Kv8Geom kg{P, D, g.Hkv};
   const int group = threadIdx.x / S::T, tid = threadIdx.x % S::T, warp = tid >> 5, lane = tid & 31;   // in the group
@@ -235,15 +234,15 @@ __global__ void __launch_bounds__(kThreads, F32 ? 3 : 4) kv8_write_kernel(const 
   auto tail_of = [&](int unit) {
     return a.tail + ((size_t)a.layer * g.max_req + it.slot) * kv8_tail_req_elems(g) + (size_t)unit * P * D;
   };
-  // A unit is (kv head, K | V) of a page of the span.  The next ones' rows are on their way, by asynchronous copies into
-  // words of shared memory that only this thread reads again, while this one's are worked on.
+  // A unit is (kv head, K | V) of a page of the span.  The next one's rows are on their way, by asynchronous copies into
+  // words of shared memory that only this thread (float32: its warp) reads again, while this one's are worked on.
   constexpr int WD = F32 ? 2 : 1;           // 16-byte words of eight input values
   const int units = 2 * g.Hkv, step = gridDim.y * S::NU;
   // (page of the span, unit) of this group's current work and of the next to fetch
   auto advance = [&](int& page, int& unit) {
     for (unit += step; unit >= units; unit -= units) ++page;
   };
-  int page = 0, unit = blockIdx.y * S::NU + group, buffer = 0;
+  int page = 0, unit = blockIdx.y * S::NU + group;
   for (; unit >= units; unit -= units) ++page;
   int next_page = page, next_unit = unit;
   // Float32 rows are fetched as each lane's 16 bytes of a run, and read as each thread's 32: word w of a row lies at place
@@ -252,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, F32 ? 3 : 4) kv8_write_kernel(const 
   const long long rs_k = a.k_stride * S::RS * E, rs_v = a.v_stride * S::RS * E;   // bytes between a thread's rows
   const uint8_t *from_k = nullptr, *from_v = nullptr;                               // of the page that is fetched
   int from_page = -1;
-  auto fetch = [&](int at) {                // into buffer `at`
+  auto fetch = [&] {
     if (next_page < it.pages) {
       const int t0 = (it.page + next_page) * P + row;
       if (next_page != from_page) {
@@ -262,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, F32 ? 3 : 4) kv8_write_kernel(const 
       }
       const uint8_t* from = ((next_unit & 1) ? from_v : from_k) + (next_unit >> 1) * D * E;
       const long long rs = (next_unit & 1) ? rs_v : rs_k;
-      uint4* to = ahead + at * S::V * WD * kThreads + place0;
+      uint4* to = ahead + place0;
       const bool mixed = (it.page + next_page) * P < it.start;   // rows of the old tail among them
 #pragma unroll
       for (int k = 0; k < S::V; ++k) {
@@ -278,20 +277,19 @@ __global__ void __launch_bounds__(kThreads, F32 ? 3 : 4) kv8_write_kernel(const 
         }
       }
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
     advance(next_page, next_unit);
   };
-  for (int i = 0; i < kAhead; ++i) fetch(i);
+  fetch();
   __syncthreads();                          // (the pages' ids)
   for (const int pages = max(it.pages, 1); page < pages; advance(page, unit)) {
     const int kv = unit & 1, h = unit >> 1;
     uint16_t* tail = tail_of(unit);
     if (it.pages > 0) {
       const int pid = s_pid[page];
-      asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+      asm volatile("cp.async.wait_all;" ::: "memory");
       if constexpr (F32) __syncwarp();
       uint4 x[S::V];
-      const uint4* from = ahead + buffer * S::V * WD * kThreads + place0 + mine;
+      const uint4* from = ahead + place0 + mine;
       const bool mixed = (it.page + page) * P < it.start;
 #pragma unroll
       for (int k = 0; k < S::V; ++k) {
@@ -301,8 +299,7 @@ __global__ void __launch_bounds__(kThreads, F32 ? 3 : 4) kv8_write_kernel(const 
         }
       }
       if constexpr (F32) __syncwarp();
-      fetch(buffer);
-      buffer = buffer + 1 == kAhead ? 0 : buffer + 1;
+      fetch();
       // the channels' smallest and largest values (K), and from them, or directly (V), the largest magnitude
       uint4 lo = x[0], hi = x[0];
       auto fold = [&](const uint4& l, const uint4& u) {
@@ -358,8 +355,8 @@ __global__ void __launch_bounds__(kThreads, F32 ? 3 : 4) kv8_write_kernel(const 
         for (int k = 0; k < S::V; ++k) {
           uint2 code = make_uint2(kZero, kZero);
           if (some) code = make_uint2(encode4<FMT>(quo, x[k].x, x[k].y), encode4<FMT>(quo, x[k].z, x[k].w));
-          // (rows RS apart have the same turn, but for V's at RS = 4, where it changes by 4 chunks)
-          const int off = kv ? v_place ^ (S::RS == 4 && (k & 1) ? 64 : 0) : k_place;
+          // V's turn in rows k RS on: the same at RS = 8, 4 chunks off at every second k at RS = 4, 2 (k & 3) at RS = 2
+          const int off = kv ? v_place ^ ((k * S::RS / 2 & 3) * 32) : k_place;
           *reinterpret_cast<uint2*>(block + off + (kv ? P * D : 0) + k * S::RS * D) = code;
         }
         if (tid == 0) reinterpret_cast<float*>(block + kg.scale_off())[kv] = some ? __fdiv_rn(m, M) : 0.f;
@@ -405,16 +402,15 @@ template <int D, int P, int FMT>
 int launch_write(const Kv8WriteArgs& a, cudaStream_t s, bool pdl) {
   using S = Shape<D, P>;
   const int items = a.cu_seqlens ? a.total_tokens / (P * S::SPAN) + a.batch : a.batch;
-  // several units a group where there are CTAs enough: one look-up of the item, and loads that never pause
-  // (16 units each at 8 x 32K tokens: 265 us, 8 each 271 us; one each without prefetch 411 us)
+  // Several units a group where there are CTAs enough: one look-up of the item, and loads that never pause.  (A CTA for
+  // each unit took 411 us at 8 x 32K tokens; 4 and 8 CTAs a slot instead of 2 took 2 and 8 % more at 8 x 8K, d = 64.)
   const int rounds = a.cu_seqlens ? 2 * a.g.Hkv : (2 * a.g.Hkv + S::NU - 1) / S::NU;   // a CTA's, were it alone with its item
-  static const int TG = getenv("TG") ? atoi(getenv("TG")) : 4;
-  long long per = (long long)items * rounds / (152LL * 4 * TG);
+  long long per = (long long)items * rounds / (152LL * 4 * 2);
   if (per < 1) per = 1;
   if (per > rounds) per = rounds;
   const dim3 grid(items, (unsigned)((rounds + per - 1) / per));
   const bool f32 = a.dtype == kDtypeF32;
-  const size_t smem = (size_t)kAhead * S::V * kThreads * (f32 ? 2 : 1) * sizeof(uint4);
+  const size_t smem = (size_t)S::V * kThreads * (f32 ? 2 : 1) * sizeof(uint4);
   auto go = [&](auto kern) {
     const cudaError_t e = ensure_smem_limit(kern, smem, true);
     return e != cudaSuccess ? (int)e : launch_pdl(kern, grid, dim3(kThreads), smem, s, pdl, a);
