@@ -15,7 +15,9 @@
 //           relative to the block's largest).
 // Codes are exact f16 numbers, so the only roundings are float32's.  The block's scales multiply scores
 // and sums in float32, and the weights are relative to the 16-token block's own maximum, so a quiet page
-// next to a loud one keeps its digits.  The tail rows go the same way with BF16 operands, 16 rows a warp, in
+// next to a loud one keeps its digits.  (CTAs that stay and take one split after another through the same ring, the next
+// split's pages ahead, were slower: 64 ragged requests 468 us instead of 423, the warps waiting at every split's end.  So
+// were four CTAs an SM with three stages, 531 us, and two with six, 451.)  The tail rows go the same way with BF16 operands, 16 rows a warp, in
 // the CTA of the request's last pages while its first pages are on their way.
 #include "kv8.cuh"
 
@@ -46,6 +48,11 @@ __device__ __forceinline__ bool length_ok(const Kv8DecodeArgs& a, int n) {
 // Partial of a split (m, l, -, -, acc[D]).
 __device__ __forceinline__ float* partial(const Kv8DecodeArgs& a, int b, int head, int split, int D) {
   return a.part + (((size_t)b * a.g.Hq + head) * a.wl.max_splits + split) * (D + 4);
+}
+
+__device__ __forceinline__ void store_out(const Kv8DecodeArgs& a, size_t i, float y) {
+  if (a.out_dtype == kDtypeBF16) static_cast<__nv_bfloat16*>(a.out)[i] = __float2bfloat16_rn(y);
+  else static_cast<float*>(a.out)[i] = y;
 }
 
 // Splits of a request with `have` page entries: one at least, for its tail.
@@ -165,7 +172,7 @@ __device__ __forceinline__ void tail_block(const Kv8DecodeArgs& a, int b, int h,
 // G8: eight query heads per kv head (an MMA column is a head, low halves go through a second MMA); otherwise
 // up to four (columns 2 h and 2 h + 1 are the high and the low half of head h).
 template <int D, int FMT, bool G8, bool QF32>
-__global__ void __launch_bounds__(kThreads, 3) kv8_decode_kernel(const __grid_constant__ Kv8DecodeArgs a) {
+__global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 3) kv8_decode_kernel(const __grid_constant__ Kv8DecodeArgs a) {
   using L = Layout<D>;
   constexpr int KS = D / 16;               // k-steps of a score, and channel tiles of a sum
   constexpr int NH = G8 ? 2 : 1;           // heads whose weights a lane holds
@@ -200,14 +207,17 @@ __global__ void __launch_bounds__(kThreads, 3) kv8_decode_kernel(const __grid_co
     if (list) early = e < a.n_select ? list[e] : -1;
     else early = e < a.bt_stride ? bt[e] : -1;
   }
-  if (!length_ok(a, n)) {
-    if (tid == 0 && blockIdx.x == 0) flag_error(a.status, kDevBadLen);
+  const bool sound = length_ok(a, n);
+  if (!sound && tid == 0 && split == 0) flag_error(a.status, kDevBadLen);
+  if (!sound || n == 0) {
+    if (a.wl.max_splits == 1)  // (else the merge writes the zeros)
+      for (int i = tid; i < G * D; i += kThreads) store_out(a, ((size_t)b * g.Hq + (size_t)h * G) * D + i, 0.f);
     return;
   }
   const int pages = n / P;
   const int have = a.page_idx ? a.n_select : pages;
   const int splits = split_count(a, have);
-  if (n == 0 || split >= splits) return;
+  if (split >= splits) return;
   const int e1 = min(e0 + a.wl.stages_per_split * per_stage, have);
   const int stages = (e1 - e0 + per_stage - 1) / per_stage;
   const int page_stride = L::page_stride(P), stage_bytes = L::stage_bytes(P);
@@ -490,6 +500,10 @@ __global__ void __launch_bounds__(kThreads, 3) kv8_decode_kernel(const __grid_co
       l = fmaf(f, row[1], l);
       o = fmaf(f, row[2 + ch], o);
     }
+    if (a.wl.max_splits == 1) {  // nothing to merge with
+      store_out(a, ((size_t)b * g.Hq + h * G + hh) * D + ch, l > 0.f ? o / l : 0.f);
+      continue;
+    }
     float* pp = partial(a, b, h * G + hh, split, D);
     pp[4 + ch] = o;
     if (ch == 0) {
@@ -548,10 +562,7 @@ __global__ void __launch_bounds__(32 * W) kv8_combine_kernel(const __grid_consta
     sum += s_l[w];
     o += s_o[w][tid];
   }
-  const float y = sum > 0.f ? o / sum : 0.f;
-  const size_t at = ((size_t)b * g.Hq + head) * D + tid;
-  if (a.out_dtype == kDtypeBF16) static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(y);
-  else static_cast<float*>(a.out)[at] = y;
+  store_out(a, ((size_t)b * g.Hq + head) * D + tid, sum > 0.f ? o / sum : 0.f);
 }
 
 template <int D, int FMT>
@@ -575,7 +586,7 @@ Kv8DecodeWs kv8_plan(const Geom& g, int batch, long long max_pages) {
   const int per_stage = kKv8StageTokens / g.P;
   const long long stages = (max_pages + per_stage - 1) / per_stage;
   const long long pairs = (long long)batch * g.Hkv > 0 ? (long long)batch * g.Hkv : 1;
-  const long long wave = 152LL * 3;        // resident CTAs
+  const long long wave = 152LL * (g.D == 64 ? 4 : 3);        // resident CTAs
   // The split that takes the fewest rounds of (its stages + 6, a CTA's start and end in stages): it fills one wave of CTAs
   // where it can (batch 1 at 32K: 9 stages 18.3 us, 8 23.1, 11 18.3) and keeps CTAs long in large batches (64 ragged
   // requests: 16 stages 472 us, 32 434, 64 423).
@@ -585,6 +596,10 @@ Kv8DecodeWs kv8_plan(const Geom& g, int batch, long long max_pages) {
     const long long c = ((ctas + wave - 1) / wave) * (per + 6);
     if (cost < 0 || c < cost) best = per, cost = c;
   }
+  // Up to 8 stages one CTA takes them all and writes the output itself.  On the device the merge pays from 5 stages on
+  // (batch 1, 8 stages: 6.4 us in one launch, 4.9 in two), but its launch costs the host 2 us, which is what a caller
+  // without a graph waits for (8.9 us a call against 10.7).
+  if (stages <= 8) best = stages > 0 ? stages : 1;
   w.stages_per_split = (int)best;
   w.max_splits = stages > 0 ? (int)((stages + best - 1) / best) : 1;
   w.total = (size_t)batch * g.Hq * w.max_splits * (g.D + 4) * sizeof(float);

@@ -163,6 +163,7 @@ oscar_status attend(oscar_ctx* ctx, int32_t layer, const void* q, int64_t q_stri
     ls.done(e);
     if (e) return cuda_fail(e, "8-bit decode launch");
   }
+  if (a.wl.max_splits == 1) return OSCAR_OK;  // the one split of a request has written its output
   LaunchScope ls(ctx, "kv8_combine", stream);
   const int e = oscar::launch_kv8_combine(a, stream, pdl);
   ls.done(e);

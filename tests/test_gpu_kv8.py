@@ -748,11 +748,13 @@ def test_offsets_past_32_bits(osc):
 def test_kernel_times_by_name(osc):
     rng = np.random.default_rng(47)
     lens = [100]
-    rig, bt, slots = filled(osc, rng, lens)
+    rig, bt, slots = filled(osc, rng, lens, per_req=200)
     with rig as r:
         osc.oscar_set_timing(r.ctx, True)
         q = acts(rng, (1, 4, 64), False)
-        r.decode(q, 1, 0, bt, lens, slots, pages=r.select(q, 1, bt, lens, 0, 0, 2))
-        for name in ("kv8_select", "kv8_decode", "kv8_combine"):
+        r.select(q, 1, bt, lens, 0, 0, 2)
+        r.check(r.decode(q, 1, 0, bt, lens, slots, max_seq=3200), q, 1, 0, bt, lens, slots)    # split: decode and merge
+        r.check(r.decode(q, 1, 0, bt, lens, slots), q, 1, 0, bt, lens, slots)                  # short: decode alone
+        for name, calls in (("kv8_select", 1), ("kv8_decode", 2), ("kv8_combine", 1)):
             ms, count = osc.oscar_kernel_time(r.ctx, name)
-            assert ms > 0 and count == 1
+            assert ms > 0 and count == calls, name
