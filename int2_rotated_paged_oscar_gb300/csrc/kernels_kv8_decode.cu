@@ -27,7 +27,13 @@ namespace {
 constexpr int kConsumers = 4;
 constexpr int kThreads = 32 * (kConsumers + 1);
 constexpr int kStages = 4;
-constexpr float kLog2e = 1.4426950408889634f;
+// log2(e) / sqrt(d) as two floats: a score is far larger than its distance from the largest one, which is what counts, so
+// scale and distance are formed without a rounding of the score itself.
+template <int D>
+struct Scale {
+  static constexpr double kValue = 1.4426950408889634 / (D == 128 ? 11.313708498984761 : 8.0);
+  static constexpr float hi = (float)kValue, lo = (float)(kValue - (double)(float)kValue);
+};
 
 template <int D>
 struct Layout {
@@ -76,7 +82,7 @@ __device__ __forceinline__ void split3(float x, float y, uint32_t (&t)[3]) {
 // Keys and values are BF16 operands as they are, queries and weights sums of up to three.
 template <int D, bool G8, bool QF32, int NH>
 __device__ __forceinline__ void tail_block(const Kv8DecodeArgs& a, int b, int h, const uint16_t* krows, const uint16_t* vrows, int cnt,
-                                           float sm_log2, float (&m_run)[NH], float (&l_run)[NH], float (&acc)[D / 16][2 * NH]) {
+                                           float (&m_run)[NH], float (&l_run)[NH], float (&acc)[D / 16][2 * NH]) {
   constexpr int KS = D / 16;
   const int G = a.g.gq(), lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
   const int head = G8 ? gid : gid >> 1;
@@ -116,14 +122,13 @@ __device__ __forceinline__ void tail_block(const Kv8DecodeArgs& a, int b, int h,
 #pragma unroll
   for (int i = 0; i < NH; ++i) {
     // (BF16 queries leave their odd columns empty: an infinite key times their 0 would be NaN)
-    const float sa = gid < cnt ? (G8 ? sc[i] : QF32 ? sc[0] + sc[1] : sc[0]) * sm_log2 : -INFINITY;
-    const float sb = gid + 8 < cnt ? (G8 ? sc[2 + i] : QF32 ? sc[2] + sc[3] : sc[2]) * sm_log2 : -INFINITY;
-    float m = fmaxf(sa, sb);
+    const float ca = G8 ? sc[i] : QF32 ? sc[0] + sc[1] : sc[0], cb = G8 ? sc[2 + i] : QF32 ? sc[2] + sc[3] : sc[2];
+    float m = fmaxf(gid < cnt ? ca * Scale<D>::hi : -INFINITY, gid + 8 < cnt ? cb * Scale<D>::hi : -INFINITY);
     m = warp_max_xor(m, 4);
     m = warp_max_xor(m, 8);
     m = warp_max_xor(m, 16);
-    pr[i][0] = gid < cnt ? ex2(sa - m) : 0.f;
-    pr[i][1] = gid + 8 < cnt ? ex2(sb - m) : 0.f;
+    pr[i][0] = gid < cnt ? ex2(fmaf(ca, Scale<D>::lo, fmaf(ca, Scale<D>::hi, -m))) : 0.f;
+    pr[i][1] = gid + 8 < cnt ? ex2(fmaf(cb, Scale<D>::lo, fmaf(cb, Scale<D>::hi, -m))) : 0.f;
     m_run[i] = m;
     l_run[i] = pr[i][0] + pr[i][1];
   }
@@ -222,7 +227,6 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 3) kv8_decode_kernel(c
   const int stages = (e1 - e0 + per_stage - 1) / per_stage;
   const int page_stride = L::page_stride(P), stage_bytes = L::stage_bytes(P);
   __syncthreads();
-  const float sm_log2 = kLog2e * rsqrtf((float)D);
   const int gid = lane >> 2, tig = lane & 3;
   float m_run[NH], l_run[NH], acc[KS][2 * NH];
 #pragma unroll
@@ -334,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 3) kv8_decode_kernel(c
         }
 #pragma unroll
       for (int i = 0; i < NH; ++i)  // columns 2 tig (+ 1) of this lane: head 2 tig + i (G8) or head tig
-        qs[i] = __shfl_sync(0xffffffffu, down, (G8 ? 2 * tig + i : 2 * tig) * 4) * sm_log2;
+        qs[i] = __shfl_sync(0xffffffffu, down, (G8 ? 2 * tig + i : 2 * tig) * 4) * Scale<D>::hi;
     }
     const int pi = warp * 16 / P;                       // page of the stage, and the block's first token in it
     const int t0 = warp * 16 % P;
@@ -347,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 3) kv8_decode_kernel(c
       if (slot >= 0 && slot < g.max_req) {
         const uint16_t* rows = a.tail + ((size_t)a.layer * g.max_req + slot) * kv8_tail_req_elems(g) +
                                ((size_t)h * 2 * P + warp * 16) * D;
-        tail_block<D, G8, QF32>(a, b, h, rows, rows + (size_t)P * D, n % P - warp * 16, sm_log2, m_run, l_run, acc);
+        tail_block<D, G8, QF32>(a, b, h, rows, rows + (size_t)P * D, n % P - warp * 16, m_run, l_run, acc);
       } else if (lane == 0) {
         flag_error(a.status, kDevBadSlot);
       }
@@ -373,22 +377,27 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 3) kv8_decode_kernel(c
             const uint4 v = *reinterpret_cast<const uint4*>(page + at);
             kw[r][4 * c] = v.x, kw[r][4 * c + 1] = v.y, kw[r][4 * c + 2] = v.z, kw[r][4 * c + 3] = v.w;
           }
-        float sc[4] = {0.f, 0.f, 0.f, 0.f};
+        // (in two chains: the tensor cores' sums lose a last place or so a step, and the scores' errors count in full)
+        float sc[4] = {0.f, 0.f, 0.f, 0.f}, sd[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int kk = 0; kk < KS; ++kk) {
           const uint32_t a0 = kv8_pair<FMT, 0>(kw[0][kk]), a1 = kv8_pair<FMT, 0>(kw[1][kk]);
           const uint32_t a2 = kv8_pair<FMT, 1>(kw[0][kk]), a3 = kv8_pair<FMT, 1>(kw[1][kk]);
-          mma_f16(sc, a0, a1, a2, a3, qf[kk][0], qf[kk][1]);
-          if constexpr (G8 && QF32) mma_f16(sc, a0, a1, a2, a3, ql[kk][0], ql[kk][1]);
+          mma_f16(kk & 1 ? sd : sc, a0, a1, a2, a3, qf[kk][0], qf[kk][1]);
+          if constexpr (G8 && QF32) mma_f16(kk & 1 ? sd : sc, a0, a1, a2, a3, ql[kk][0], ql[kk][1]);
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sc[i] += sd[i];
         // weights relative to the block's maximum
         float w_acc[NH], alpha[NH];
         uint32_t pb[G8 ? 4 : 2];
         float pr[NH][2];
 #pragma unroll
         for (int i = 0; i < NH; ++i) {
-          const float f = sc2.x * qs[i];
-          const float sa = (G8 ? sc[i] : sc[0] + sc[1]) * f, sb = (G8 ? sc[2 + i] : sc[2] + sc[3]) * f;
+          const float fh = sc2.x * qs[i];
+          const float fl = fmaf(sc2.x, qs[i], -fh) + fh * (Scale<D>::lo / Scale<D>::hi);
+          const float ca = G8 ? sc[i] : sc[0], cb = G8 ? sc[2 + i] : sc[2];
+          const float sa = ca * fh, sb = cb * fh;  // (only to choose m: any m near the largest will do)
           float m = fmaxf(sa, sb);
           m = warp_max_xor(m, 4);
           m = warp_max_xor(m, 8);
@@ -396,8 +405,13 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 3) kv8_decode_kernel(c
           const float m_new = fmaxf(m_run[i], m);
           alpha[i] = ex2(m_run[i] - m_new);
           const float beta = ex2(m - m_new);
-          pr[i][0] = ex2(sa - m);
-          pr[i][1] = ex2(sb - m);
+          float da = fmaf(ca, fl, fmaf(ca, fh, -m)), db = fmaf(cb, fl, fmaf(cb, fh, -m));
+          if constexpr (!G8 && QF32) {             // the low halves' columns
+            da = fmaf(sc[1], fh, da);
+            db = fmaf(sc[3], fh, db);
+          }
+          pr[i][0] = ex2(da);
+          pr[i][1] = ex2(db);
           l_run[i] = fmaf(l_run[i], alpha[i], beta * (pr[i][0] + pr[i][1]));
           m_run[i] = m_new;
           w_acc[i] = beta * sc2.y;
