@@ -577,8 +577,8 @@ oscar_status oscar_set_decode_form(oscar_ctx* ctx, int32_t form);
  * last reset (synchronises the recorded events).  Names: "decode_splitk",
  * "decode_combine", "q_rotate", "step_prep", "append", "evict", "write", "bf16_prepare",
  * "bf16_decode", "bf16_combine", "extend", "selftest", "kv8_write", "kv8_append", "kv8_decode",
- * "kv8_combine" (contexts of more than 512 tokens or selected tokens), "kv8_select", "kv8_fork", "copy_pages", "remap_table".  Launches
- * recorded into a CUDA graph get external event-record nodes: replay the graph
+ * "kv8_combine" (not launched for contexts or selections of up to 512 tokens, 1024 at d = 64
+ * and P >= 32), "kv8_select", "kv8_fork", "copy_pages", "remap_table".  Launches recorded into a CUDA graph get external event-record nodes: replay the graph
  * once, then read; the events return to the library when read, so a graph
  * captured with timing on is replayed at most once.  With timing on, the decode
  * kernels are launched without programmatic dependent launch. */

@@ -6,15 +6,16 @@
 // merges the partials.  What it must read is 2 d bytes per token and kv head, so it is bound by memory;
 // 4 d flops per token and query head run on the tensor cores.
 //
-// A CTA has one producer warp and four consumer warps around a ring of stages of 64 tokens (64 / P pages,
-// each one bulk copy of codes and scales).  Consumer warp w takes tokens 16 w .. 16 w + 15 of a stage:
+// A CTA has one producer warp and four consumer warps around a ring of stages of 64 tokens (128 at
+// d = 64 and P >= 32; each page one bulk copy of codes and scales).  A consumer warp takes a quarter of a stage,
+// one block of 16 tokens or two of one page:
 //   scores: A = 16 tokens x 16 channels of codes, B = the query as f16 (a power of two brings its largest
 //           component to 2^14; BF16 queries are exact in one f16, float32 ones take a high and a low half);
 //           channels are taken in the order in which a lane's 16-byte loads hold them.
 //   values: A = 16 channels x 16 tokens of codes, B = the weights as f16 high and low halves (24 bits
-//           relative to the block's largest).
+//           relative to the blocks' largest).
 // Codes are exact f16 numbers, so the only roundings are float32's.  The block's scales multiply scores
-// and sums in float32, and the weights are relative to the 16-token block's own maximum, so a quiet page
+// and sums in float32, and the weights are relative to the maximum of a warp's own blocks, all of one page, so a quiet page
 // next to a loud one keeps its digits.  (CTAs that stay and take one split after another through the same ring, the next
 // split's pages ahead, were slower: 64 ragged requests 468 us instead of 423, the warps waiting at every split's end.  So
 // were four CTAs an SM with three stages, 531 us, and two with six, 451.)  The tail rows go the same way with BF16 operands, 16 rows a warp, in
@@ -26,7 +27,6 @@ namespace {
 
 constexpr int kConsumers = 4;
 constexpr int kThreads = 32 * (kConsumers + 1);
-constexpr int kStages = 4;
 // log2(e) / sqrt(d) as two floats: a score is far larger than its distance from the largest one, which is what counts, so
 // scale and distance are formed without a rounding of the score itself.
 template <int D>
@@ -35,11 +35,20 @@ struct Scale {
   static constexpr float hi = (float)kValue, lo = (float)(kValue - (double)(float)kValue);
 };
 
-template <int D>
+// CTAs an SM: four where their stages are small or, with fewer heads' sums, their registers few.  (d = 64, P = 64, 32 requests
+// of 8K to 16K tokens: up to four heads 72 us with four CTAs of three stages, 75 with three of four; eight heads 87 and 85,
+// in float32 98 and 86.)
+OSCAR_HD constexpr int resident(int D, int stage_tokens, bool g8) { return D == 64 && !(stage_tokens == 128 && g8) ? 4 : 3; }
+
+// NB: blocks of 16 tokens that a warp takes of a stage.
+template <int D, int NB, bool G8>
 struct Layout {
+  static constexpr int kTokens = 64 * NB;
+  static constexpr int kResident = resident(D, kTokens, G8);
+  static constexpr int kStages = NB == 2 && kResident == 4 ? 3 : 4;
   static constexpr int kPad = 128;  // scales, and the 128-byte alignment of the next page
   OSCAR_HD static int page_stride(int P) { return 2 * P * D + kPad; }
-  OSCAR_HD static int stage_bytes(int P) { return (kKv8StageTokens / P) * page_stride(P); }
+  OSCAR_HD static int stage_bytes(int P) { return (kTokens / P) * page_stride(P); }
   static size_t smem(int P) {
     const size_t ring = (size_t)kStages * stage_bytes(P);
     const size_t merge = kConsumers * 8 * (D + 2) * sizeof(float);
@@ -63,7 +72,7 @@ __device__ __forceinline__ void store_out(const Kv8DecodeArgs& a, size_t i, floa
 
 // Splits of a request with `have` page entries: one at least, for its tail.
 __device__ __forceinline__ int split_count(const Kv8DecodeArgs& a, int have) {
-  const int per = a.wl.stages_per_split * (kKv8StageTokens / a.g.P);
+  const int per = a.wl.stages_per_split * (kv8_stage_tokens(a.g.D, a.g.P) / a.g.P);
   return max((have + per - 1) / per, 1);
 }
 
@@ -176,9 +185,10 @@ __device__ __forceinline__ void tail_block(const Kv8DecodeArgs& a, int b, int h,
 // ------------------------------------------------------------------ pages
 // G8: eight query heads per kv head (an MMA column is a head, low halves go through a second MMA); otherwise
 // up to four (columns 2 h and 2 h + 1 are the high and the low half of head h).
-template <int D, int FMT, bool G8, bool QF32>
-__global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 3) kv8_decode_kernel(const __grid_constant__ Kv8DecodeArgs a) {
-  using L = Layout<D>;
+template <int D, int FMT, bool G8, bool QF32, int NB>
+__global__ void __launch_bounds__(kThreads, (Layout<D, NB, G8>::kResident)) kv8_decode_kernel(const __grid_constant__ Kv8DecodeArgs a) {
+  using L = Layout<D, NB, G8>;
+  constexpr int kStages = L::kStages;
   constexpr int KS = D / 16;               // k-steps of a score, and channel tiles of a sum
   constexpr int NH = G8 ? 2 : 1;           // heads whose weights a lane holds
   extern __shared__ __align__(128) uint8_t smem_raw[];
@@ -190,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 3) kv8_decode_kernel(c
   const int b = blockIdx.z, h = blockIdx.y, split = blockIdx.x;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = g.gq(), P = g.P;
-  const int per_stage = kKv8StageTokens / P;
+  const int per_stage = L::kTokens / P;
   const int e0 = split * a.wl.stages_per_split * per_stage;
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -206,11 +216,15 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 3) kv8_decode_kernel(c
   // the producer's first table entries travel with the length
   const int* bt = a.block_table + (size_t)b * a.bt_stride;
   const int* list = a.page_idx ? a.page_idx + ((size_t)b * g.Hkv + h) * a.n_select : nullptr;
-  int early = -1;
+  int early = -1, early_before = -1;
   if (warp == kConsumers) {
     const int e = e0 + lane;
-    if (list) early = e < a.n_select ? list[e] : -1;
-    else early = e < a.bt_stride ? bt[e] : -1;
+    if (list) {
+      early = e < a.n_select ? list[e] : -1;
+      early_before = e > 0 && e <= a.n_select ? list[e - 1] : -1;
+    } else {
+      early = e < a.bt_stride ? bt[e] : -1;
+    }
   }
   const bool sound = length_ok(a, n);
   if (!sound && tid == 0 && split == 0) flag_error(a.status, kDevBadLen);
@@ -245,14 +259,13 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 3) kv8_decode_kernel(c
     const uint64_t policy = l2_evict_first_policy();
     const uint32_t bytes = 2 * P * D + 16;
     const uint8_t* layer = a.pool + (size_t)a.layer * g.num_pages * kg.page_bytes() + (size_t)h * kg.block_bytes();
-    // page of entry e (value: the list's or the table's word for it); -1: nothing to copy
-    auto lookup = [&](int e, int value) {
+    // page of entry e (value: the list's or the table's word for it, before: the list's word before it); -1: nothing to copy
+    auto lookup = [&](int e, int value, int before) {
       if (e >= e1) return -1;
       int pid = value;
       if (list) {
-        const int before = e > 0 ? list[e - 1] : -1;
         if (value < 0) return -1;
-        if (value >= pages || (e > 0 && before < 0) || before >= value) {
+        if (value >= pages || before >= value || (e > 0 && before < 0)) {
           flag_error(a.status, kDevBadPage);
           return -1;
         }
@@ -264,8 +277,11 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 3) kv8_decode_kernel(c
       }
       return pid;
     };
-    auto word = [&](int e) { return e >= e1 ? -1 : list ? list[e] : e < a.bt_stride ? bt[e] : -1; };
-    int pid_now = lookup(e0 + lane, early), pid_next = lookup(e0 + 32 + lane, word(e0 + 32 + lane));
+    auto later = [&](int e) {  // the same for entries after the first 32
+      if (e >= e1) return -1;
+      return list ? lookup(e, list[e], list[e - 1]) : lookup(e, e < a.bt_stride ? bt[e] : -1, -1);
+    };
+    int pid_now = lookup(e0 + lane, early, early_before), pid_next = later(e0 + 32 + lane);
     int it = 0;
     bool good = true;
     for (; it < stages; ++it) {
@@ -278,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 3) kv8_decode_kernel(c
       const int at = it * per_stage;                    // first entry of the stage, relative to e0
       if (at > 0 && at % 32 == 0) {
         pid_now = pid_next;
-        pid_next = lookup(e0 + at + 32 + lane, word(e0 + at + 32 + lane));
+        pid_next = later(e0 + at + 32 + lane);
       }
       const int pid = __shfl_sync(0xffffffffu, pid_now, (at & 31) + (lane % per_stage));
       const unsigned there = __ballot_sync(0xffffffffu, lane < per_stage && pid >= 0);
@@ -340,8 +356,8 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 3) kv8_decode_kernel(c
       for (int i = 0; i < NH; ++i)  // columns 2 tig (+ 1) of this lane: head 2 tig + i (G8) or head tig
         qs[i] = __shfl_sync(0xffffffffu, down, (G8 ? 2 * tig + i : 2 * tig) * 4) * Scale<D>::hi;
     }
-    const int pi = warp * 16 / P;                       // page of the stage, and the block's first token in it
-    const int t0 = warp * 16 % P;
+    const int pi = warp * 16 * NB / P;                  // page of the stage, and the first block's first token in it
+    const int t0 = warp * 16 * NB % P;
     // byte offsets inside a page: K row gid (+ 8), chunk tig (+ 4); V rows 2 tig (+ 1, + 8, + 9), chunk of channels gid D / 8
     const uint32_t k_off = D == 128 ? (t0 + gid) * 128 + ((tig ^ (4 * (gid & 1))) << 4) : (t0 + gid) * 64 + tig * 16;
     const uint32_t v_off = P * D + (D == 128 ? (t0 + 2 * tig) * 128 + ((gid ^ (2 * tig)) << 4)
@@ -368,102 +384,128 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 3) kv8_decode_kernel(c
         const uint8_t* page = smem + s * stage_bytes + pi * page_stride;
         const float2 sc2 = *reinterpret_cast<const float2*>(page + 2 * P * D);
         // scores
-        uint32_t kw[2][KS];
+        float sc[NB][4];
+        float m[NH];
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+        for (int i = 0; i < NH; ++i) m[i] = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < KS / 4; ++c) {
-            const uint32_t at = D == 128 ? (k_off ^ (64 * c)) + r * 8 * D : k_off + r * 8 * D;
-            const uint4 v = *reinterpret_cast<const uint4*>(page + at);
-            kw[r][4 * c] = v.x, kw[r][4 * c + 1] = v.y, kw[r][4 * c + 2] = v.z, kw[r][4 * c + 3] = v.w;
+        for (int nb = 0; nb < NB; ++nb) {
+          uint32_t kw[2][KS];
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int c = 0; c < KS / 4; ++c) {
+              const uint32_t at = D == 128 ? (k_off ^ (64 * c)) + (2 * nb + r) * 8 * D : k_off + (2 * nb + r) * 8 * D;
+              const uint4 v = *reinterpret_cast<const uint4*>(page + at);
+              kw[r][4 * c] = v.x, kw[r][4 * c + 1] = v.y, kw[r][4 * c + 2] = v.z, kw[r][4 * c + 3] = v.w;
+            }
+          // (in two chains: the tensor cores' sums lose a last place or so a step, and the scores' errors count in full)
+          float sd[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sc[nb][i] = 0.f;
+#pragma unroll
+          for (int kk = 0; kk < KS; ++kk) {
+            const uint32_t a0 = kv8_pair<FMT, 0>(kw[0][kk]), a1 = kv8_pair<FMT, 0>(kw[1][kk]);
+            const uint32_t a2 = kv8_pair<FMT, 1>(kw[0][kk]), a3 = kv8_pair<FMT, 1>(kw[1][kk]);
+            mma_f16(kk & 1 ? sd : sc[nb], a0, a1, a2, a3, qf[kk][0], qf[kk][1]);
+            if constexpr (G8 && QF32) mma_f16(kk & 1 ? sd : sc[nb], a0, a1, a2, a3, ql[kk][0], ql[kk][1]);
           }
-        // (in two chains: the tensor cores' sums lose a last place or so a step, and the scores' errors count in full)
-        float sc[4] = {0.f, 0.f, 0.f, 0.f}, sd[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int kk = 0; kk < KS; ++kk) {
-          const uint32_t a0 = kv8_pair<FMT, 0>(kw[0][kk]), a1 = kv8_pair<FMT, 0>(kw[1][kk]);
-          const uint32_t a2 = kv8_pair<FMT, 1>(kw[0][kk]), a3 = kv8_pair<FMT, 1>(kw[1][kk]);
-          mma_f16(kk & 1 ? sd : sc, a0, a1, a2, a3, qf[kk][0], qf[kk][1]);
-          if constexpr (G8 && QF32) mma_f16(kk & 1 ? sd : sc, a0, a1, a2, a3, ql[kk][0], ql[kk][1]);
+          for (int i = 0; i < 4; ++i) sc[nb][i] += sd[i];
+#pragma unroll
+          for (int i = 0; i < NH; ++i) {  // (only to choose m: any m near the largest will do)
+            const float f = sc2.x * qs[i];
+            m[i] = fmaxf(m[i], fmaxf((G8 ? sc[nb][i] : sc[nb][0]) * f, (G8 ? sc[nb][2 + i] : sc[nb][2]) * f));
+          }
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sc[i] += sd[i];
-        // weights relative to the block's maximum
-        float w_acc[NH], alpha[NH];
-        uint32_t pb[G8 ? 4 : 2];
-        float pr[NH][2];
+        // weights relative to the blocks' maximum
+        float beta[NH], alpha[NH];
 #pragma unroll
         for (int i = 0; i < NH; ++i) {
-          const float fh = sc2.x * qs[i];
-          const float fl = fmaf(sc2.x, qs[i], -fh) + fh * (Scale<D>::lo / Scale<D>::hi);
-          const float ca = G8 ? sc[i] : sc[0], cb = G8 ? sc[2 + i] : sc[2];
-          const float sa = ca * fh, sb = cb * fh;  // (only to choose m: any m near the largest will do)
-          float m = fmaxf(sa, sb);
-          m = warp_max_xor(m, 4);
-          m = warp_max_xor(m, 8);
-          m = warp_max_xor(m, 16);
-          const float m_new = fmaxf(m_run[i], m);
+          m[i] = warp_max_xor(m[i], 4);
+          m[i] = warp_max_xor(m[i], 8);
+          m[i] = warp_max_xor(m[i], 16);
+          const float m_new = fmaxf(m_run[i], m[i]);
           alpha[i] = ex2(m_run[i] - m_new);
-          const float beta = ex2(m - m_new);
-          float da = fmaf(ca, fl, fmaf(ca, fh, -m)), db = fmaf(cb, fl, fmaf(cb, fh, -m));
-          if constexpr (!G8 && QF32) {             // the low halves' columns
-            da = fmaf(sc[1], fh, da);
-            db = fmaf(sc[3], fh, db);
-          }
-          pr[i][0] = ex2(da);
-          pr[i][1] = ex2(db);
-          l_run[i] = fmaf(l_run[i], alpha[i], beta * (pr[i][0] + pr[i][1]));
+          beta[i] = ex2(m[i] - m_new);
           m_run[i] = m_new;
-          w_acc[i] = beta * sc2.y;
+          l_run[i] *= alpha[i];
         }
-        if constexpr (G8) {
+        uint32_t pb[NB][G8 ? 4 : 2];
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const uint32_t hi = pack_half2(pr[0][r], pr[1][r]);
-            const __half2 hh = *reinterpret_cast<const __half2*>(&hi);
-            pb[r] = transpose_8x8(hi);
-            pb[2 + r] = transpose_8x8(pack_half2(pr[0][r] - __low2float(hh), pr[1][r] - __high2float(hh)));
+        for (int nb = 0; nb < NB; ++nb) {
+          float pr[NH][2];
+#pragma unroll
+          for (int i = 0; i < NH; ++i) {
+            const float fh = sc2.x * qs[i];
+            const float fl = fmaf(sc2.x, qs[i], -fh) + fh * (Scale<D>::lo / Scale<D>::hi);
+            const float ca = G8 ? sc[nb][i] : sc[nb][0], cb = G8 ? sc[nb][2 + i] : sc[nb][2];
+            float da = fmaf(ca, fl, fmaf(ca, fh, -m[i])), db = fmaf(cb, fl, fmaf(cb, fh, -m[i]));
+            if constexpr (!G8 && QF32) {             // the low halves' columns
+              da = fmaf(sc[nb][1], fh, da);
+              db = fmaf(sc[nb][3], fh, db);
+            }
+            pr[i][0] = ex2(da);
+            pr[i][1] = ex2(db);
+            l_run[i] = fmaf(beta[i], pr[i][0] + pr[i][1], l_run[i]);
           }
-        } else {
+          if constexpr (G8) {
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const float hi = __half2float(__float2half_rn(pr[0][r]));
-            pb[r] = transpose_8x8(pack_half2(hi, pr[0][r] - hi));
-          }
-        }
-        // sums
-        uint32_t vw[4][KS / 2];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if constexpr (D == 128) {
-            const uint4 v = *reinterpret_cast<const uint4*>(page + v_off + ((j & 1) + 8 * (j >> 1)) * 128);
-            vw[j][0] = v.x, vw[j][1] = v.y, vw[j][2] = v.z, vw[j][3] = v.w;
+            for (int r = 0; r < 2; ++r) {
+              const uint32_t hi = pack_half2(pr[0][r], pr[1][r]);
+              const __half2 hh = *reinterpret_cast<const __half2*>(&hi);
+              pb[nb][r] = transpose_8x8(hi);
+              pb[nb][2 + r] = transpose_8x8(pack_half2(pr[0][r] - __low2float(hh), pr[1][r] - __high2float(hh)));
+            }
           } else {
-            // row 2 tig + 1 is the other half of the 128-byte line: four chunks on
-            const uint2 v = *reinterpret_cast<const uint2*>(page + ((v_off - P * D) ^ (64 * (j & 1))) + P * D + (j >> 1) * 512);
-            vw[j][0] = v.x, vw[j][1] = v.y;
-          }
-        }
 #pragma unroll
-        for (int w = 0; w < KS / 2; ++w)
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const uint32_t x01 = prmt(vw[0][w], vw[1][w], u ? 0x7362u : 0x5140u);
-            const uint32_t x23 = prmt(vw[2][w], vw[3][w], u ? 0x7362u : 0x5140u);
-            const uint32_t a0 = kv8_pair<FMT, 0>(x01), a1 = kv8_pair<FMT, 1>(x01);
-            const uint32_t a2 = kv8_pair<FMT, 0>(x23), a3 = kv8_pair<FMT, 1>(x23);
-            float o[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_f16(o, a0, a1, a2, a3, pb[0], pb[1]);
-            if constexpr (G8) mma_f16(o, a0, a1, a2, a3, pb[2], pb[3]);
-            const int mt = 2 * w + u;
-            if constexpr (G8) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) acc[mt][i] = fmaf(acc[mt][i], alpha[i & 1], o[i] * w_acc[i & 1]);
-            } else {
-              acc[mt][0] = fmaf(acc[mt][0], alpha[0], (o[0] + o[1]) * w_acc[0]);
-              acc[mt][1] = fmaf(acc[mt][1], alpha[0], (o[2] + o[3]) * w_acc[0]);
+            for (int r = 0; r < 2; ++r) {
+              const float hi = __half2float(__float2half_rn(pr[0][r]));
+              pb[nb][r] = transpose_8x8(pack_half2(hi, pr[0][r] - hi));
             }
           }
+        }
+        // sums: acc = acc alpha + o beta scale, o over the blocks
+#pragma unroll
+        for (int i = 0; i < NH; ++i) beta[i] *= sc2.y;
+        float o[KS][4];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          uint32_t vw[4][KS / 2];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if constexpr (D == 128) {
+              const uint4 v = *reinterpret_cast<const uint4*>(page + v_off + (16 * nb + (j & 1) + 8 * (j >> 1)) * 128);
+              vw[j][0] = v.x, vw[j][1] = v.y, vw[j][2] = v.z, vw[j][3] = v.w;
+            } else {
+              // row 2 tig + 1 is the other half of the 128-byte line: four chunks on
+              const uint2 v = *reinterpret_cast<const uint2*>(page + ((v_off - P * D) ^ (64 * (j & 1))) + P * D + (2 * nb + (j >> 1)) * 512);
+              vw[j][0] = v.x, vw[j][1] = v.y;
+            }
+          }
+#pragma unroll
+          for (int w = 0; w < KS / 2; ++w)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const int mt = 2 * w + u;
+              const uint32_t x01 = prmt(vw[0][w], vw[1][w], u ? 0x7362u : 0x5140u);
+              const uint32_t x23 = prmt(vw[2][w], vw[3][w], u ? 0x7362u : 0x5140u);
+              const uint32_t a0 = kv8_pair<FMT, 0>(x01), a1 = kv8_pair<FMT, 1>(x01);
+              const uint32_t a2 = kv8_pair<FMT, 0>(x23), a3 = kv8_pair<FMT, 1>(x23);
+              if (nb == 0) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
+              mma_f16(o[mt], a0, a1, a2, a3, pb[nb][0], pb[nb][1]);
+              if constexpr (G8) mma_f16(o[mt], a0, a1, a2, a3, pb[nb][2], pb[nb][3]);
+              if (nb == NB - 1) {
+                if constexpr (G8) {
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) acc[mt][i] = fmaf(acc[mt][i], alpha[i & 1], o[mt][i] * beta[i & 1]);
+                } else {
+                  acc[mt][0] = fmaf(acc[mt][0], alpha[0], (o[mt][0] + o[mt][1]) * beta[0]);
+                  acc[mt][1] = fmaf(acc[mt][1], alpha[0], (o[mt][2] + o[mt][3]) * beta[0]);
+                }
+              }
+            }
+        }
       }
       __syncwarp();
       if (lane == 0) {
@@ -579,28 +621,33 @@ __global__ void __launch_bounds__(32 * W) kv8_combine_kernel(const __grid_consta
   store_out(a, ((size_t)b * g.Hq + head) * D + tid, sum > 0.f ? o / sum : 0.f);
 }
 
-template <int D, int FMT>
+template <int D, int FMT, int NB>
 int launch_pages(const Kv8DecodeArgs& a, cudaStream_t s, bool pdl) {
   const dim3 grid(a.wl.max_splits, a.g.Hkv, a.batch);
-  const size_t smem = Layout<D>::smem(a.g.P);
+  const size_t smem = a.g.gq() == 8 ? Layout<D, NB, true>::smem(a.g.P) : Layout<D, NB, false>::smem(a.g.P);
   auto go = [&](auto kern) {
     const cudaError_t e = ensure_smem_limit(kern, smem, true);
     if (e != cudaSuccess) return (int)e;
     return launch_pdl(kern, grid, dim3(kThreads), smem, s, pdl, a);
   };
   const bool f32 = a.q_dtype == kDtypeF32;
-  if (a.g.gq() == 8) return f32 ? go(kv8_decode_kernel<D, FMT, true, true>) : go(kv8_decode_kernel<D, FMT, true, false>);
-  return f32 ? go(kv8_decode_kernel<D, FMT, false, true>) : go(kv8_decode_kernel<D, FMT, false, false>);
+  if (a.g.gq() == 8) return f32 ? go(kv8_decode_kernel<D, FMT, true, true, NB>) : go(kv8_decode_kernel<D, FMT, true, false, NB>);
+  return f32 ? go(kv8_decode_kernel<D, FMT, false, true, NB>) : go(kv8_decode_kernel<D, FMT, false, false, NB>);
+}
+
+template <int D, int NB>
+int launch_format(const Kv8DecodeArgs& a, cudaStream_t s, bool pdl) {
+  return a.fmt == kKv8Int8 ? launch_pages<D, kKv8Int8, NB>(a, s, pdl) : launch_pages<D, kKv8E4m3, NB>(a, s, pdl);
 }
 
 }  // namespace
 
 Kv8DecodeWs kv8_plan(const Geom& g, int batch, long long max_pages) {
   Kv8DecodeWs w{};
-  const int per_stage = kKv8StageTokens / g.P;
+  const int per_stage = kv8_stage_tokens(g.D, g.P) / g.P;
   const long long stages = (max_pages + per_stage - 1) / per_stage;
   const long long pairs = (long long)batch * g.Hkv > 0 ? (long long)batch * g.Hkv : 1;
-  const long long wave = 152LL * (g.D == 64 ? 4 : 3);        // resident CTAs
+  const long long wave = 152LL * resident(g.D, kv8_stage_tokens(g.D, g.P), g.gq() == 8);
   // The split that takes the fewest rounds of (its stages + 6, a CTA's start and end in stages): it fills one wave of CTAs
   // where it can (batch 1 at 32K: 9 stages 18.3 us, 8 23.1, 11 18.3) and keeps CTAs long in large batches (64 ragged
   // requests: 16 stages 472 us, 32 434, 64 423).
@@ -622,8 +669,8 @@ Kv8DecodeWs kv8_plan(const Geom& g, int batch, long long max_pages) {
 
 int launch_kv8_decode(const Kv8DecodeArgs& a, void* stream, bool pdl) {
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (a.g.D == 128) return a.fmt == kKv8Int8 ? launch_pages<128, kKv8Int8>(a, s, pdl) : launch_pages<128, kKv8E4m3>(a, s, pdl);
-  return a.fmt == kKv8Int8 ? launch_pages<64, kKv8Int8>(a, s, pdl) : launch_pages<64, kKv8E4m3>(a, s, pdl);
+  if (a.g.D == 128) return launch_format<128, 1>(a, s, pdl);
+  return kv8_stage_tokens(a.g.D, a.g.P) == 128 ? launch_format<64, 2>(a, s, pdl) : launch_format<64, 1>(a, s, pdl);
 }
 
 int launch_kv8_combine(const Kv8DecodeArgs& a, void* stream, bool pdl) {

@@ -9,7 +9,9 @@ constexpr int kKv8E4m3 = 1;
 // A block whose largest finite magnitude is below this is stored as zeros with scale 0
 // (2^-100: scale and quotients of larger ones stay normal float32 numbers).
 constexpr float kKv8Smallest = 7.888609052210118e-31f;
-constexpr int kKv8StageTokens = 64;  // attention walks whole pages, 64 tokens' worth at a time
+// Attention walks whole pages in stages of 64 tokens, or of 128 where that is no more than 16 KB of codes and a quarter of it
+// lies in one page.
+OSCAR_HD constexpr int kv8_stage_tokens(int D, int P) { return D == 64 && P >= 32 ? 128 : 64; }
 
 // Byte layout of one (layer, page, kv head) block:
 //   K codes [P][D] | V codes [P][D] | K scale, V scale (float32), 8 unused bytes | K lo [D] | K hi [D] | pad to 128
@@ -52,7 +54,7 @@ struct Kv8WriteArgs {
 };
 
 struct Kv8DecodeWs {
-  int stages_per_split;  // 64-token stages of one split CTA
+  int stages_per_split;  // stages of one split CTA
   int max_splits;        // splits of a request, one at least
   size_t total;          // bytes: partials [batch][Hq][max_splits][D + 4] float32
 };
