@@ -10,16 +10,21 @@
 // d = 64 and P >= 32; each page one bulk copy of codes and scales).  A consumer warp takes a quarter of a stage,
 // one block of 16 tokens or two of one page:
 //   scores: A = 16 tokens x 16 channels of codes, B = the query as f16 (a power of two brings its largest
-//           component to 2^14; BF16 queries are exact in one f16, float32 ones take a high and a low half);
+//           component to 2^14; BF16 queries are exact in one f16 down to 2^-28 of it, float32 ones take two);
 //           channels are taken in the order in which a lane's 16-byte loads hold them.
 //   values: A = 16 channels x 16 tokens of codes, B = the weights as f16 high and low halves (24 bits
 //           relative to the blocks' largest).
 // Codes are exact f16 numbers, so the only roundings are float32's.  The block's scales multiply scores
 // and sums in float32, and the weights are relative to the maximum of a warp's own blocks, all of one page, so a quiet page
-// next to a loud one keeps its digits.  (CTAs that stay and take one split after another through the same ring, the next
-// split's pages ahead, were slower: 64 ragged requests 468 us instead of 423, the warps waiting at every split's end.  So
-// were four CTAs an SM with three stages, 531 us, and two with six, 451.)  The tail rows go the same way with BF16 operands, 16 rows a warp, in
-// the CTA of the request's last pages while its first pages are on their way.
+// next to a loud one keeps its digits.  The tail rows go the same way with BF16 operands, 16 rows a warp, in the CTA of the
+// request's last pages while its first pages are on their way.
+//
+// Measured (8 kv heads of 128 channels, pages of 64, layers larger than L2): batch 1 at 32K, INT8, 4 heads a kv head 16.9 us
+// (67 MB, 0.59 of the measured copy bandwidth: the start, the end and the merge take 7 us); 64 requests of 8K to 32K, E4M3,
+// 8 heads a kv head 430 us (2.7 GB, 0.92).  At d = 64 instructions count as much as bytes (0.82 with up to four heads a kv
+// head, 0.70 with eight).  Not kept, at the 64 requests: CTAs that stay and take one split after another through the same
+// ring, the next split's pages ahead (468 us: the warps wait at every split's end); four CTAs an SM with three stages
+// (531); two with six (451); a rescaling of the sums only where a maximum moved (434).
 #include "kv8.cuh"
 
 namespace oscar {

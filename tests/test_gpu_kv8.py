@@ -520,6 +520,24 @@ def test_select_ties_and_near_ties(osc, fmt):
         assert np.array_equal(r.select(q * 0, 1, bt, [P * pages], 0, 0, 9).cpu().numpy()[0], np.stack([np.arange(9)] * 2))
 
 
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("P,d", [(16, 64), (32, 128)])
+def test_select_where_the_loudest_query_channel_meets_no_key(osc, fmt, P, d):
+    """A query component 10^12 times the others over a channel of zero keys: the order is that of the others."""
+    rng = np.random.default_rng([d, fmt])
+    lens = [40 * P + 3]
+    with Rig(osc, fmt, P, d, heads=2, G=2, per_req=41, pages=41) as r:
+        bt = tables(rng, 1, 41, 41, [40])
+        K = rng.normal(size=(lens[0], 2, d))
+        K[:, :, 3] = 0
+        r.write([K], [K], 1, lens, [0], bt, [0])
+        q = rng.normal(size=(1, 4, d))
+        q[:, :, 3] = 1e12
+        for k in (1, 7, 39):
+            got = r.select(q, 0, bt, lens, 0, 0, k).cpu().numpy()[0]
+            assert np.array_equal(got, r.ref.select(q[0].astype(np.float32).astype(np.float64), bt[0], lens[0], 0, 0, k))
+
+
 def test_select_long(osc):
     rng = np.random.default_rng(29)
     P, d, pages = 16, 64, 4500
