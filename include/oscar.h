@@ -462,8 +462,9 @@ oscar_status oscar_kv8_bind(oscar_ctx* ctx, int32_t format, void* pool, void* ta
 /* Varlen write (prefill or extend) of tokens [start_pos[b], start_pos[b]+len_b) of each
  * request b; cu_seqlens, start_pos, req_slot, block_table and total_tokens as for
  * oscar_write_kv.  K, V: [total_tokens][n_kv_heads][d] in dtype, tokens k_stride and
- * v_stride elements apart.  The cache must hold exactly start_pos[b] tokens of request b
- * (its tail rows are read).  Every page that the chunk completes must be mapped (else
+ * v_stride elements apart.  cu_seqlens must not decrease (else OSCAR_DEV_BAD_LEN, and rows
+ * of other requests may be missing too).  The cache must hold exactly start_pos[b] tokens of
+ * request b (its tail rows are read).  Every page that the chunk completes must be mapped (else
  * OSCAR_DEV_BAD_PAGE and that page is not stored). */
 oscar_status oscar_kv8_write(oscar_ctx* ctx, int32_t layer, const void* K, int64_t k_stride, const void* V,
                              int64_t v_stride, int32_t dtype, const int32_t* cu_seqlens, const int32_t* start_pos,

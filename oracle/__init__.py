@@ -21,6 +21,8 @@ cache      the paged mixed-precision cache image: INT2 page pool + BF16
            sink/recent window; prefill/extend write, append-with-eviction.
 attention  decode attention over the mixed cache (plain and fused forms) and
            textbook attention over an all-BF16 paged cache.
+kv8        the 8-bit paged cache: its codes, its attention and page selection
+           (pinned by ``tests/test_kv8_host.py``).
 
 Pinning status: every function here is pinned by ``tests/test_oracle_pins.py``
 (closed forms, brute force on tiny inputs, invariants).  Two things stay
@@ -28,4 +30,4 @@ Pinning status: every function here is pinned by ``tests/test_oracle_pins.py``
 accuracy benefit of OSCAR's rotation (needs trained weights and datasets) and
 the pages' own kernel outputs.
 """
-from . import rotation, quant, cache, attention  # noqa: F401
+from . import rotation, quant, cache, attention, kv8  # noqa: F401
