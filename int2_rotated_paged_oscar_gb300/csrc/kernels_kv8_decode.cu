@@ -562,13 +562,13 @@ __global__ void __launch_bounds__(kThreads, (Layout<D, NB, G8>::kResident)) kv8_
       o = fmaf(f, row[2 + ch], o);
     }
     if (a.wl.max_splits == 1) {  // nothing to merge with
-      store_out(a, ((size_t)b * g.Hq + h * G + hh) * D + ch, l > 0.f ? o / l : 0.f);
+      store_out(a, ((size_t)b * g.Hq + h * G + hh) * D + ch, l == 0.f ? 0.f : o / l);
       continue;
     }
     float* pp = partial(a, b, h * G + hh, split, D);
     pp[4 + ch] = o;
     if (ch == 0) {
-      pp[0] = M;
+      pp[0] = l == l ? M : INFINITY;  // the merge takes no partial at -infinity: a NaN must not look like one
       pp[1] = l;
     }
   }
@@ -644,7 +644,7 @@ __global__ void __launch_bounds__(32 * W) kv8_combine_kernel(const __grid_consta
     sum = fmaf(f, s_ml[w].y, sum);
     o = fmaf(f, s_o[w][tid], o);
   }
-  store_out(a, ((size_t)b * g.Hq + head) * D + tid, sum > 0.f ? o / sum : 0.f);
+  store_out(a, ((size_t)b * g.Hq + head) * D + tid, sum == 0.f ? 0.f : o / sum);
 }
 
 template <int D, int FMT, int NB>

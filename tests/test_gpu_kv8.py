@@ -474,6 +474,43 @@ def test_decode_reports_bad_arguments_on_the_device(osc):
                 assert np.all(np.abs(out[1].double().cpu().numpy() - want) <= bound)
 
 
+@pytest.mark.parametrize("G,fmt,qd", [(2, 0, 0), (2, 1, 1), (8, 0, 1), (8, 1, 0)])
+@pytest.mark.parametrize("n", [1, 16 * 3, 16 * 3 + 5, 16 * 80 + 7])
+def test_decode_carries_nan(osc, G, fmt, qd, n):
+    """A NaN or an infinity in a query head, or a NaN in a tail row, makes NaN of what depends on it and of nothing else."""
+    rng = np.random.default_rng([G, fmt, n])
+    P, d, heads = 16, 64, 2
+    rig, bt, slots = filled(osc, rng, [n], fmt=fmt, P=P, d=d, G=G, heads=heads, per_req=81, pages=81)
+    with rig as r:
+        lists = np.full((1, heads, 81), -1, np.int32)
+        lists[:, :, :n // P] = np.arange(n // P)
+        q = acts(rng, (1, heads * G, d), False)
+        for pages in (None, lists) if n >= P else (None,):
+            good = r.decode(q, qd, 0, bt, [n], slots, pages=pages)
+            assert torch.isfinite(good).all()
+            for bad in (np.nan, np.inf, -np.inf):
+                x = q.copy()
+                x[0, G, 7] = bad                      # the second kv head's first query head
+                out = r.decode(x, qd, 0, bt, [n], slots, pages=pages)
+                keep = torch.arange(heads * G, device="cuda") != G
+                assert torch.isnan(out[0, G]).all() and torch.equal(out[0, keep], good[0, keep])
+            if n % P == 0:
+                continue
+            rows = r.tail[r.layer, slots[0], 1]       # [2][P][d] of the second kv head
+            for kv in range(2):
+                was = rows[kv, n % P - 1, 9].clone()
+                rows[kv, n % P - 1, 9] = float("nan")
+                out = r.decode(q, qd, 0, bt, [n], slots, pages=pages)
+                rows[kv, n % P - 1, 9] = was
+                reach = torch.zeros_like(out, dtype=torch.bool)
+                reach[0, G:] = True
+                if kv:
+                    reach[:] = False
+                    reach[0, G:, 9] = True
+                assert torch.isnan(out[reach]).all() and torch.equal(out[~reach], good[~reach])
+        assert r.status() == 0
+
+
 # ------------------------------------------------------------------------------------------------ selection, sparse decode
 @pytest.mark.parametrize("P,d", GEO)
 @pytest.mark.parametrize("G,fmt,qd", [(1, 0, 1), (4, 1, 0), (8, 0, 0), (8, 1, 1)])
