@@ -168,7 +168,6 @@ struct Shape {
   static_assert(T >= 32 && T % 32 == 0 && T % CH == 0, "a group is whole warps and whole rows");
   __device__ __forceinline__ static void sync(int group) {
     if constexpr (T == 32) __syncwarp();
-    else if constexpr (T == kThreads) __syncthreads();
     else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(T) : "memory");
   }
 };
@@ -403,7 +402,8 @@ int launch_write(const Kv8WriteArgs& a, cudaStream_t s, bool pdl) {
   using S = Shape<D, P>;
   const int items = a.cu_seqlens ? a.total_tokens / (P * S::SPAN) + a.batch : a.batch;
   // Several units a group where there are CTAs enough: one look-up of the item, and loads that never pause.  (A CTA for
-  // each unit took 411 us at 8 x 32K tokens; 4 and 8 CTAs a slot instead of 2 took 2 and 8 % more at 8 x 8K, d = 64.)
+  // each unit took 411 us at 8 x 32K tokens; 4 CTAs a slot instead of 2 took 10 to 23 % more at 8 x 8K, d = 64, and the
+  // same time at d = 128.)
   const int rounds = a.cu_seqlens ? 2 * a.g.Hkv : (2 * a.g.Hkv + S::NU - 1) / S::NU;   // a CTA's, were it alone with its item
   long long per = (long long)items * rounds / (152LL * 4 * 2);
   if (per < 1) per = 1;
