@@ -123,7 +123,7 @@ _SIGS = {
 }
 
 _lib: Optional[ctypes.CDLL] = None
-_configs: dict = {}   # context -> its configuration
+_configs: dict = {}   # context -> its configuration, with the device of its 8-bit cache as .device (None: not bound)
 
 
 def load() -> ctypes.CDLL:
@@ -182,9 +182,12 @@ def _current_raw_stream() -> int:
 
 def _i32_array(seq: Sequence[int]):
     n = len(seq)
-    if n > 16:   # long lists of pages: numpy's conversion
+    if n > 16:   # long lists of page ids: numpy's conversion, where it is the same
         import numpy as np
-        return (ctypes.c_int32 * n).from_buffer(np.array(seq, dtype=np.int32))
+        if isinstance(seq, np.ndarray) or (isinstance(seq, (list, tuple)) and set(map(type, seq)) == {int}):
+            arr = np.asarray(seq)
+            if arr.shape == (n,) and arr.dtype.kind == "i":
+                return (ctypes.c_int32 * n).from_buffer(arr.astype(np.int32))
     return (ctypes.c_int32 * n)(*[int(v) for v in seq])
 
 
@@ -208,7 +211,9 @@ def oscar_page_block_bytes(cfg: oscar_config) -> int:
 def oscar_create(cfg: oscar_config, int2_pool=None, window_slab=None) -> int:
     out = ctypes.c_void_p()
     _check(load().oscar_create(ctypes.byref(cfg), ptr(int2_pool), ptr(window_slab), ctypes.byref(out)))
-    _configs[out.value] = oscar_config.from_buffer_copy(cfg)
+    mine = oscar_config.from_buffer_copy(cfg)
+    mine.device = None
+    _configs[out.value] = mine
     return out.value
 
 
@@ -379,31 +384,37 @@ def _types() -> dict:
     return _torch_types
 
 
-def _dense(x, name: str, count: int = 0, dtype="i32") -> Optional[int]:
+def _placed(x, device: Optional[int]) -> bool:
+    """Whether a tensor is on the cache's device (None: on any CUDA device)."""
+    return x.get_device() == device if device is not None else x.is_cuda
+
+
+def _dense(x, name: str, device: Optional[int], count: int = 0, dtype="i32") -> Optional[int]:
     """Address of a dense CUDA tensor of at least ``count`` elements of one type (dtype None: count bytes of any type)."""
     if x is None or isinstance(x, int):
         return x
-    if x.is_cuda and x.is_contiguous():
+    if _placed(x, device) and x.is_contiguous():
         if dtype is None:
             if x.numel() * x.element_size() >= count:
                 return x.data_ptr()
         elif x.numel() >= count and x.dtype is (_torch_types or _types()).get(dtype, x.dtype):
             return x.data_ptr()
-    raise OscarError(ERR_INVALID, f"{name} must be a contiguous CUDA tensor of at least {count} "
-                                  f"{'bytes' if dtype is None else _types().get(dtype, 'elements')}, not {x.dtype} "
+    raise OscarError(ERR_INVALID, f"{name} must be a contiguous tensor of at least {count} "
+                                  f"{'bytes' if dtype is None else _types().get(dtype, 'elements')} on CUDA device "
+                                  f"{'' if device is None else device}, not {x.dtype} "
                                   f"{tuple(x.shape)} on {x.device} with strides {tuple(x.stride())}")
 
 
-def _rows(x, name: str, dtype: int, tokens: int, heads: int, d: int):
+def _rows(x, name: str, device: Optional[int], dtype: int, tokens: int, heads: int, d: int):
     """(address, elements between tokens) of [tokens][heads][d] rows; the tokens may lie further apart than their rows
     are long."""
     if x is None or isinstance(x, int):
         return x, 0
     shape = x.shape
-    if not x.is_cuda or x.dtype is not (_torch_types or _types()).get(dtype, x.dtype) or len(shape) != 3 \
+    if not _placed(x, device) or x.dtype is not (_torch_types or _types()).get(dtype, x.dtype) or len(shape) != 3 \
             or shape[0] < tokens or shape[1] != heads or shape[2] != d:
-        raise OscarError(ERR_INVALID, f"{name} must be a [{tokens}][{heads}][{d}] CUDA tensor of {_types().get(dtype)}, "
-                                      f"not {x.dtype} {tuple(shape)} on {x.device}")
+        raise OscarError(ERR_INVALID, f"{name} must be a [{tokens}][{heads}][{d}] tensor of {_types().get(dtype)} on CUDA "
+                                      f"device {'' if device is None else device}, not {x.dtype} {tuple(shape)} on {x.device}")
     t, h, c = x.stride()
     if c != 1 or (heads > 1 and h != d):
         raise OscarError(ERR_INVALID, f"the heads and channels of {name} must be adjacent, not strided {(t, h, c)}")
@@ -433,32 +444,44 @@ def oscar_kv8_pages_needed(cfg: oscar_config, seq_len: int) -> int:
     return load().oscar_kv8_pages_needed(ctypes.byref(cfg), seq_len)
 
 
+def _current_device(*tensors) -> Optional[int]:
+    """The current device, on which a context's buffers have to be; None where no argument is a CUDA tensor."""
+    if any(getattr(x, "is_cuda", False) for x in tensors):
+        import torch
+        return torch.cuda.current_device()
+    return None
+
+
 def oscar_kv8_bind(ctx: int, fmt: int, pool, tail) -> None:
     """Bind an 8-bit cache: device buffers of oscar_kv8_pool_bytes and oscar_kv8_tail_bytes (any element type)."""
     cfg = _config(ctx)
-    _check(load().oscar_kv8_bind(ctx, fmt, _dense(pool, "pool", oscar_kv8_pool_bytes(cfg), None),
-                                 _dense(tail, "tail", oscar_kv8_tail_bytes(cfg), None)))
+    dev = _current_device(pool, tail)
+    _check(load().oscar_kv8_bind(ctx, fmt, _dense(pool, "pool", dev, oscar_kv8_pool_bytes(cfg), None),
+                                 _dense(tail, "tail", dev, oscar_kv8_tail_bytes(cfg), None)))
+    cfg.device = dev
 
 
 def oscar_kv8_write(ctx, layer, K, V, dtype, cu_seqlens, start_pos, batch, total_tokens, block_table, bt_stride,
                     req_slot, stream=None) -> None:
     cfg = _config(ctx)
-    k, ks = _rows(K, "K", dtype, total_tokens, cfg.n_kv_heads, cfg.head_dim)
-    v, vs = _rows(V, "V", dtype, total_tokens, cfg.n_kv_heads, cfg.head_dim)
-    _check(load().oscar_kv8_write(ctx, layer, k, ks, v, vs, dtype, _dense(cu_seqlens, "cu_seqlens", batch + 1),
-                                  _dense(start_pos, "start_pos", batch), batch, total_tokens,
-                                  _dense(block_table, "block_table", batch * bt_stride), bt_stride,
-                                  _dense(req_slot, "req_slot", batch), stream_ptr(stream)))
+    dev = cfg.device
+    k, ks = _rows(K, "K", dev, dtype, total_tokens, cfg.n_kv_heads, cfg.head_dim)
+    v, vs = _rows(V, "V", dev, dtype, total_tokens, cfg.n_kv_heads, cfg.head_dim)
+    _check(load().oscar_kv8_write(ctx, layer, k, ks, v, vs, dtype, _dense(cu_seqlens, "cu_seqlens", dev, batch + 1),
+                                  _dense(start_pos, "start_pos", dev, batch), batch, total_tokens,
+                                  _dense(block_table, "block_table", dev, batch * bt_stride), bt_stride,
+                                  _dense(req_slot, "req_slot", dev, batch), stream_ptr(stream)))
 
 
 def oscar_kv8_append(ctx, layer, K_new, V_new, dtype, seq_lens_before, batch, block_table, bt_stride, req_slot,
                      stream=None) -> None:
     cfg = _config(ctx)
-    k, ks = _rows(K_new, "K_new", dtype, batch, cfg.n_kv_heads, cfg.head_dim)
-    v, vs = _rows(V_new, "V_new", dtype, batch, cfg.n_kv_heads, cfg.head_dim)
-    _check(load().oscar_kv8_append(ctx, layer, k, ks, v, vs, dtype, _dense(seq_lens_before, "seq_lens_before", batch),
-                                   batch, _dense(block_table, "block_table", batch * bt_stride), bt_stride,
-                                   _dense(req_slot, "req_slot", batch), stream_ptr(stream)))
+    dev = cfg.device
+    k, ks = _rows(K_new, "K_new", dev, dtype, batch, cfg.n_kv_heads, cfg.head_dim)
+    v, vs = _rows(V_new, "V_new", dev, dtype, batch, cfg.n_kv_heads, cfg.head_dim)
+    _check(load().oscar_kv8_append(ctx, layer, k, ks, v, vs, dtype, _dense(seq_lens_before, "seq_lens_before", dev, batch),
+                                   batch, _dense(block_table, "block_table", dev, batch * bt_stride), bt_stride,
+                                   _dense(req_slot, "req_slot", dev, batch), stream_ptr(stream)))
 
 
 def _size(fn, cfg, a: int, b: int) -> int:
@@ -482,39 +505,40 @@ def oscar_kv8_sparse_workspace_size(cfg: oscar_config, batch: int, n_select: int
 def oscar_kv8_decode_attn(ctx, layer, q, q_dtype, out, out_dtype, block_table, bt_stride, seq_lens, req_slot, batch,
                           max_seq, workspace, ws_bytes, stream=None) -> None:
     cfg = _config(ctx)
-    hq, d = cfg.n_q_heads, cfg.head_dim
-    qp, qs = _rows(q, "q", q_dtype, batch, hq, d)
+    dev, hq, d = cfg.device, cfg.n_q_heads, cfg.head_dim
+    qp, qs = _rows(q, "q", dev, q_dtype, batch, hq, d)
     _check(load().oscar_kv8_decode_attn(ctx, layer, qp, qs, q_dtype,
-                                        _dense(out, "out", batch * hq * d, out_dtype), out_dtype,
-                                        _dense(block_table, "block_table", batch * bt_stride), bt_stride,
-                                        _dense(seq_lens, "seq_lens", batch), _dense(req_slot, "req_slot", batch), batch,
-                                        max_seq, _dense(workspace, "workspace", ws_bytes, None), ws_bytes,
+                                        _dense(out, "out", dev, batch * hq * d, out_dtype), out_dtype,
+                                        _dense(block_table, "block_table", dev, batch * bt_stride), bt_stride,
+                                        _dense(seq_lens, "seq_lens", dev, batch), _dense(req_slot, "req_slot", dev, batch), batch,
+                                        max_seq, _dense(workspace, "workspace", dev, ws_bytes, None), ws_bytes,
                                         stream_ptr(stream)))
 
 
 def oscar_kv8_select_pages(ctx, layer, q, q_dtype, block_table, bt_stride, seq_lens, batch, max_seq, keep_first,
                            keep_last, n_select, page_idx, workspace, ws_bytes, stream=None) -> None:
     cfg = _config(ctx)
-    qp, qs = _rows(q, "q", q_dtype, batch, cfg.n_q_heads, cfg.head_dim)
+    dev = cfg.device
+    qp, qs = _rows(q, "q", dev, q_dtype, batch, cfg.n_q_heads, cfg.head_dim)
     _check(load().oscar_kv8_select_pages(ctx, layer, qp, qs, q_dtype,
-                                         _dense(block_table, "block_table", batch * bt_stride), bt_stride,
-                                         _dense(seq_lens, "seq_lens", batch), batch, max_seq, keep_first, keep_last,
-                                         n_select, _dense(page_idx, "page_idx", batch * cfg.n_kv_heads * n_select),
-                                         _dense(workspace, "workspace", ws_bytes, None), ws_bytes, stream_ptr(stream)))
+                                         _dense(block_table, "block_table", dev, batch * bt_stride), bt_stride,
+                                         _dense(seq_lens, "seq_lens", dev, batch), batch, max_seq, keep_first, keep_last,
+                                         n_select, _dense(page_idx, "page_idx", dev, batch * cfg.n_kv_heads * n_select),
+                                         _dense(workspace, "workspace", dev, ws_bytes, None), ws_bytes, stream_ptr(stream)))
 
 
 def oscar_kv8_sparse_decode_attn(ctx, layer, q, q_dtype, out, out_dtype, page_idx, n_select, block_table, bt_stride,
                                  seq_lens, req_slot, batch, workspace, ws_bytes, stream=None) -> None:
     cfg = _config(ctx)
-    hq, d = cfg.n_q_heads, cfg.head_dim
-    qp, qs = _rows(q, "q", q_dtype, batch, hq, d)
+    dev, hq, d = cfg.device, cfg.n_q_heads, cfg.head_dim
+    qp, qs = _rows(q, "q", dev, q_dtype, batch, hq, d)
     _check(load().oscar_kv8_sparse_decode_attn(ctx, layer, qp, qs, q_dtype,
-                                               _dense(out, "out", batch * hq * d, out_dtype),
+                                               _dense(out, "out", dev, batch * hq * d, out_dtype),
                                                out_dtype,
-                                               _dense(page_idx, "page_idx", batch * cfg.n_kv_heads * n_select), n_select,
-                                               _dense(block_table, "block_table", batch * bt_stride), bt_stride,
-                                               _dense(seq_lens, "seq_lens", batch), _dense(req_slot, "req_slot", batch),
-                                               batch, _dense(workspace, "workspace", ws_bytes, None), ws_bytes,
+                                               _dense(page_idx, "page_idx", dev, batch * cfg.n_kv_heads * n_select), n_select,
+                                               _dense(block_table, "block_table", dev, batch * bt_stride), bt_stride,
+                                               _dense(seq_lens, "seq_lens", dev, batch), _dense(req_slot, "req_slot", dev, batch),
+                                               batch, _dense(workspace, "workspace", dev, ws_bytes, None), ws_bytes,
                                                stream_ptr(stream)))
 
 
@@ -539,11 +563,13 @@ def oscar_compact_pages(ctx: int, block_table, rows: int, bt_stride: int, num_pa
     """Compact the context's pages; returns (map, live): map int32 [num_pages] holds every page's new id, -1 for a free
     page.  num_pages is the configuration's.  block_table may be None (rows = 0); a host-only context takes stream=0."""
     import numpy as np
-    if num_pages != _config(ctx).num_pages:
+    cfg = _config(ctx)
+    if num_pages != cfg.num_pages:
         raise OscarError(ERR_INVALID, f"num_pages {num_pages} is not the configuration's")
+    dev = _current_device(block_table) if cfg.device is None else cfg.device
     table = np.empty(num_pages, np.int32)
     live = ctypes.c_int32()
-    _check(load().oscar_compact_pages(ctx, _dense(block_table, "block_table", rows * bt_stride), rows, bt_stride,
+    _check(load().oscar_compact_pages(ctx, _dense(block_table, "block_table", dev, rows * bt_stride), rows, bt_stride,
                                       table.ctypes.data, ctypes.byref(live), stream_ptr(stream) if stream != 0 else None))
     return table, live.value
 

@@ -167,6 +167,53 @@ def test_tensors_on_the_host_are_refused(osc):
         osc.oscar_destroy(ctx)
 
 
+class Elsewhere:
+    """What the binding asks of a tensor, on the given CUDA device."""
+
+    def __init__(self, t, device):
+        self.t, self.device, self.is_cuda = t, f"cuda:{device}", True
+        self.get_device = lambda: device
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+def test_tensors_on_another_device_are_refused(osc):
+    torch = pytest.importorskip("torch")
+    ctx = osc.oscar_create(_cfg(osc))
+    try:
+        osc._configs[ctx].device = 0              # as after a bind on device 0; the library has no cache, so it refuses all
+        rows, ints, byte = torch.zeros(1, 2, 64), torch.zeros(12, dtype=torch.int32), torch.zeros(64, dtype=torch.uint8)
+        q = torch.zeros(1, 8, 64)
+        calls = (
+            (osc.oscar_kv8_write, [rows, rows, osc.DTYPE_F32, ints, ints, 1, 1, ints, 12, ints]),
+            (osc.oscar_kv8_append, [rows, rows, osc.DTYPE_F32, ints, 1, ints, 12, ints]),
+            (osc.oscar_kv8_decode_attn, [q, osc.DTYPE_F32, q, osc.DTYPE_F32, ints, 12, ints, ints, 1, 100, byte, 64]),
+            (osc.oscar_kv8_select_pages, [q, osc.DTYPE_F32, ints, 12, ints, 1, 100, 0, 0, 2, ints, byte, 64]),
+            (osc.oscar_kv8_sparse_decode_attn, [q, osc.DTYPE_F32, q, osc.DTYPE_F32, ints, 2, ints, 12, ints, ints, 1, byte, 64]))
+        for call, args in calls:
+            on = [Elsewhere(x, 0) if torch.is_tensor(x) else x for x in args]
+            with pytest.raises(osc.OscarError, match="no 8-bit cache"):
+                call(ctx, 0, *on, stream=256)
+            for i, x in enumerate(args):
+                if torch.is_tensor(x):
+                    with pytest.raises(osc.OscarError, match="device 0"):
+                        call(ctx, 0, *on[:i], Elsewhere(x, 1), *on[i + 1:], stream=256)
+        with pytest.raises(osc.OscarError, match="device 0"):
+            osc.oscar_compact_pages(ctx, Elsewhere(ints, 1), 1, 12, osc._configs[ctx].num_pages, stream=0)
+    finally:
+        osc.oscar_destroy(ctx)
+
+
+def test_long_lists_of_pages_take_what_short_ones_take(osc):
+    np = pytest.importorskip("numpy")
+    torch = pytest.importorskip("torch")
+    want = list(range(20))
+    for seq in (want, tuple(want), np.arange(20), np.arange(20, dtype=np.int16), torch.arange(20), [np.int64(i) for i in want],
+                list(torch.arange(20)), range(20), [float(i) for i in want]):
+        assert list(osc._i32_array(seq)) == want
+
+
 # ------------------------------------------------------------------------------------------------ host part of page moves
 def test_fork_shares_complete_pages(osc):
     ctx = osc.oscar_create(_cfg(osc))
