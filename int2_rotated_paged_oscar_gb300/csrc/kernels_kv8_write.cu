@@ -4,14 +4,24 @@
 // finite |x| and M the largest code:
 //     scale = m / M,   code = round(x M / m),   and for K: lo, hi = the smallest and largest code of each channel.
 // Rounding is monotone, so lo and hi are the codes of a channel's smallest and largest x.  It reads 2 d (or 4 d) bytes
-// and writes d + (2 d + 16) / P bytes per K or V row, so it is bound by memory: one CTA holds a block's P x d values in
-// registers as BF16 pairs, from 16-byte copies, for both passes over them (the maximum, then the codes).
-// 8 x 32K tokens, 8 kv heads of 128 channels, BF16 to E4M3: 250 us, 6.5 TB/s, 0.95 of the measured copy bandwidth; float32
-// rows come to 0.6 of it.
+// and writes d + (2 d + 16) / P bytes per K or V row, so it is bound by memory: a group of warps holds a block's P x d
+// values in registers as BF16 pairs for both passes over them (the maximum, then the codes), while the next block's rows
+// travel to shared memory as one tile.
+// 8 x 32K tokens, 8 kv heads of 128 channels, BF16 to E4M3: 249 us, 6.5 TB/s, 0.96 of the measured copy bandwidth.  8 x 8K:
+// BF16 0.88 to 0.90 of it at d = 128, 0.71 to 0.78 at d = 64, whose 39 us hold 5 of start and end; float32 rows 0.90 to 0.94
+// and 0.83 to 0.89 (0.55 to 0.61 with each thread's 16-byte asynchronous copies instead of tiles, 165 us instead of 107: the
+// copies' instructions and their bank conflicts filled the load/store queue).
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <type_traits>
+
 #include "kv8.cuh"
 
 namespace oscar {
 namespace {
+
+#include "tc_common.cuh"
 
 constexpr int kThreads = 256;
 struct Item {
@@ -172,16 +182,41 @@ struct Shape {
   }
 };
 
-template <int D, int P, int FMT, bool F32>
-__global__ void __launch_bounds__(kThreads, F32 ? 2 : 3) kv8_write_kernel(const __grid_constant__ Kv8WriteArgs a) {
+// The row tensors of a write as tiles of P rows of one head.
+struct RowMaps {
+  CUtensorMap k, v;
+};
+struct NoMaps {};
+
+// TILED: a write, whose pages' rows come as one tile a unit; otherwise an append, where all but the new row of a completed page
+// are in the tail.
+template <int D, int P, bool F32, bool TILED>
+struct Ahead {
   using S = Shape<D, P>;
+  static constexpr int WD = F32 && TILED ? 2 : 1;        // 16-byte words of eight values
+  // units of a group on their way (BF16 rows at 8 x 8K tokens, d = 128: two 66 to 69 us, one 68 to 70)
+  static constexpr int NB = F32 || !TILED ? 1 : 2;
+  static constexpr int kWords = S::V * S::T * WD;        // of a unit
+  // CTAs an SM.  (8 x 8K tokens, BF16 rows, a group a warp: four 42.6, 38.5 and 67.9 us at d = 64 with P = 16, 32 and d = 128
+  // with P = 16, three 44.7, 39.6 and 69.1; float32 rows 57.8, 59.9 and 112 against 60.4, 56.5 and 107.)
+  static constexpr int kResident = S::T == 32 && !F32 ? 4 : 3;
+  static constexpr int kBytes = S::NU * NB * kWords * 16;
+};
+
+template <int D, int P, int FMT, bool F32, bool TILED>
+__global__ void __launch_bounds__(kThreads, (Ahead<D, P, F32, TILED>::kResident))
+    kv8_write_kernel(const __grid_constant__ Kv8WriteArgs a, const __grid_constant__ std::conditional_t<TILED, RowMaps, NoMaps> maps) {
+  using S = Shape<D, P>;
+  using A = Ahead<D, P, F32, TILED>;
   constexpr int W = S::T / 32;             // warps of a group
   constexpr float M = FMT == kKv8Int8 ? 127.f : 448.f;
+  constexpr int kGaveUp = 0x10000;         // above every magnitude's bits: a wait of the group ran out
   __shared__ Item s_item;
   __shared__ int s_have, s_pid[S::SPAN];
   __shared__ int s_max_all[kThreads / 32], s_fin_all[kThreads / 32];
   __shared__ uint4 s_lo_all[kThreads / 32][S::CH], s_hi_all[kThreads / 32][S::CH];
-  extern __shared__ uint4 ahead[];         // [V][words][threads]
+  __shared__ uint64_t full_all[S::NU][A::NB];
+  extern __shared__ uint8_t ahead_raw[];
   const Geom& g = a.g;
   const Kv8Geom kg{P, D, g.Hkv};
   const int group = threadIdx.x / S::T, tid = threadIdx.x % S::T, warp = tid >> 5, lane = tid & 31;   // in the group
@@ -189,12 +224,21 @@ __global__ void __launch_bounds__(kThreads, F32 ? 2 : 3) kv8_write_kernel(const 
   int* s_fin = s_fin_all + group * W;
   auto s_lo = s_lo_all + group * W;
   auto s_hi = s_hi_all + group * W;
+  uint64_t* full = full_all[group];
+  uint4* ahead = reinterpret_cast<uint4*>((reinterpret_cast<uintptr_t>(ahead_raw) + 127) & ~uintptr_t(127)) +
+                 group * A::NB * A::kWords;
+  if constexpr (TILED) {
+    if (tid == 0) {
+      for (int i = 0; i < A::NB; ++i) mbar_init(&full[i], 1);
+      fence_barrier_init();
+    }
+  }
   pdl_wait();
   pdl_launch_dependents();
   if (threadIdx.x < 32) {
     Item it;
     bool have;
-    if (a.cu_seqlens) {
+    if constexpr (TILED) {
       have = find_item(a, S::SPAN, blockIdx.x, &it);
     } else {
       int start, len, row0, slot;
@@ -220,22 +264,18 @@ __global__ void __launch_bounds__(kThreads, F32 ? 2 : 3) kv8_write_kernel(const 
     }
     s_pid[threadIdx.x] = pid;
   }
-  // this thread's channels of input row t of K or V, head 0
-  constexpr int E = F32 ? 4 : 2;
-  auto input_at = [&](int kv, int t) {
-    return static_cast<const uint8_t*>(kv ? a.V : a.K) + ((long long)(it.row0 + (t - it.start)) * (kv ? a.v_stride : a.k_stride) + ch) * E;
-  };
-  auto input = [&](int kv, int h, int t) {  // as BF16 pairs
-    const uint4* p = reinterpret_cast<const uint4*>(input_at(kv, t) + h * D * E);
+  // this thread's channels of head h of input row t of K or V, as BF16 pairs
+  auto input = [&](int kv, int h, int t) {
+    const size_t i = (size_t)((long long)(it.row0 + (t - it.start)) * (kv ? a.v_stride : a.k_stride) + h * D + ch);
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(kv ? a.V : a.K) + i * (F32 ? 4 : 2));
     if constexpr (F32) return to_bf16(p[0], p[1]);
     return p[0];
   };
   auto tail_of = [&](int unit) {
     return a.tail + ((size_t)a.layer * g.max_req + it.slot) * kv8_tail_req_elems(g) + (size_t)unit * P * D;
   };
-  // A unit is (kv head, K | V) of a page of the span.  The next one's rows are on their way, by asynchronous copies into
-  // words of shared memory that only this thread (float32: its warp) reads again, while this one's are worked on.
-  constexpr int WD = F32 ? 2 : 1;           // 16-byte words of eight input values
+  // A unit is (kv head, K | V) of a page of the span.  The next one's (or two's) rows are on their way to shared memory
+  // while this one's are worked on.
   const int units = 2 * g.Hkv, step = gridDim.y * S::NU;
   // (page of the span, unit) of this group's current work and of the next to fetch
   auto advance = [&](int& page, int& unit) {
@@ -243,62 +283,65 @@ __global__ void __launch_bounds__(kThreads, F32 ? 2 : 3) kv8_write_kernel(const 
   };
   int page = 0, unit = blockIdx.y * S::NU + group;
   for (; unit >= units; unit -= units) ++page;
-  int next_page = page, next_unit = unit;
-  // Float32 rows are fetched as each lane's 16 bytes of a run, and read as each thread's 32: word w of a row lies at place
-  // (w & 1) CH + w / 2 of its 2 CH places, so neither crosses banks more than twice.
-  const int place0 = threadIdx.x / S::CH * S::CH * WD, mine = threadIdx.x % S::CH;
-  const long long rs_k = a.k_stride * S::RS * E, rs_v = a.v_stride * S::RS * E;   // bytes between a thread's rows
-  const uint8_t *from_k = nullptr, *from_v = nullptr;                               // of the page that is fetched
-  int from_page = -1;
+  int next_page = page, next_unit = unit, issued = 0, taken = 0;
   auto fetch = [&] {
-    if (next_page < it.pages) {
-      const int t0 = (it.page + next_page) * P + row;
-      if (next_page != from_page) {
-        from_page = next_page;
-        from_k = input_at(0, t0);
-        from_v = input_at(1, t0);
+    if constexpr (TILED) {                  // (one thread of the group)
+      if (next_page < it.pages) {
+        uint64_t* bar = &full[issued % A::NB];
+        mbar_arrive_expect_tx(bar, A::kWords * 16);
+        tma_load_2d_tc(ahead + issued % A::NB * A::kWords, (next_unit & 1) ? &maps.v : &maps.k, (next_unit >> 1) * D,
+                       it.row0 + ((it.page + next_page) * P - it.start), bar);
+        ++issued;
       }
-      const uint8_t* from = ((next_unit & 1) ? from_v : from_k) + (next_unit >> 1) * D * E;
-      const long long rs = (next_unit & 1) ? rs_v : rs_k;
-      uint4* to = ahead + place0;
-      const bool mixed = (it.page + next_page) * P < it.start;   // rows of the old tail among them
+    } else {                                // words that only this thread reads again
+      if (next_page < it.pages) {
 #pragma unroll
-      for (int k = 0; k < S::V; ++k) {
-        uint4* slab = to + k * WD * kThreads;
-        if (mixed && t0 + k * S::RS < it.start) {
-          copy_async(slab + mine, tail_of(next_unit) + (size_t)(row + k * S::RS) * D + ch);
-        } else if constexpr (F32) {
-          const uint8_t* line = from + k * rs - mine * 32;
-          copy_async(slab + (mine & 1) * S::CH + mine / 2, line + mine * 16);
-          copy_async(slab + (mine & 1) * S::CH + (mine + S::CH) / 2, line + (mine + S::CH) * 16);
-        } else {
-          copy_async(slab + mine, from + k * rs);
-        }
+        for (int k = 0; k < S::V; ++k)
+          if (row + k * S::RS < P - 1) copy_async(ahead + tid + k * S::T, tail_of(next_unit) + (size_t)(row + k * S::RS) * D + ch);
       }
     }
     advance(next_page, next_unit);
   };
-  fetch();
+  if (!TILED || tid == 0)
+    for (int i = 0; i < A::NB; ++i) fetch();
   __syncthreads();                          // (the pages' ids)
   for (const int pages = max(it.pages, 1); page < pages; advance(page, unit)) {
     const int kv = unit & 1, h = unit >> 1;
     uint16_t* tail = tail_of(unit);
     if (it.pages > 0) {
       const int pid = s_pid[page];
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      if constexpr (F32) __syncwarp();
       uint4 x[S::V];
-      const uint4* from = ahead + place0 + mine;
-      const bool mixed = (it.page + page) * P < it.start;
+      bool good = true;
+      if constexpr (TILED) {
+        good = mbar_wait_bounded(&full[taken % A::NB], (taken / A::NB) & 1, a.status);
+        good = __all_sync(0xffffffffu, good);
+        const uint4* from = ahead + taken % A::NB * A::kWords;
+        ++taken;
 #pragma unroll
-      for (int k = 0; k < S::V; ++k) {
-        x[k] = from[k * WD * kThreads];
-        if constexpr (F32) {
-          if (!(mixed && (it.page + page) * P + row + k * S::RS < it.start)) x[k] = to_bf16(x[k], from[k * WD * kThreads + S::CH]);
+        for (int k = 0; k < S::V; ++k) {
+          if constexpr (F32) {  // every other four threads take their second word first: no bank is met twice
+            const int i = 2 * (tid + k * S::T), turn = (tid >> 2) & 1;
+            const uint4 u = from[i + turn], v = from[i + 1 - turn];
+            const uint2 pu = make_uint2(pack_bf162(__uint_as_float(u.x), __uint_as_float(u.y)), pack_bf162(__uint_as_float(u.z), __uint_as_float(u.w)));
+            const uint2 pv = make_uint2(pack_bf162(__uint_as_float(v.x), __uint_as_float(v.y)), pack_bf162(__uint_as_float(v.z), __uint_as_float(v.w)));
+            x[k] = turn ? make_uint4(pv.x, pv.y, pu.x, pu.y) : make_uint4(pu.x, pu.y, pv.x, pv.y);
+          } else {
+            x[k] = from[tid + k * S::T];
+          }
         }
+        const int old = it.start - (it.page + page) * P;   // the page's first rows may be in the tail
+        if (old > 0) {
+#pragma unroll
+          for (int k = 0; k < S::V; ++k)
+            if (row + k * S::RS < old) x[k] = *reinterpret_cast<const uint4*>(tail + (size_t)(row + k * S::RS) * D + ch);
+        }
+      } else {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll
+        for (int k = 0; k < S::V; ++k)
+          x[k] = row + k * S::RS < P - 1 ? ahead[tid + k * S::T] : input(kv, h, it.start);
+        fetch();
       }
-      if constexpr (F32) __syncwarp();
-      fetch();
       // the channels' smallest and largest values (K), and from them, or directly (V), the largest magnitude
       uint4 lo = x[0], hi = x[0];
       auto fold = [&](const uint4& l, const uint4& u) {
@@ -317,11 +360,17 @@ __global__ void __launch_bounds__(kThreads, F32 ? 2 : 3) kv8_write_kernel(const 
         for (int k = 0; k < S::V; ++k)
           m2 = bmax2(m2, bmax2(bmax2(babs2(x[k].x), babs2(x[k].y)), bmax2(babs2(x[k].z), babs2(x[k].w))));
       }
-      int big = (int)__reduce_max_sync(0xffffffffu, max(m2 & 0xffffu, m2 >> 16));
-      if constexpr (W > 1) {
-        if (lane == 0) s_max[warp] = big;
-        S::sync(group);
-        big = (int)__reduce_max_sync(0xffffffffu, (unsigned)s_max[lane % W]);
+      int big = good ? (int)__reduce_max_sync(0xffffffffu, max(m2 & 0xffffu, m2 >> 16)) : kGaveUp;
+      if (W > 1 && lane == 0) s_max[warp] = big;
+      S::sync(group);   // (and a tile's words are read)
+      if constexpr (W > 1) big = (int)__reduce_max_sync(0xffffffffu, (unsigned)s_max[lane % W]);
+      if constexpr (TILED) {
+        if (big == kGaveUp) {  // let the tiles in flight land before the CTA ends
+          if (tid == 0)
+            for (int i = taken - 1; i < issued; ++i) (void)mbar_wait_bounded(&full[i % A::NB], (i / A::NB) & 1, nullptr);
+          return;
+        }
+        if (tid == 0) fetch();
       }
       if (big >= 0x7f80) {
         // infinities and NaNs: the scale is the finite values'; an infinity becomes the largest of them, a NaN 0
@@ -397,25 +446,59 @@ __global__ void __launch_bounds__(kThreads, F32 ? 2 : 3) kv8_write_kernel(const 
   }
 }
 
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    cudaDriverEntryPointQueryResult q;
+    void* p = nullptr;
+    const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+                    q == cudaDriverEntryPointSuccess;
+    return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p) : nullptr;
+  }();
+  return fn;
+}
+
+// [total_tokens][Hkv x D] rows in boxes of P rows of one head.  (The values pass unread, as words of their size.)
+template <int D, int P>
+int row_map(CUtensorMap* map, const void* base, long long row_stride, const Kv8WriteArgs& a) {
+  auto encode = tensor_map_encoder();
+  if (!encode) return (int)cudaErrorNotSupported;
+  const bool f32 = a.dtype == kDtypeF32;
+  const cuuint64_t dims[2] = {(cuuint64_t)a.g.Hkv * D, (cuuint64_t)a.total_tokens};
+  const cuuint64_t strides[1] = {(cuuint64_t)row_stride * (f32 ? 4 : 2)};
+  const cuuint32_t box[2] = {D, P}, ones[2] = {1, 1};
+  const CUresult r = encode(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims,
+                            strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? 0 : (int)cudaErrorInvalidValue;
+}
+
 template <int D, int P, int FMT>
 int launch_write(const Kv8WriteArgs& a, cudaStream_t s, bool pdl) {
   using S = Shape<D, P>;
   const int items = a.cu_seqlens ? a.total_tokens / (P * S::SPAN) + a.batch : a.batch;
   // Several units a group where there are CTAs enough: one look-up of the item, and loads that never pause.  (A CTA for
-  // each unit took 411 us at 8 x 32K tokens; 4 CTAs a slot instead of 2 took 10 to 23 % more at 8 x 8K, d = 64, and the
-  // same time at d = 128.)
+  // each unit took 411 us at 8 x 32K tokens.  At 8 x 8K, half again as many CTAs took up to 5 % more with BF16 rows and up to
+  // 4 % less with float32 rows, three quarters of them up to 5 % more.)
   const int rounds = a.cu_seqlens ? 2 * a.g.Hkv : (2 * a.g.Hkv + S::NU - 1) / S::NU;   // a CTA's, were it alone with its item
   long long per = (long long)items * rounds / (152LL * 4 * 2);
   if (per < 1) per = 1;
   if (per > rounds) per = rounds;
   const dim3 grid(items, (unsigned)((rounds + per - 1) / per));
   const bool f32 = a.dtype == kDtypeF32;
-  const size_t smem = (size_t)S::V * kThreads * (f32 ? 2 : 1) * sizeof(uint4);
-  auto go = [&](auto kern) {
+  auto go = [&](auto kern, size_t bytes, const auto& maps) {
+    const size_t smem = bytes + 128;
     const cudaError_t e = ensure_smem_limit(kern, smem, true);
-    return e != cudaSuccess ? (int)e : launch_pdl(kern, grid, dim3(kThreads), smem, s, pdl, a);
+    return e != cudaSuccess ? (int)e : launch_pdl(kern, grid, dim3(kThreads), smem, s, pdl, a, maps);
   };
-  return f32 ? go(kv8_write_kernel<D, P, FMT, true>) : go(kv8_write_kernel<D, P, FMT, false>);
+  if (!a.cu_seqlens)
+    return f32 ? go(kv8_write_kernel<D, P, FMT, true, false>, Ahead<D, P, true, false>::kBytes, NoMaps{})
+               : go(kv8_write_kernel<D, P, FMT, false, false>, Ahead<D, P, false, false>::kBytes, NoMaps{});
+  RowMaps maps;
+  int e = row_map<D, P>(&maps.k, a.K, a.k_stride, a);
+  if (!e) e = row_map<D, P>(&maps.v, a.V, a.v_stride, a);
+  if (e) return e;
+  return f32 ? go(kv8_write_kernel<D, P, FMT, true, true>, Ahead<D, P, true, true>::kBytes, maps)
+             : go(kv8_write_kernel<D, P, FMT, false, true>, Ahead<D, P, false, true>::kBytes, maps);
 }
 
 template <int D, int P>

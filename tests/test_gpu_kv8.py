@@ -449,6 +449,28 @@ def test_decode_magnitudes(osc, fmt, loud):
         r.check(r.decode(q, 0, 0, bt, [n], [2]), q, 0, 0, bt, [n], [2])
 
 
+@pytest.mark.parametrize("P,d", [(16, 64), (32, 128), (64, 64)])
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_write_from_slices_of_one_projection(osc, P, d, dtype):
+    """K and V as 16-byte aligned slices of one wider tensor, from an odd row on; then a chunk that completes the page."""
+    rng = np.random.default_rng([P, d, dtype])
+    heads, unit = 2, 4 if dtype == 0 else 8                       # elements of 16 bytes
+    with Rig(osc, P=P, d=d, heads=heads, fmt=O.E4M3) as r:
+        bt, lens = tables(rng, 2, 12, 48, [4, 2]), [2 * P + 5, P + 1]
+        at = [0, 0]
+        for step in (lens, [P, 1]):
+            x = torch.from_numpy(rng.normal(size=(sum(step) + 3, 3 * unit + 2 * heads * d)).astype(np.float32)).to(DT[dtype]).cuda()
+            k = x[3:, unit:unit + heads * d].unflatten(1, (heads, d))
+            v = x[3:, 2 * unit + heads * d:2 * unit + 2 * heads * d].unflatten(1, (heads, d))
+            bt_d = dev(bt)
+            osc.oscar_kv8_write(r.ctx, r.layer, k, v, dtype, dev([0, step[0], sum(step)]), dev(at), 2, sum(step), bt_d, 12, dev([3, 1]))
+            for b, (lo, hi) in enumerate(((0, step[0]), (step[0], sum(step)))):
+                r.ref.write(bt[b], [3, 1][b], at[b], bf16(k[lo:hi].float().cpu().numpy()), bf16(v[lo:hi].float().cpu().numpy()))
+            at = [a + s for a, s in zip(at, step)]
+        r.same()
+        assert r.status() == 0
+
+
 def test_decode_reports_bad_arguments_on_the_device(osc):
     rng = np.random.default_rng(17)
     lens = [50, 60, 70]
