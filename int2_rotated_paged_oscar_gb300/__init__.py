@@ -9,6 +9,7 @@ a kernel entry point without a GPU, fails loudly.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 from typing import Optional, Sequence
@@ -182,12 +183,10 @@ def _current_raw_stream() -> int:
 
 def _i32_array(seq: Sequence[int]):
     n = len(seq)
-    if n > 16:   # long lists of page ids: numpy's conversion, where it is the same
-        import numpy as np
-        if isinstance(seq, np.ndarray) or (isinstance(seq, (list, tuple)) and set(map(type, seq)) == {int}):
-            arr = np.asarray(seq)
-            if arr.shape == (n,) and arr.dtype.kind == "i":
-                return (ctypes.c_int32 * n).from_buffer(arr.astype(np.int32))
+    try:
+        return (ctypes.c_int32 * n).from_buffer(array.array("i", seq))   # integers that fit: the faster conversion
+    except (TypeError, OverflowError, ValueError):
+        pass
     return (ctypes.c_int32 * n)(*[int(v) for v in seq])
 
 
