@@ -529,7 +529,9 @@ oscar_status oscar_kv8_sparse_decode_attn(oscar_ctx* ctx, int32_t layer, const v
  * -1).  The n / P complete pages are shared (each refcount + n_dst); the n mod P tail rows are
  * copied to every destination slot, in every layer, by one kernel on stream.  On an error
  * nothing is forked.  Without a bound cache only the host part is done.  The allocator changes
- * at the call, so the call is not for graph capture. */
+ * at the call, so the call is not for graph capture.  It copies no
+ * INT2 window, and oscar_fork_prefix neither 8-bit blocks nor tail rows: a request that is
+ * forked keeps its tokens in one of the two caches. */
 oscar_status oscar_kv8_fork(oscar_ctx* ctx, const int32_t* src_bt, int32_t n, int32_t src_slot,
                             const int32_t* dst_slots, int32_t n_dst, int32_t* dst_bt, void* stream);
 

@@ -310,6 +310,7 @@ oscar_status oscar_kv8_select_pages(oscar_ctx* ctx, int32_t layer, const void* q
   const int e = oscar::launch_kv8_select(a, stream, !ctx->timing);
   ls.done(e);
   if (e) return cuda_fail(e, "page selection launch");
+  if (a.max_pages > n_select) ctx->launches++;  // the scope counts one: the scores have a kernel of their own
   return OSCAR_OK;
 }
 

@@ -835,3 +835,18 @@ def test_kernel_times_by_name(osc):
         for name, calls in (("kv8_select", 1), ("kv8_decode", 2), ("kv8_combine", 1)):
             ms, count = osc.oscar_kernel_time(r.ctx, name)
             assert ms > 0 and count == calls, name
+
+
+def test_launch_count(osc):
+    """Every kernel counts: two of a selection that has to choose, one of one that takes every page."""
+    rng = np.random.default_rng(53)
+    lens = [100]
+    rig, bt, slots = filled(osc, rng, lens, per_req=200)
+    with rig as r:
+        q = acts(rng, (1, 4, 64), False)
+        for call, kernels in ((lambda: r.select(q, 1, bt, lens, 0, 0, 2), 2), (lambda: r.select(q, 1, bt, lens, 0, 0, 9), 1),
+                              (lambda: r.decode(q, 1, 0, bt, lens, slots), 1),
+                              (lambda: r.decode(q, 1, 0, bt, lens, slots, max_seq=3200), 2)):
+            before = osc.oscar_launch_count(r.ctx)
+            call()
+            assert osc.oscar_launch_count(r.ctx) - before == kernels
