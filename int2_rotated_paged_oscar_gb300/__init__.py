@@ -176,8 +176,8 @@ def _current_raw_stream() -> int:
         import torch
         torch.cuda.current_stream()   # initialises CUDA
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        _raw_stream = (lambda: raw(torch.cuda.current_device())) if raw else \
-            (lambda: torch.cuda.current_stream().cuda_stream)
+        device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        _raw_stream = (lambda: raw(device())) if raw else (lambda: torch.cuda.current_stream().cuda_stream)
     return _raw_stream()
 
 
@@ -383,16 +383,12 @@ def _types() -> dict:
     return _torch_types
 
 
-def _placed(x, device: Optional[int]) -> bool:
-    """Whether a tensor is on the cache's device (None: on any CUDA device)."""
-    return x.get_device() == device if device is not None else x.is_cuda
-
-
 def _dense(x, name: str, device: Optional[int], count: int = 0, dtype="i32") -> Optional[int]:
-    """Address of a dense CUDA tensor of at least ``count`` elements of one type (dtype None: count bytes of any type)."""
+    """Address of a dense tensor on the cache's device (None: on any CUDA device) of at least ``count`` elements of one
+    type (dtype None: count bytes of any type)."""
     if x is None or isinstance(x, int):
         return x
-    if _placed(x, device) and x.is_contiguous():
+    if (x.get_device() == device or device is None and x.is_cuda) and x.is_contiguous():
         if dtype is None:
             if x.numel() * x.element_size() >= count:
                 return x.data_ptr()
@@ -410,14 +406,15 @@ def _rows(x, name: str, device: Optional[int], dtype: int, tokens: int, heads: i
     if x is None or isinstance(x, int):
         return x, 0
     shape = x.shape
-    if not _placed(x, device) or x.dtype is not (_torch_types or _types()).get(dtype, x.dtype) or len(shape) != 3 \
-            or shape[0] < tokens or shape[1] != heads or shape[2] != d:
+    rows, hs, ds = shape if len(shape) == 3 else (-1, 0, 0)
+    if rows < tokens or hs != heads or ds != d or x.dtype is not (_torch_types or _types()).get(dtype, x.dtype) \
+            or not (x.get_device() == device or device is None and x.is_cuda):
         raise OscarError(ERR_INVALID, f"{name} must be a [{tokens}][{heads}][{d}] tensor of {_types().get(dtype)} on CUDA "
                                       f"device {'' if device is None else device}, not {x.dtype} {tuple(shape)} on {x.device}")
     t, h, c = x.stride()
     if c != 1 or (heads > 1 and h != d):
         raise OscarError(ERR_INVALID, f"the heads and channels of {name} must be adjacent, not strided {(t, h, c)}")
-    return x.data_ptr(), t if shape[0] > 1 else 0
+    return x.data_ptr(), t if rows > 1 else 0
 
 
 def _config(ctx) -> oscar_config:

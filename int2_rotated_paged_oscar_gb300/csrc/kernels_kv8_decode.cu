@@ -672,21 +672,23 @@ Kv8DecodeWs kv8_plan(const Geom& g, int batch, long long max_pages) {
   Kv8DecodeWs w{};
   const int per_stage = kv8_stage_tokens(g.D, g.P) / g.P;
   const long long stages = (max_pages + per_stage - 1) / per_stage;
-  const long long pairs = (long long)batch * g.Hkv > 0 ? (long long)batch * g.Hkv : 1;
-  const long long wave = 152LL * resident(g.D, kv8_stage_tokens(g.D, g.P), g.gq() == 8);
-  // The split that takes the fewest rounds of (its stages + 6, a CTA's start and end in stages): it fills one wave of CTAs
-  // where it can (batch 1 at 32K: 9 stages 18.3 us, 8 23.1, 11 18.3) and keeps CTAs long in large batches (64 ragged
-  // requests: 16 stages 472 us, 32 434, 64 423).
-  long long best = 1, cost = -1;
-  for (long long per = 1; per <= 64; ++per) {
-    const long long ctas = pairs * ((stages + per - 1) / per);
-    const long long c = ((ctas + wave - 1) / wave) * (per + 6);
-    if (cost < 0 || c < cost) best = per, cost = c;
-  }
   // Up to 8 stages one CTA takes them all and writes the output itself.  On the device the merge pays from 5 stages on
   // (batch 1, 8 stages: 6.4 us in one launch, 4.9 in two), but its launch costs the host 2 us, which is what a caller
   // without a graph waits for (8.9 us a call against 10.7).
-  if (stages <= 8) best = stages > 0 ? stages : 1;
+  long long best = stages > 0 ? stages : 1;
+  if (stages > 8) {
+    const long long pairs = (long long)batch * g.Hkv > 0 ? (long long)batch * g.Hkv : 1;
+    const long long wave = 152LL * resident(g.D, kv8_stage_tokens(g.D, g.P), g.gq() == 8);
+    // The split that takes the fewest rounds of (its stages + 6, a CTA's start and end in stages): it fills one wave of CTAs
+    // where it can (batch 1 at 32K: 9 stages 18.3 us, 8 23.1, 11 18.3) and keeps CTAs long in large batches (64 ragged
+    // requests: 16 stages 472 us, 32 434, 64 423).
+    long long cost = -1;
+    for (long long per = 1; per <= 64 && per <= stages; ++per) {
+      const long long ctas = pairs * ((stages + per - 1) / per);
+      const long long c = ((ctas + wave - 1) / wave) * (per + 6);
+      if (cost < 0 || c < cost) best = per, cost = c;
+    }
+  }
   w.stages_per_split = (int)best;
   w.max_splits = stages > 0 ? (int)((stages + best - 1) / best) : 1;
   w.total = (size_t)batch * g.Hq * w.max_splits * (g.D + 4) * sizeof(float);
