@@ -414,7 +414,9 @@ def _rows(x, name: str, device: Optional[int], dtype: int, tokens: int, heads: i
     t, h, c = x.stride()
     if c != 1 or (heads > 1 and h != d):
         raise OscarError(ERR_INVALID, f"the heads and channels of {name} must be adjacent, not strided {(t, h, c)}")
-    return x.data_ptr(), t if rows > 1 else 0
+    if tokens > 1 and t < heads * d:   # (a broadcast row's stride of 0 would mean adjacent rows to the library)
+        raise OscarError(ERR_INVALID, f"the tokens of {name} must lie at least {heads * d} elements apart, not {t}")
+    return x.data_ptr(), t if tokens > 1 else 0
 
 
 def _config(ctx) -> oscar_config:

@@ -205,6 +205,44 @@ def test_tensors_on_another_device_are_refused(osc):
         osc.oscar_destroy(ctx)
 
 
+@pytest.mark.parametrize("layout", ["broadcast", "overlapping"])
+def test_rows_that_share_memory_are_refused(osc, layout):
+    """One row for every token (the step after a fork, say) has a token stride of 0, which means adjacent rows to the library:
+    it would read past the tensor's end.  A single token has no such stride."""
+    torch = pytest.importorskip("torch")
+    ctx = osc.oscar_create(_cfg(osc))
+    try:
+        osc._configs[ctx].device = 0
+        on = lambda x: Elsewhere(x, 0)  # noqa: E731
+
+        def rows(n, heads):
+            one = torch.zeros(1, heads, 64)
+            return on(one.expand(n, heads, 64) if layout == "broadcast" else
+                      torch.zeros(4 * n + heads * 64).as_strided((n, heads, 64), (4, 64, 1)))
+
+        i, t, byte = on(torch.zeros(12, dtype=torch.int32)), on(torch.zeros(72, dtype=torch.int32)), on(torch.zeros(64, dtype=torch.uint8))
+        f32 = osc.DTYPE_F32
+
+        def calls(B):
+            kv, q, good = rows(B, 2), rows(B, 8), on(torch.zeros(B, 8, 64))
+            good_kv = on(torch.zeros(B, 2, 64))
+            return ((osc.oscar_kv8_write, (kv, good_kv, f32, i, i, 1, B, t, 12, i)), (osc.oscar_kv8_write, (good_kv, kv, f32, i, i, 1, B, t, 12, i)),
+                    (osc.oscar_kv8_append, (kv, good_kv, f32, i, B, t, 12, i)), (osc.oscar_kv8_append, (good_kv, kv, f32, i, B, t, 12, i)),
+                    (osc.oscar_kv8_decode_attn, (q, f32, good, f32, t, 12, i, i, B, 100, byte, 64)),
+                    (osc.oscar_kv8_select_pages, (q, f32, t, 12, i, B, 100, 0, 0, 1, t, byte, 64)),
+                    (osc.oscar_kv8_sparse_decode_attn, (q, f32, good, f32, t, 1, t, 12, i, i, B, byte, 64)))
+
+        for call, args in calls(5):
+            with pytest.raises(osc.OscarError, match="elements apart"):
+                call(ctx, 0, *args, stream=256)
+        for call, args in calls(1):
+            with pytest.raises(osc.OscarError, match="no 8-bit cache"):
+                call(ctx, 0, *args, stream=256)
+        assert osc._rows(rows(5, 2), "K", 0, f32, 1, 2, 64)[1] == 0         # one of several rows is read
+    finally:
+        osc.oscar_destroy(ctx)
+
+
 def test_long_lists_of_pages_take_what_short_ones_take(osc):
     np = pytest.importorskip("numpy")
     torch = pytest.importorskip("torch")
