@@ -386,6 +386,8 @@ def _types() -> dict:
 def _dense(x, name: str, device: Optional[int], count: int = 0, dtype="i32") -> Optional[int]:
     """Address of a dense tensor on the cache's device (None: on any CUDA device) of at least ``count`` elements of one
     type (dtype None: count bytes of any type)."""
+    if count < 0:   # (a size that the library would take for a very large one)
+        raise OscarError(ERR_INVALID, f"{name} cannot have {count} {'bytes' if dtype is None else 'elements'}")
     if x is None or isinstance(x, int):
         return x
     if (x.get_device() == device or device is None and x.is_cuda) and x.is_contiguous():

@@ -243,6 +243,27 @@ def test_rows_that_share_memory_are_refused(osc, layout):
         osc.oscar_destroy(ctx)
 
 
+def test_negative_workspace_sizes_are_refused(osc):
+    """As a size_t a negative number of bytes is a very large one, and no buffer would be too small for the library."""
+    torch = pytest.importorskip("torch")
+    ctx = osc.oscar_create(_cfg(osc))
+    try:
+        osc._configs[ctx].device = 0
+        q, i, byte = (Elsewhere(x, 0) for x in (torch.zeros(1, 8, 64), torch.zeros(12, dtype=torch.int32), torch.zeros(64, dtype=torch.uint8)))
+        f32 = osc.DTYPE_F32
+        for ws in (byte, 256):
+            for call, args in ((osc.oscar_kv8_decode_attn, (q, f32, q, f32, i, 12, i, i, 1, 100, ws)),
+                               (osc.oscar_kv8_select_pages, (q, f32, i, 12, i, 1, 100, 0, 0, 2, i, ws)),
+                               (osc.oscar_kv8_sparse_decode_attn, (q, f32, q, f32, i, 2, i, 12, i, i, 1, ws))):
+                with pytest.raises(osc.OscarError, match="no 8-bit cache"):
+                    call(ctx, 0, *args, 64, stream=256)
+                for bad in (-1, -64, -(1 << 40)):
+                    with pytest.raises(osc.OscarError, match="workspace cannot have"):
+                        call(ctx, 0, *args, bad, stream=256)
+    finally:
+        osc.oscar_destroy(ctx)
+
+
 def test_long_lists_of_pages_take_what_short_ones_take(osc):
     np = pytest.importorskip("numpy")
     torch = pytest.importorskip("torch")
