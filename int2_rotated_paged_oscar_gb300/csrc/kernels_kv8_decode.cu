@@ -16,7 +16,8 @@
 //           relative to the blocks' largest).
 // Codes are exact f16 numbers, so the only roundings are float32's.  The block's scales multiply scores
 // and sums in float32, and the weights are relative to the maximum of a warp's own blocks, all of one page, so a quiet page
-// next to a loud one keeps its digits.  The tail rows go the same way with BF16 operands, 16 rows a warp, in the CTA of the
+// next to a loud one keeps its digits.  A token's distance from that maximum is formed from the raw sums, before any scale:
+// it is 0 at the maximum and below 0 elsewhere whatever the scores' size, so no weight leaves [0, 1].  The tail rows go the same way with BF16 operands, 16 rows a warp, in the CTA of the
 // request's last pages while its first pages are on their way.
 //
 // Measured (8 kv heads of 128 channels, pages of 64, layers larger than L2): batch 1 at 32K, INT8, 4 heads a kv head 16.9 us
@@ -33,7 +34,8 @@ namespace {
 constexpr int kConsumers = 4;
 constexpr int kThreads = 32 * (kConsumers + 1);
 // log2(e) / sqrt(d) as two floats: a score is far larger than its distance from the largest one, which is what counts, so
-// scale and distance are formed without a rounding of the score itself.
+// scale and distance are formed without a rounding of the score itself; what the rounding of the largest one's logarithm
+// leaves out goes into its block's weight.
 template <int D>
 struct Scale {
   static constexpr double kValue = 1.4426950408889634 / (D == 128 ? 11.313708498984761 : 8.0);
@@ -59,6 +61,16 @@ struct Layout {
     const size_t merge = kConsumers * 8 * (D + 2) * sizeof(float);
     return (ring > merge ? ring : merge) + 128;
   }
+};
+
+// A block's largest raw sum cm times f = fh + fl, the scale of a score: m is the product rounded down, over(r) the product
+// less r to float32's digits, with r the larger of m and another block's.  A weight 2^over(r) is that of the exact product.
+// Where scores are so large, 2^28 and more, that a last place of one is many units, it stays a finite number (64 at most), and
+// where r is m it is no less than 1 but for roundings of the difference itself.
+struct Top {
+  float cm, fh, fl, m;
+  __device__ __forceinline__ Top(float c, float h, float l) : cm(c), fh(h), fl(l) { m = __fmaf_rd(c, h, c * l); }
+  __device__ __forceinline__ float over(float r) const { return fminf(fmaf(cm, fl, fmaf(cm, fh, -r)), 64.f); }
 };
 
 __device__ __forceinline__ bool length_ok(const Kv8DecodeArgs& a, int n) {
@@ -137,13 +149,16 @@ __device__ __forceinline__ void tail_block(const Kv8DecodeArgs& a, int b, int h,
   for (int i = 0; i < NH; ++i) {
     // (BF16 queries leave their odd columns empty: an infinite key times their 0 would be NaN)
     const float ca = G8 ? sc[i] : QF32 ? sc[0] + sc[1] : sc[0], cb = G8 ? sc[2 + i] : QF32 ? sc[2] + sc[3] : sc[2];
-    float m = fmaxf(gid < cnt ? ca * Scale<D>::hi : -INFINITY, gid + 8 < cnt ? cb * Scale<D>::hi : -INFINITY);
-    m = warp_max_xor(m, 4);
-    m = warp_max_xor(m, 8);
-    m = warp_max_xor(m, 16);
-    pr[i][0] = gid < cnt ? ex2(fmaf(ca, Scale<D>::lo, fmaf(ca, Scale<D>::hi, -m))) : 0.f;
-    pr[i][1] = gid + 8 < cnt ? ex2(fmaf(cb, Scale<D>::lo, fmaf(cb, Scale<D>::hi, -m))) : 0.f;
-    m_run[i] = m;
+    float cm = fmaxf(gid < cnt ? ca : -INFINITY, gid + 8 < cnt ? cb : -INFINITY);
+    cm = warp_max_xor(cm, 4);
+    cm = warp_max_xor(cm, 8);
+    cm = warp_max_xor(cm, 16);
+    const Top top(cm, Scale<D>::hi, Scale<D>::lo);
+    const float r = top.over(top.m);
+    const float da = ca - cm, db = cb - cm;
+    pr[i][0] = gid < cnt ? ex2(fmaf(da, Scale<D>::hi, fmaf(da, Scale<D>::lo, r))) : 0.f;
+    pr[i][1] = gid + 8 < cnt ? ex2(fmaf(db, Scale<D>::hi, fmaf(db, Scale<D>::lo, r))) : 0.f;
+    m_run[i] = top.m;
     l_run[i] = pr[i][0] + pr[i][1];
   }
 #pragma unroll
@@ -390,9 +405,9 @@ __global__ void __launch_bounds__(kThreads, (Layout<D, NB, G8>::kResident)) kv8_
         const float2 sc2 = *reinterpret_cast<const float2*>(page + 2 * P * D);
         // scores
         float sc[NB][4];
-        float m[NH];
+        float cm[NH];                                   // the blocks' largest raw sum
 #pragma unroll
-        for (int i = 0; i < NH; ++i) m[i] = -INFINITY;
+        for (int i = 0; i < NH; ++i) cm[i] = -INFINITY;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
           uint32_t kw[2][KS];
@@ -417,22 +432,26 @@ __global__ void __launch_bounds__(kThreads, (Layout<D, NB, G8>::kResident)) kv8_
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i) sc[nb][i] += sd[i];
-#pragma unroll
-          for (int i = 0; i < NH; ++i) {  // (only to choose m: any m near the largest will do)
-            const float f = sc2.x * qs[i];
-            m[i] = fmaxf(m[i], fmaxf((G8 ? sc[nb][i] : sc[nb][0]) * f, (G8 ? sc[nb][2 + i] : sc[nb][2]) * f));
+          if constexpr (!G8 && QF32) {                  // the low halves' columns
+            sc[nb][0] += sc[nb][1];
+            sc[nb][2] += sc[nb][3];
           }
+#pragma unroll
+          for (int i = 0; i < NH; ++i) cm[i] = fmaxf(cm[i], fmaxf(G8 ? sc[nb][i] : sc[nb][0], G8 ? sc[nb][2 + i] : sc[nb][2]));
         }
         // weights relative to the blocks' maximum
-        float beta[NH], alpha[NH];
+        float beta[NH], alpha[NH], fh[NH];
 #pragma unroll
         for (int i = 0; i < NH; ++i) {
-          m[i] = warp_max_xor(m[i], 4);
-          m[i] = warp_max_xor(m[i], 8);
-          m[i] = warp_max_xor(m[i], 16);
-          const float m_new = fmaxf(m_run[i], m[i]);
+          cm[i] = warp_max_xor(cm[i], 4);
+          cm[i] = warp_max_xor(cm[i], 8);
+          cm[i] = warp_max_xor(cm[i], 16);
+          fh[i] = sc2.x * qs[i];
+          const float fl = fmaf(fh[i], Scale<D>::lo / Scale<D>::hi, fmaf(sc2.x, qs[i], -fh[i]));
+          const Top top(cm[i], fh[i], fl);
+          const float m_new = fmaxf(m_run[i], top.m);
           alpha[i] = ex2(m_run[i] - m_new);
-          beta[i] = ex2(m[i] - m_new);
+          beta[i] = ex2(top.over(m_new));
           m_run[i] = m_new;
           l_run[i] *= alpha[i];
         }
@@ -442,16 +461,9 @@ __global__ void __launch_bounds__(kThreads, (Layout<D, NB, G8>::kResident)) kv8_
           float pr[NH][2];
 #pragma unroll
           for (int i = 0; i < NH; ++i) {
-            const float fh = sc2.x * qs[i];
-            const float fl = fmaf(sc2.x, qs[i], -fh) + fh * (Scale<D>::lo / Scale<D>::hi);
-            const float ca = G8 ? sc[nb][i] : sc[nb][0], cb = G8 ? sc[nb][2 + i] : sc[nb][2];
-            float da = fmaf(ca, fl, fmaf(ca, fh, -m[i])), db = fmaf(cb, fl, fmaf(cb, fh, -m[i]));
-            if constexpr (!G8 && QF32) {             // the low halves' columns
-              da = fmaf(sc[nb][1], fh, da);
-              db = fmaf(sc[nb][3], fh, db);
-            }
-            pr[i][0] = ex2(da);
-            pr[i][1] = ex2(db);
+            const float da = (G8 ? sc[nb][i] : sc[nb][0]) - cm[i], db = (G8 ? sc[nb][2 + i] : sc[nb][2]) - cm[i];
+            pr[i][0] = ex2(da * fh[i]);                 // (w log2 w is small: here f's rounding does not count)
+            pr[i][1] = ex2(db * fh[i]);
             l_run[i] = fmaf(beta[i], pr[i][0] + pr[i][1], l_run[i]);
           }
           if constexpr (G8) {

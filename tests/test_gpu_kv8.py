@@ -449,6 +449,54 @@ def test_decode_magnitudes(osc, fmt, loud):
         r.check(r.decode(q, 0, 0, bt, [n], [2]), q, 0, 0, bt, [n], [2])
 
 
+@pytest.mark.parametrize("G,qd", [(1, 0), (2, 0), (4, 0), (8, 0), (4, 1), (8, 1)])
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("P,d", [(16, 64), (64, 64), (64, 128)])
+def test_decode_large_scores(osc, P, d, fmt, G, qd):
+    """Scores of 2e4 to 1e5, nearly the same for every token, from query components whose digits beyond f16's count for tens
+    in the exponent, in either direction."""
+    rng = np.random.default_rng([P, d, fmt, G])
+    lens, loud = [3 * P, 3 * P + 5, P // 2], [513.25, 513.75, 700.3, -513.25, -700.3, 1201.7, 2100.1, -1999.9]
+    with Rig(osc, fmt, P, d, heads=2, G=G) as r:
+        bt, slots = tables(rng, 3, 12, 48, [3, 3, 0]), [1, 4, 0]
+        K, V = ([rng.normal(size=(n, 2, d)) for n in lens] for _ in range(2))
+        for k in K:
+            k[:, :, 0] = 500 * (1 if d == 64 else 1.5)
+        r.write(K, V, 0, lens, [0] * 3, bt, slots)
+        for i in range(0, 8, G):
+            q = rng.normal(size=(3, 2 * G, d))
+            q[:, :, 0] = (loud * 2)[i:i + 2 * G]
+            out = r.decode(q, qd, 0, bt, lens, slots)
+            assert torch.isfinite(out).all()
+            r.check(out, q, qd, 0, bt, lens, slots)
+        assert r.status() == 0
+
+
+@pytest.mark.parametrize("G,qd", [(2, 0), (4, 1), (8, 0), (8, 1)])
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("size", [1e8, 1e11, 1e15, 1e25, 1e33])
+def test_decode_where_one_key_leads_by_far(osc, fmt, G, qd, size):
+    """Finite scores up to 1e33 of which one is twice the next: the output is that token's value row, in a page or in the
+    tail.  The others' weights are exp(-size / 2) = 0 whatever a score's rounding, so what is left is the roundings of one
+    weight, its scales and its division: 8 of 2^-24."""
+    rng = np.random.default_rng([fmt, G])
+    P, d = 16, 64
+    for n, top in ((5 * P + 3, 2 * P + 7), (5 * P + 3, 5 * P + 1), (3, 2), (90 * P, 77 * P)):
+        with Rig(osc, fmt, P, d, heads=2, G=G, per_req=90, pages=90) as r:
+            bt = tables(rng, 1, 90, 90, [n // P])
+            K, V = (rng.normal(size=(n, 2, d)) for _ in range(2))
+            K[:, :, 5] = 0.5 * size ** 0.5
+            K[top, :, 5] = size ** 0.5
+            r.write([K], [V], 0, [n], [0], bt, [0])
+            q = rng.normal(size=(1, 2 * G, d))
+            q[:, :, 5] = 8 * size ** 0.5
+            out = r.decode(q, qd, 0, bt, [n], [0])[0].double().cpu().numpy()
+            for h in range(2):
+                v = r.ref.rows(bt[0], 0, n, h)[1][top]
+                assert np.all(np.abs(out[h * G:(h + 1) * G] - v) <= 8 * 2.0 ** -24 * np.abs(v)), (n, top)
+            assert r.status() == 0
+
+
 @pytest.mark.parametrize("P,d", [(16, 64), (32, 128), (64, 64)])
 @pytest.mark.parametrize("dtype", [0, 1])
 def test_write_from_slices_of_one_projection(osc, P, d, dtype):
