@@ -14,7 +14,8 @@
 //           channels are taken in the order in which a lane's 16-byte loads hold them.
 //   values: A = 16 channels x 16 tokens of codes, B = the weights as f16 high and low halves (24 bits
 //           relative to the blocks' largest).
-// Codes are exact f16 numbers, so the only roundings are float32's.  The block's scales multiply scores
+// Codes are exact f16 numbers, so the only roundings are float32's, but for a query's components far below its largest one; where
+// those decide, the split is taken again in plain float32 (plain_split).  The block's scales multiply scores
 // and sums in float32, and the weights are relative to the maximum of a warp's own blocks, all of one page, so a quiet page
 // next to a loud one keeps its digits.  A token's distance from that maximum is formed from the raw sums, before any scale:
 // it is 0 at the maximum and below 0 elsewhere whatever the scores' size, so no weight leaves [0, 1].  The tail rows go the same way with BF16 operands, 16 rows a warp, in the CTA of the
@@ -91,6 +92,14 @@ __device__ __forceinline__ void store_out(const Kv8DecodeArgs& a, size_t i, floa
 __device__ __forceinline__ int split_count(const Kv8DecodeArgs& a, int have) {
   const int per = a.wl.stages_per_split * (kv8_stage_tokens(a.g.D, a.g.P) / a.g.P);
   return max((have + per - 1) / per, 1);
+}
+
+// The tail's K rows of request b and kv head h (the V rows follow P rows on); null for a bad slot.
+__device__ __forceinline__ const uint16_t* tail_of(const Kv8DecodeArgs& a, int b, int h) {
+  const Geom& g = a.g;
+  const int slot = a.req_slot[b];
+  if (slot < 0 || slot >= g.max_req) return nullptr;
+  return a.tail + ((size_t)a.layer * g.max_req + slot) * kv8_tail_req_elems(g) + (size_t)h * 2 * g.P * g.D;
 }
 
 // x, y as three BF16 pairs whose sum has float32's digits.
@@ -202,6 +211,83 @@ __device__ __forceinline__ void tail_block(const Kv8DecodeArgs& a, int b, int h,
   }
 }
 
+// ------------------------------------------------------------------ a split in plain float32
+// A query component is held to 2^-25 (its head's largest being 2^14 to 2^15), so a raw sum to L = D M 2^-25, M the largest
+// code, and a score of scale f to L f.  That is no more than 2^-20 while f <= 32 / (D M); and it is below 2^-18 of the sum's own
+// terms, a float32 sum's error, where the sums whose weights count, those down to 30 / f below the largest one cm, are not
+// near 0: |cm| >= 2 D M > D M / 128 + 30 / f.  A block that meets neither has keys of 0 under the loudest components of a query
+// whose quiet ones still decide its weights.
+template <int D, int FMT>
+__device__ __forceinline__ bool digits_lost(float f, float cm) {
+  constexpr float kSum = D * (FMT == kKv8Int8 ? 127.f : 448.f);
+  return f > 32.f / kSum && fabsf(cm) < 2.f * kSum;
+}
+
+// What the warps leave for the merge ([warp][head][m, l, acc]) of a split in which such a block was met: all of it again, a
+// token at a time from global memory, channels over the lanes, one head after another.  (Where every split needs it: batch 1 at
+// 32K 260 us, 64 ragged requests 37 ms.  Its test costs the other calls 1 %, up to 6 % at d = 64 with eight heads.)
+template <int D, int FMT, bool QF32, typename Page>
+__device__ void plain_split(const Kv8DecodeArgs& a, int b, int h, int e0, int e1, Page page_of, const uint16_t* tail, int rows, float* mg) {
+  constexpr int C = D / 32;                             // channels of a lane
+  const Geom& g = a.g;
+  const Kv8Geom kg{g.P, D, g.Hkv};
+  const int G = g.gq(), warp = threadIdx.x >> 5, lane = threadIdx.x & 31, ch = lane * C;
+  const uint8_t* layer = a.pool + (size_t)a.layer * g.num_pages * kg.page_bytes() + (size_t)h * kg.block_bytes();
+  for (int hh = 0; hh < G; ++hh) {
+    float q[C], o[C], big = 0.f, m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      q[i] = kv8_load(a.q, (size_t)b * a.q_stride + (size_t)(h * G + hh) * D + ch + i, QF32 ? kDtypeF32 : kDtypeBF16);
+      o[i] = 0.f;
+      big = fmaxf(big, fabsf(q[i]));
+    }
+#pragma unroll
+    for (int x = 16; x; x >>= 1) big = warp_max_xor(big, x);
+    float up, down;
+    power_of_two(big, &up, &down);
+    // a token of score c f and values v
+    auto token = [&](float c, float f, const float (&v)[C]) {
+#pragma unroll
+      for (int x = 16; x; x >>= 1) c += __shfl_xor_sync(0xffffffffu, c, x);
+      const float s = c * f, m_new = fmaxf(m, s), alpha = ex2(m - m_new), p = ex2(s - m_new);
+      l = fmaf(l, alpha, p);
+#pragma unroll
+      for (int i = 0; i < C; ++i) o[i] = fmaf(o[i], alpha, p * v[i]);
+      m = m_new;
+    };
+    for (int r = warp; r < rows; r += kConsumers) {
+      const uint16_t* k = tail + (size_t)r * D + ch;
+      float c = 0.f, v[C];
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        c = fmaf(__uint_as_float((uint32_t)k[i] << 16), q[i], c);
+        v[i] = __uint_as_float((uint32_t)k[(size_t)g.P * D + i] << 16);
+      }
+      token(c, Scale<D>::hi, v);
+    }
+    for (int e = e0 + warp; e < e1; e += kConsumers) {
+      const int pid = page_of(e);
+      if (pid < 0) continue;
+      const uint8_t* block = layer + (size_t)pid * kg.page_bytes();
+      const float2 scale = *reinterpret_cast<const float2*>(block + kg.scale_off());
+      for (int t = 0; t < g.P; ++t) {
+        const uint8_t *k = block + kv8_place<D, false>(t, ch), *w = block + kg.v_off() + kv8_place<D, true>(t, ch);
+        float c = 0.f, v[C];
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+          c = fmaf(kv8_value<FMT>(k[i]), q[i] * up, c);
+          v[i] = kv8_value<FMT>(w[i]) * scale.y;
+        }
+        token(c, scale.x * (down * Scale<D>::hi), v);
+      }
+    }
+    float* row = mg + (warp * 8 + hh) * (D + 2);
+    if (lane == 0) row[0] = m, row[1] = l;
+#pragma unroll
+    for (int i = 0; i < C; ++i) row[2 + ch + i] = o[i];
+  }
+}
+
 // ------------------------------------------------------------------ pages
 // G8: eight query heads per kv head (an MMA column is a head, low halves go through a second MMA); otherwise
 // up to four (columns 2 h and 2 h + 1 are the high and the low half of head h).
@@ -259,6 +345,7 @@ __global__ void __launch_bounds__(kThreads, (Layout<D, NB, G8>::kResident)) kv8_
   if (split >= splits) return;
   const int e1 = min(e0 + a.wl.stages_per_split * per_stage, have);
   const int stages = (e1 - e0 + per_stage - 1) / per_stage;
+  const int tail_rows = split == splits - 1 ? n % P : 0;
   const int page_stride = L::page_stride(P), stage_bytes = L::stage_bytes(P);
   __syncthreads();
   const int gid = lane >> 2, tig = lane & 3;
@@ -273,30 +360,31 @@ __global__ void __launch_bounds__(kThreads, (Layout<D, NB, G8>::kResident)) kv8_
 #pragma unroll
     for (int i = 0; i < 2 * NH; ++i) acc[mt][i] = 0.f;
 
+  // page of entry e (value: the list's or the table's word for it, before: the list's word before it); -1: nothing to copy
+  auto lookup = [&](int e, int value, int before) {
+    if (e >= e1) return -1;
+    int pid = value;
+    if (list) {
+      if (value < 0) return -1;
+      if (value >= pages || before >= value || (e > 0 && before < 0)) {
+        flag_error(a.status, kDevBadPage);
+        return -1;
+      }
+      pid = value < a.bt_stride ? bt[value] : -1;
+    }
+    if (pid < 0 || pid >= g.num_pages) {
+      flag_error(a.status, kDevBadPage);
+      return -1;
+    }
+    return pid;
+  };
+  bool lost = false;                                    // a block's scores need more digits of the query
   if (warp == kConsumers) {
     // ---------------------------------------------------------------- producer
     const Kv8Geom kg{P, D, g.Hkv};
     const uint64_t policy = l2_evict_first_policy();
     const uint32_t bytes = 2 * P * D + 16;
     const uint8_t* layer = a.pool + (size_t)a.layer * g.num_pages * kg.page_bytes() + (size_t)h * kg.block_bytes();
-    // page of entry e (value: the list's or the table's word for it, before: the list's word before it); -1: nothing to copy
-    auto lookup = [&](int e, int value, int before) {
-      if (e >= e1) return -1;
-      int pid = value;
-      if (list) {
-        if (value < 0) return -1;
-        if (value >= pages || before >= value || (e > 0 && before < 0)) {
-          flag_error(a.status, kDevBadPage);
-          return -1;
-        }
-        pid = value < a.bt_stride ? bt[value] : -1;
-      }
-      if (pid < 0 || pid >= g.num_pages) {
-        flag_error(a.status, kDevBadPage);
-        return -1;
-      }
-      return pid;
-    };
     auto later = [&](int e) {  // the same for entries after the first 32
       if (e >= e1) return -1;
       return list ? lookup(e, list[e], list[e - 1]) : lookup(e, e < a.bt_stride ? bt[e] : -1, -1);
@@ -355,8 +443,9 @@ __global__ void __launch_bounds__(kThreads, (Layout<D, NB, G8>::kResident)) kv8_
         }
       big = warp_max_xor(big, 1);
       big = warp_max_xor(big, 2);
-      const int k = min(max((int)(__float_as_uint(big) >> 23) - 127, -100), 127);
-      const float up = __uint_as_float((uint32_t)(127 + 14 - k) << 23), down = __uint_as_float((uint32_t)(127 - 14 + k) << 23);
+      float up, down;
+      power_of_two(big, &up, &down);
+      if (!live) down = 0.f;
 #pragma unroll
       for (int kk = 0; kk < KS; ++kk)
 #pragma unroll
@@ -382,12 +471,10 @@ __global__ void __launch_bounds__(kThreads, (Layout<D, NB, G8>::kResident)) kv8_
     const uint32_t k_off = D == 128 ? (t0 + gid) * 128 + ((tig ^ (4 * (gid & 1))) << 4) : (t0 + gid) * 64 + tig * 16;
     const uint32_t v_off = P * D + (D == 128 ? (t0 + 2 * tig) * 128 + ((gid ^ (2 * tig)) << 4)
                                              : (t0 / 2 + tig) * 128 + (((gid >> 1) ^ (2 * tig)) << 4) + (gid & 1) * 8);
-    if (split == splits - 1 && warp * 16 < n % P) {
-      const int slot = a.req_slot[b];
-      if (slot >= 0 && slot < g.max_req) {
-        const uint16_t* rows = a.tail + ((size_t)a.layer * g.max_req + slot) * kv8_tail_req_elems(g) +
-                               ((size_t)h * 2 * P + warp * 16) * D;
-        tail_block<D, G8, QF32>(a, b, h, rows, rows + (size_t)P * D, n % P - warp * 16, m_run, l_run, acc);
+    if (warp * 16 < tail_rows) {
+      if (const uint16_t* rows = tail_of(a, b, h)) {
+        rows += (size_t)warp * 16 * D;
+        tail_block<D, G8, QF32>(a, b, h, rows, rows + (size_t)P * D, tail_rows - warp * 16, m_run, l_run, acc);
       } else if (lane == 0) {
         flag_error(a.status, kDevBadSlot);
       }
@@ -448,6 +535,7 @@ __global__ void __launch_bounds__(kThreads, (Layout<D, NB, G8>::kResident)) kv8_
           cm[i] = warp_max_xor(cm[i], 16);
           fh[i] = sc2.x * qs[i];
           const float fl = fmaf(fh[i], Scale<D>::lo / Scale<D>::hi, fmaf(sc2.x, qs[i], -fh[i]));
+          lost |= digits_lost<D, FMT>(fh[i], cm[i]);
           const Top top(cm[i], fh[i], fl);
           const float m_new = fmaxf(m_run[i], top.m);
           alpha[i] = ex2(m_run[i] - m_new);
@@ -530,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, (Layout<D, NB, G8>::kResident)) kv8_
       }
     }
   }
-  __syncthreads();
+  const bool again = __syncthreads_or(lost);
   if (abort_flag) {  // a wait ran out: let the copies in flight land before the CTA ends
     if (tid == 0)
       for (int k = max(issued - kStages, 0); k < issued; ++k)
@@ -540,7 +628,15 @@ __global__ void __launch_bounds__(kThreads, (Layout<D, NB, G8>::kResident)) kv8_
   }
   // merge the four warps' partials: [warp][head][D + 2] in the ring's memory
   float* mg = reinterpret_cast<float*>(smem);
-  if (warp < kConsumers) {
+  if (again) {
+    if (warp < kConsumers) {
+      const uint16_t* rows = tail_rows > 0 ? tail_of(a, b, h) : nullptr;
+      auto page_of = [&](int e) {
+        return list ? lookup(e, list[e], e > 0 ? list[e - 1] : -1) : lookup(e, e < a.bt_stride ? bt[e] : -1, -1);
+      };
+      plain_split<D, FMT, QF32>(a, b, h, e0, e1, page_of, rows, rows ? tail_rows : 0, mg);
+    }
+  } else if (warp < kConsumers) {
 #pragma unroll
     for (int i = 0; i < NH; ++i) {
       l_run[i] += __shfl_xor_sync(0xffffffffu, l_run[i], 4);

@@ -79,13 +79,6 @@ __device__ __forceinline__ bool kept(const Kv8SelectArgs& a, int p, int pages) {
   return p < a.keep_first || p >= pages - a.keep_last;
 }
 
-// 2^e and its inverse with big 2^e in [2^14, 2^15).
-__device__ __forceinline__ void power_of_two(float big, float* up, float* down) {
-  const int k = min(max((int)(__float_as_uint(big) >> 23) - 127, -100), 127);
-  *up = __uint_as_float((uint32_t)(127 + 14 - k) << 23);
-  *down = __uint_as_float((uint32_t)(127 - 14 + k) << 23);
-}
-
 // A sum of float32 numbers kept as hi + lo, about 48 bits: the second scoring.  (The card's float64 rate is a sixtieth of
 // float32's.)  The additions are Knuth's exact two-number sum.
 struct Sum2 {

@@ -50,6 +50,13 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
   return r;
 }
 
+// 2^e and its inverse with big 2^e in [2^14, 2^15).
+__device__ __forceinline__ void power_of_two(float big, float* up, float* down) {
+  const int k = min(max((int)(__float_as_uint(big) >> 23) - 127, -100), 127);
+  *up = __uint_as_float((uint32_t)(127 + 14 - k) << 23);
+  *down = __uint_as_float((uint32_t)(127 - 14 + k) << 23);
+}
+
 // Four neighbouring query components.
 template <bool QF32>
 __device__ __forceinline__ float4 kv8_load4(const void* q, size_t i) {

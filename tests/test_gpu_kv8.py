@@ -497,6 +497,33 @@ def test_decode_where_one_key_leads_by_far(osc, fmt, G, qd, size):
             assert r.status() == 0
 
 
+@pytest.mark.parametrize("G,qd", [(1, 1), (2, 0), (4, 1), (4, 0), (8, 0), (8, 1)])
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("P,d", [(16, 64), (64, 64), (32, 128), (64, 128)])
+def test_decode_where_the_loudest_query_channel_meets_no_key(osc, P, d, fmt, G, qd):
+    """A query component 10^3 to 10^30 times the others over a channel of zero keys: the others decide the weights."""
+    rng = np.random.default_rng([P, d, fmt, G])
+    lens = [9 * P, 9 * P + 3]
+    with Rig(osc, fmt, P, d, heads=2, G=G) as r:
+        bt, slots = tables(rng, 2, 12, 48, [9, 9]), [1, 4]
+        K, V = ([rng.normal(size=(n, 2, d)) for n in lens] for _ in range(2))
+        for k in K:
+            k[:, :, 3] = 0
+            k[4 * P:5 * P, 0, 3] = 1e-30                 # (a code of 0 as well, but for this page of one head)
+            k[4 * P:5 * P, 0] *= 1e-30
+        r.write(K, V, 0, lens, [0, 0], bt, slots)
+        for loud in (1e3, 1e6, 1e9, 1e12, 1e20, 1e30):
+            q = 3 * rng.normal(size=(2, 2 * G, d))
+            q[:, ::2, 3] = loud
+            q[:, 1::2, 3] = -loud
+            r.check(r.decode(q, qd, 0, bt, lens, slots), q, qd, 0, bt, lens, slots)
+            pages = np.tile(np.array([1, 3, 4, 8, -1], np.int32), (2, 2, 1))
+            r.check(r.decode(q, qd, 0, bt, lens, slots, pages=pages), q, qd, 0, bt, lens, slots, pages)
+            small = q * (1e-25 if loud > 1e6 else 1e-3)     # and where the query as a whole is quiet
+            r.check(r.decode(small, 0, 0, bt, lens, slots), small, 0, 0, bt, lens, slots)
+        assert r.status() == 0
+
+
 @pytest.mark.parametrize("P,d", [(16, 64), (32, 128), (64, 64)])
 @pytest.mark.parametrize("dtype", [0, 1])
 def test_write_from_slices_of_one_projection(osc, P, d, dtype):
