@@ -13,11 +13,12 @@
 //
 // The order is that of bounds exact to about 48 bits, the scores are float32's.  One is off by at most
 //   E_p = 2^-14 A_p,   A_p = scale_p sum_c (a_c |hi_pc| + b_c |lo_pc|):
-// the sums over 8 heads take 7 roundings of half a step (2^-24), the halves leave out 2^-22 of a weight, the scale takes 2
-// roundings, and each of the 2 d / 16 <= 16 matrix instructions adds 17 numbers and loses less than a step (2^-23) of the
-// largest for each: 7 + 4 + 2 + 16 x 17 x 2 = 557 half steps, where 2^-14 is 1024; A_p itself comes from the same
+// the sums over 8 heads take 7 roundings of half a step (2^-24), the halves leave out 2^-22 of a weight, the scale takes a
+// rounding, and each of the 2 d / 16 <= 16 matrix instructions adds 17 numbers and loses less than a step (2^-23) of the
+// largest for each: 7 + 4 + 1 + 16 x 17 x 2 = 556 half steps, where 2^-14 is 1024; A_p itself comes from the same
 // instructions on the magnitudes, off by as little.  Weights below f16's normal numbers are off by up to 2^-25 (the largest
-// being 2^14), which adds 2 d M 2^-25 in these units, M the largest code.
+// being 2^14), which adds 2 d M 2^-25 in these units, M the largest code; a product of sum and scale among float32's subnormal numbers
+// is off by 2^-150, for which 2^-140 is added.
 // With E the largest E_p and t the n-th largest float32 score, the n-th largest exact score lies within E of
 // t; so a page above t + 2 E is in, one below t - 2 E is out, and only the ones between, mostly the n-th
 // alone, are scored again to about 48 bits and ranked.
@@ -196,10 +197,10 @@ __global__ void __launch_bounds__(32 * kScoreWarps) kv8_score_kernel(const __gri
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
     const int p = p0 + gid + 8 * r;
-    const float f = scale[r] * down;
-    const float score = (sc[2 * r] + sc[2 * r + 1]) * f;
+    // (without the query's power of two, which is the same for every page: with it, scale and all could leave the normal numbers)
+    const float score = (sc[2 * r] + sc[2 * r + 1]) * scale[r];
     constexpr float kFloor = 2 * D * (FMT == kKv8Int8 ? 127.f : 448.f) * 0x1p-25f;
-    const float e = fmaf(sa[2 * r] + sa[2 * r + 1], 0x1p-14f, kFloor) * f + 0x1p-140f;   // (and float32's own subnormal numbers)
+    const float e = fmaf(sa[2 * r] + sa[2 * r + 1], 0x1p-14f, kFloor) * scale[r] + 0x1p-140f;   // (and float32's own subnormal numbers)
     if (tig == 0 && p < pages) keys[p] = pid[r] >= 0 ? key_of(score) : 0u;
     // no finite bound, or a score that overflowed: every page is scored again
     if (tig == 0 && pid[r] >= 0) bound = (e <= 3e38f && fabsf(score) <= 3e38f) ? fmaxf(bound, e) : INFINITY;

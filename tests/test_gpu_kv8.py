@@ -672,6 +672,23 @@ def test_select_where_the_loudest_query_channel_meets_no_key(osc, fmt, P, d):
             assert np.array_equal(got, r.ref.select(q[0].astype(np.float32).astype(np.float64), bt[0], lens[0], 0, 0, k))
 
 
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("keys,query", [(-75, -50), (-75, -60), (-90, -40), (-90, -20), (-60, -66), (-60, -90), (-97, 100), (90, 20), (110, 100)])
+def test_select_where_scores_leave_the_normal_numbers(osc, fmt, keys, query):
+    """Keys near 2^keys and queries near 2^query: bounds whose size float32 holds with few digits, or not at all."""
+    rng = np.random.default_rng([fmt, 200 + keys, 200 + query])
+    lens = [60 * 16 + 3]
+    with Rig(osc, fmt, 16, 64, heads=2, G=2, per_req=61, pages=61) as r:
+        bt = tables(rng, 1, 61, 61, [60])
+        K = rng.normal(size=(lens[0], 2, 64)) * 2.0 ** keys
+        r.write([K], [K], 0, lens, [0], bt, [0])
+        q = (rng.normal(size=(1, 4, 64)) * 2.0 ** query).astype(np.float32).astype(np.float64)
+        for k in (1, 7, 30, 59):
+            got = r.select(q, 0, bt, lens, 0, 0, k).cpu().numpy()[0]
+            assert np.array_equal(got, r.ref.select(q[0], bt[0], lens[0], 0, 0, k)), k
+        assert r.status() == 0
+
+
 def test_select_long(osc):
     rng = np.random.default_rng(29)
     P, d, pages = 16, 64, 4500
