@@ -505,7 +505,8 @@ oscar_status oscar_kv8_decode_attn(oscar_ctx* ctx, int32_t layer, const void* q,
  * of the request, then those of the largest U_p, the lowest index first among equal
  * ones; every complete page when there are no more than n_select.  1 <= n_select,
  * keep_first + keep_last <= n_select.  Pages are ordered by U_p to about 48 bits (a NaN in q
- * counts as 0; a page that is not mapped comes last and sets OSCAR_DEV_BAD_PAGE).  The list may
+ * counts as 0, an infinity leaves the choice open; a page that is not mapped comes last and sets
+ * OSCAR_DEV_BAD_PAGE).  The list may
  * serve several calls (later tokens, other layers) as long as its pages are complete. */
 oscar_status oscar_kv8_select_workspace_size(const oscar_config* cfg, int32_t batch, int32_t max_seq, size_t* bytes);
 oscar_status oscar_kv8_select_pages(oscar_ctx* ctx, int32_t layer, const void* q, int64_t q_stride, int32_t q_dtype,

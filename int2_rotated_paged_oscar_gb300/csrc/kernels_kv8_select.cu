@@ -40,6 +40,9 @@ struct Pick {
 };
 constexpr int kFew = 64;           // keys that are ranked one by one
 constexpr int kTile = 64;          // pages scored again are ranked against tiles of this many
+// Up to this many of them.  More, where equal or nearly equal pages leave all of them open, are chosen digit by digit: a query
+// of zeros over 64, 128, 256, 1024 and 8192 pages 15.8, 22, 47, 443 and 7167 us ranked, 17.4, 21, 30, 82 and 211 by digits.
+constexpr int kRanked = 128;
 using Key = unsigned long long;
 
 // Workspace: float32 keys [batch][Hkv][max_pages], 64-bit keys of the band (same count), its page indexes,
@@ -221,8 +224,8 @@ __global__ void __launch_bounds__(Pick<SMALL>::kThreads, 2) kv8_pick_kernel(cons
   __shared__ uint32_t u_lo[kPickThreads / 32], u_hi[kPickThreads / 32];
   __shared__ float f_e[kPickThreads / 32];
   __shared__ int sums[kPickThreads / 32];
-  __shared__ uint32_t s_prefix;
-  __shared__ int s_need, s_count, s_few_n, s_band, s_above;
+  __shared__ uint32_t s_nth;
+  __shared__ int s_bin, s_need, s_count, s_few_n, s_band, s_above;
   __shared__ float s_q[8 * D];
   __shared__ __align__(16) float w_hi[2][D], w_lo[2][D];   // [a, b]: the weights of a second scoring as two numbers
   __shared__ float s_big[kPickThreads / 32];
@@ -270,7 +273,6 @@ __global__ void __launch_bounds__(Pick<SMALL>::kThreads, 2) kv8_pick_kernel(cons
   for (int i = tid; i < chunks; i += kPickThreads) e = fmaxf(e, bounds[i]);
   for (int i = tid; i < kBins; i += kPickThreads) hist[i] = 0;
   if (tid == 0) {
-    s_prefix = 0;
     s_need = need0;
     s_band = s_above = s_few_n = 0;
   }
@@ -292,50 +294,53 @@ __global__ void __launch_bounds__(Pick<SMALL>::kThreads, 2) kv8_pick_kernel(cons
   // keys over `above` are in, those under `below` out (need0 == 0: only the kept pages are in).  Both come from float32
   // arithmetic rounded outwards: float64 comparisons of every page took 8 us of 21 at 131K tokens.
   uint32_t above = ~0u, below = ~0u;
+  // s_bin: the bin of hist, counted from the largest, with the s_need-th; s_need: which of that bin's s_count it is
+  auto find_bin = [&] {
+    // thread t holds the kBins / kPickThreads below kBins - 1 - t kBins / kPickThreads
+    constexpr int kPer = kBins / kPickThreads;
+    int c[kPer], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) sum += c[i] = hist[kBins - 1 - tid * kPer - i];
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    if (lane == 31) sums[warp] = incl;
+    const int want = s_need;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPickThreads / 32; ++i) incl += i < warp ? sums[i] : 0;
+    int before = incl - sum;
+    if (before < want && want <= incl) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        if (before < want && want <= before + c[i]) {
+          s_need = want - before;
+          s_count = c[i];
+          s_bin = kBins - 1 - tid * kPer - i;
+        }
+        before += c[i];
+      }
+    }
+    __syncthreads();
+  };
   if (need0 > 0) {
     // the need-th largest of keys - lo, a digit at a time from the highest bit in which they differ, until few
     // enough keys share its digits to be ranked one by one
     int shift = max(0, 32 - kBinBits - __clz((hi - lo) | 1)), width = kBinBits;
     bool top = true;
-    uint32_t found;
+    uint32_t found = 0;
     while (true) {
-      const uint32_t prefix = s_prefix;
       for (int i = first + tid; i < last; i += kPickThreads) {
         const uint32_t k = keys[i] - lo;
-        if (top || (k >> (shift + width)) == (prefix >> (shift + width)))
+        if (top || (k >> (shift + width)) == (found >> (shift + width)))
           atomicAdd(&hist[(k >> shift) & ((1 << width) - 1)], 1);
       }
       __syncthreads();
-      // bins from the largest down: thread t holds the kBins / kPickThreads below kBins - 1 - t kBins / kPickThreads
-      constexpr int kPer = kBins / kPickThreads;
-      int c[kPer], sum = 0;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) sum += c[i] = hist[kBins - 1 - tid * kPer - i];
-      int incl = sum;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += x;
-      }
-      if (lane == 31) sums[warp] = incl;
-      const int want = s_need;
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < kPickThreads / 32; ++i) incl += i < warp ? sums[i] : 0;
-      int before = incl - sum;
-      if (before < want && want <= incl) {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          if (before < want && want <= before + c[i]) {
-            s_need = want - before;
-            s_count = c[i];
-            s_prefix = prefix | ((uint32_t)(kBins - 1 - tid * kPer - i) << shift);
-          }
-          before += c[i];
-        }
-      }
-      __syncthreads();
-      found = s_prefix;
+      find_bin();
+      found |= (uint32_t)s_bin << shift;
       if (shift == 0) break;
       if (s_count <= kFew) {
         for (int i = first + tid; i < last; i += kPickThreads) {
@@ -352,10 +357,10 @@ __global__ void __launch_bounds__(Pick<SMALL>::kThreads, 2) kv8_pick_kernel(cons
             more += s_few[i] > k;
             same += s_few[i] == k;
           }
-          if (more < left && left <= more + same) s_prefix = k;
+          if (more < left && left <= more + same) s_nth = k;
         }
         __syncthreads();
-        found = s_prefix;
+        found = s_nth;
         break;
       }
       for (int i = tid; i < kBins; i += kPickThreads) hist[i] = 0;
@@ -434,23 +439,54 @@ __global__ void __launch_bounds__(Pick<SMALL>::kThreads, 2) kv8_pick_kernel(cons
       if (sub == 0 && j < band) band_key[j] = pid >= 0 ? key_of(((double)u.hi + (double)u.lo) * scale) : 0ull;
     }
     __syncthreads();
-    // rank of each: those with a larger key, or an equal one and a lower index
-    for (int j0 = 0; j0 < band; j0 += kPickThreads) {
-      const int j = j0 + tid;
-      const Key k = j < band ? band_key[j] : 0;
-      const int at = j < band ? band_at[j] : 0;
-      int r = 0;
-      for (int i0 = 0; i0 < band; i0 += kTile) {
-        __syncthreads();
-        if (tid < kTile && i0 + tid < band) {
-          tile[tid] = band_key[i0 + tid];
-          tile_at[tid] = band_at[i0 + tid];
+    if (band <= kRanked) {
+      // rank of each: those with a larger key, or an equal one and a lower index
+      for (int j0 = 0; j0 < band; j0 += kPickThreads) {
+        const int j = j0 + tid;
+        const Key k = j < band ? band_key[j] : 0;
+        const int at = j < band ? band_at[j] : 0;
+        int r = 0;
+        for (int i0 = 0; i0 < band; i0 += kTile) {
+          __syncthreads();
+          if (tid < kTile && i0 + tid < band) {
+            tile[tid] = band_key[i0 + tid];
+            tile_at[tid] = band_at[i0 + tid];
+          }
+          __syncthreads();
+          const int m = min(kTile, band - i0);
+          for (int i = 0; i < m; ++i) r += tile[i] > k || (tile[i] == k && tile_at[i] < at);
         }
-        __syncthreads();
-        const int m = min(kTile, band - i0);
-        for (int i = 0; i < m; ++i) r += tile[i] > k || (tile[i] == k && tile_at[i] < at);
+        if (j < band) keys[at] = r < need ? ~0u : 0u;
       }
-      if (j < band) keys[at] = r < need ? ~0u : 0u;
+    } else {
+      // the need-th in that order, a digit at a time, first of the keys, then of the indexes of the ones equal to its key
+      auto nth = [&](int bits, auto value, auto among) {
+        Key prefix = 0;
+        for (int shift = bits; shift > 0;) {
+          const int top_bits = shift, width = min(kBinBits, shift);
+          shift -= width;
+          for (int i = tid; i < kBins; i += kPickThreads) hist[i] = 0;
+          __syncthreads();
+          for (int j = tid; j < band; j += kPickThreads) {
+            const Key v = value(j);
+            if (among(j) && (top_bits == bits || (v >> top_bits) == (prefix >> top_bits)))
+              atomicAdd(&hist[(int)(v >> shift) & ((1 << width) - 1)], 1);
+          }
+          __syncthreads();
+          find_bin();
+          prefix |= (Key)s_bin << shift;
+          if (s_need == s_count) break;                 // every one with these digits is in
+        }
+        return prefix;
+      };
+      if (tid == 0) s_need = need;
+      const Key key = nth(64, [&](int j) { return band_key[j]; }, [](int) { return true; });
+      const bool ties = s_need < s_count;
+      __syncthreads();
+      Key low = 0;
+      if (ties) low = nth(32, [&](int j) { return (Key)~(uint32_t)band_at[j]; }, [&](int j) { return band_key[j] == key; });
+      for (int j = tid; j < band; j += kPickThreads)
+        keys[band_at[j]] = band_key[j] > key || (band_key[j] == key && (Key)~(uint32_t)band_at[j] >= low) ? ~0u : 0u;
     }
     __syncthreads();
   }

@@ -689,6 +689,50 @@ def test_select_where_scores_leave_the_normal_numbers(osc, fmt, keys, query):
         assert r.status() == 0
 
 
+@pytest.mark.parametrize("pages", [2100, 9000])
+@pytest.mark.parametrize("fmt", [0, 1])
+def test_select_among_thousands_of_equal_and_nearly_equal_pages(osc, fmt, pages):
+    """More pages than are ranked one by one: equal ones by the lower index, nearly equal ones in their float64 order."""
+    rng = np.random.default_rng([fmt, pages])
+    P, d = 16, 64
+    with Rig(osc, fmt, P, d, heads=1, G=2, per_req=pages, pages=pages, layers=1, layer=0, oracle=False) as r:
+        bt, n = rng.permutation(pages)[None].astype(np.int32), [pages * P]
+        K = np.tile(acts(rng, (P, 1, d)), (pages, 1, 1))
+        r.write([K], [K], 1, n, [0], bt, [0], ref=False)
+        r.ref = O.Cache(P, d, 1, fmt, r.pool[0].cpu().numpy().copy(), np.zeros((5, 1, 2, P, d)))
+        q = acts(rng, (1, 2, d), False)
+        some = (1, 45, pages // 2, pages - 1)
+        for k in some:                                                  # every page the same
+            want = np.concatenate([np.arange(k - 1), [pages - 1]])
+            assert np.array_equal(r.select(q, 1, bt, n, 0, 1, k).cpu().numpy()[0, 0], want)
+            assert np.array_equal(r.select(q * 0, 1, bt, n, 0, 0, k).cpu().numpy()[0, 0], np.arange(k))
+        at = torch.from_numpy(bt[0].astype(np.int64)).cuda()
+        field = (0, at, slice(None), slice(2 * P * d, 2 * P * d + 4))
+        step = torch.from_numpy(rng.integers(-3, 4, (pages, 1, 1)).astype(np.int32)).cuda()
+        r.pool[field] = (r.pool[field].contiguous().view(torch.int32) + step).view(torch.uint8)
+        r.ref.pool[:] = r.pool[0].cpu().numpy()
+        for k in some:
+            got = r.select(q, 1, bt, n, 0, 1, k).cpu().numpy()[0]
+            assert np.array_equal(got, r.ref.select(bf16(q)[0], bt[0], n[0], 0, 1, k))
+        assert r.status() == 0
+
+
+@pytest.mark.parametrize("bad", [np.inf, -np.inf, 3.4e38])
+def test_select_lists_stay_valid(osc, bad):
+    """Whatever a query holds, a list is full, ascending and of complete pages, the kept ones among them."""
+    rng = np.random.default_rng(59)
+    lens = [40 * 16 + 3]
+    rig, bt, slots = filled(osc, rng, lens, fmt=1, G=4, per_req=41, pages=41)
+    with rig as r:
+        q = acts(rng, (1, 8, 64), False)
+        q[0, 2, 7] = bad
+        idx = r.select(q, 0, bt, lens, 2, 1, 9).cpu().numpy()[0]
+        assert np.all(np.diff(idx, axis=1) > 0) and idx.min() == 0 and idx.max() == 39
+        assert np.array_equal(idx[:, [0, 1, 8]], [[0, 1, 39]] * 2)
+        good = r.ref.select(q[0].astype(np.float32).astype(np.float64), bt[0], lens[0], 2, 1, 9) if np.isfinite(bad) else idx
+        assert np.array_equal(idx, good) and r.status() == 0
+
+
 def test_select_long(osc):
     rng = np.random.default_rng(29)
     P, d, pages = 16, 64, 4500
