@@ -547,7 +547,8 @@ oscar_status oscar_kv8_fork(oscar_ctx* ctx, const int32_t* src_bt, int32_t n, in
  * *out_live receives live.  Refcounts move with their pages, and fresh pages are handed out from
  * live upwards.  The copies and the rewriting run on stream; every block table that maps a moved
  * page must be rewritten before its next use, and work on other streams that reads those pages
- * must be ordered around the call.  Not for graph capture (the allocator changes at the call). */
+ * must be ordered around the call.  On an error no page has moved and block_table has its old
+ * entries.  Not for graph capture (the allocator changes at the call). */
 oscar_status oscar_compact_pages(oscar_ctx* ctx, int32_t* block_table, int32_t rows, int32_t bt_stride,
                                  int32_t* out_map, int32_t* out_live, void* stream);
 

@@ -415,20 +415,25 @@ oscar_status oscar_compact_pages(oscar_ctx* ctx, int32_t* block_table, int32_t r
     std::vector<int32_t> stack;
     stack.reserve(g.num_pages);
     for (int i = g.num_pages - 1; i >= live; --i) stack.push_back(i);  // lowest id first
-    // every copy before any table entry changes: after a failed launch the old pages still hold
+    // Every copy before any table entry changes, and the entries back to the old ids (dst is as ascending as src) when a later
+    // launch fails: the old pages still hold, and the allocator has not changed.
     const int moves = (int)src.size();
+    auto run = [&](int pass, const int* from, const int* to, int n) {
+      LaunchScope ls(ctx, pass < 2 ? "copy_pages" : "remap_table", stream);
+      const int e = pass == 0   ? oscar::launch_copy_pages(ctx->pool, g.L, g.num_pages, g.Hkv * g.block_bytes(), from, to, n, stream)
+                    : pass == 1 ? oscar::launch_copy_pages(ctx->kv8_pool, g.L, g.num_pages, oscar::kv8_geom(g).page_bytes(), from, to, n, stream)
+                                : oscar::launch_remap_table(block_table, rows, bt_stride, from, to, n, stream);
+      ls.done(e);
+      return e;
+    };
     for (int pass = 0; pass < 3 && device; ++pass) {
       if (pass == 0 ? !ctx->pool : pass == 1 ? !ctx->kv8_pool : rows == 0) continue;
       for (int at = 0; at < moves; at += oscar::kMostPairs) {
-        const int n = std::min(moves - at, oscar::kMostPairs);
-        const int *from = src.data() + at, *to = dst.data() + at;
-        LaunchScope ls(ctx, pass < 2 ? "copy_pages" : "remap_table", stream);
-        const int e =
-            pass == 0   ? oscar::launch_copy_pages(ctx->pool, g.L, g.num_pages, g.Hkv * g.block_bytes(), from, to, n, stream)
-            : pass == 1 ? oscar::launch_copy_pages(ctx->kv8_pool, g.L, g.num_pages, oscar::kv8_geom(g).page_bytes(), from, to, n, stream)
-                        : oscar::launch_remap_table(block_table, rows, bt_stride, from, to, n, stream);
-        ls.done(e);
-        if (e) return cuda_fail(e, "page move launch");
+        const int e = run(pass, src.data() + at, dst.data() + at, std::min(moves - at, oscar::kMostPairs));
+        if (!e) continue;
+        for (int back = 0; pass == 2 && back < at; back += oscar::kMostPairs)
+          (void)run(2, dst.data() + back, src.data() + back, oscar::kMostPairs);
+        return cuda_fail(e, "page move launch");
       }
     }
     for (int i = 0; i < g.num_pages; ++i) out_map[i] = ctx->refcount[i] > 0 ? i : -1;

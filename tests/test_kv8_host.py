@@ -324,3 +324,19 @@ def test_compaction_plan(osc):
             osc.oscar_compact_pages(ctx, 256, 2, 4, 40, stream=0)               # a table, but no device buffers
     finally:
         osc.oscar_destroy(ctx)
+
+
+def test_failed_launches_leave_pages_and_tables_as_they_were(tmp_path):
+    """Compactions of more pages than one launch takes, each launch of one failing in turn, and a fork whose copy fails."""
+    import os
+    import shutil
+    import subprocess
+    from int2_rotated_paged_oscar_gb300 import build
+    here = os.path.dirname(os.path.abspath(__file__))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(build._nvcc())))
+    program = tmp_path / "page_moves"
+    r = subprocess.run([shutil.which("g++"), "-std=c++17", "-O1", "-I", os.path.join(cuda, "include"), "-o", str(program),
+                        os.path.join(here, "page_moves_host.cpp"), os.path.join(build.CSRC, "kv8_abi.cpp")], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    r = subprocess.run([str(program)], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0, r.stdout + r.stderr
