@@ -533,7 +533,7 @@ oscar_status oscar_kv8_sparse_decode_attn(oscar_ctx* ctx, int32_t layer, const v
  * -1).  The n / P complete pages are shared (each refcount + n_dst); the n mod P tail rows are
  * copied to every destination slot, in every layer, by one kernel on stream.  On an error
  * nothing is forked.  Without a bound cache only the host part is done.  The allocator changes
- * at the call, so the call is not for graph capture.  It copies no
+ * at the call, so a stream that is being captured is refused.  It copies no
  * INT2 window, and oscar_fork_prefix neither 8-bit blocks nor tail rows: a request that is
  * forked keeps its tokens in one of the two caches. */
 oscar_status oscar_kv8_fork(oscar_ctx* ctx, const int32_t* src_bt, int32_t n, int32_t src_slot,
@@ -548,7 +548,7 @@ oscar_status oscar_kv8_fork(oscar_ctx* ctx, const int32_t* src_bt, int32_t n, in
  * live upwards.  The copies and the rewriting run on stream; every block table that maps a moved
  * page must be rewritten before its next use, and work on other streams that reads those pages
  * must be ordered around the call.  On an error no page has moved and block_table has its old
- * entries.  Not for graph capture (the allocator changes at the call). */
+ * entries.  The allocator changes at the call, so a stream that is being captured is refused. */
 oscar_status oscar_compact_pages(oscar_ctx* ctx, int32_t* block_table, int32_t rows, int32_t bt_stride,
                                  int32_t* out_map, int32_t* out_live, void* stream);
 

@@ -31,6 +31,17 @@ oscar_status check_device(const oscar_ctx* ctx) {
   return OSCAR_OK;
 }
 
+// The allocator changes at the call: a captured one would move pages by an old plan at every replay.
+oscar_status check_not_capturing(void* stream, const char* name) {
+  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(static_cast<cudaStream_t>(stream), &cs) != cudaSuccess) {
+    (void)cudaGetLastError();  // (the legacy stream during another one's capture: a launch there reports it)
+    return OSCAR_OK;
+  }
+  if (cs != cudaStreamCaptureStatusNone) return fail(OSCAR_ERR_INVALID, "%s cannot be captured into a graph", name);
+  return OSCAR_OK;
+}
+
 oscar_status need_kv8(oscar_ctx* ctx) {
   if (!ctx) return fail(OSCAR_ERR_INVALID, "context is null");
   if (!ctx->kv8_pool) return fail(OSCAR_ERR_INVALID, "no 8-bit cache is bound to the context (oscar_kv8_bind)");
@@ -361,7 +372,8 @@ oscar_status oscar_kv8_fork(oscar_ctx* ctx, const int32_t* src_bt, int32_t n, in
     return fail(OSCAR_ERR_OOM, "host allocation failed");
   }
   if (ctx->kv8_pool) {
-    const oscar_status st = check_device(ctx);
+    oscar_status st = check_device(ctx);
+    if (st == OSCAR_OK) st = check_not_capturing(stream, "oscar_kv8_fork");
     if (st != OSCAR_OK) return st;
   }
   {
@@ -400,7 +412,8 @@ oscar_status oscar_compact_pages(oscar_ctx* ctx, int32_t* block_table, int32_t r
   const bool device = ctx->pool || ctx->kv8_pool;
   if (rows > 0 && !device) return fail(OSCAR_ERR_INVALID, "context was created without device buffers");
   if (device) {
-    const oscar_status st = check_device(ctx);
+    oscar_status st = check_device(ctx);
+    if (st == OSCAR_OK) st = check_not_capturing(stream, "oscar_compact_pages");
     if (st != OSCAR_OK) return st;
   }
   try {

@@ -11,6 +11,7 @@ namespace {
 
 int launches = 0, fails_at = -1;   // the launch that returns an error, counted from 0
 bool launch_fails() { return launches++ == fails_at; }
+bool capturing = false;
 int failed = 0;
 void expect(bool ok, const char* what, int at) {
   if (!ok) std::printf("launch %d fails: %s\n", at, what), ++failed;
@@ -24,7 +25,11 @@ cudaError_t cudaMalloc(void**, size_t) { return cudaErrorMemoryAllocation; }
 cudaError_t cudaFree(void*) { return cudaSuccess; }
 cudaError_t cudaMemset(void*, int, size_t) { return cudaSuccess; }
 cudaError_t cudaEventRecordWithFlags(cudaEvent_t, cudaStream_t, unsigned) { return cudaSuccess; }
-cudaError_t cudaStreamIsCapturing(cudaStream_t, cudaStreamCaptureStatus* s) { return *s = cudaStreamCaptureStatusNone, cudaSuccess; }
+cudaError_t cudaStreamIsCapturing(cudaStream_t, cudaStreamCaptureStatus* s) {
+  *s = capturing ? cudaStreamCaptureStatusActive : cudaStreamCaptureStatusNone;
+  return cudaSuccess;
+}
+cudaError_t cudaGetLastError() { return cudaSuccess; }
 }
 
 namespace oscar {
@@ -109,6 +114,15 @@ int main() {
     expect(holds(table), "a page is lost", fails_at);
   }
   fails_at = -1;
+  // a stream that is being captured: refused, before anything changes
+  const int32_t dst[2] = {1, 3};
+  std::vector<int32_t> rows(2 * kPages);
+  capturing = true;
+  expect(compact() == OSCAR_ERR_INVALID && launches == 0 && table == table0, "a captured compaction", -1);
+  for (int n : {2 * 16, 2 * 16 + 5})
+    expect(oscar_kv8_fork(&ctx, table.data(), n, 0, dst, 2, rows.data(), nullptr) == OSCAR_ERR_INVALID && launches == 0, "a captured fork", -1);
+  expect(ctx.refcount == refs0 && ctx.free_stack == free0, "the allocator after captures", -1);
+  capturing = false;
   expect(compact() == OSCAR_OK && live == kLive && launches == 2 * kLists, "the call after the failures", -1);
   bool right = (int)ctx.free_stack.size() == kPages - kLive;
   for (size_t e = 0; e + 1 < table0.size(); ++e)
@@ -116,8 +130,6 @@ int main() {
   expect(right && holds(table), "the table after the call", -1);
   // a fork whose copy fails leaves the refcounts as they were
   const std::vector<int> refs = ctx.refcount;
-  const int32_t dst[2] = {1, 3};
-  std::vector<int32_t> rows(2 * kPages);
   launches = fails_at = 0;
   expect(oscar_kv8_fork(&ctx, table.data(), 16 * 20 + 5, 0, dst, 2, rows.data(), nullptr) == OSCAR_ERR_CUDA, "no error of the fork", 0);
   expect(ctx.refcount == refs, "the fork's refcounts", 0);

@@ -928,6 +928,28 @@ def test_graphs_streams_and_shared_workspace(osc):
         assert r.status() == 0
 
 
+def test_page_moves_are_refused_during_capture(osc):
+    """The allocator changes at the call, so neither can be part of a graph; the capture goes on."""
+    with Rig(osc, O.INT8, layers=2, layer=0) as r:
+        src = osc.oscar_alloc_pages(r.ctx, 5)
+        osc.oscar_unref_pages(r.ctx, src[:2])
+        t, x = dev([src[2:]]), torch.zeros(4, device="cuda")
+        x.add_(1)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            x.add_(1)
+            for n in (16, 20):
+                with pytest.raises(osc.OscarError, match="captured"):
+                    osc.oscar_kv8_fork(r.ctx, src[2:], n, 0, [1], 12)
+            with pytest.raises(osc.OscarError, match="captured"):
+                osc.oscar_compact_pages(r.ctx, t, 1, 3, 48)
+        graph.replay()
+        assert torch.all(x == 2) and t.tolist() == [src[2:]]
+        assert [osc.oscar_page_refcount(r.ctx, p) for p in src] == [0, 0, 1, 1, 1]
+        osc.oscar_kv8_fork(r.ctx, src[2:], 20, 0, [1], 12)
+        assert osc.oscar_compact_pages(r.ctx, t, 1, 3, 48)[1] == 3 and sorted(t[0].tolist()) == [0, 1, 2] and r.status() == 0
+
+
 def test_offsets_past_32_bits(osc):
     """A pool of 4.7 GB: pages at its end are written, read, selected and moved."""
     rng = np.random.default_rng(43)
