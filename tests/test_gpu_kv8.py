@@ -928,6 +928,25 @@ def test_graphs_streams_and_shared_workspace(osc):
         assert r.status() == 0
 
 
+def test_outputs_repeat_bit_for_bit(osc):
+    """The same call gives the same bits, wherever its request lies in a batch: nothing is summed in the order of arrival."""
+    rng = np.random.default_rng(61)
+    lens = [16 * 150 + 3] * 3
+    rig, bt, slots = filled(osc, rng, lens, fmt=1, G=8, per_req=151, pages=460)
+    with rig as r:
+        q = np.tile(acts(rng, (1, 16, 64), False), (3, 1, 1))
+        pages = r.select(q, 0, bt, lens, 1, 1, 40)
+        for idx in (None, pages):
+            first = r.decode(q, 0, 0, bt, lens, slots, pages=idx)
+            for _ in range(5):
+                assert torch.equal(r.decode(q, 0, 0, bt, lens, slots, pages=idx), first)
+            turned = r.decode(q, 0, 0, bt[[2, 0, 1]], lens, slots[[2, 0, 1]], pages=None if idx is None else idx[[2, 0, 1]].contiguous())
+            assert torch.equal(turned, first[[2, 0, 1]])
+        for _ in range(5):
+            assert torch.equal(r.select(q, 0, bt, lens, 1, 1, 40), pages)
+        assert r.status() == 0
+
+
 def test_page_moves_are_refused_during_capture(osc):
     """The allocator changes at the call, so neither can be part of a graph; the capture goes on."""
     with Rig(osc, O.INT8, layers=2, layer=0) as r:
