@@ -400,10 +400,13 @@ oscar_status oscar_bf16_decode_attn(oscar_ctx* ctx, int32_t layer, const void* b
                                     void* workspace, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------- 8-bit cache
- * A paged cache at 8 bits beside the INT2 one, for layers or models that need more
+ * A paged cache at 8 bits beside the INT2 one, for requests or models that need more
  * than 2 bits (no rotation, no clip threshold), with its own attention calls.  It
  * shares the context's page allocator and block tables: page id p addresses block p
- * of the 8-bit pool as it does in the INT2 pool.
+ * of the 8-bit pool as it does in the INT2 pool.  Its pool spans every layer of the
+ * context, and a fork carries a request in one of the two caches: a model that keeps
+ * some layers at 2 bits and others at 8 takes a context for each kind, with page ids
+ * of its own.
  *
  * Tokens.  Page j of a request holds tokens j*P .. j*P + P-1.  A page is quantised
  * when its last token arrives; the n % P tokens of the page that is not complete yet
@@ -433,8 +436,8 @@ oscar_status oscar_bf16_decode_attn(oscar_ctx* ctx, int32_t layer, const void* b
  * row t mod P.
  *
  * Row arguments (K, V, q) have heads x d adjacent elements per token and a stride in
- * elements between tokens (a slice of a wider projection needs no copy; 0: adjacent
- * tokens); the address and the stride in bytes must be multiples of 16.  Every kernel call must be made
+ * elements between tokens, heads x d at least (a slice of a wider projection needs no copy;
+ * 0: adjacent tokens, not one row for all of them); the address and the stride in bytes must be multiples of 16.  Every kernel call must be made
  * with the device current on which the buffers were bound (else OSCAR_ERR_INVALID),
  * takes at most 65535 requests (else OSCAR_ERR_UNSUPPORTED), needs no allocation and
  * can be captured into a graph (after one such call outside a capture).  Requests of one
@@ -541,7 +544,8 @@ oscar_status oscar_kv8_fork(oscar_ctx* ctx, const int32_t* src_bt, int32_t n, in
 
 /* Move the allocated pages down to ids [0, live), live = pages in use, so that the rest of
  * the pools holds nothing: every allocated page with an id >= live moves to a free id below,
- * in every layer of the INT2 pool and of the bound 8-bit pool.  block_table [rows][bt_stride]
+ * in every layer of the INT2 pool and of the bound 8-bit pool (not of a caller's BF16
+ * comparison pool).  block_table [rows][bt_stride]
  * (device int32, adjacent rows; rows = 0 for none) is rewritten to the new ids; out_map [num_pages]
  * (host) gives every page's new id (-1 for a free one) for block tables on the host, and
  * *out_live receives live.  Refcounts move with their pages, and fresh pages are handed out from

@@ -23,8 +23,8 @@
 //
 // Measured (8 kv heads of 128 channels, pages of 64, layers larger than L2): batch 1 at 32K, INT8, 4 heads a kv head 16.9 us
 // (67 MB, 0.59 of the measured copy bandwidth: the start, the end and the merge take 7 us); 64 requests of 8K to 32K, E4M3,
-// 8 heads a kv head 430 us (2.7 GB, 0.92).  At d = 64 instructions count as much as bytes (0.82 with up to four heads a kv
-// head, 0.70 with eight).  Not kept, at the 64 requests: CTAs that stay and take one split after another through the same
+// 8 heads a kv head 434 us (2.7 GB, 0.91).  32 requests of 8K to 16K at d = 64: 0.75 to 0.81 with up to four heads a kv head,
+// 0.66 to 0.71 with eight; with pages of 16, half again as many instructions a byte, 0.62 to 0.68 and 0.55 to 0.59.  Not kept, at the 64 requests: CTAs that stay and take one split after another through the same
 // ring, the next split's pages ahead (468 us: the warps wait at every split's end); four CTAs an SM with three stages
 // (531); two with six (451); a rescaling of the sums only where a maximum moved (434).
 #include "kv8.cuh"

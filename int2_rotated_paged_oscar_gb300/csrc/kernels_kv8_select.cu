@@ -2,8 +2,9 @@
 //
 //   U_p = scale_p sum_c (a_c hi_pc - b_c lo_pc),  a = sum_h max(q_h, 0),  b = sum_h max(-q_h, 0)
 //
-// over the heads h that share a kv head, and of the pages the n_select largest, equal ones by the lower
-// index.  It reads 2 d + 4 bytes per page and kv head, 1 / P of what dense attention reads, so latency
+// over the heads h that share a kv head (scoring pages by their channels' smallest and largest keys is the method of Tang et
+// al., "Quest: Query-Aware Sparsity for Efficient Long-Context LLM Inference", 2024), and of the pages the n_select largest,
+// equal ones by the lower index.  It reads 2 d + 4 bytes per page and kv head, 1 / P of what dense attention reads, so latency
 // decides: a score kernel over all pages and a pick kernel per (request, kv head).
 //
 // A score is a product of a page's 2 d codes (exact f16 numbers) with one vector per (request, kv head), taken on the
