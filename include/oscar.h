@@ -530,6 +530,26 @@ oscar_status oscar_kv8_sparse_decode_attn(oscar_ctx* ctx, int32_t layer, const v
                                           const int32_t* seq_lens, const int32_t* req_slot, int32_t batch,
                                           void* workspace, size_t ws_bytes, void* stream);
 
+/* Decode attention of requests that share a prefix: what oscar_kv8_decode_attn returns, with the shared pages of a
+ * group read once for all of its requests (samples or beams of one prompt, conversations behind one
+ * system prompt).  Group i holds requests group_starts[i] .. group_starts[i + 1] - 1 of the batch, and the first
+ * shared_pages[i] entries of their block-table rows are the same pages (forks of n tokens share n / P).
+ * group_starts [n_groups + 1], from 0 to batch, and shared_pages [n_groups]: device int32; a group may hold one
+ * request or none, and share no page.  A group's shared pages are found through the row of its first request that
+ * is not empty.  max_shared (pages) bounds shared_pages and max_own (tokens) what the requests hold behind them
+ * (host values, they size the grids and the workspace); the other arguments as for
+ * oscar_kv8_decode_attn.  A request of length 0 (a padded batch) gets zeros; one that no group holds, that is shorter
+ * than its group's shared pages or beyond the bounds gets zeros and sets OSCAR_DEV_BAD_LEN; a page that is not
+ * mapped is left out and sets OSCAR_DEV_BAD_PAGE. */
+oscar_status oscar_kv8_shared_workspace_size(const oscar_config* cfg, int32_t batch, int32_t n_groups, int32_t max_shared,
+                                             int32_t max_own, size_t* bytes);
+oscar_status oscar_kv8_shared_decode_attn(oscar_ctx* ctx, int32_t layer, const void* q, int64_t q_stride, int32_t q_dtype,
+                                          void* out, int32_t out_dtype, const int32_t* group_starts,
+                                          const int32_t* shared_pages, int32_t n_groups, int32_t max_shared,
+                                          const int32_t* block_table, int32_t bt_stride, const int32_t* seq_lens,
+                                          const int32_t* req_slot, int32_t batch, int32_t max_own, void* workspace,
+                                          size_t ws_bytes, void* stream);
+
 /* Fork n_dst requests off request src at its current length n in the 8-bit cache (parallel
  * sampling, beams, a shared prompt).  Host arrays: src_bt (n / P entries are read), dst_slots
  * [n_dst] (distinct, not src_slot), dst_bt [n_dst][max_pages_per_req] (written; unused entries
@@ -541,6 +561,43 @@ oscar_status oscar_kv8_sparse_decode_attn(oscar_ctx* ctx, int32_t layer, const v
  * forked keeps its tokens in one of the two caches. */
 oscar_status oscar_kv8_fork(oscar_ctx* ctx, const int32_t* src_bt, int32_t n, int32_t src_slot,
                             const int32_t* dst_slots, int32_t n_dst, int32_t* dst_bt, void* stream);
+
+/* The states of beams after a selection: request b * beams + j of the new batch continues request
+ * b * beams + parents[b][j] of the old one (1 <= beams <= 64; -1: an empty request, of length 0 and with a row of -1).
+ * new_block_table [batch * beams][bt_stride] and new_seq_lens [batch * beams] receive the parents' rows and lengths.
+ * new_req_slot: a parent's first child (the lowest j) keeps its slot; every other beam, in ascending order of j,
+ * takes the slot of an old beam without a child, in ascending order of those, and unless it is empty
+ * its parent's seq_lens mod P tail rows are copied there in every layer (other rows of the slab stay as they are).  So
+ * an item's slots are the same ones before and after, and a beam's tail moves only if its parent has
+ * several children.  All arguments are device int32 and the outputs must not overlap the inputs.  A parent out of
+ * range counts as -1 and sets OSCAR_DEV_BAD_SLOT; so does a slot out of range, whose rows are not copied; a length out
+ * of range sets OSCAR_DEV_BAD_LEN and its rows are not copied.  The call can be captured into a graph: it does not touch
+ * the page allocator, whose refcounts follow with oscar_ref_pages of the parent's pages for every further child and
+ * oscar_unref_pages of the pages of every beam without one, before the next page is allocated. */
+oscar_status oscar_kv8_reorder(oscar_ctx* ctx, const int32_t* parents, int32_t batch, int32_t beams, const int32_t* block_table,
+                               int32_t bt_stride, const int32_t* seq_lens, const int32_t* req_slot, int32_t* new_block_table,
+                               int32_t* new_seq_lens, int32_t* new_req_slot, void* stream);
+
+/* The next beams of a beam search.  Candidate (i, v) of a batch item continues beam i with token v and has
+ *     key = scores[i] + ((x_v - m) - log sum_u e^(x_u - m)),  x = logits[i], m = max x,
+ * the sum of log probabilities so far.  The n_out candidates of the largest keys, in descending order and the
+ * lowest i * vocab + v first among equal ones: out_scores [batch][n_out] (float32 keys), out_tokens (v) and
+ * out_parents (i, as oscar_kv8_reorder takes them), both int32.
+ *  logits: rows [batch][beams][vocab] of dtype (BF16 or F32), row_stride elements apart (0: adjacent) and aligned to
+ *  their elements only (16-byte aligned rows are read fastest).  scores: [batch][beams] float32; a beam at -infinity has no
+ *  candidates (beams 1 .. of a first step).  finished [batch][beams] (bytes; NULL: none): a beam that is not 0 there has one candidate,
+ *  (i, pad_token) with its score unchanged, and its logits are not read.
+ * A candidate at -infinity (a masked token) is never taken: where there are fewer than n_out others,
+ * the rest of the outputs is -infinity, -1, -1.  A NaN or +infinity among a beam's logits or as its score
+ * leaves the beam out and sets OSCAR_DEV_BAD_VALUE.  Exponentials and their sums are float32's (the normaliser is good to
+ * 10^-6): candidates of different beams whose keys differ by less may come in either order; equal rows and scores
+ * are equal.  1 <= beams, n_out <= 64, vocab <= 2^24.  The context is any one with device buffers; the workspace's
+ * rules are those of the 8-bit cache's calls, the outputs must not overlap the inputs. */
+oscar_status oscar_beam_select_workspace_size(int32_t batch, int32_t beams, int32_t vocab, int32_t n_out, size_t* bytes);
+oscar_status oscar_beam_select(oscar_ctx* ctx, const void* logits, int64_t row_stride, int32_t dtype, const float* scores,
+                               const uint8_t* finished, int32_t pad_token, int32_t batch, int32_t beams, int32_t vocab,
+                               int32_t n_out, float* out_scores, int32_t* out_tokens, int32_t* out_parents, void* workspace,
+                               size_t ws_bytes, void* stream);
 
 /* Move the allocated pages down to ids [0, live), live = pages in use, so that the rest of
  * the pools holds nothing: every allocated page with an id >= live moves to a free id below,
@@ -591,7 +648,7 @@ oscar_status oscar_set_decode_form(oscar_ctx* ctx, int32_t form);
  * "decode_combine", "q_rotate", "step_prep", "append", "evict", "write", "bf16_prepare",
  * "bf16_decode", "bf16_combine", "extend", "selftest", "kv8_write", "kv8_append", "kv8_decode",
  * "kv8_combine" (not launched for contexts or selections of up to 512 tokens, 1024 at d = 64
- * and P >= 32), "kv8_select", "kv8_fork", "copy_pages", "remap_table".  Launches recorded into a CUDA graph get external event-record nodes: replay the graph
+ * and P >= 32), "kv8_select", "kv8_fork", "kv8_prefix", "kv8_reorder", "beam_chunks", "beam_pick", "copy_pages", "remap_table".  Launches recorded into a CUDA graph get external event-record nodes: replay the graph
  * once, then read; the events return to the library when read, so a graph
  * captured with timing on is replayed at most once.  With timing on, the decode
  * kernels are launched without programmatic dependent launch. */

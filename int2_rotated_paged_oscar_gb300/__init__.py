@@ -112,6 +112,13 @@ _SIGS = {
     "oscar_kv8_sparse_workspace_size": (_i32, [_cfgp, _i32, _i32, _szp]),
     "oscar_kv8_sparse_decode_attn": (_i32, [_vp, _i32, _vp, _i64, _i32, _vp, _i32, _vp, _i32, _vp, _i32, _vp, _vp,
                                             _i32, _vp, ctypes.c_size_t, _vp]),
+    "oscar_kv8_shared_workspace_size": (_i32, [_cfgp, _i32, _i32, _i32, _i32, _szp]),
+    "oscar_kv8_shared_decode_attn": (_i32, [_vp, _i32, _vp, _i64, _i32, _vp, _i32, _vp, _vp, _i32, _i32, _vp, _i32, _vp, _vp,
+                                            _i32, _i32, _vp, ctypes.c_size_t, _vp]),
+    "oscar_kv8_reorder": (_i32, [_vp, _vp, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "oscar_beam_select_workspace_size": (_i32, [_i32, _i32, _i32, _i32, _szp]),
+    "oscar_beam_select": (_i32, [_vp, _vp, _i64, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp,
+                                 ctypes.c_size_t, _vp]),
     "oscar_kv8_fork": (_i32, [_vp, _vp, _i32, _i32, _vp, _i32, _vp, _vp]),
     "oscar_compact_pages": (_i32, [_vp, _vp, _i32, _i32, _vp, _c_i32p, _vp]),
     "oscar_selftest_wait_timeout": (_i32, [_vp, _i32, _vp]),
@@ -540,6 +547,80 @@ def oscar_kv8_sparse_decode_attn(ctx, layer, q, q_dtype, out, out_dtype, page_id
                                                _dense(seq_lens, "seq_lens", dev, batch), _dense(req_slot, "req_slot", dev, batch),
                                                batch, _dense(workspace, "workspace", dev, ws_bytes, None), ws_bytes,
                                                stream_ptr(stream)))
+
+
+def oscar_kv8_shared_workspace_size(cfg: oscar_config, batch: int, n_groups: int, max_shared: int, max_own: int) -> int:
+    out = ctypes.c_size_t()
+    _check(load().oscar_kv8_shared_workspace_size(ctypes.byref(cfg), batch, n_groups, max_shared, max_own, ctypes.byref(out)))
+    return out.value
+
+
+def oscar_kv8_shared_decode_attn(ctx, layer, q, q_dtype, out, out_dtype, group_starts, shared_pages, n_groups, max_shared,
+                                 block_table, bt_stride, seq_lens, req_slot, batch, max_own, workspace, ws_bytes,
+                                 stream=None) -> None:
+    cfg = _config(ctx)
+    dev, hq, d = cfg.device, cfg.n_q_heads, cfg.head_dim
+    qp, qs = _rows(q, "q", dev, q_dtype, batch, hq, d)
+    _check(load().oscar_kv8_shared_decode_attn(ctx, layer, qp, qs, q_dtype, _dense(out, "out", dev, batch * hq * d, out_dtype),
+                                               out_dtype, _dense(group_starts, "group_starts", dev, n_groups + 1),
+                                               _dense(shared_pages, "shared_pages", dev, n_groups), n_groups, max_shared,
+                                               _dense(block_table, "block_table", dev, batch * bt_stride), bt_stride,
+                                               _dense(seq_lens, "seq_lens", dev, batch), _dense(req_slot, "req_slot", dev, batch),
+                                               batch, max_own, _dense(workspace, "workspace", dev, ws_bytes, None), ws_bytes,
+                                               stream_ptr(stream)))
+
+
+def oscar_kv8_reorder(ctx, parents, batch, beams, block_table, bt_stride, seq_lens, req_slot, new_block_table, new_seq_lens,
+                      new_req_slot, stream=None) -> None:
+    dev = _config(ctx).device
+    rows = batch * beams
+    _check(load().oscar_kv8_reorder(ctx, _dense(parents, "parents", dev, rows), batch, beams,
+                                    _dense(block_table, "block_table", dev, rows * bt_stride), bt_stride,
+                                    _dense(seq_lens, "seq_lens", dev, rows), _dense(req_slot, "req_slot", dev, rows),
+                                    _dense(new_block_table, "new_block_table", dev, rows * bt_stride),
+                                    _dense(new_seq_lens, "new_seq_lens", dev, rows),
+                                    _dense(new_req_slot, "new_req_slot", dev, rows), stream_ptr(stream)))
+
+
+def oscar_beam_select_workspace_size(batch: int, beams: int, vocab: int, n_out: int) -> int:
+    out = ctypes.c_size_t()
+    _check(load().oscar_beam_select_workspace_size(batch, beams, vocab, n_out, ctypes.byref(out)))
+    return out.value
+
+
+def _logits(x, device: Optional[int], dtype: int, batch: int, beams: int, vocab: int):
+    """(address, elements between rows) of [batch][beams][vocab] or [batch * beams][vocab] logits."""
+    if x is None or isinstance(x, int):
+        return x, 0
+    shape, stride = tuple(x.shape), tuple(x.stride())
+    if len(shape) == 3 and (shape[0] <= 1 or shape[1] <= 1 or stride[0] == shape[1] * stride[1]):
+        step = stride[1] if shape[1] > 1 else stride[0]
+        shape, stride = (shape[0] * shape[1], shape[2]), (step, stride[2])
+    if len(shape) != 2 or shape[0] < batch * beams or shape[1] != vocab or x.dtype is not (_torch_types or _types()).get(dtype, x.dtype) \
+            or not (x.get_device() == device or device is None and x.is_cuda):
+        raise OscarError(ERR_INVALID, f"logits must be [{batch}][{beams}][{vocab}] of {_types().get(dtype)} in evenly spaced rows on "
+                                      f"CUDA device {'' if device is None else device}, not {x.dtype} {tuple(x.shape)} on "
+                                      f"{x.device} with strides {tuple(x.stride())}")
+    if vocab > 1 and stride[1] != 1 or shape[0] > 1 and stride[0] < vocab:
+        raise OscarError(ERR_INVALID, f"the logits of a row must be adjacent and rows at least {vocab} elements apart, not strided "
+                                      f"{tuple(x.stride())}")
+    return x.data_ptr(), stride[0] if shape[0] > 1 else 0
+
+
+def oscar_beam_select(ctx, logits, dtype, scores, finished, pad_token, batch, beams, vocab, n_out, out_scores, out_tokens,
+                      out_parents, workspace, ws_bytes, stream=None) -> None:
+    """The next beams; finished is a uint8 or bool tensor of batch * beams elements, or None."""
+    cfg = _config(ctx)
+    dev = _current_device(logits, scores) if cfg.device is None else cfg.device
+    lp, ls = _logits(logits, dev, dtype, batch, beams, vocab)
+    if getattr(finished, "element_size", lambda: 1)() != 1:
+        raise OscarError(ERR_INVALID, f"finished must have elements of one byte, not {finished.dtype}")
+    _check(load().oscar_beam_select(ctx, lp, ls, dtype, _dense(scores, "scores", dev, batch * beams, DTYPE_F32),
+                                    _dense(finished, "finished", dev, batch * beams, None), pad_token, batch, beams, vocab, n_out,
+                                    _dense(out_scores, "out_scores", dev, batch * n_out, DTYPE_F32),
+                                    _dense(out_tokens, "out_tokens", dev, batch * n_out),
+                                    _dense(out_parents, "out_parents", dev, batch * n_out),
+                                    _dense(workspace, "workspace", dev, ws_bytes, None), ws_bytes, stream_ptr(stream)))
 
 
 def oscar_kv8_fork(ctx: int, src_bt: Sequence[int], n: int, src_slot: int, dst_slots: Sequence[int], max_pages: int,

@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, (Layout<D, NB, G8>::kResident)) kv8_
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = g.gq(), P = g.P;
   const int per_stage = L::kTokens / P;
-  const int e0 = split * a.wl.stages_per_split * per_stage;
+  int e0 = split * a.wl.stages_per_split * per_stage;
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
@@ -319,6 +319,11 @@ __global__ void __launch_bounds__(kThreads, (Layout<D, NB, G8>::kResident)) kv8_
   pdl_wait();
   pdl_launch_dependents();
   const int n = a.seq_lens[b];
+  int first = 0;                                        // pages of the request that the prefix kernel reads
+  if (a.groups.n) {
+    first = kv8_shared_of(a, b);
+    e0 += max(first, 0);
+  }
   // the producer's first table entries travel with the length
   const int* bt = a.block_table + (size_t)b * a.bt_stride;
   const int* list = a.page_idx ? a.page_idx + ((size_t)b * g.Hkv + h) * a.n_select : nullptr;
@@ -332,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, (Layout<D, NB, G8>::kResident)) kv8_
       early = e < a.bt_stride ? bt[e] : -1;
     }
   }
-  const bool sound = length_ok(a, n);
+  const bool sound = a.groups.n ? n == 0 || kv8_own_sound(a, n, first) : length_ok(a, n);
   if (!sound && tid == 0 && split == 0) flag_error(a.status, kDevBadLen);
   if (!sound || n == 0) {
     if (a.wl.max_splits == 1)  // (else the merge writes the zeros)
@@ -341,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, (Layout<D, NB, G8>::kResident)) kv8_
   }
   const int pages = n / P;
   const int have = a.page_idx ? a.n_select : pages;
-  const int splits = split_count(a, have);
+  const int splits = split_count(a, have - first);
   if (split >= splits) return;
   const int e1 = min(e0 + a.wl.stages_per_split * per_stage, have);
   const int stages = (e1 - e0 + per_stage - 1) / per_stage;
@@ -673,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, (Layout<D, NB, G8>::kResident)) kv8_
       store_out(a, ((size_t)b * g.Hq + h * G + hh) * D + ch, l == 0.f ? 0.f : o / l);
       continue;
     }
-    float* pp = partial(a, b, h * G + hh, split, D);
+    float* pp = partial(a, b, h * G + hh, a.groups.slots + split, D);
     pp[4 + ch] = o;
     if (ch == 0) {
       pp[0] = l == l ? M : INFINITY;  // the merge takes no partial at -infinity: a NaN must not look like one
@@ -695,7 +700,17 @@ __global__ void __launch_bounds__(32 * W) kv8_combine_kernel(const __grid_consta
   const Geom& g = a.g;
   const int head = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int n = a.seq_lens[b];
-  const int count = length_ok(a, n) && n > 0 ? split_count(a, a.page_idx ? a.n_select : n / g.P) : 0;
+  int count = 0, gap_at = 0x7fffffff, gap = 0;          // partials from gap_at on lie gap places further on
+  if (a.groups.n) {
+    const int first = kv8_shared_of(a, b);
+    if (n > 0 && kv8_own_sound(a, n, first)) {
+      gap_at = kv8_prefix_splits(a, first);
+      gap = a.groups.slots - gap_at;
+      count = gap_at + split_count(a, n / g.P - first);
+    }
+  } else if (length_ok(a, n) && n > 0) {
+    count = split_count(a, a.page_idx ? a.n_select : n / g.P);
+  }
   const float* base = partial(a, b, head, 0, D);
   pdl_wait();
   pdl_launch_dependents();
@@ -707,7 +722,8 @@ __global__ void __launch_bounds__(32 * W) kv8_combine_kernel(const __grid_consta
     float v[N][C];
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      const float* p = base + (size_t)min(i0 + k * W, count - 1) * (D + 4);
+      const int at = min(i0 + k * W, count - 1);
+      const float* p = base + (size_t)(at >= gap_at ? at + gap : at) * (D + 4);
       ml[k] = *reinterpret_cast<const float2*>(p);
       if constexpr (C == 4) {
         const float4 x = *reinterpret_cast<const float4*>(p + 4 + lane * 4);
@@ -757,7 +773,7 @@ __global__ void __launch_bounds__(32 * W) kv8_combine_kernel(const __grid_consta
 
 template <int D, int FMT, int NB>
 int launch_pages(const Kv8DecodeArgs& a, cudaStream_t s, bool pdl) {
-  const dim3 grid(a.wl.max_splits, a.g.Hkv, a.batch);
+  const dim3 grid(a.splits, a.g.Hkv, a.batch);
   const size_t smem = a.g.gq() == 8 ? Layout<D, NB, true>::smem(a.g.P) : Layout<D, NB, false>::smem(a.g.P);
   auto go = [&](auto kern) {
     const cudaError_t e = ensure_smem_limit(kern, smem, true);

@@ -70,4 +70,28 @@ __device__ __forceinline__ float kv8_load(const void* p, size_t i, int dtype) {
   return static_cast<const float*>(p)[i];
 }
 
+// ------------------------------------------------------------------ requests in groups
+// Whether length n >= 0 of request b, in a group with `shared` shared pages, is one that the call allows.
+__device__ __forceinline__ bool kv8_own_sound(const Kv8DecodeArgs& a, int n, int shared) {
+  const long long own = n - (long long)shared * a.g.P;
+  return shared >= 0 && shared <= a.groups.max_shared && own >= 0 && own <= a.groups.max_own &&
+         n <= (long long)a.g.max_pages_per_req * a.g.P;
+}
+
+// Group of request b and its shared pages, found by a whole warp; -1 where the groups do not hold it.
+__device__ __forceinline__ int kv8_shared_of(const Kv8DecodeArgs& a, int b) {
+  int c = 0;
+  for (int i = threadIdx.x & 31; i < a.groups.n; i += 32) c += a.groups.starts[i] <= b;
+  const int at = __reduce_add_sync(0xffffffffu, c) - 1;
+  if (at < 0) return -1;
+  const int lo = a.groups.starts[at], hi = a.groups.starts[at + 1], s = a.groups.shared[at];
+  return lo >= 0 && lo <= b && b < hi && hi <= a.batch ? s : -1;
+}
+
+// Prefix partials of a row whose group shares s pages.
+__device__ __forceinline__ int kv8_prefix_splits(const Kv8DecodeArgs& a, int s) {
+  const int per = a.groups.units_per_split * (kPrefixUnit / a.g.P);
+  return (s + per - 1) / per;
+}
+
 }  // namespace oscar

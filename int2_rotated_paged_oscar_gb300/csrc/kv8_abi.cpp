@@ -3,10 +3,13 @@
 #include <new>
 #include <vector>
 
-#include "kv8_internal.h"
-#include "oscar_ctx.h"
+#include "kv8_checks.h"
 
+using oscar::check_batch;
+using oscar::check_device;
 using oscar::check_layer;
+using oscar::check_query;
+using oscar::check_rows;
 using oscar::check_workspace;
 using oscar::cuda_fail;
 using oscar::fail;
@@ -15,21 +18,10 @@ using oscar::Kv8DecodeArgs;
 using oscar::Kv8SelectArgs;
 using oscar::Kv8WriteArgs;
 using oscar::LaunchScope;
+using oscar::need_kv8;
 using oscar::validate;
 
 namespace {
-
-constexpr int kMaxGrid = 65535;  // of the grid's second and third dimension
-
-// The buffers were bound on one device and the kernels run on the current one.
-oscar_status check_device(const oscar_ctx* ctx) {
-  int dev = 0;
-  const cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return cuda_fail(e, "current device");
-  if (dev != ctx->device)
-    return fail(OSCAR_ERR_INVALID, "the context's buffers are on device %d, the current device is %d", ctx->device, dev);
-  return OSCAR_OK;
-}
 
 // The allocator changes at the call: a captured one would move pages by an old plan at every replay.
 oscar_status check_not_capturing(void* stream, const char* name) {
@@ -39,32 +31,6 @@ oscar_status check_not_capturing(void* stream, const char* name) {
     return OSCAR_OK;
   }
   if (cs != cudaStreamCaptureStatusNone) return fail(OSCAR_ERR_INVALID, "%s cannot be captured into a graph", name);
-  return OSCAR_OK;
-}
-
-oscar_status need_kv8(oscar_ctx* ctx) {
-  if (!ctx) return fail(OSCAR_ERR_INVALID, "context is null");
-  if (!ctx->kv8_pool) return fail(OSCAR_ERR_INVALID, "no 8-bit cache is bound to the context (oscar_kv8_bind)");
-  return check_device(ctx);
-}
-
-// Rows of heads x d elements, *stride elements apart (0: adjacent), read in 16-byte vectors.
-oscar_status check_rows(const char* name, const void* p, int64_t* stride, int heads, int d, int dtype) {
-  if (*stride == 0) *stride = (int64_t)heads * d;
-  const long long row_stride = *stride;
-  if (dtype != OSCAR_DTYPE_BF16 && dtype != OSCAR_DTYPE_F32) return fail(OSCAR_ERR_INVALID, "bad dtype %d of %s", dtype, name);
-  const long long elem = dtype == OSCAR_DTYPE_BF16 ? 2 : 4;
-  if (!p) return fail(OSCAR_ERR_INVALID, "%s is null", name);
-  if (row_stride < (long long)heads * d)
-    return fail(OSCAR_ERR_INVALID, "row stride %lld of %s is below the row's %d elements", row_stride, name, heads * d);
-  if ((reinterpret_cast<uintptr_t>(p) & 15) || (row_stride * elem) % 16)
-    return fail(OSCAR_ERR_INVALID, "%s and its row stride must be 16-byte aligned", name);
-  return OSCAR_OK;
-}
-
-oscar_status check_batch(int32_t batch, int32_t bt_stride) {
-  if (batch < 0 || bt_stride < 1) return fail(OSCAR_ERR_INVALID, "bad batch/bt_stride");
-  if (batch > kMaxGrid) return fail(OSCAR_ERR_UNSUPPORTED, "batch %d exceeds %d", batch, kMaxGrid);
   return OSCAR_OK;
 }
 
@@ -116,18 +82,6 @@ oscar_status check_select(int32_t n_select) {
   return OSCAR_OK;
 }
 
-// What the two attention calls and the selection have in common.
-oscar_status check_query(oscar_ctx* ctx, int32_t layer, const void* q, int64_t* q_stride, int32_t q_dtype,
-                         const int32_t* block_table, int32_t bt_stride, const int32_t* seq_lens, int32_t batch) {
-  oscar_status st = need_kv8(ctx);
-  if (st != OSCAR_OK) return st;
-  if ((st = check_layer(ctx, layer)) != OSCAR_OK) return st;
-  if ((st = check_batch(batch, bt_stride)) != OSCAR_OK) return st;
-  if (batch == 0) return OSCAR_OK;
-  if (!block_table || !seq_lens) return fail(OSCAR_ERR_INVALID, "null tensor argument");
-  return check_rows("q", q, q_stride, ctx->g.Hq, ctx->g.D, q_dtype);
-}
-
 oscar_status check_max_seq(const oscar_ctx* ctx, int32_t max_seq) {
   if (max_seq < 0) return fail(OSCAR_ERR_INVALID, "max_seq %d is negative", max_seq);
   if ((long long)max_seq > (long long)ctx->g.max_pages_per_req * ctx->g.P)
@@ -166,6 +120,7 @@ oscar_status attend(oscar_ctx* ctx, int32_t layer, const void* q, int64_t q_stri
   a.status = ctx->d_status;
   a.part = static_cast<float*>(workspace);
   a.wl = oscar::kv8_plan(ctx->g, batch, page_idx ? n_select : max_seq / ctx->g.P);
+  a.splits = a.wl.max_splits;
   if (ws_bytes < a.wl.total) return fail(OSCAR_ERR_INVALID, "workspace too small: %zu < %zu bytes", ws_bytes, a.wl.total);
   const bool pdl = !ctx->timing;
   {

@@ -59,6 +59,20 @@ struct Kv8DecodeWs {
   size_t total;          // bytes: partials [batch][Hq][max_splits][D + 4] float32
 };
 
+// Tokens by which the shared pages of a group are split.
+constexpr int kPrefixUnit = 128;
+
+// Requests that share their first pages, group by group (n = 0: none do).
+struct Kv8Groups {
+  const int* starts;             // [n + 1]: group i holds requests starts[i] .. starts[i + 1] - 1
+  const int* shared;             // [n]: pages that a group's requests share
+  int n, max_shared;             // max_shared bounds shared
+  int max_own;                   // bounds the tokens behind them
+  int units_per_split;           // units of tokens of one CTA of the prefix kernel
+  int max_tiles;                 // row tiles of all groups, at most
+  int slots;                     // partials of a row for the prefix: places 0 .. slots - 1
+};
+
 struct Kv8DecodeArgs {
   Geom g;
   int fmt, layer;
@@ -79,6 +93,8 @@ struct Kv8DecodeArgs {
   int* status;
   float* part;
   Kv8DecodeWs wl;
+  Kv8Groups groups;              // the pages before shared[] are another kernel's
+  int splits;                    // CTAs of a request and kv head; wl.max_splits of them, or less where the prefix has places
 };
 
 struct Kv8SelectArgs {
@@ -111,10 +127,13 @@ struct IntPairs {
 };
 
 Kv8DecodeWs kv8_plan(const Geom& g, int batch, long long max_pages);
+// the same for requests in groups: the plan of their own parts, with room for the prefixes' partials
+Kv8DecodeWs kv8_shared_plan(const Geom& g, int batch, int n_groups, int max_shared, int max_own, Kv8Groups* groups, int* own_splits);
 size_t kv8_select_ws_bytes(const Geom& g, int batch, int max_seq);
 
 int launch_kv8_write(const Kv8WriteArgs& a, void* stream, bool pdl);
 int launch_kv8_decode(const Kv8DecodeArgs& a, void* stream, bool pdl);
+int launch_kv8_shared_prefix(const Kv8DecodeArgs& a, void* stream, bool pdl);
 int launch_kv8_combine(const Kv8DecodeArgs& a, void* stream, bool pdl);
 int launch_kv8_select(const Kv8SelectArgs& a, void* stream, bool pdl);
 // rows [0, n_rows) of the src slot's tail to every dst slot (n <= kMostPairs of them), in every layer

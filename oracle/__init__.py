@@ -23,6 +23,8 @@ attention  decode attention over the mixed cache (plain and fused forms) and
            textbook attention over an all-BF16 paged cache.
 kv8        the 8-bit paged cache: its codes, its attention and page selection
            (pinned by ``tests/test_kv8_host.py``).
+beams      the choice of the next beams and the places of their states
+           (pinned by ``tests/test_beams_host.py``).
 
 Pinning status: every function here is pinned by ``tests/test_oracle_pins.py``
 (closed forms, brute force on tiny inputs, invariants).  Two things stay
@@ -30,4 +32,4 @@ Pinning status: every function here is pinned by ``tests/test_oracle_pins.py``
 accuracy benefit of OSCAR's rotation (needs trained weights and datasets) and
 the pages' own kernel outputs.
 """
-from . import rotation, quant, cache, attention, kv8  # noqa: F401
+from . import rotation, quant, cache, attention, kv8, beams  # noqa: F401
