@@ -7,11 +7,12 @@
 // The codes of a page are read once per 128 rows instead of once per 8; 4 d flops per token and row are on the tensor cores
 // (tcgen05), so it is bound by memory up to 128 rows of a kv head and by the tensor cores and the exponentials beyond.
 //
-// Roles in a CTA, around two buffers of a token tile (128 tokens; 64 for float32 queries, whose three terms take the room):
-//   8 warps   codes from global memory through registers, two tiles ahead, to BF16 keys and f16 values in shared memory.  Both
-//             are exact.  Rows are tokens: for S the channels of a row are the contracted dimension, for O the tokens are.
-//   1 warp    issues S(i) and then O += P(i - 1) V(i - 1).
-//   4 warps   a thread per row: S from tensor memory, the running maximum and sum, P to tensor memory.
+// Roles in a CTA, around a ring of token tiles of 64 tokens:
+//   8 warps   codes from global memory through registers, four tiles ahead, to BF16 keys and f16 values in shared memory.  Both
+//             are exact.  Rows are tokens: for S the channels of a row are the contracted dimension, for O the tokens are.  They
+//             issue S(i) in turn.
+//   2 x 4     warps, even and odd tiles, a thread per row: S from tensor memory, the running maximum and sum, P to tensor memory in
+//             the place of S, and one of them issues O += P(i) V(i).  Each half has sums of its own, joined at the end.
 // Queries are BF16 operands as they are (float32 ones sums of three), brought near 2^14 by a power of two.  A score is scaled in
 // the exponent's multiplication by its page's scale, a weight by its page's V scale after it.  Weights are f16: one number (11
 // bits) for BF16 outputs, which are rounded to 8 bits at the end, and two (22 bits) for float32 ones.
@@ -24,34 +25,37 @@ namespace {
 
 #include "tc_common.cuh"
 
-constexpr int kSoft = 4, kConv = 8;                       // warps
-constexpr int kThreads = 32 * (kSoft + kConv + 1);
-constexpr int kRows = 128;
+constexpr int kSoft = 8, kConv = 8;                       // warps
+constexpr int kThreads = 32 * (kSoft + kConv);
+constexpr int kRows = 128, NT = 64, NG = NT / 16;         // rows and tokens of a tile; groups of 16 tokens, each of one page
+constexpr int kAhead = 4;                                 // tiles whose codes are under way
 constexpr int kMostPages = 2048;                          // pages of a split
-// Tensor memory: scores of two tiles, sums, weights.
-constexpr uint32_t kColS = 0, kColO = 256, kColP = 384, kCols = 512;
+// Tensor memory: scores, then weights, of the ring's tiles; sums of the two halves.
+constexpr uint32_t kColS = 0, kColO = 256, kCols = 512;
 // A row's reference exponent follows its maximum when it is kLag behind; V scales are relative to a power of two that follows
 // the largest when it is 2^kScaleLag behind; a weight of 1 at scale 1 is 2^kBase: below 2^(kLag + kScaleLag + 1 + kBase) = 2^15.
 constexpr float kLag = 8.f;
 constexpr int kScaleLag = 3, kBase = 3;
+constexpr float kFar = 4194304.f;                         // scores (log2) whose last place counts
 
 template <int D, bool QF32>
 struct Lay {
-  static constexpr int NT = QF32 ? 64 : 128;              // tokens of a tile
   static constexpr int QT = QF32 ? 3 : 1;                 // BF16 terms of a query
+  static constexpr int NB = QF32 ? 2 : 4;                 // tiles of the ring
   static constexpr int kQ = kRows * D * 2, kKV = NT * D * 2;
-  static constexpr int oQ = 0, oK = oQ + QT * kQ, oV = oK + 2 * kKV, oPages = oV + 2 * kKV;
+  static constexpr int oQ = 0, oK = oQ + QT * kQ, oV = oK + NB * kKV, oPages = oV + NB * kKV;
   static constexpr int kSmem = oPages + kMostPages * 4 + 1024;
   static constexpr int kTasks = NT * D / 16 / (32 * kConv);  // 16-byte chunks of keys (and of values) a thread takes of a tile
 };
 
 struct Shared {
-  uint64_t k_full[2], k_empty[2], v_full[2], sc_full[2], s_full[2], p_full[2], pv_done[2], end;
-  float ks[2][8], vs[2][8];      // per 16 tokens: K scale, V scale relative to 2^E (2^kBase at 1)
-  float ratio[2];                // 2^(the E before - E)
-  int mask[2], e[2];
+  uint64_t k_full[4], v_full[4], sc_full[4], s_full[4], p_full[4], pv_done[4], end;
+  float ks[4][NG], vs[4][NG];    // per 16 tokens: K scale, V scale relative to 2^e (2^kBase at 1)
+  int mask[4], e[4];
+  float m[2][kRows], l[2][kRows];  // of the halves, at the end
+  int e_sum[2];
   uint32_t tmem;
-  int lo, size, shared, tile, holder, abort;
+  int lo, size, shared, tile, holder;
 };
 
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
@@ -81,10 +85,128 @@ __device__ __forceinline__ uint64_t desc_rows(uint32_t saddr, uint32_t across) {
          (uint64_t)2 << 61;
 }
 
-template <int D, int FMT, bool QF32>
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) { return (uint64_t)hi << 32 | lo; }
+__device__ __forceinline__ uint64_t pair(float lo, float hi) { return pair(__float_as_uint(lo), __float_as_uint(hi)); }
+__device__ __forceinline__ float first(uint64_t x) { return __uint_as_float((uint32_t)x); }
+__device__ __forceinline__ float second(uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+
+// Weights of a row's scores in a tile: 2^(score - m) by the page's V scale, as TERMS f16 numbers.  The sum of the weights before
+// the V scale is returned.  A score's scale f = K scale x query scale has a rounding; what it leaves out at a page's largest
+// score goes into the page's weights where they are held to 22 bits.
+template <int TERMS>
+__device__ __forceinline__ float weigh(const uint32_t (&x)[NT], const float (&cm)[NG], const float (&f)[NG], uint32_t at, const float* ks,
+                                       const float* vs, float qs, float qs_lo, float ref) {
+  const uint64_t bias = pair(-ref, -ref);
+  float total = 0.f;
+#pragma unroll
+  for (int c = 0; c < NT / 32; ++c) {
+    uint32_t hi[16], lo[16];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int k = 2 * c + u;
+      float g = vs[k], fix = 1.f;
+      if constexpr (TERMS == 2) {
+        fix = ex2(fminf(cm[k] * fmaf(ks[k], qs_lo, fmaf(ks[k], qs, -f[k])), 1.f));
+        g *= fix;
+      }
+      const uint64_t ff = pair(f[k], f[k]), gg = pair(g, g);
+      uint64_t sum[2] = {0, 0};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint64_t e = fma2(pair(x[32 * c + 16 * u + 2 * j], x[32 * c + 16 * u + 2 * j + 1]), ff, bias);
+        const uint64_t p = pair(ex2(first(e)), ex2(second(e)));
+        sum[j & 1] = add2(sum[j & 1], p);
+        const uint64_t w = mul2(p, gg);
+        hi[8 * u + j] = pack_half2(first(w), second(w));
+        if constexpr (TERMS == 2) {
+          const __half2 h = *reinterpret_cast<const __half2*>(&hi[8 * u + j]);
+          lo[8 * u + j] = pack_half2(first(w) - __low2float(h), second(w) - __high2float(h));
+        }
+      }
+      const uint64_t both = add2(sum[0], sum[1]);
+      total = fmaf(first(both) + second(both), fix, total);
+    }
+    tmem_st16(at + 16 * c, hi);
+    if constexpr (TERMS == 2) tmem_st16(at + NT / 2 + 16 * c, lo);
+  }
+  return total;
+}
+
+// The same where some groups are not there, or some row's scores are so large (kFar) that a last place of one counts: there
+// distances are formed from the raw sums, 0 at a group's largest.  Other rows come out as from weigh, bit for bit.
+template <int TERMS>
+__device__ __noinline__ float weigh_with_care(uint32_t at, const float* ks, const float* vs, float qs, float qs_lo, float ref, int mask) {
+  const bool far = fabsf(ref) >= kFar;
+  float total = 0.f;
+  float v[2][32];
+  tmem_ld32(at, v[0]);
+  tmem_ld32(at + 32, v[1]);
+#pragma unroll
+  for (int c = 0; c < NT / 32; ++c) {
+    uint32_t hi[16], lo[16];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int k = 2 * c + u;
+      const bool there = mask >> k & 1;
+      const float f = ks[k] * qs;
+      float g = vs[k], fix = 1.f, cm = v[c][16 * u];
+#pragma unroll
+      for (int j = 1; j < 16; ++j) cm = fmaxf(cm, v[c][16 * u + j]);
+      const bool apart = far && cm > -INFINITY;
+      if constexpr (TERMS == 2) {
+        if (!apart && there) fix = ex2(fminf(cm * fmaf(ks[k], qs_lo, fmaf(ks[k], qs, -f)), 1.f));
+        g *= fix;
+      }
+      const float off = apart ? cm : 0.f, bias = apart ? fminf(fmaf(cm, f, -ref), kLag) : -ref;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float w[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float p = there ? ex2(fmaf(v[c][16 * u + 2 * j + e] - off, f, bias)) : 0.f;
+          sum[2 * (j & 1) + e] += p;
+          w[e] = there ? p * g : 0.f;
+        }
+        hi[8 * u + j] = pack_half2(w[0], w[1]);
+        const __half2 h = *reinterpret_cast<const __half2*>(&hi[8 * u + j]);
+        lo[8 * u + j] = pack_half2(w[0] - __low2float(h), w[1] - __high2float(h));
+      }
+      total = fmaf((sum[0] + sum[2]) + (sum[1] + sum[3]), fix, total);
+    }
+    tmem_st16(at + 16 * c, hi);
+    if constexpr (TERMS == 2) tmem_st16(at + NT / 2 + 16 * c, lo);
+  }
+  return total;
+}
+
+// 16 bytes that no one writes while the kernel runs, read once by each SM; in the order of the code (the compiler would move a
+// plain load down to its use).
+__device__ __forceinline__ uint4 load_codes(const uint8_t* p) {
+  uint4 r;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+  return r;
+}
+
+template <int D, int FMT, bool QF32, int TERMS>
 __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_constant__ Kv8DecodeArgs a) {
   using L = Lay<D, QF32>;
-  constexpr int NT = L::NT, QT = L::QT, NG = NT / 16;
+  constexpr int QT = L::QT, NB = L::NB;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ Shared sh;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -93,22 +215,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.y, split = blockIdx.x / a.groups.max_tiles, tile = blockIdx.x % a.groups.max_tiles;
   const int G = g.gq(), P = g.P;
-  const int terms = a.out_dtype == kDtypeF32 ? 2 : 1;     // of a weight
   // The grid before this one is the decode kernel of the same call: all that this one reads was there before it.  What it leaves
   // (for the merge, which follows this grid) is waited for at the end.
   pdl_launch_dependents();
   if (tid == 0) {
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < NB; ++b) {
       mbar_init(&sh.k_full[b], kConv);
-      mbar_init(&sh.k_empty[b], 1);
       mbar_init(&sh.v_full[b], kConv);
       mbar_init(&sh.sc_full[b], 1);
       mbar_init(&sh.s_full[b], 1);
-      mbar_init(&sh.p_full[b], kSoft);
+      mbar_init(&sh.p_full[b], kSoft / 2);
       mbar_init(&sh.pv_done[b], 1);
     }
-    mbar_init(&sh.end, 1);
-    sh.abort = 0;
+    mbar_init(&sh.end, kSoft + kConv);
     fence_barrier_init();
   }
   if (warp == 0) {
@@ -160,8 +279,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
   // the row of a softmax thread
   bool valid = false;
   int req = 0, head = 0;
+  const int row = tid & (kRows - 1), half = warp >> 2;     // two softmax threads a row
   if (pages > 0 && warp < kSoft) {
-    const int r = sh.tile * kRows + tid;
+    const int r = sh.tile * kRows + row;
     req = sh.lo + r / G;
     head = h * G + r % G;
     if (r < sh.size * G) {
@@ -173,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
     pdl_wait();
     return;
   }
-  if (warp == kSoft + kConv) tmem_alloc(&sh.tmem, kCols);
+  if (warp == 0) tmem_alloc(&sh.tmem, kCols);
   {
     const int* bt = a.block_table + (size_t)sh.holder * a.bt_stride;
     for (int i = tid; i < pages; i += kThreads) {
@@ -185,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
       page_ids[i] = pid;
     }
   }
-  float qs = 0.f;                                         // what a score's raw sum is multiplied by, but for the page's scale
+  float qs = 0.f, qs_lo = 0.f;                            // what a score's raw sum is multiplied by, but for the page's scale
   const bool live = __any_sync(0xffffffffu, valid);
   if (warp < kSoft && live) {
     const size_t at = (size_t)req * a.q_stride + (size_t)head * D;
@@ -199,8 +319,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
     power_of_two(big, &up, &down);
     constexpr double kScale = 1.4426950408889634 / (D == 128 ? 11.313708498984761 : 8.0);
     qs = down * (float)kScale;
+    qs_lo = down * (float)(kScale - (double)(float)kScale);
 #pragma unroll 2
-    for (int c = 0; c < D; c += 8) {
+    for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 8) {
       float x[8] = {};
       if (valid) {
         const float4 u = kv8_load4<QF32>(a.q, at + c), w = kv8_load4<QF32>(a.q, at + c + 4);
@@ -217,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
           x[2 * k] -= bf16_lo(w[k]);
           x[2 * k + 1] -= bf16_hi(w[k]);
         }
-        *reinterpret_cast<uint4*>(smem + L::oQ + t * L::kQ + sw128_offset(tid, c, kRows)) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(smem + L::oQ + t * L::kQ + sw128_offset(row, c, kRows)) = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
   }
@@ -228,294 +349,248 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
   const uint32_t tmem = sh.tmem;
   const int tiles = (pages * P + NT - 1) / NT;
   bool good = true;
+  float m = -INFINITY, l = 0.f;
+  int e_mine = 0;                                         // the half's sums are in units of 2^(e_mine - kBase)
+  const uint32_t base = tmem + ((uint32_t)(warp & 3) << 21);  // a softmax warp's 32 lanes
+  const uint32_t o_at = kColO + 128 * half;
 
   if (warp < kSoft) {
     // ---------------------------------------------------------------- softmax
-    const uint32_t base = tmem + ((uint32_t)warp << 21);  // 32 lanes a warp
-    const int p_bufs = terms * NT <= 128 ? 2 : 1;
-    float m = -INFINITY, l = 0.f;
-    for (int i = 0; i < tiles; ++i) {
-      const int b = i & 1, ph = (i >> 1) & 1;
-      good = mbar_wait_bounded(&sh.s_full[b], ph, a.status) && mbar_wait_bounded(&sh.sc_full[b], ph, a.status);
+    constexpr uint32_t kIdescO = idesc_f16_f32(kRows, D) | (1u << 16);  // the second operand's contracted dimension along its rows
+    const uint64_t v_desc = desc_rows(smem_u32(smem + L::oV), NT * 128);
+    for (int i = half; i < tiles; i += 2) {
+      const int b = i % NB, ph = (i / NB) & 1;
+      good = mbar_wait_sleep_bounded(&sh.sc_full[b], ph, a.status) && mbar_wait_sleep_bounded(&sh.s_full[b], ph, a.status);
       good = __all_sync(0xffffffffu, good);
       if (!good) break;
       tc_fence_after();
       if (live) {
-        const uint32_t s_at = base + kColS + 128 * b, p_at = base + kColP + (p_bufs == 2 ? b * terms * (NT / 2) : 0);
-        const int mask = sh.mask[b];
-        const bool all = mask == (1 << NG) - 1;
+        const uint32_t at = base + kColS + NT * b;
+        const int mask = sh.mask[b], e = sh.e[b];
+        uint32_t x[NT];
+        tmem_ld32_nowait(at, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
+        tmem_ld32_nowait(at + 32, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
         float f[NG], cm[NG], top = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < NT / 32; ++c) {
-          float v[32];
-          tmem_ld32(s_at + 32 * c, v);
+        for (int k = 0; k < NG; ++k) f[k] = sh.ks[b][k] * qs;
+        tmem_wait_ld();
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int k = 2 * c + u;
-            float x = v[16 * u];
+        for (int k = 0; k < NG; ++k) {
+          float y[4];
 #pragma unroll
-            for (int j = 1; j < 16; ++j) x = fmaxf(x, v[16 * u + j]);
-            f[k] = sh.ks[b][k] * qs;
-            cm[k] = all || (mask >> k & 1) ? x : -INFINITY;
-            top = fmaxf(top, __fmul_rd(cm[k], f[k]));
-          }
+          for (int j = 0; j < 4; ++j)
+            y[j] = fmaxf(fmaxf(__uint_as_float(x[16 * k + 4 * j]), __uint_as_float(x[16 * k + 4 * j + 1])),
+                         fmaxf(__uint_as_float(x[16 * k + 4 * j + 2]), __uint_as_float(x[16 * k + 4 * j + 3])));
+          cm[k] = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+          if (mask >> k & 1) top = fmaxf(top, __fmul_rd(cm[k], f[k]));
         }
-        const float ratio = sh.ratio[b];
         const bool follow = top > m + kLag || (m == -INFINITY && top > m);
-        if (i == 0) {
+        if (i < 2) {
           m = top;
-        } else if (__any_sync(0xffffffffu, follow || ratio != 1.f)) {
-          const float m_new = follow ? top : m, alpha = follow ? ex2(m - m_new) : 1.f;
-          m = m_new;
+          e_mine = e;
+        } else if (__any_sync(0xffffffffu, follow) || e != e_mine) {
+          const float alpha = follow ? ex2(m - top) : 1.f, scale = alpha * exp2f((float)(e_mine - e));
+          if (follow) m = top;
           l *= alpha;
-          good = mbar_wait_bounded(&sh.pv_done[b ^ 1], ((i - 1) >> 1) & 1, a.status);
+          e_mine = e;
+          good = mbar_wait_sleep_bounded(&sh.pv_done[(i - 2) % NB], ((i - 2) / NB) & 1, a.status);
           good = __all_sync(0xffffffffu, good);
           if (!good) break;
           tc_fence_after();
-          const float scale = alpha * ratio;
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            float v[32];
-            tmem_ld32(base + kColO + c, v);
-            uint32_t w[32];
+          for (int c = 0; c < D; c += 16) {
+            uint32_t w[16];
+            tmem_ld16(base + o_at + c, w);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(v[j] * scale);
-            tmem_st32(base + kColO + c, w);
+            for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(__uint_as_float(w[j]) * scale);
+            tmem_st16(base + o_at + c, w);
           }
-          tmem_wait_st();
-        }
-        if (i >= p_bufs) {                                // the sums of the tile whose weights were here
-          const int j = i - p_bufs;
-          good = mbar_wait_bounded(&sh.pv_done[j & 1], (j >> 1) & 1, a.status);
-          good = __all_sync(0xffffffffu, good);
-          if (!good) break;
-          tc_fence_after();
         }
         const float ref = m == -INFINITY ? 0.f : m;
-        // Where scores are so large that a last place of one counts, distances are formed from the raw sums: 0 at a page's largest.
-        const bool far = fabsf(ref) >= 4194304.f, any_far = __any_sync(0xffffffffu, far);
-        float sum = 0.f;
-#pragma unroll
-        for (int c = 0; c < NT / 32; ++c) {
-          float v[32];
-          tmem_ld32(s_at + 32 * c, v);
-          if (!all) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (!(mask >> (2 * c + j / 16) & 1)) v[j] = -INFINITY;
-          }
-          uint32_t hi[16], lo[16];
-          float part[2] = {0.f, 0.f};
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int k = 2 * c + u;
-            const float vs = sh.vs[b][k];
-            const float bias = far ? fminf(fmaf(cm[k], f[k], -ref), kLag) : -ref;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              float w[2];
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                float x = v[16 * u + 2 * j + e];
-                if (any_far) x = far && cm[k] > -INFINITY ? x - cm[k] : x;
-                const float p = ex2(fmaf(x, f[k], bias));
-                part[e] += p;
-                w[e] = p * vs;
-              }
-              hi[8 * u + j] = pack_half2(w[0], w[1]);
-              const __half2 hh = *reinterpret_cast<const __half2*>(&hi[8 * u + j]);
-              lo[8 * u + j] = pack_half2(w[0] - __low2float(hh), w[1] - __high2float(hh));
-            }
-          }
-          sum += part[0] + part[1];
-          tmem_st16(p_at + 16 * c, hi);
-          if (terms == 2) tmem_st16(p_at + NT / 2 + 16 * c, lo);
-        }
-        l += sum;
+        if (mask == (1 << NG) - 1 && !__any_sync(0xffffffffu, fabsf(ref) >= kFar))
+          l += weigh<TERMS>(x, cm, f, at, sh.ks[b], sh.vs[b], qs, qs_lo, ref);
+        else
+          l += weigh_with_care<TERMS>(at, sh.ks[b], sh.vs[b], qs, qs_lo, ref, mask);
         tmem_wait_st();
         tc_fence_before();
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.p_full[b]);
-    }
-    // ---------------------------------------------------------------- the split's partial
-    if (good) {
-      good = mbar_wait_bounded(&sh.pv_done[(tiles - 1) & 1], ((tiles - 1) >> 1) & 1, a.status);
-      good = __all_sync(0xffffffffu, good);
-      tc_fence_after();
-    }
-    if (good && live) {
-      const float scale = pow2(sh.e[(tiles - 1) & 1] - kBase);
-      float* pp = a.part + (((size_t)req * g.Hq + head) * a.wl.max_splits + split) * (D + 4);
-      if (valid) *reinterpret_cast<float2*>(pp) = make_float2(l == l ? m : INFINITY, l);  // (a NaN must not look like no partial)
-#pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        float v[32];
-        tmem_ld32(base + kColO + c, v);
-        if (valid)
-#pragma unroll
-          for (int j = 0; j < 32; j += 4)
-            *reinterpret_cast<float4*>(pp + 4 + c + j) = make_float4(v[j] * scale, v[j + 1] * scale, v[j + 2] * scale, v[j + 3] * scale);
-      }
-    }
-  } else if (warp < kSoft + kConv) {
-    // ---------------------------------------------------------------- codes to operands
-    constexpr int T = L::kTasks;
-    const int ct = tid - 32 * kSoft, p = ct & 7, log_p = 31 - __clz(P);
-    const Kv8Geom kg{P, D, g.Hkv};
-    const uint8_t* layer = a.pool + (size_t)a.layer * g.num_pages * kg.page_bytes() + (size_t)h * kg.block_bytes();
-    const size_t page_bytes = kg.page_bytes();
-    const int pages_per_tile = NT >> log_p;
-    // 128-byte line ct / 8 (+ 32, ...) of a tile's codes: its first token, and the logical chunk at place p of it
-    const int t0 = D == 128 ? ct >> 3 : 2 * (ct >> 3);    // (+ 32 or 64 tokens a task: the turns stay)
-    constexpr int kStep = D == 128 ? 32 : 64;
-    auto dest = [&](int turn) {                           // bytes of the chunk's first half, and what leads to its second
-      const int idx = p ^ turn, t = D == 128 ? t0 : t0 + (idx >> 2), j = D == 128 ? idx : idx & 3;
-      const int u = D == 128 ? j >> 2 : 0;                // (which half goes first: eight lanes then touch every bank once)
-      return (uint32_t)((D == 128 ? (j >> 2) * NT * 128 : 0) + t * 128 + (((2 * (j & 3) + u) ^ (t & 7)) << 4)) | (u ? 0x80000000u : 0u);
-    };
-    const uint32_t dk = dest(D == 128 ? 4 * (t0 & 1) : 0), dv = dest(2 * ((t0 >> 1) & 3));
-    const uint32_t nothing = FMT == kKv8Int8 ? 0x80808080u : 0u;
-    uint4 kw[2][T], vw[2][T];
-    float2 sc[2] = {};
-    bool there[2] = {};
-    auto load = [&](int i, uint4 (&x)[T], bool is_v) {
-#pragma unroll
-      for (int k = 0; k < T; ++k) {
-        const int t = t0 + k * kStep, e = i * pages_per_tile + (t >> log_p);
-        const int pid = e < pages ? page_ids[e] : -1;
-        x[k] = make_uint4(nothing, nothing, nothing, nothing);
-        if (pid >= 0)
-          x[k] = __ldg(reinterpret_cast<const uint4*>(layer + pid * page_bytes + (is_v ? P * D : 0) + (t & (P - 1)) * D + p * 16));
-      }
-    };
-    auto load_scale = [&](int i, float2& s, bool& some) {  // lane k: of the tile's k-th 16 tokens
-      if (warp != kSoft || lane >= NG) return;
-      const int e = i * pages_per_tile + ((lane * 16) >> log_p);
-      const int pid = e < pages ? page_ids[e] : -1;
-      some = pid >= 0;
-      s = make_float2(1.f, 0.f);
-      if (some) s = __ldg(reinterpret_cast<const float2*>(layer + pid * page_bytes + kg.scale_off()));
-    };
-    auto store = [&](uint8_t* to, uint32_t d, const uint4 (&x)[T], bool is_v) {
-      const bool second = d >> 31;
-      d &= 0x7FFFFFFFu;
-#pragma unroll
-      for (int k = 0; k < T; ++k) {
-        const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-        uint32_t y[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          y[2 * j] = is_v ? kv8_pair<FMT, 0>(w[j]) : bf16_pair<FMT, 0>(w[j]);
-          y[2 * j + 1] = is_v ? kv8_pair<FMT, 1>(w[j]) : bf16_pair<FMT, 1>(w[j]);
-        }
-        const uint4 first = make_uint4(y[0], y[1], y[2], y[3]), next = make_uint4(y[4], y[5], y[6], y[7]);
-        uint8_t* at = to + d + k * kStep * 128;
-        *reinterpret_cast<uint4*>(at) = second ? next : first;
-        *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(reinterpret_cast<uintptr_t>(at) ^ 16)) = second ? first : next;
-      }
-    };
-    int e_ref = 0;
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      load(b, kw[b], false);
-      load(b, vw[b], true);
-      load_scale(b, sc[b], there[b]);
-    }
-    for (int i0 = 0; i0 < tiles && good; i0 += 2) {
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int i = i0 + b;
-        if (i >= tiles || !good) continue;
-        if (i >= 2) good = mbar_wait_bounded(&sh.k_empty[b], ((i >> 1) - 1) & 1, a.status);
-        good = __all_sync(0xffffffffu, good);
-        if (!good) continue;
-        store(smem + L::oK + b * L::kKV, dk, kw[b], false);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.k_full[b]);
-        load(i + 2, kw[b], false);
-        if (i >= 2) good = mbar_wait_bounded(&sh.pv_done[b], ((i >> 1) - 1) & 1, a.status);
-        good = __all_sync(0xffffffffu, good);
-        if (!good) continue;
-        if (warp == kSoft) {
-          const unsigned mask = __ballot_sync(0xffffffffu, lane < NG && there[b]);
-          int e = lane < NG ? max((int)(__float_as_uint(sc[b].y) >> 23) - 127, -110) : -110;
-          e = __reduce_max_sync(0xffffffffu, e);
-          const int e_new = i == 0 || e > e_ref + kScaleLag ? e : e_ref;
-          if (lane < NG) {
-            sh.ks[b][lane] = sc[b].x;
-            sh.vs[b][lane] = sc[b].y * pow2(kBase - e_new);
-          }
-          if (lane == 0) {
-            sh.ratio[b] = i == 0 ? 1.f : exp2f((float)(e_ref - e_new));
-            sh.mask[b] = (int)mask;
-            sh.e[b] = e_new;
-          }
-          e_ref = e_new;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.sc_full[b]);
-          load_scale(i + 2, sc[b], there[b]);
-        }
-        store(smem + L::oV + b * L::kKV, dv, vw[b], true);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.v_full[b]);
-        load(i + 2, vw[b], true);
-      }
-    }
-  } else {
-    // ---------------------------------------------------------------- MMA issue
-    constexpr uint32_t kIdescS = idesc_bf16_f32(kRows, NT);
-    constexpr uint32_t kIdescO = idesc_f16_f32(kRows, D) | (1u << 16);  // the second operand's contracted dimension along its rows
-    const uint32_t q_at = smem_u32(smem + L::oQ);
-    const int p_bufs = terms * NT <= 128 ? 2 : 1;
-    for (int i = 0; i <= tiles; ++i) {
-      if (i < tiles) {
-        const int b = i & 1;
-        good = mbar_wait_bounded(&sh.k_full[b], (i >> 1) & 1, a.status);
+      if ((warp & 3) == 0) {                              // O += P V
+        good = mbar_wait_sleep_bounded(&sh.p_full[b], ph, a.status) && mbar_wait_sleep_bounded(&sh.v_full[b], ph, a.status);
         good = __all_sync(0xffffffffu, good);
         if (!good) break;
+        fence_proxy_async_smem();
         tc_fence_after();
         if (lane == 0) {
-          const uint32_t k_at = smem_u32(smem + L::oK + b * L::kKV);
+          const uint64_t vd = v_desc + b * (L::kKV >> 4);
 #pragma unroll
-          for (int t = 0; t < QT; ++t)
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              tc_mma(tmem + kColS + 128 * b, smem_desc_sw128(q_at + t * L::kQ + (kk >> 2) * (kRows * 128) + (kk & 3) * 32),
-                     smem_desc_sw128(k_at + (kk >> 2) * (NT * 128) + (kk & 3) * 32), kIdescS, t || kk);
-          tc_commit(&sh.s_full[b]);
-          tc_commit(&sh.k_empty[b]);
-        }
-        __syncwarp();
-      }
-      if (i > 0) {
-        const int j = i - 1, b = j & 1, ph = (j >> 1) & 1;
-        good = mbar_wait_bounded(&sh.p_full[b], ph, a.status) && mbar_wait_bounded(&sh.v_full[b], ph, a.status);
-        good = __all_sync(0xffffffffu, good);
-        if (!good) break;
-        tc_fence_after();
-        if (lane == 0) {
-          const uint32_t v_at = smem_u32(smem + L::oV + b * L::kKV), p_at = tmem + kColP + (p_bufs == 2 ? b * terms * (NT / 2) : 0);
-          for (int t = 0; t < terms; ++t)
+          for (int t = TERMS - 1; t >= 0; --t)
 #pragma unroll
             for (int kk = 0; kk < NT / 16; ++kk)
-              tc_mma_ts(tmem + kColO, p_at + t * (NT / 2) + 8 * kk, desc_rows(v_at + kk * 2048, NT * 128), kIdescO, j || t || kk);
+              tc_mma_ts(tmem + o_at, tmem + kColS + NT * b + t * (NT / 2) + 8 * kk, vd + ((kk * 2048) >> 4), kIdescO,
+                        i >= 2 || t < TERMS - 1 || kk);
           tc_commit(&sh.pv_done[b]);
         }
         __syncwarp();
       }
     }
-    if (lane == 0) {                                      // nothing is under way when the tensor memory is freed
-      tc_commit(&sh.end);
-      (void)mbar_wait_bounded(&sh.end, 0, a.status);
+    // the half's last sums
+    const int last = tiles - 1 - ((tiles - 1 - half) & 1);
+    if (good && last >= 0) {
+      good = mbar_wait_sleep_bounded(&sh.pv_done[last % NB], (last / NB) & 1, a.status);
+      good = __all_sync(0xffffffffu, good);
     }
-    __syncwarp();
+    sh.m[half][row] = m;
+    sh.l[half][row] = l;
+    if (lane == 0 && (warp & 3) == 0) sh.e_sum[half] = e_mine;
+  } else {
+    // ---------------------------------------------------------------- codes to operands
+    constexpr int T = L::kTasks;
+    constexpr uint32_t kIdescS = idesc_bf16_f32(kRows, NT);
+    const uint64_t q_desc = smem_desc_sw128(smem_u32(smem + L::oQ)), k_desc = smem_desc_sw128(smem_u32(smem + L::oK));
+    const int ct = tid - 32 * kSoft, log_p = 31 - __clz(P);
+    const Kv8Geom kg{P, D, g.Hkv};
+    const uint8_t* layer = a.pool + (size_t)a.layer * g.num_pages * kg.page_bytes() + (size_t)h * kg.block_bytes();
+    const size_t page_bytes = kg.page_bytes();
+    // Chunk j of token t0 (+ 32 a task: the turns stay).  Eight neighbouring lanes take the four chunks of 64 channels of two
+    // neighbouring tokens: their halves' first (or second) 16 bytes lie in different banks.
+    const int t0 = D == 128 ? 4 * (ct >> 5) + 2 * (lane >> 4) + ((lane >> 2) & 1) : ct >> 2;
+    const int j = D == 128 ? (lane & 3) + 4 * ((lane >> 3) & 1) : ct & 3;
+    auto place = [&](int turn) {                          // of the chunk in its tokens' 128-byte line, in bytes
+      return D == 128 ? (j ^ turn) * 16 : ((4 * (t0 & 1) + j) ^ turn) * 16;
+    };
+    const uint32_t k_src = place(D == 128 ? 4 * (t0 & 1) : 0), v_src = P * D + place(2 * ((t0 >> 1) & 3));
+    const uint32_t dst = (j >> 2) * NT * 128 + t0 * 128 + (((2 * (j & 3)) ^ (t0 & 7)) << 4);
+    const uint32_t nothing = FMT == kKv8Int8 ? 0x80808080u : 0u;
+    uint4 kw[kAhead][T], vw[kAhead][T];
+    float2 sc[kAhead];
+    bool there[kAhead];
+    auto load = [&](int i, uint4 (&x)[T], uint4 (&y)[T], float2& s, bool& some) {
+#pragma unroll
+      for (int k = 0; k < T; ++k) {
+        const int t = i * NT + t0 + 32 * k, e = t >> log_p;
+        const int pid = e < pages ? page_ids[e] : -1;
+        x[k] = y[k] = make_uint4(nothing, nothing, nothing, nothing);
+        if (pid >= 0) {
+          const uint8_t* p = layer + pid * page_bytes + (t & (P - 1) & (D == 64 ? ~1 : ~0)) * D;
+          x[k] = load_codes(p + k_src);
+          y[k] = load_codes(p + v_src);
+        }
+      }
+      if (warp == kSoft && lane < NG) {                   // the scales of the tile's groups
+        const int e = (i * NT + lane * 16) >> log_p, pid = e < pages ? page_ids[e] : -1;
+        some = pid >= 0;
+        s = make_float2(1.f, 0.f);
+        if (some) s = __ldg(reinterpret_cast<const float2*>(layer + pid * page_bytes + kg.scale_off()));
+      }
+    };
+    auto store = [&](uint8_t* to, const uint4 (&x)[T], bool is_v) {
+#pragma unroll
+      for (int k = 0; k < T; ++k) {
+        const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+        uint32_t y[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          y[2 * i] = is_v ? kv8_pair<FMT, 0>(w[i]) : bf16_pair<FMT, 0>(w[i]);
+          y[2 * i + 1] = is_v ? kv8_pair<FMT, 1>(w[i]) : bf16_pair<FMT, 1>(w[i]);
+        }
+        *reinterpret_cast<uint4*>(to + dst + k * 32 * 128) = make_uint4(y[0], y[1], y[2], y[3]);
+        *reinterpret_cast<uint4*>(to + (dst ^ 16) + k * 32 * 128) = make_uint4(y[4], y[5], y[6], y[7]);
+      }
+    };
+    int e_ref = 0;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) load(u, kw[u], vw[u], sc[u], there[u]);
+    for (int i0 = 0; i0 < tiles && good; i0 += kAhead) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int i = i0 + u, b = u % NB, ph = (i / NB) & 1;
+        if (i >= tiles || !good) break;
+        if (i >= NB) good = mbar_wait_sleep_bounded(&sh.pv_done[b], ph ^ 1, a.status);
+        good = __all_sync(0xffffffffu, good);
+        if (!good) break;
+        if (warp == kSoft) {
+          const unsigned mask = __ballot_sync(0xffffffffu, lane < NG && there[u]);
+          int e = lane < NG ? max((int)(__float_as_uint(sc[u].y) >> 23) - 127, -110) : -110;
+          e = __reduce_max_sync(0xffffffffu, e);
+          e_ref = i == 0 || e > e_ref + kScaleLag ? e : e_ref;
+          if (lane < NG) {
+            sh.ks[b][lane] = sc[u].x;
+            sh.vs[b][lane] = sc[u].y * pow2(kBase - e_ref);
+          }
+          if (lane == 0) {
+            sh.mask[b] = (int)mask;
+            sh.e[b] = e_ref;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.sc_full[b]);
+        }
+        store(smem + L::oK + b * L::kKV, kw[u], false);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.k_full[b]);
+        store(smem + L::oV + b * L::kKV, vw[u], true);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.v_full[b]);
+        load(i + kAhead, kw[u], vw[u], sc[u], there[u]);
+        if (warp == kSoft + (i & (kConv - 1))) {          // S = Q K^T
+          good = mbar_wait_sleep_bounded(&sh.k_full[b], ph, a.status);
+          good = __all_sync(0xffffffffu, good);
+          if (!good) break;
+          // (what the other warps wrote, for the tensor cores)
+          fence_proxy_async_smem();
+          tc_fence_after();
+          if (lane == 0) {
+            const uint64_t kd = k_desc + b * (L::kKV >> 4);
+#pragma unroll
+            for (int t = QT - 1; t >= 0; --t)             // (the small terms first: a sum loses less of them)
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk)
+                tc_mma(tmem + kColS + NT * b, q_desc + ((t * L::kQ + (kk >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4),
+                       kd + (((kk >> 2) * (NT * 128) + (kk & 3) * 32) >> 4), kIdescS, t < QT - 1 || kk);
+            tc_commit(&sh.s_full[b]);
+          }
+          __syncwarp();
+        }
+      }
+    }
   }
+  // Nothing is under way when the tensor memory is freed, a wait that ran out or not.
+  if (lane == 0) tc_commit(&sh.end);
+  good = mbar_wait_sleep_bounded(&sh.end, 0, a.status) && good;
   tc_fence_before();
+  good = !__syncthreads_or(!good);
+  tc_fence_after();
+  // ------------------------------------------------------------------ the split's partial: the two halves, joined
+  if (good && warp < kSoft && live) {
+    const bool both = tiles > 1;
+    const float m0 = sh.m[0][row], m1 = both ? sh.m[1][row] : -INFINITY, top = fmaxf(m0, m1);
+    float s0 = m0 == -INFINITY ? 0.f : ex2(m0 - top), s1 = m1 == -INFINITY ? 0.f : ex2(m1 - top);
+    const float sum = sh.l[0][row] * s0 + (both ? sh.l[1][row] * s1 : 0.f);
+    s0 *= pow2(sh.e_sum[0] - kBase);
+    s1 *= both ? pow2(sh.e_sum[1] - kBase) : 0.f;
+    float* pp = a.part + (((size_t)req * g.Hq + head) * a.wl.max_splits + split) * (D + 4);
+    if (valid && half == 0) *reinterpret_cast<float2*>(pp) = make_float2(sum == sum ? top : INFINITY, sum);  // (a NaN must not look like no partial)
+#pragma unroll 1
+    for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {  // (each half of the threads stores half of the channels)
+      uint32_t x[16], y[16];
+      tmem_ld16(base + kColO + c, x);
+      if (both) tmem_ld16(base + kColO + 128 + c, y);
+      if (valid)
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+          float o[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            o[k] = __uint_as_float(x[j + k]) * s0;
+            if (both) o[k] = fmaf(__uint_as_float(y[j + k]), s1, o[k]);
+          }
+          *reinterpret_cast<float4*>(pp + 4 + c + j) = make_float4(o[0], o[1], o[2], o[3]);
+        }
+    }
+  }
   __syncthreads();
-  if (warp == kSoft + kConv) tmem_dealloc(tmem, kCols);
+  if (warp == 0) tmem_dealloc(tmem, kCols);
   pdl_wait();
 }
 
@@ -557,8 +632,11 @@ static int launch_prefix(const Kv8DecodeArgs& a, cudaStream_t s, bool pdl) {
     if (e != cudaSuccess) return (int)e;
     return launch_pdl(kern, grid, dim3(kThreads), smem, s, pdl, a);
   };
-  return a.q_dtype == kDtypeF32 ? go(kv8_prefix_kernel<D, FMT, true>, Lay<D, true>::kSmem)
-                                : go(kv8_prefix_kernel<D, FMT, false>, Lay<D, false>::kSmem);
+  if (a.out_dtype == kDtypeF32)
+    return a.q_dtype == kDtypeF32 ? go(kv8_prefix_kernel<D, FMT, true, 2>, Lay<D, true>::kSmem)
+                                  : go(kv8_prefix_kernel<D, FMT, false, 2>, Lay<D, false>::kSmem);
+  return a.q_dtype == kDtypeF32 ? go(kv8_prefix_kernel<D, FMT, true, 1>, Lay<D, true>::kSmem)
+                                : go(kv8_prefix_kernel<D, FMT, false, 1>, Lay<D, false>::kSmem);
 }
 
 int launch_kv8_shared_prefix(const Kv8DecodeArgs& a, void* stream, bool pdl) {
