@@ -7,15 +7,16 @@
 // The codes of a page are read once per 128 rows instead of once per 8; 4 d flops per token and row are on the tensor cores
 // (tcgen05), so it is bound by memory up to 128 rows of a kv head and by the tensor cores and the exponentials beyond.
 //
-// Roles in a CTA, around a ring of token tiles of 64 tokens:
-//   8 warps   codes from global memory through registers, four tiles ahead, to BF16 keys and f16 values in shared memory.  Both
-//             are exact.  Rows are tokens: for S the channels of a row are the contracted dimension, for O the tokens are.  They
-//             issue S(i) in turn.
-//   2 x 4     warps, even and odd tiles, a thread per row: S from tensor memory, the running maximum and sum, P to tensor memory in
-//             the place of S, and one of them issues O += P(i) V(i).  Each half has sums of its own, joined at the end.
-// Queries are BF16 operands as they are (float32 ones sums of three), brought near 2^14 by a power of two.  A score is scaled in
-// the exponent's multiplication by its page's scale, a weight by its page's V scale after it.  Weights are f16: one number (11
-// bits) for BF16 outputs, which are rounded to 8 bits at the end, and two (22 bits) for float32 ones.
+// Roles in a CTA, around two buffers of a tile of 128 tokens (64 for float32 queries, whose three terms take the room):
+//   8 warps   codes from global memory through registers, two tiles ahead, to keys and values in shared memory, exactly.  Rows are
+//             tokens: for S the channels of a row are the contracted dimension, for O the tokens are.
+//   2 warps   issue S = Q K^T and O += P V.
+//   2 x 4     warps, one half of a tile's tokens each, a thread per row: S from tensor memory, the running maximum and sum, P to
+//             tensor memory in the place of S.  Each half has sums O of its own, joined at the end.
+// BF16 queries, brought near 2^14 by a power of two, are f16 numbers but for components below 2^-31 of the largest: keys and
+// queries are f16 operands, or BF16 ones where a query has such components; float32 queries are sums of three BF16 operands.
+// A score is scaled in the exponent's multiplication by its page's scale, a weight by its page's V scale after it.  Weights are
+// f16: one number (11 bits) for BF16 outputs, which are rounded to 8 bits at the end, and two (22 bits) for float32 ones.
 #include <cuda.h>
 
 #include "kv8.cuh"
@@ -26,11 +27,10 @@ namespace {
 #include "tc_common.cuh"
 
 constexpr int kSoft = 8, kConv = 8;                       // warps
-constexpr int kThreads = 32 * (kSoft + kConv);
-constexpr int kRows = 128, NT = 64, NG = NT / 16;         // rows and tokens of a tile; groups of 16 tokens, each of one page
-constexpr int kAhead = 4;                                 // tiles whose codes are under way
+constexpr int kThreads = 32 * (kSoft + kConv + 2);
+constexpr int kRows = 128;
 constexpr int kMostPages = 2048;                          // pages of a split
-// Tensor memory: scores, then weights, of the ring's tiles; sums of the two halves.
+// Tensor memory, all of it (so that it begins at 0): scores, then weights, of two tiles; sums of the two halves.
 constexpr uint32_t kColS = 0, kColO = 256, kCols = 512;
 // A row's reference exponent follows its maximum when it is kLag behind; V scales are relative to a power of two that follows
 // the largest when it is 2^kScaleLag behind; a weight of 1 at scale 1 is 2^kBase: below 2^(kLag + kScaleLag + 1 + kBase) = 2^15.
@@ -40,22 +40,25 @@ constexpr float kFar = 4194304.f;                         // scores (log2) whose
 
 template <int D, bool QF32>
 struct Lay {
-  static constexpr int QT = QF32 ? 3 : 1;                 // BF16 terms of a query
-  static constexpr int NB = QF32 ? 2 : 4;                 // tiles of the ring
+  static constexpr int QT = QF32 ? 3 : 1;                 // terms of a query
+  static constexpr int NT = QF32 ? 64 : 128;              // tokens of a tile
+  static constexpr int HC = NT / 2;                       // tokens of a half
   static constexpr int kQ = kRows * D * 2, kKV = NT * D * 2;
-  static constexpr int oQ = 0, oK = oQ + QT * kQ, oV = oK + NB * kKV, oPages = oV + NB * kKV;
+  static constexpr int oQ = 0, oK = oQ + QT * kQ, oV = oK + 2 * kKV, oPages = oV + 2 * kKV;
   static constexpr int kSmem = oPages + kMostPages * 4 + 1024;
   static constexpr int kTasks = NT * D / 16 / (32 * kConv);  // 16-byte chunks of keys (and of values) a thread takes of a tile
 };
 
 struct Shared {
-  uint64_t k_full[4], v_full[4], sc_full[4], s_full[4], p_full[4], pv_done[4], end;
-  float ks[4][NG], vs[4][NG];    // per 16 tokens: K scale, V scale relative to 2^e (2^kBase at 1)
-  int mask[4], e[4];
+  // K(i) written and S's place free; S(i) there and scales written; P(i) of a half there and V(i) written; K, V read
+  uint64_t qk_ready[2], s_full[2], pv_ready[2][2], k_empty[2], v_empty[2], end;
+  float ks[2][8], vs[2][8];      // per group of 16 tokens (of one page): K scale, V scale relative to 2^e (2^kBase at 1)
+  int mask[2], e[2];             // groups that are there
   float m[2][kRows], l[2][kRows];  // of the halves, at the end
   int e_sum[2];
+  uint32_t there[kMostPages / 32];  // pages that are mapped
   uint32_t tmem;
-  int lo, size, shared, tile, holder;
+  int lo, size, shared, tile, holder, holes;
 };
 
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
@@ -108,13 +111,13 @@ __device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
 // Weights of a row's scores in a tile: 2^(score - m) by the page's V scale, as TERMS f16 numbers.  The sum of the weights before
 // the V scale is returned.  A score's scale f = K scale x query scale has a rounding; what it leaves out at a page's largest
 // score goes into the page's weights where they are held to 22 bits.
-template <int TERMS>
-__device__ __forceinline__ float weigh(const uint32_t (&x)[NT], const float (&cm)[NG], const float (&f)[NG], uint32_t at, const float* ks,
+template <int HC, int TERMS>
+__device__ __forceinline__ float weigh(const uint32_t (&x)[HC], const float (&cm)[HC / 16], const float (&f)[HC / 16], uint32_t at, const float* ks,
                                        const float* vs, float qs, float qs_lo, float ref) {
   const uint64_t bias = pair(-ref, -ref);
   float total = 0.f;
 #pragma unroll
-  for (int c = 0; c < NT / 32; ++c) {
+  for (int c = 0; c < HC / 32; ++c) {
     uint32_t hi[16], lo[16];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -142,22 +145,22 @@ __device__ __forceinline__ float weigh(const uint32_t (&x)[NT], const float (&cm
       total = fmaf(first(both) + second(both), fix, total);
     }
     tmem_st16(at + 16 * c, hi);
-    if constexpr (TERMS == 2) tmem_st16(at + NT / 2 + 16 * c, lo);
+    if constexpr (TERMS == 2) tmem_st16(at + HC / 2 + 16 * c, lo);
   }
   return total;
 }
 
 // The same where some groups are not there, or some row's scores are so large (kFar) that a last place of one counts: there
 // distances are formed from the raw sums, 0 at a group's largest.  Other rows come out as from weigh, bit for bit.
-template <int TERMS>
+template <int HC, int TERMS>
 __device__ __noinline__ float weigh_with_care(uint32_t at, const float* ks, const float* vs, float qs, float qs_lo, float ref, int mask) {
   const bool far = fabsf(ref) >= kFar;
   float total = 0.f;
-  float v[2][32];
-  tmem_ld32(at, v[0]);
-  tmem_ld32(at + 32, v[1]);
+  float v[HC / 32][32];
 #pragma unroll
-  for (int c = 0; c < NT / 32; ++c) {
+  for (int c = 0; c < HC / 32; ++c) tmem_ld32(at + 32 * c, v[c]);
+#pragma unroll
+  for (int c = 0; c < HC / 32; ++c) {
     uint32_t hi[16], lo[16];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -190,7 +193,7 @@ __device__ __noinline__ float weigh_with_care(uint32_t at, const float* ks, cons
       total = fmaf((sum[0] + sum[2]) + (sum[1] + sum[3]), fix, total);
     }
     tmem_st16(at + 16 * c, hi);
-    if constexpr (TERMS == 2) tmem_st16(at + NT / 2 + 16 * c, lo);
+    if constexpr (TERMS == 2) tmem_st16(at + HC / 2 + 16 * c, lo);
   }
   return total;
 }
@@ -206,11 +209,11 @@ __device__ __forceinline__ uint4 load_codes(const uint8_t* p) {
 template <int D, int FMT, bool QF32, int TERMS>
 __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_constant__ Kv8DecodeArgs a) {
   using L = Lay<D, QF32>;
-  constexpr int QT = L::QT, NB = L::NB;
+  constexpr int QT = L::QT, NT = L::NT, HC = L::HC, NG = HC / 16;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ Shared sh;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  int* page_ids = reinterpret_cast<int*>(smem + L::oPages);
+  uint32_t* page_at = reinterpret_cast<uint32_t*>(smem + L::oPages);  // of the split's pages, in units of 128 bytes
   const Geom& g = a.g;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.y, split = blockIdx.x / a.groups.max_tiles, tile = blockIdx.x % a.groups.max_tiles;
@@ -219,16 +222,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
   // (for the merge, which follows this grid) is waited for at the end.
   pdl_launch_dependents();
   if (tid == 0) {
-    for (int b = 0; b < NB; ++b) {
-      mbar_init(&sh.k_full[b], kConv);
-      mbar_init(&sh.v_full[b], kConv);
-      mbar_init(&sh.sc_full[b], 1);
-      mbar_init(&sh.s_full[b], 1);
-      mbar_init(&sh.p_full[b], kSoft / 2);
-      mbar_init(&sh.pv_done[b], 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sh.qk_ready[b], kConv + 2);
+      mbar_init(&sh.s_full[b], 2);
+      mbar_init(&sh.pv_ready[b][0], kSoft / 2 + kConv);
+      mbar_init(&sh.pv_ready[b][1], kSoft / 2 + kConv);
+      mbar_init(&sh.k_empty[b], 1);
+      mbar_init(&sh.v_empty[b], 2);
     }
-    mbar_init(&sh.end, kSoft + kConv);
+    mbar_init(&sh.end, 2);
+    sh.holes = 0;
     fence_barrier_init();
+    for (int b = 0; b < 2; ++b)                           // the first S of a place waits for no product
+      for (int k = 0; k < 2; ++k) mbar_arrive(&sh.qk_ready[b]);
   }
   if (warp == 0) {
     // the group of this row tile, and its first request that is not empty
@@ -296,17 +302,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
   if (warp == 0) tmem_alloc(&sh.tmem, kCols);
   {
     const int* bt = a.block_table + (size_t)sh.holder * a.bt_stride;
-    for (int i = tid; i < pages; i += kThreads) {
-      int pid = e0 + i < a.bt_stride ? bt[e0 + i] : -1;
-      if (pid < 0 || pid >= g.num_pages) {
-        flag_error(a.status, kDevBadPage);
-        pid = -1;
+    const uint32_t unit = (uint32_t)(Kv8Geom{P, D, g.Hkv}.page_bytes() / 128);
+    for (int i0 = 32 * warp; i0 < pages; i0 += kThreads) {
+      const int i = i0 + lane, e = e0 + i, pid = i < pages && e < a.bt_stride ? bt[e] : -1;
+      const bool some = pid >= 0 && pid < g.num_pages;
+      if (i < pages) {
+        if (!some) {
+          flag_error(a.status, kDevBadPage);
+          sh.holes = 1;
+        }
+        page_at[i] = some ? pid * unit : 0;
       }
-      page_ids[i] = pid;
+      const unsigned all = __ballot_sync(0xffffffffu, some);
+      if (lane == 0) sh.there[i0 >> 5] = all;
     }
   }
   float qs = 0.f, qs_lo = 0.f;                            // what a score's raw sum is multiplied by, but for the page's scale
   const bool live = __any_sync(0xffffffffu, valid);
+  float up = 1.f;
   if (warp < kSoft && live) {
     const size_t at = (size_t)req * a.q_stride + (size_t)head * D;
     float big = 0.f;
@@ -315,16 +328,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
         const float4 x = kv8_load4<QF32>(a.q, at + c);
         big = fmaxf(fmaxf(big, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(x.z), fabsf(x.w)));
       }
-    float up, down;
+    float down;
     power_of_two(big, &up, &down);
     constexpr double kScale = 1.4426950408889634 / (D == 128 ? 11.313708498984761 : 8.0);
     qs = down * (float)kScale;
     qs_lo = down * (float)(kScale - (double)(float)kScale);
+  }
+  // Half of a row's channels a thread, times up, as operands; whether f16 ones hold them
+  auto put_query = [&](bool f16) {
+    bool exact = true;
 #pragma unroll 2
     for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 8) {
       float x[8] = {};
       if (valid) {
-        const float4 u = kv8_load4<QF32>(a.q, at + c), w = kv8_load4<QF32>(a.q, at + c + 4);
+        const size_t at = (size_t)req * a.q_stride + (size_t)head * D + c;
+        const float4 u = kv8_load4<QF32>(a.q, at), w = kv8_load4<QF32>(a.q, at + 4);
         x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = w.x, x[5] = w.y, x[6] = w.z, x[7] = w.w;
       }
 #pragma unroll
@@ -334,45 +352,53 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
         uint32_t w[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          w[k] = pack_bf162(x[2 * k], x[2 * k + 1]);
-          x[2 * k] -= bf16_lo(w[k]);
-          x[2 * k + 1] -= bf16_hi(w[k]);
+          if (f16) {
+            w[k] = pack_half2(x[2 * k], x[2 * k + 1]);
+            const __half2 h = *reinterpret_cast<const __half2*>(&w[k]);
+            exact &= __low2float(h) == x[2 * k] && __high2float(h) == x[2 * k + 1];
+          } else {
+            w[k] = pack_bf162(x[2 * k], x[2 * k + 1]);
+            x[2 * k] -= bf16_lo(w[k]);
+            x[2 * k + 1] -= bf16_hi(w[k]);
+          }
         }
         *reinterpret_cast<uint4*>(smem + L::oQ + t * L::kQ + sw128_offset(row, c, kRows)) = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
-  }
+    return exact;
+  };
+  bool exact = !QF32;                                     // keys and queries are f16 operands
+  if constexpr (!QF32) exact = !__syncthreads_or(warp < kSoft && live && !put_query(true));
+  if (!exact && warp < kSoft && live) put_query(false);
   fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sh.tmem;
   const int tiles = (pages * P + NT - 1) / NT;
   bool good = true;
   float m = -INFINITY, l = 0.f;
   int e_mine = 0;                                         // the half's sums are in units of 2^(e_mine - kBase)
-  const uint32_t base = tmem + ((uint32_t)(warp & 3) << 21);  // a softmax warp's 32 lanes
+  const uint32_t base = (uint32_t)(warp & 3) << 21;  // a softmax warp's 32 lanes
   const uint32_t o_at = kColO + 128 * half;
 
   if (warp < kSoft) {
     // ---------------------------------------------------------------- softmax
-    constexpr uint32_t kIdescO = idesc_f16_f32(kRows, D) | (1u << 16);  // the second operand's contracted dimension along its rows
-    const uint64_t v_desc = desc_rows(smem_u32(smem + L::oV), NT * 128);
-    for (int i = half; i < tiles; i += 2) {
-      const int b = i % NB, ph = (i / NB) & 1;
-      good = mbar_wait_sleep_bounded(&sh.sc_full[b], ph, a.status) && mbar_wait_sleep_bounded(&sh.s_full[b], ph, a.status);
+    for (int i = 0; i < tiles; ++i) {
+      const int b = i & 1;
+      good = mbar_wait_sleep_bounded(&sh.s_full[b], (i >> 1) & 1, a.status);
       good = __all_sync(0xffffffffu, good);
       if (!good) break;
       tc_fence_after();
       if (live) {
-        const uint32_t at = base + kColS + NT * b;
-        const int mask = sh.mask[b], e = sh.e[b];
-        uint32_t x[NT];
-        tmem_ld32_nowait(at, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
-        tmem_ld32_nowait(at + 32, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
+        const uint32_t at = base + kColS + NT * b + HC * half;
+        const int mask = sh.mask[b] >> (NG * half) & ((1 << NG) - 1), e = sh.e[b];
+        const float *ks = sh.ks[b] + NG * half, *vs = sh.vs[b] + NG * half;
+        uint32_t x[HC];
+#pragma unroll
+        for (int c = 0; c < HC; c += 32) tmem_ld32_nowait(at + c, *reinterpret_cast<uint32_t(*)[32]>(&x[c]));
         float f[NG], cm[NG], top = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < NG; ++k) f[k] = sh.ks[b][k] * qs;
+        for (int k = 0; k < NG; ++k) f[k] = ks[k] * qs;
         tmem_wait_ld();
 #pragma unroll
         for (int k = 0; k < NG; ++k) {
@@ -385,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
           if (mask >> k & 1) top = fmaxf(top, __fmul_rd(cm[k], f[k]));
         }
         const bool follow = top > m + kLag || (m == -INFINITY && top > m);
-        if (i < 2) {
+        if (i == 0) {
           m = top;
           e_mine = e;
         } else if (__any_sync(0xffffffffu, follow) || e != e_mine) {
@@ -393,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
           if (follow) m = top;
           l *= alpha;
           e_mine = e;
-          good = mbar_wait_sleep_bounded(&sh.pv_done[(i - 2) % NB], ((i - 2) / NB) & 1, a.status);
+          good = mbar_wait_sleep_bounded(&sh.v_empty[b ^ 1], ((i - 1) >> 1) & 1, a.status);  // the sums so far are done
           good = __all_sync(0xffffffffu, good);
           if (!good) break;
           tc_fence_after();
@@ -408,189 +434,200 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
         }
         const float ref = m == -INFINITY ? 0.f : m;
         if (mask == (1 << NG) - 1 && !__any_sync(0xffffffffu, fabsf(ref) >= kFar))
-          l += weigh<TERMS>(x, cm, f, at, sh.ks[b], sh.vs[b], qs, qs_lo, ref);
+          l += weigh<HC, TERMS>(x, cm, f, at, ks, vs, qs, qs_lo, ref);
         else
-          l += weigh_with_care<TERMS>(at, sh.ks[b], sh.vs[b], qs, qs_lo, ref, mask);
+          l += weigh_with_care<HC, TERMS>(at, ks, vs, qs, qs_lo, ref, mask);
         tmem_wait_st();
         tc_fence_before();
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.p_full[b]);
-      if ((warp & 3) == 0) {                              // O += P V
-        good = mbar_wait_sleep_bounded(&sh.p_full[b], ph, a.status) && mbar_wait_sleep_bounded(&sh.v_full[b], ph, a.status);
-        good = __all_sync(0xffffffffu, good);
-        if (!good) break;
-        fence_proxy_async_smem();
-        tc_fence_after();
-        if (lane == 0) {
-          const uint64_t vd = v_desc + b * (L::kKV >> 4);
-#pragma unroll
-          for (int t = TERMS - 1; t >= 0; --t)
-#pragma unroll
-            for (int kk = 0; kk < NT / 16; ++kk)
-              tc_mma_ts(tmem + o_at, tmem + kColS + NT * b + t * (NT / 2) + 8 * kk, vd + ((kk * 2048) >> 4), kIdescO,
-                        i >= 2 || t < TERMS - 1 || kk);
-          tc_commit(&sh.pv_done[b]);
-        }
-        __syncwarp();
-      }
-    }
-    // the half's last sums
-    const int last = tiles - 1 - ((tiles - 1 - half) & 1);
-    if (good && last >= 0) {
-      good = mbar_wait_sleep_bounded(&sh.pv_done[last % NB], (last / NB) & 1, a.status);
-      good = __all_sync(0xffffffffu, good);
+      if (lane == 0) mbar_arrive(&sh.pv_ready[b][half]);
     }
     sh.m[half][row] = m;
     sh.l[half][row] = l;
     if (lane == 0 && (warp & 3) == 0) sh.e_sum[half] = e_mine;
-  } else {
+  } else if (warp < kSoft + kConv) {
     // ---------------------------------------------------------------- codes to operands
-    constexpr int T = L::kTasks;
-    constexpr uint32_t kIdescS = idesc_bf16_f32(kRows, NT);
-    const uint64_t q_desc = smem_desc_sw128(smem_u32(smem + L::oQ)), k_desc = smem_desc_sw128(smem_u32(smem + L::oK));
+    constexpr int T = L::kTasks, kStep = D == 128 ? 32 : 64;
     const int ct = tid - 32 * kSoft, log_p = 31 - __clz(P);
     const Kv8Geom kg{P, D, g.Hkv};
     const uint8_t* layer = a.pool + (size_t)a.layer * g.num_pages * kg.page_bytes() + (size_t)h * kg.block_bytes();
-    const size_t page_bytes = kg.page_bytes();
-    // Chunk j of token t0 (+ 32 a task: the turns stay).  Eight neighbouring lanes take the four chunks of 64 channels of two
+    // Chunk j of token t0 (+ kStep a task: the turns stay).  Eight neighbouring lanes take the four chunks of 64 channels of two
     // neighbouring tokens: their halves' first (or second) 16 bytes lie in different banks.
     const int t0 = D == 128 ? 4 * (ct >> 5) + 2 * (lane >> 4) + ((lane >> 2) & 1) : ct >> 2;
     const int j = D == 128 ? (lane & 3) + 4 * ((lane >> 3) & 1) : ct & 3;
     auto place = [&](int turn) {                          // of the chunk in its tokens' 128-byte line, in bytes
       return D == 128 ? (j ^ turn) * 16 : ((4 * (t0 & 1) + j) ^ turn) * 16;
     };
-    const uint32_t k_src = place(D == 128 ? 4 * (t0 & 1) : 0), v_src = P * D + place(2 * ((t0 >> 1) & 3));
+    const uint8_t *k_src = layer + place(D == 128 ? 4 * (t0 & 1) : 0), *v_src = layer + P * D + place(2 * ((t0 >> 1) & 3));
     const uint32_t dst = (j >> 2) * NT * 128 + t0 * 128 + (((2 * (j & 3)) ^ (t0 & 7)) << 4);
     const uint32_t nothing = FMT == kKv8Int8 ? 0x80808080u : 0u;
-    uint4 kw[kAhead][T], vw[kAhead][T];
-    float2 sc[kAhead];
-    bool there[kAhead];
-    auto load = [&](int i, uint4 (&x)[T], uint4 (&y)[T], float2& s, bool& some) {
+    const bool holes = sh.holes;
+    uint4 kw[2][T], vw[T];
+    auto load = [&](int i, uint4 (&x)[T], const uint8_t* src) {
 #pragma unroll
       for (int k = 0; k < T; ++k) {
-        const int t = i * NT + t0 + 32 * k, e = t >> log_p;
-        const int pid = e < pages ? page_ids[e] : -1;
-        x[k] = y[k] = make_uint4(nothing, nothing, nothing, nothing);
-        if (pid >= 0) {
-          const uint8_t* p = layer + pid * page_bytes + (t & (P - 1) & (D == 64 ? ~1 : ~0)) * D;
-          x[k] = load_codes(p + k_src);
-          y[k] = load_codes(p + v_src);
-        }
-      }
-      if (warp == kSoft && lane < NG) {                   // the scales of the tile's groups
-        const int e = (i * NT + lane * 16) >> log_p, pid = e < pages ? page_ids[e] : -1;
-        some = pid >= 0;
-        s = make_float2(1.f, 0.f);
-        if (some) s = __ldg(reinterpret_cast<const float2*>(layer + pid * page_bytes + kg.scale_off()));
+        const int t = i * NT + t0 + kStep * k, e = min(t >> log_p, pages - 1);
+        x[k] = load_codes(src + (size_t)page_at[e] * 128 + (t & (P - 1) & (D == 64 ? ~1 : ~0)) * D);
       }
     };
-    auto store = [&](uint8_t* to, const uint4 (&x)[T], bool is_v) {
+    auto store = [&](uint8_t* to, const uint4 (&x)[T], bool f16, int i) {
 #pragma unroll
       for (int k = 0; k < T; ++k) {
-        const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+        uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+        if (holes) {  // what was read for a page that is not there may be any bytes: it has no weight, but a NaN times 0 is one
+          const int e = min((i * NT + t0 + kStep * k) >> log_p, pages - 1);
+          if (!(sh.there[e >> 5] >> (e & 31) & 1)) w[0] = w[1] = w[2] = w[3] = nothing;
+        }
         uint32_t y[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          y[2 * i] = is_v ? kv8_pair<FMT, 0>(w[i]) : bf16_pair<FMT, 0>(w[i]);
-          y[2 * i + 1] = is_v ? kv8_pair<FMT, 1>(w[i]) : bf16_pair<FMT, 1>(w[i]);
+          y[2 * i] = f16 ? kv8_pair<FMT, 0>(w[i]) : bf16_pair<FMT, 0>(w[i]);
+          y[2 * i + 1] = f16 ? kv8_pair<FMT, 1>(w[i]) : bf16_pair<FMT, 1>(w[i]);
         }
-        *reinterpret_cast<uint4*>(to + dst + k * 32 * 128) = make_uint4(y[0], y[1], y[2], y[3]);
-        *reinterpret_cast<uint4*>(to + (dst ^ 16) + k * 32 * 128) = make_uint4(y[4], y[5], y[6], y[7]);
+        *reinterpret_cast<uint4*>(to + dst + k * kStep * 128) = make_uint4(y[0], y[1], y[2], y[3]);
+        *reinterpret_cast<uint4*>(to + (dst ^ 16) + k * kStep * 128) = make_uint4(y[4], y[5], y[6], y[7]);
       }
     };
-    int e_ref = 0;
+    load(0, kw[0], k_src);
+    load(0, vw, v_src);
+    load(1, kw[1], k_src);
+    for (int i0 = 0; i0 < tiles && good; i0 += 2) {
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) load(u, kw[u], vw[u], sc[u], there[u]);
-    for (int i0 = 0; i0 < tiles && good; i0 += kAhead) {
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int i = i0 + u, b = u % NB, ph = (i / NB) & 1;
-        if (i >= tiles || !good) break;
-        if (i >= NB) good = mbar_wait_sleep_bounded(&sh.pv_done[b], ph ^ 1, a.status);
+      for (int b = 0; b < 2; ++b) {
+        const int i = i0 + b, ph = (i >> 1) & 1;
+        if (i >= tiles) break;
+        if (i >= 2) good = mbar_wait_sleep_bounded(&sh.k_empty[b], ph ^ 1, a.status);
         good = __all_sync(0xffffffffu, good);
         if (!good) break;
-        if (warp == kSoft) {
-          const unsigned mask = __ballot_sync(0xffffffffu, lane < NG && there[u]);
-          int e = lane < NG ? max((int)(__float_as_uint(sc[u].y) >> 23) - 127, -110) : -110;
-          e = __reduce_max_sync(0xffffffffu, e);
-          e_ref = i == 0 || e > e_ref + kScaleLag ? e : e_ref;
-          if (lane < NG) {
-            sh.ks[b][lane] = sc[u].x;
-            sh.vs[b][lane] = sc[u].y * pow2(kBase - e_ref);
-          }
-          if (lane == 0) {
-            sh.mask[b] = (int)mask;
-            sh.e[b] = e_ref;
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.sc_full[b]);
-        }
-        store(smem + L::oK + b * L::kKV, kw[u], false);
+        if (exact) store(smem + L::oK + b * L::kKV, kw[b], true, i);
+        else store(smem + L::oK + b * L::kKV, kw[b], false, i);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.k_full[b]);
-        store(smem + L::oV + b * L::kKV, vw[u], true);
+        if (lane == 0) mbar_arrive(&sh.qk_ready[b]);
+        load(i + 2, kw[b], k_src);
+        if (i >= 2) good = mbar_wait_sleep_bounded(&sh.v_empty[b], ph ^ 1, a.status);
+        good = __all_sync(0xffffffffu, good);
+        if (!good) break;
+        store(smem + L::oV + b * L::kKV, vw, true, i);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.v_full[b]);
-        load(i + kAhead, kw[u], vw[u], sc[u], there[u]);
-        if (warp == kSoft + (i & (kConv - 1))) {          // S = Q K^T
-          good = mbar_wait_sleep_bounded(&sh.k_full[b], ph, a.status);
-          good = __all_sync(0xffffffffu, good);
-          if (!good) break;
-          // (what the other warps wrote, for the tensor cores)
-          fence_proxy_async_smem();
-          tc_fence_after();
-          if (lane == 0) {
-            const uint64_t kd = k_desc + b * (L::kKV >> 4);
-#pragma unroll
-            for (int t = QT - 1; t >= 0; --t)             // (the small terms first: a sum loses less of them)
-#pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk)
-                tc_mma(tmem + kColS + NT * b, q_desc + ((t * L::kQ + (kk >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4),
-                       kd + (((kk >> 2) * (NT * 128) + (kk & 3) * 32) >> 4), kIdescS, t < QT - 1 || kk);
-            tc_commit(&sh.s_full[b]);
-          }
-          __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sh.pv_ready[b][0]);
+          mbar_arrive(&sh.pv_ready[b][1]);
         }
+        load(i + 1, vw, v_src);
       }
     }
+  } else if (warp == kSoft + kConv) {
+    // ---------------------------------------------------------------- S = Q K^T
+    const uint32_t idesc = exact ? idesc_f16_f32(kRows, NT) : idesc_bf16_f32(kRows, NT);
+    const uint64_t q_desc = smem_desc_sw128(smem_u32(smem + L::oQ)), k_desc = smem_desc_sw128(smem_u32(smem + L::oK));
+    // and the scales of the tile's groups of 16 tokens, a lane each, two tiles ahead
+    const Kv8Geom kg{P, D, g.Hkv};
+    const uint8_t* scales = a.pool + (size_t)a.layer * g.num_pages * kg.page_bytes() + (size_t)h * kg.block_bytes() + kg.scale_off();
+    int e_ref = 0;
+    uint2 sc[2];
+    auto page_of = [&](int i) { return (i * NT + (lane & (2 * NG - 1)) * 16) >> (31 - __clz(P)); };
+    auto load_scales = [&](int i, uint2& s) {
+      asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(s.x), "=r"(s.y) : "l"(scales + (size_t)page_at[min(page_of(i), pages - 1)] * 128));
+    };
+    load_scales(0, sc[0]);
+    load_scales(1, sc[1]);
+    for (int i = 0; i < tiles; ++i) {
+      const int b = i & 1;
+      good = mbar_wait_sleep_bounded(&sh.qk_ready[b], (i >> 1) & 1, a.status);
+      good = __all_sync(0xffffffffu, good);
+      if (!good) break;
+      fence_proxy_async_smem();                           // (what the other warps wrote, for the tensor cores)
+      tc_fence_after();
+      if (lane == 0) {
+        const uint64_t kd = k_desc + b * (L::kKV >> 4);
+#pragma unroll
+        for (int t = QT - 1; t >= 0; --t)                 // (the small terms first: a sum loses less of them)
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            tc_mma(kColS + NT * b, q_desc + ((t * L::kQ + (kk >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4),
+                   kd + (((kk >> 2) * (NT * 128) + (kk & 3) * 32) >> 4), idesc, t < QT - 1 || kk);
+        tc_commit(&sh.s_full[b]);
+        tc_commit(&sh.k_empty[b]);
+      }
+      __syncwarp();
+      const uint2 now = b ? sc[1] : sc[0];
+      const int e_page = page_of(i);
+      const bool some = e_page < pages && (sh.there[e_page >> 5] >> (e_page & 31) & 1);
+      const unsigned mask = __ballot_sync(0xffffffffu, some && lane < 2 * NG);
+      const int e = __reduce_max_sync(0xffffffffu, some ? max((int)(now.y >> 23) - 127, -110) : -110);
+      e_ref = i == 0 || e > e_ref + kScaleLag ? e : e_ref;
+      if (lane < 2 * NG) {
+        sh.ks[b][lane] = some ? __uint_as_float(now.x) : 1.f;
+        sh.vs[b][lane] = some ? __uint_as_float(now.y) * pow2(kBase - e_ref) : 0.f;
+      }
+      if (lane == 0) {
+        sh.mask[b] = (int)mask;
+        sh.e[b] = e_ref;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.s_full[b]);
+      if (b) load_scales(i + 2, sc[1]);
+      else load_scales(i + 2, sc[0]);
+    }
+    if (lane == 0) tc_commit(&sh.end);
+  } else {
+    // ---------------------------------------------------------------- O += P V
+    constexpr uint32_t kIdesc = idesc_f16_f32(kRows, D) | (1u << 16);  // the second operand's contracted dimension along its rows
+    const uint64_t v_desc = desc_rows(smem_u32(smem + L::oV), NT * 128);
+    for (int i = 0; i < 2 * tiles; ++i) {
+      const int t = i >> 1, b = t & 1, side = i & 1;
+      good = mbar_wait_sleep_bounded(&sh.pv_ready[b][side], (t >> 1) & 1, a.status);
+      good = __all_sync(0xffffffffu, good);
+      if (!good) break;
+      fence_proxy_async_smem();
+      tc_fence_after();
+      if (lane == 0) {
+        const uint64_t vd = v_desc + ((b * L::kKV + side * (HC / 16) * 2048) >> 4);
+#pragma unroll
+        for (int u = TERMS - 1; u >= 0; --u)
+#pragma unroll
+          for (int kk = 0; kk < HC / 16; ++kk)
+            tc_mma_ts(kColO + 128 * side, kColS + NT * b + HC * side + u * (HC / 2) + 8 * kk, vd + ((kk * 2048) >> 4), kIdesc,
+                      t > 0 || u < TERMS - 1 || kk);
+        tc_commit(&sh.qk_ready[b]);
+        tc_commit(&sh.v_empty[b]);
+      }
+      __syncwarp();
+    }
+    if (lane == 0) tc_commit(&sh.end);
   }
   // Nothing is under way when the tensor memory is freed, a wait that ran out or not.
-  if (lane == 0) tc_commit(&sh.end);
   good = mbar_wait_sleep_bounded(&sh.end, 0, a.status) && good;
   tc_fence_before();
   good = !__syncthreads_or(!good);
   tc_fence_after();
   // ------------------------------------------------------------------ the split's partial: the two halves, joined
   if (good && warp < kSoft && live) {
-    const bool both = tiles > 1;
-    const float m0 = sh.m[0][row], m1 = both ? sh.m[1][row] : -INFINITY, top = fmaxf(m0, m1);
+    const float m0 = sh.m[0][row], m1 = sh.m[1][row], top = fmaxf(m0, m1);
     float s0 = m0 == -INFINITY ? 0.f : ex2(m0 - top), s1 = m1 == -INFINITY ? 0.f : ex2(m1 - top);
-    const float sum = sh.l[0][row] * s0 + (both ? sh.l[1][row] * s1 : 0.f);
+    const float sum = sh.l[0][row] * s0 + sh.l[1][row] * s1;
     s0 *= pow2(sh.e_sum[0] - kBase);
-    s1 *= both ? pow2(sh.e_sum[1] - kBase) : 0.f;
+    s1 *= pow2(sh.e_sum[1] - kBase);
     float* pp = a.part + (((size_t)req * g.Hq + head) * a.wl.max_splits + split) * (D + 4);
     if (valid && half == 0) *reinterpret_cast<float2*>(pp) = make_float2(sum == sum ? top : INFINITY, sum);  // (a NaN must not look like no partial)
 #pragma unroll 1
     for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {  // (each half of the threads stores half of the channels)
       uint32_t x[16], y[16];
       tmem_ld16(base + kColO + c, x);
-      if (both) tmem_ld16(base + kColO + 128 + c, y);
+      tmem_ld16(base + kColO + 128 + c, y);
       if (valid)
 #pragma unroll
         for (int j = 0; j < 16; j += 4) {
           float o[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            o[k] = __uint_as_float(x[j + k]) * s0;
-            if (both) o[k] = fmaf(__uint_as_float(y[j + k]), s1, o[k]);
-          }
+          for (int k = 0; k < 4; ++k) o[k] = fmaf(__uint_as_float(y[j + k]), s1, __uint_as_float(x[j + k]) * s0);
           *reinterpret_cast<float4*>(pp + 4 + c + j) = make_float4(o[0], o[1], o[2], o[3]);
         }
     }
   }
   __syncthreads();
-  if (warp == 0) tmem_dealloc(tmem, kCols);
+  if (warp == 0) tmem_dealloc(sh.tmem, kCols);
   pdl_wait();
 }
 
