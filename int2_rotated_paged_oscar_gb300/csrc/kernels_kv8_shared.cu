@@ -12,7 +12,7 @@
 //             tokens: for S the channels of a row are the contracted dimension, for O the tokens are.
 //   2 warps   issue S = Q K^T and O += P V.
 //   2 x 4     warps, one half of a tile's tokens each, a thread per row: S from tensor memory, the running maximum and sum, P to
-//             tensor memory in the place of S.  Each half has sums O of its own, joined at the end.
+//             tensor memory in the place of S, which holds three tiles.
 // BF16 queries, brought near 2^14 by a power of two, are f16 numbers but for components below 2^-31 of the largest: keys and
 // queries are f16 operands, or BF16 ones where a query has such components; float32 queries are sums of three BF16 operands.
 // A score is scaled in the exponent's multiplication by its page's scale, a weight by its page's V scale after it.  Weights are
@@ -30,12 +30,14 @@ constexpr int kSoft = 8, kConv = 8;                       // warps
 constexpr int kThreads = 32 * (kSoft + kConv + 2);
 constexpr int kRows = 128;
 constexpr int kMostPages = 2048;                          // pages of a split
-// Tensor memory, all of it (so that it begins at 0): scores, then weights, of two tiles; sums of the two halves.
-constexpr uint32_t kColS = 0, kColO = 256, kCols = 512;
+// Tensor memory, all of it (so that it begins at 0): scores, then weights, of three tiles; sums.
+constexpr uint32_t kColO = 384, kCols = 512;
+constexpr int NS = 3;
+OSCAR_HD constexpr uint32_t col_s(int s) { return 128 * s; }
 // A row's reference exponent follows its maximum when it is kLag behind; V scales are relative to a power of two that follows
 // the largest when it is 2^kScaleLag behind; a weight of 1 at scale 1 is 2^kBase: below 2^(kLag + kScaleLag + 1 + kBase) = 2^15.
-constexpr float kLag = 8.f;
-constexpr int kScaleLag = 3, kBase = 3;
+constexpr float kLag = 10.f;
+constexpr int kScaleLag = 1, kBase = 3;
 constexpr float kFar = 4194304.f;                         // scores (log2) whose last place counts
 
 template <int D, bool QF32>
@@ -50,12 +52,12 @@ struct Lay {
 };
 
 struct Shared {
-  // K(i) written and S's place free; S(i) there and scales written; P(i) of a half there and V(i) written; K, V read
-  uint64_t qk_ready[2], s_full[2], pv_ready[2][2], k_empty[2], v_empty[2], end;
-  float ks[2][8], vs[2][8];      // per group of 16 tokens (of one page): K scale, V scale relative to 2^e (2^kBase at 1)
-  int mask[2], e[2];             // groups that are there
-  float m[2][kRows], l[2][kRows];  // of the halves, at the end
-  int e_sum[2];
+  // K(i) written and S's place free; S(i) there and scales written; P(i) there and V(i) written; K read; V read and P V done
+  uint64_t qk_ready[NS], s_full[NS], pv_ready[NS], k_empty[2], v_empty[2], end;
+  float ks[NS][8], vs[NS][8];    // per group of 16 tokens (of one page): K scale, V scale relative to 2^e (2^kBase at 1)
+  int mask[NS], e[NS];           // groups that are there
+  float top[2][2][kRows];        // a half's largest scores, of even and odd tiles
+  float l[2][kRows];             // a half's sum, at the end
   uint32_t there[kMostPages / 32];  // pages that are mapped
   uint32_t tmem;
   int lo, size, shared, tile, holder, holes;
@@ -198,6 +200,21 @@ __device__ __noinline__ float weigh_with_care(uint32_t at, const float* ks, cons
   return total;
 }
 
+// A row's sums times scale.
+template <int D>
+__device__ __forceinline__ void scale_sums(uint32_t at, float scale) {
+  uint32_t w[2][32];
+  tmem_ld32_nowait(at, w[0]);
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) {
+    tmem_wait_ld();
+    if (c + 1 < D / 32) tmem_ld32_nowait(at + 32 * (c + 1), w[(c + 1) & 1]);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) w[c & 1][j] = __float_as_uint(__uint_as_float(w[c & 1][j]) * scale);
+    tmem_st32(at + 32 * c, w[c & 1]);
+  }
+}
+
 // 16 bytes that no one writes while the kernel runs, read once by each SM; in the order of the code (the compiler would move a
 // plain load down to its use).
 __device__ __forceinline__ uint4 load_codes(const uint8_t* p) {
@@ -222,19 +239,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
   // (for the merge, which follows this grid) is waited for at the end.
   pdl_launch_dependents();
   if (tid == 0) {
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(&sh.qk_ready[b], kConv + 2);
+    for (int b = 0; b < NS; ++b) {
+      mbar_init(&sh.qk_ready[b], kConv + 1);
       mbar_init(&sh.s_full[b], 2);
-      mbar_init(&sh.pv_ready[b][0], kSoft / 2 + kConv);
-      mbar_init(&sh.pv_ready[b][1], kSoft / 2 + kConv);
+      mbar_init(&sh.pv_ready[b], kSoft + kConv);
+    }
+    for (int b = 0; b < 2; ++b) {
       mbar_init(&sh.k_empty[b], 1);
-      mbar_init(&sh.v_empty[b], 2);
+      mbar_init(&sh.v_empty[b], 1);
     }
     mbar_init(&sh.end, 2);
     sh.holes = 0;
     fence_barrier_init();
-    for (int b = 0; b < 2; ++b)                           // the first S of a place waits for no product
-      for (int k = 0; k < 2; ++k) mbar_arrive(&sh.qk_ready[b]);
+    for (int b = 0; b < NS; ++b) mbar_arrive(&sh.qk_ready[b]);  // the first S of a place waits for no product
   }
   if (warp == 0) {
     // the group of this row tile, and its first request that is not empty
@@ -377,20 +394,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
   const int tiles = (pages * P + NT - 1) / NT;
   bool good = true;
   float m = -INFINITY, l = 0.f;
-  int e_mine = 0;                                         // the half's sums are in units of 2^(e_mine - kBase)
+  int e_mine = 0;                                         // the sums are in units of 2^(e_mine - kBase)
   const uint32_t base = (uint32_t)(warp & 3) << 21;  // a softmax warp's 32 lanes
-  const uint32_t o_at = kColO + 128 * half;
 
   if (warp < kSoft) {
     // ---------------------------------------------------------------- softmax
-    for (int i = 0; i < tiles; ++i) {
-      const int b = i & 1;
-      good = mbar_wait_sleep_bounded(&sh.s_full[b], (i >> 1) & 1, a.status);
-      good = __all_sync(0xffffffffu, good);
-      if (!good) break;
-      tc_fence_after();
+    for (int i = 0, b = 0, ph = 0; i < tiles; ++i) {
+      if (good) {
+        good = mbar_wait_sleep_bounded(&sh.s_full[b], ph, a.status);
+        good = __all_sync(0xffffffffu, good);
+        tc_fence_after();
+      }
       if (live) {
-        const uint32_t at = base + kColS + NT * b + HC * half;
+        const uint32_t at = base + col_s(b) + HC * half;
         const int mask = sh.mask[b] >> (NG * half) & ((1 << NG) - 1), e = sh.e[b];
         const float *ks = sh.ks[b] + NG * half, *vs = sh.vs[b] + NG * half;
         uint32_t x[HC];
@@ -410,42 +426,37 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
           cm[k] = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
           if (mask >> k & 1) top = fmaxf(top, __fmul_rd(cm[k], f[k]));
         }
-        const bool follow = top > m + kLag || (m == -INFINITY && top > m);
-        if (i == 0) {
-          m = top;
-          e_mine = e;
-        } else if (__any_sync(0xffffffffu, follow) || e != e_mine) {
-          const float alpha = follow ? ex2(m - top) : 1.f, scale = alpha * exp2f((float)(e_mine - e));
+        // the largest of both halves: a pair of warps meets once a tile, after a wait that ran out too
+        sh.top[i & 1][half][row] = top;
+        asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");
+        top = fmaxf(top, sh.top[i & 1][half ^ 1][row]);
+        if (good) {
+          const bool follow = top > m + kLag || (m == -INFINITY && top > m);
+          const float alpha = follow && i > 0 ? ex2(m - top) : 1.f;
+          const int e_old = i > 0 ? e_mine : e;
           if (follow) m = top;
           l *= alpha;
           e_mine = e;
-          good = mbar_wait_sleep_bounded(&sh.v_empty[b ^ 1], ((i - 1) >> 1) & 1, a.status);  // the sums so far are done
-          good = __all_sync(0xffffffffu, good);
-          if (!good) break;
-          tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < D; c += 16) {
-            uint32_t w[16];
-            tmem_ld16(base + o_at + c, w);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(__uint_as_float(w[j]) * scale);
-            tmem_st16(base + o_at + c, w);
+          const float ref = m == -INFINITY ? 0.f : m;
+          if (mask == (1 << NG) - 1 && !__any_sync(0xffffffffu, fabsf(ref) >= kFar))
+            l += weigh<HC, TERMS>(x, cm, f, at, ks, vs, qs, qs_lo, ref);
+          else
+            l += weigh_with_care<HC, TERMS>(at, ks, vs, qs, qs_lo, ref, mask);
+          if (__any_sync(0xffffffffu, alpha != 1.f) || e != e_old) {  // (the weights first: by now the sums so far are done)
+            good = mbar_wait_sleep_bounded(&sh.v_empty[(i - 1) & 1], ((i - 1) >> 1) & 1, a.status);
+            good = __all_sync(0xffffffffu, good);
+            tc_fence_after();
+            if (good) scale_sums<D / 2>(base + kColO + half * (D / 2), alpha * exp2f((float)(e_old - e)));
           }
+          tmem_wait_st();
+          tc_fence_before();
         }
-        const float ref = m == -INFINITY ? 0.f : m;
-        if (mask == (1 << NG) - 1 && !__any_sync(0xffffffffu, fabsf(ref) >= kFar))
-          l += weigh<HC, TERMS>(x, cm, f, at, ks, vs, qs, qs_lo, ref);
-        else
-          l += weigh_with_care<HC, TERMS>(at, ks, vs, qs, qs_lo, ref, mask);
-        tmem_wait_st();
-        tc_fence_before();
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.pv_ready[b][half]);
+      if (lane == 0 && good) mbar_arrive(&sh.pv_ready[b]);
+      if (++b == NS) b = 0, ph ^= 1;
     }
-    sh.m[half][row] = m;
     sh.l[half][row] = l;
-    if (lane == 0 && (warp & 3) == 0) sh.e_sum[half] = e_mine;
   } else if (warp < kSoft + kConv) {
     // ---------------------------------------------------------------- codes to operands
     constexpr int T = L::kTasks, kStep = D == 128 ? 32 : 64;
@@ -492,9 +503,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
     load(0, kw[0], k_src);
     load(0, vw, v_src);
     load(1, kw[1], k_src);
-    for (int i0 = 0; i0 < tiles && good; i0 += 2) {
+    for (int i0 = 0, s = 0; i0 < tiles && good; i0 += 2) {
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
+      for (int b = 0; b < 2; ++b, s = s == NS - 1 ? 0 : s + 1) {
         const int i = i0 + b, ph = (i >> 1) & 1;
         if (i >= tiles) break;
         if (i >= 2) good = mbar_wait_sleep_bounded(&sh.k_empty[b], ph ^ 1, a.status);
@@ -503,17 +514,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
         if (exact) store(smem + L::oK + b * L::kKV, kw[b], true, i);
         else store(smem + L::oK + b * L::kKV, kw[b], false, i);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.qk_ready[b]);
+        if (lane == 0) mbar_arrive(&sh.qk_ready[s]);
         load(i + 2, kw[b], k_src);
         if (i >= 2) good = mbar_wait_sleep_bounded(&sh.v_empty[b], ph ^ 1, a.status);
         good = __all_sync(0xffffffffu, good);
         if (!good) break;
         store(smem + L::oV + b * L::kKV, vw, true, i);
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&sh.pv_ready[b][0]);
-          mbar_arrive(&sh.pv_ready[b][1]);
-        }
+        if (lane == 0) mbar_arrive(&sh.pv_ready[s]);
         load(i + 1, vw, v_src);
       }
     }
@@ -532,9 +540,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
     };
     load_scales(0, sc[0]);
     load_scales(1, sc[1]);
-    for (int i = 0; i < tiles; ++i) {
+    for (int i = 0, s = 0, ph = 0; i < tiles; ++i) {
       const int b = i & 1;
-      good = mbar_wait_sleep_bounded(&sh.qk_ready[b], (i >> 1) & 1, a.status);
+      good = mbar_wait_sleep_bounded(&sh.qk_ready[s], ph, a.status);
       good = __all_sync(0xffffffffu, good);
       if (!good) break;
       fence_proxy_async_smem();                           // (what the other warps wrote, for the tensor cores)
@@ -545,9 +553,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
         for (int t = QT - 1; t >= 0; --t)                 // (the small terms first: a sum loses less of them)
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            tc_mma(kColS + NT * b, q_desc + ((t * L::kQ + (kk >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4),
+            tc_mma(col_s(s), q_desc + ((t * L::kQ + (kk >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4),
                    kd + (((kk >> 2) * (NT * 128) + (kk & 3) * 32) >> 4), idesc, t < QT - 1 || kk);
-        tc_commit(&sh.s_full[b]);
+        tc_commit(&sh.s_full[s]);
         tc_commit(&sh.k_empty[b]);
       }
       __syncwarp();
@@ -558,42 +566,44 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
       const int e = __reduce_max_sync(0xffffffffu, some ? max((int)(now.y >> 23) - 127, -110) : -110);
       e_ref = i == 0 || e > e_ref + kScaleLag ? e : e_ref;
       if (lane < 2 * NG) {
-        sh.ks[b][lane] = some ? __uint_as_float(now.x) : 1.f;
-        sh.vs[b][lane] = some ? __uint_as_float(now.y) * pow2(kBase - e_ref) : 0.f;
+        sh.ks[s][lane] = some ? __uint_as_float(now.x) : 1.f;
+        sh.vs[s][lane] = some ? __uint_as_float(now.y) * pow2(kBase - e_ref) : 0.f;
       }
       if (lane == 0) {
-        sh.mask[b] = (int)mask;
-        sh.e[b] = e_ref;
+        sh.mask[s] = (int)mask;
+        sh.e[s] = e_ref;
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.s_full[b]);
+      if (lane == 0) mbar_arrive(&sh.s_full[s]);
       if (b) load_scales(i + 2, sc[1]);
       else load_scales(i + 2, sc[0]);
+      if (++s == NS) s = 0, ph ^= 1;
     }
     if (lane == 0) tc_commit(&sh.end);
   } else {
     // ---------------------------------------------------------------- O += P V
     constexpr uint32_t kIdesc = idesc_f16_f32(kRows, D) | (1u << 16);  // the second operand's contracted dimension along its rows
     const uint64_t v_desc = desc_rows(smem_u32(smem + L::oV), NT * 128);
-    for (int i = 0; i < 2 * tiles; ++i) {
-      const int t = i >> 1, b = t & 1, side = i & 1;
-      good = mbar_wait_sleep_bounded(&sh.pv_ready[b][side], (t >> 1) & 1, a.status);
+    for (int i = 0, s = 0, ph = 0; i < tiles; ++i) {
+      const int b = i & 1;
+      good = mbar_wait_sleep_bounded(&sh.pv_ready[s], ph, a.status);
       good = __all_sync(0xffffffffu, good);
       if (!good) break;
       fence_proxy_async_smem();
       tc_fence_after();
       if (lane == 0) {
-        const uint64_t vd = v_desc + ((b * L::kKV + side * (HC / 16) * 2048) >> 4);
+        const uint64_t vd = v_desc + b * (L::kKV >> 4);
 #pragma unroll
         for (int u = TERMS - 1; u >= 0; --u)
 #pragma unroll
-          for (int kk = 0; kk < HC / 16; ++kk)
-            tc_mma_ts(kColO + 128 * side, kColS + NT * b + HC * side + u * (HC / 2) + 8 * kk, vd + ((kk * 2048) >> 4), kIdesc,
-                      t > 0 || u < TERMS - 1 || kk);
-        tc_commit(&sh.qk_ready[b]);
+          for (int kk = 0; kk < NT / 16; ++kk)            // (a half's weights: its first terms, then its second ones)
+            tc_mma_ts(kColO, col_s(s) + HC * (kk / NG) + u * (HC / 2) + 8 * (kk % NG), vd + ((kk * 2048) >> 4), kIdesc,
+                      i > 0 || u < TERMS - 1 || kk);
+        tc_commit(&sh.qk_ready[s]);
         tc_commit(&sh.v_empty[b]);
       }
       __syncwarp();
+      if (++s == NS) s = 0, ph ^= 1;
     }
     if (lane == 0) tc_commit(&sh.end);
   }
@@ -602,28 +612,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
   tc_fence_before();
   good = !__syncthreads_or(!good);
   tc_fence_after();
-  // ------------------------------------------------------------------ the split's partial: the two halves, joined
+  // ------------------------------------------------------------------ the split's partial
   if (good && warp < kSoft && live) {
-    const float m0 = sh.m[0][row], m1 = sh.m[1][row], top = fmaxf(m0, m1);
-    float s0 = m0 == -INFINITY ? 0.f : ex2(m0 - top), s1 = m1 == -INFINITY ? 0.f : ex2(m1 - top);
-    const float sum = sh.l[0][row] * s0 + sh.l[1][row] * s1;
-    s0 *= pow2(sh.e_sum[0] - kBase);
-    s1 *= pow2(sh.e_sum[1] - kBase);
+    const float sum = sh.l[0][row] + sh.l[1][row], scale = pow2(e_mine - kBase);
     float* pp = a.part + (((size_t)req * g.Hq + head) * a.wl.max_splits + split) * (D + 4);
-    if (valid && half == 0) *reinterpret_cast<float2*>(pp) = make_float2(sum == sum ? top : INFINITY, sum);  // (a NaN must not look like no partial)
+    if (valid && half == 0) *reinterpret_cast<float2*>(pp) = make_float2(sum == sum ? m : INFINITY, sum);  // (a NaN must not look like no partial)
 #pragma unroll 1
-    for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {  // (each half of the threads stores half of the channels)
-      uint32_t x[16], y[16];
-      tmem_ld16(base + kColO + c, x);
-      tmem_ld16(base + kColO + 128 + c, y);
+    for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {  // (each half of the threads stores half of the channels)
+      float v[32];
+      tmem_ld32(base + kColO + c, v);
       if (valid)
 #pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-          float o[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) o[k] = fmaf(__uint_as_float(y[j + k]), s1, __uint_as_float(x[j + k]) * s0);
-          *reinterpret_cast<float4*>(pp + 4 + c + j) = make_float4(o[0], o[1], o[2], o[3]);
-        }
+        for (int j = 0; j < 32; j += 4)
+          *reinterpret_cast<float4*>(pp + 4 + c + j) = make_float4(v[j] * scale, v[j + 1] * scale, v[j + 2] * scale, v[j + 3] * scale);
     }
   }
   __syncthreads();
