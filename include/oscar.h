@@ -648,7 +648,7 @@ oscar_status oscar_set_decode_form(oscar_ctx* ctx, int32_t form);
  * "decode_combine", "q_rotate", "step_prep", "append", "evict", "write", "bf16_prepare",
  * "bf16_decode", "bf16_combine", "extend", "selftest", "kv8_write", "kv8_append", "kv8_decode",
  * "kv8_combine" (not launched for contexts or selections of up to 512 tokens, 1024 at d = 64
- * and P >= 32), "kv8_select", "kv8_fork", "kv8_prefix", "kv8_reorder", "beam_chunks", "beam_pick", "copy_pages", "remap_table".  Launches recorded into a CUDA graph get external event-record nodes: replay the graph
+ * and P >= 32), "kv8_select", "kv8_fork", "kv8_prefix", "kv8_reorder", "beam_units", "beam_pick", "copy_pages", "remap_table".  Launches recorded into a CUDA graph get external event-record nodes: replay the graph
  * once, then read; the events return to the library when read, so a graph
  * captured with timing on is replayed at most once.  With timing on, the decode
  * kernels are launched without programmatic dependent launch. */

@@ -32,7 +32,7 @@ oscar_status oscar_beam_select_workspace_size(int32_t batch, int32_t beams, int3
   const oscar_status st = check_sizes(batch, beams, vocab, n_out);
   if (st != OSCAR_OK) return st;
   if (!bytes) return fail(OSCAR_ERR_INVALID, "bad arguments to workspace size");
-  *bytes = oscar::beam_plan(batch, beams, vocab, n_out).total;
+  *bytes = oscar::beam_ws_bytes(batch, beams, vocab);
   return OSCAR_OK;
 }
 
@@ -64,8 +64,8 @@ oscar_status oscar_beam_select(oscar_ctx* ctx, const void* logits, int64_t row_s
       return fail(OSCAR_ERR_INVALID, "the outputs must not overlap the inputs");
   if ((st = check_workspace(workspace)) != OSCAR_OK) return st;
   BeamArgs a{};
-  a.plan = oscar::beam_plan(batch, beams, vocab, n_out);
-  if (ws_bytes < a.plan.total) return fail(OSCAR_ERR_INVALID, "workspace too small: %zu < %zu bytes", ws_bytes, a.plan.total);
+  const size_t need = oscar::beam_ws_bytes(batch, beams, vocab);
+  if (ws_bytes < need) return fail(OSCAR_ERR_INVALID, "workspace too small: %zu < %zu bytes", ws_bytes, need);
   a.logits = logits;
   a.stride = row_stride;
   a.dtype = dtype;
@@ -83,8 +83,8 @@ oscar_status oscar_beam_select(oscar_ctx* ctx, const void* logits, int64_t row_s
   a.part = static_cast<float*>(workspace);
   const bool pdl = !ctx->timing;
   {
-    LaunchScope ls(ctx, "beam_chunks", stream);
-    const int e = oscar::launch_beam_chunks(a, stream, pdl);
+    LaunchScope ls(ctx, "beam_units", stream);
+    const int e = oscar::launch_beam_units(a, stream, pdl);
     ls.done(e);
     if (e) return cuda_fail(e, "beam selection launch");
   }

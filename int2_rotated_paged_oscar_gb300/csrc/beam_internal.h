@@ -7,13 +7,11 @@ namespace oscar {
 constexpr int kMaxBeams = 64;       // beams of an item
 constexpr int kMaxCandidates = 64;  // candidates taken of an item
 constexpr int kMaxVocab = 1 << 24;
-constexpr int kBeamUnit = 1024;     // logits that a warp looks through at a time; chunks are whole units
-constexpr int kMaxPairs = 1024;     // (beam, chunk) pairs of an item
+constexpr int kBeamUnit = 1024;     // logits that a warp looks through at a time
 
-struct BeamPlan {
-  int chunk, chunks;  // logits of a chunk, chunks of a row
-  size_t total;       // workspace: (maximum, sum) of every chunk
-};
+// Units of a row; the workspace holds (maximum, sum of exponentials) of each.
+OSCAR_HD inline int beam_units(int vocab) { return (vocab + kBeamUnit - 1) / kBeamUnit; }
+inline size_t beam_ws_bytes(int batch, int beams, int vocab) { return (size_t)batch * beams * beam_units(vocab) * 2 * sizeof(float); }
 
 struct BeamArgs {
   const void* logits;
@@ -27,8 +25,7 @@ struct BeamArgs {
   int* out_tokens;
   int* out_parents;
   int* status;
-  float* part;                   // [batch * beams][chunks][2]
-  BeamPlan plan;
+  float* part;                   // [batch * beams][units][2]
 };
 
 struct ReorderArgs {
@@ -46,8 +43,7 @@ struct ReorderArgs {
   int* status;
 };
 
-BeamPlan beam_plan(int batch, int beams, int vocab, int n_out);
-int launch_beam_chunks(const BeamArgs& a, void* stream, bool pdl);
+int launch_beam_units(const BeamArgs& a, void* stream, bool pdl);
 int launch_beam_pick(const BeamArgs& a, void* stream, bool pdl);
 int launch_kv8_reorder(const ReorderArgs& a, void* stream, bool pdl);
 

@@ -10,7 +10,7 @@
 namespace oscar {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kAhead = 8;  // loads of a thread that are under way
 
 __global__ void __launch_bounds__(kThreads) kv8_reorder_kernel(const __grid_constant__ ReorderArgs a) {
   __shared__ int s_par[kMaxBeams];
@@ -72,11 +72,23 @@ __global__ void __launch_bounds__(kThreads) kv8_reorder_kernel(const __grid_cons
   if (vecs == 0) return;
   const size_t half = (size_t)g.P * g.D, region = (size_t)g.Hkv * 2 * half, layer = (size_t)g.max_req * region;
   const int parts = 2 * g.Hkv, total = g.L * parts;
-  for (int u = blockIdx.x; u < total; u += gridDim.x) {
-    const size_t at = (size_t)(u / parts) * layer + (size_t)(u % parts) * half;
-    const uint4* src = reinterpret_cast<const uint4*>(a.tail + at + (size_t)src_slot * region);
-    uint4* dst = reinterpret_cast<uint4*>(a.tail + at + (size_t)slot * region);
-    for (int i = tid; i < vecs; i += kThreads) dst[i] = src[i];
+  const uint16_t* src = a.tail + (size_t)src_slot * region;
+  uint16_t* dst = a.tail + (size_t)slot * region;
+  // this CTA's share of the (layer, kv head, K or V) runs, as one range of vectors
+  const int u0 = (int)((long long)total * blockIdx.x / gridDim.x), u1 = (int)((long long)total * (blockIdx.x + 1) / gridDim.x);
+  const unsigned all = (unsigned)(u1 - u0) * vecs;      // (fits: 2 Hkv L runs of at most 1024 vectors in a grid's share)
+  for (unsigned i0 = tid; i0 < all; i0 += kAhead * kThreads) {
+    uint4 x[kAhead];
+    size_t at[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const unsigned i = min(i0 + k * kThreads, all - 1), u = i / vecs;
+      at[k] = (size_t)((u0 + u) / parts) * layer + (size_t)((u0 + u) % parts) * half + (size_t)(i - u * vecs) * 8;
+      x[k] = __ldcs(reinterpret_cast<const uint4*>(src + at[k]));
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (i0 + k * kThreads < all) __stcs(reinterpret_cast<uint4*>(dst + at[k]), x[k]);
   }
 }
 
@@ -86,7 +98,7 @@ int launch_kv8_reorder(const ReorderArgs& a, void* stream, bool pdl) {
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int rows = a.batch * a.beams, units = a.g.L * 2 * a.g.Hkv;
   // enough CTAs for every SM, and no more: most children keep their slot, and theirs end at once
-  int x = (152 * 16 + rows - 1) / rows;
+  int x = (152 * 32 + rows - 1) / rows;
   x = x < units ? x : units;
   return launch_pdl(kv8_reorder_kernel, dim3(x, rows), dim3(kThreads), 0, s, pdl, a);
 }

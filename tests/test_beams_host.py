@@ -71,10 +71,9 @@ def test_workspace_sizes(osc):
 
 @pytest.mark.parametrize("beams", [1, 2, 7, 64])
 @pytest.mark.parametrize("vocab", [1, 1024, 1025, 50021, 131072, 1 << 24])
-def test_a_plan_holds_every_logit_in_at_most_1024_chunks_of_an_item(osc, beams, vocab):
+def test_the_workspace_holds_two_numbers_for_every_1024_logits(osc, beams, vocab):
     for n_out in (1, 16, 64):
-        chunks = osc.oscar_beam_select_workspace_size(1, beams, vocab, n_out) // (8 * beams)
-        assert 1 <= chunks <= -(-vocab // 1024) and chunks * beams <= 1024
+        assert osc.oscar_beam_select_workspace_size(3, beams, vocab, n_out) == 3 * beams * -(-vocab // 1024) * 8
 
 
 def test_calls_without_a_bound_cache_are_refused(osc):

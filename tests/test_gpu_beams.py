@@ -768,7 +768,7 @@ def test_kernel_times_and_launches_by_name(osc, choose):
     before = osc.oscar_launch_count(choose.ctx)
     osc.oscar_set_timing(choose.ctx, True)
     choose(logits(rng, 1, 2, 500, torch.float32), np.zeros((1, 2)), 2)
-    assert [osc.oscar_kernel_time(choose.ctx, n)[1] for n in ("beam_chunks", "beam_pick")] == [1, 1]
+    assert [osc.oscar_kernel_time(choose.ctx, n)[1] for n in ("beam_units", "beam_pick")] == [1, 1]
     osc.oscar_set_timing(choose.ctx, False)
     osc.oscar_reset_timing(choose.ctx)
     assert osc.oscar_launch_count(choose.ctx) == before + 2
