@@ -90,9 +90,9 @@ __global__ void __launch_bounds__(kUnitThreads) beam_unit_kernel(const __grid_co
 
 // ------------------------------------------------------------------ candidates
 constexpr int kPickThreads = 1024, kPickWarps = kPickThreads / 32;
-constexpr int kMostPushed = 128;                           // candidates that a warp hands in of a unit
-constexpr int kRoom = kMaxCandidates + kPickWarps * kMostPushed;   // candidates at hand: those kept and the warps' most
-constexpr int kFirst = 4;                                  // units that are looked through first
+constexpr int kSlice = 128;                                // logits of a unit that a warp looks through, four a lane
+constexpr int kRound = kPickWarps * kSlice / kBeamUnit;    // units looked through at a time
+constexpr int kRoom = kMaxCandidates + kPickWarps * kSlice;  // candidates at hand: those kept and the warps' most
 
 // A double as an unsigned number of the same order; 0 stands for no candidate (-infinity).
 __device__ __forceinline__ unsigned long long ordered(double k) {
@@ -124,9 +124,10 @@ struct Entry {
 
 struct PickSmem {
   Entry pool[kRoom], kept[kMaxCandidates];
-  Entry group[kPickThreads / 8];
-  int group_unit[kPickThreads / 8], first[kFirst];
-  double norm[kMaxBeams];     // log of the sum of exponentials
+  float group[kPickThreads / 8];
+  int group_unit[kPickThreads / 8], first[kRound];
+  float mark[kPickWarps];
+  float norm[kMaxBeams], norm_lo[kMaxBeams];  // log of the sum of exponentials, as two numbers
   float top[kMaxBeams];       // m_i
   float score[kMaxBeams];
   int kind[kMaxBeams];        // 0: open, 1: finished, 2: no candidates
@@ -136,7 +137,7 @@ struct PickSmem {
 };
 
 __device__ __forceinline__ double key_of(const PickSmem& s, int i, float x) {
-  return (double)s.score[i] + (((double)x - (double)s.top[i]) - s.norm[i]);
+  return (double)s.score[i] + (((double)x - (double)s.top[i]) - ((double)s.norm[i] + (double)s.norm_lo[i]));
 }
 
 // Places of n entries among themselves, eight threads an entry; the first `most` of them are handed to put(place, entry).
@@ -155,8 +156,6 @@ __device__ __forceinline__ void rank_entries(int n, int most, const Entry* list,
 
 template <bool BF16>
 __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_constant__ BeamArgs a) {
-  using V = Vec<BF16>;
-  constexpr int kVecs = kBeamUnit / (32 * V::N);
   extern __shared__ __align__(16) uint8_t smem_raw[];
   PickSmem& s = *reinterpret_cast<PickSmem*>(smem_raw);
   const int b = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -178,7 +177,12 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
     int kind = a.finished && a.finished[row] ? 1 : 0;
     bool sound = score < INFINITY;                       // (false for a NaN)
     float m = -INFINITY;
-    double sum = 0.0;
+    float sum = 0.f, rest = 0.f;                          // rest: what the additions lose
+    auto add = [&](float y) {
+      const float t = sum + y, z = t - sum;
+      rest += (sum - (t - z)) + (y - z);
+      sum = t;
+    };
     if (kind == 0) {                                      // (else nothing was written there)
 #pragma unroll
       for (int k = 0; k < kHold; ++k) {
@@ -194,11 +198,15 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
       for (int d = 16; d; d >>= 1) m = warp_max_xor(m, d);
       if (m > -INFINITY) {
 #pragma unroll
-        for (int k = 0; k < kHold; ++k) sum += (double)(p[k].y * expf(p[k].x - m));
-        for (int c = lane + 32 * kHold; c < units; c += 32) sum += (double)(mine[c].y * expf(mine[c].x - m));
+        for (int k = 0; k < kHold; ++k) add(p[k].y * expf(p[k].x - m));
+        for (int c = lane + 32 * kHold; c < units; c += 32) add(mine[c].y * expf(mine[c].x - m));
       }
-#pragma unroll
-      for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+#pragma unroll 1
+      for (int d = 16; d; d >>= 1) {
+        const float other = __shfl_xor_sync(0xffffffffu, sum, d), its = __shfl_xor_sync(0xffffffffu, rest, d);
+        add(other);
+        rest += its;
+      }
       if (m == -INFINITY) kind = 2;
     }
     sound = __all_sync(0xffffffffu, sound);
@@ -206,10 +214,11 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
     if (lane == 0) {
       if (!sound) flag_error(a.status, kDevBadValue);
       // log of the sum: float32's, and a Newton step for what it leaves out
-      const float total = (float)sum, y = logf(total), rest = fmaf(total, expf(-y), -1.f);
+      const float y = logf(sum);
       s.score[i] = score;
       s.top[i] = m;
-      s.norm[i] = kind == 0 ? (double)y + (double)rest : 0.0;
+      s.norm[i] = kind == 0 ? y : 0.f;
+      s.norm_lo[i] = kind == 0 ? fmaf(sum, expf(-y), -1.f) + rest / sum : 0.f;
       s.kind[i] = kind;
     }
   }
@@ -218,94 +227,85 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
     s.count = s.n_kept = s.n_first = 0;
   }
   __syncthreads();
-  // What a unit has of candidates that can be among the first N, to the pool.  At least N of its logits are no less than the N-th
-  // largest of its lanes' largest (or half as many lanes have a second one of at least that): those before the floor among
-  // them, unless equal ones make them too many.
-  auto look_through = [&](int u) {
-    const Entry floor = s.floor;
-    const int i = u / units, at = (u - i * units) * kBeamUnit;
-    if (s.kind[i] == 1) {
-      if (lane == 0) s.pool[atomicAdd(&s.count, 1)].order = order_of(i, 0.f, a.pad_token);
-      return;
-    }
-    const void* row = row_of(a, (long long)b * K + i);
-    const bool aligned = (reinterpret_cast<uintptr_t>(row) & 15) == 0;
-    V v[kVecs];
-#pragma unroll
-    for (int k = 0; k < kVecs; ++k) v[k].load(row, at + (k * 32 + lane) * V::N, a.vocab, aligned);
-    float one = -INFINITY, two = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < kVecs; ++k)
-#pragma unroll
-      for (int j = 0; j < V::N; ++j) {
-        const float x = v[k].get(j);
-        two = fmaxf(two, fminf(one, x));
-        one = fmaxf(one, x);
-      }
-    const float mark = N <= 32 ? one : two;
-    const int need = N <= 32 ? N : (N + 1) / 2;
-    int before = 0;
-#pragma unroll
-    for (int d = 1; d < 32; ++d) {
-      const int from = (lane + d) & 31;
-      const float o = __shfl_sync(0xffffffffu, mark, from);
-      before += o > mark || (o == mark && from < lane);
-    }
-    const int src = __ffs(__ballot_sync(0xffffffffu, before == need - 1)) - 1;
-    // the least logit whose key can reach the floor, a little below it
-    float least = fmaxf(-3.402823466e38f, __shfl_sync(0xffffffffu, mark, src));
-    if (floor.key) {
-      const double t = ((from_ordered(floor.key) - (double)s.score[i]) + s.norm[i]) + (double)s.top[i];
-      least = fmaxf(least, __double2float_rd(t - fabs(t) * 1e-14 - 1e-12));
-    }
-    int mine = 0;
-#pragma unroll
-    for (int k = 0; k < kVecs; ++k)
-#pragma unroll
-      for (int j = 0; j < V::N; ++j) mine += v[k].get(j) >= least;
-    const int all = __reduce_add_sync(0xffffffffu, mine);
-    if (all == 0) return;
-    if (all <= kMostPushed) {
-      int to = 0;
-      if (lane == 0) to = atomicAdd(&s.count, all);
-      to = __shfl_sync(0xffffffffu, to, 0);
-      int sum = mine;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, sum, d);
-        if (lane >= d) sum += o;
-      }
-      to += sum - mine;
-      if (mine > 0)
-#pragma unroll
-        for (int k = 0; k < kVecs; ++k)
-#pragma unroll
-          for (int j = 0; j < V::N; ++j)
-            if (v[k].get(j) >= least)
-              s.pool[to++].order = order_of(i, v[k].get(j), at + (k * 32 + lane) * V::N + j);
-      return;
-    }
-    float last = INFINITY;                                // the unit's N first, one after another
-    int after = -1;
-    for (int n = 0; n < N; ++n) {
-      float top = -INFINITY;
-      int where = 0x7fffffff;
-#pragma unroll
-      for (int k = 0; k < kVecs; ++k)
-#pragma unroll
-        for (int j = 0; j < V::N; ++j) {
-          const float x = v[k].get(j);
-          const int p = at + (k * 32 + lane) * V::N + j;
-          if (x > top && (x < last || (x == last && p > after))) top = x, where = p;
+  // What `n` units (at most kRound) have of candidates that can be among the first N, to the pool.  A slice has N logits that are no
+  // less than the N-th largest of its lanes' largest (half as many lanes with a second one for more than 32): the best of those
+  // marks is a floor.  Of logits that equal a slice's own mark N are enough.
+  auto look_through = [&](const int* list, int n) {
+    constexpr int kShare = kPickWarps / kRound;           // warps of a unit
+    const int which = warp / kShare;
+    const int u = which < n ? list[which] : 0, i = u / units, at = (u - i * units) * kBeamUnit + (warp % kShare) * kSlice + lane * 4;
+    const bool open = which < n && s.kind[i] == 0;
+    float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, mark = -INFINITY, shift = 0.f;
+    if (which < n && !open && warp % kShare == 0 && lane == 0) s.pool[atomicAdd(&s.count, 1)].order = order_of(i, 0.f, a.pad_token);
+    if (open) {
+      const uint8_t* row = static_cast<const uint8_t*>(row_of(a, (long long)b * K + i)) + (size_t)at * (BF16 ? 2 : 4);
+      if (at + 4 <= a.vocab && (reinterpret_cast<uintptr_t>(row) & (BF16 ? 7 : 15)) == 0) {
+        if constexpr (BF16) {
+          const uint2 w = *reinterpret_cast<const uint2*>(row);
+          x[0] = bf16_lo(w.x), x[1] = bf16_hi(w.x), x[2] = bf16_lo(w.y), x[3] = bf16_hi(w.y);
+        } else {
+          const float4 w = *reinterpret_cast<const float4*>(row);
+          x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w;
         }
-      float best = top;
+      } else {
 #pragma unroll
-      for (int d = 16; d; d >>= 1) best = warp_max_xor(best, d);
-      const int first = __reduce_min_sync(0xffffffffu, top == best ? where : 0x7fffffff);
-      if (!(best >= least)) break;
-      if (lane == 0) s.pool[atomicAdd(&s.count, 1)].order = order_of(i, best, first);
-      last = best, after = first;
+        for (int j = 0; j < 4; ++j)
+          if (at + j < a.vocab)
+            x[j] = BF16 ? __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row)[j] << 16) : reinterpret_cast<const float*>(row)[j];
+      }
+      const float hi0 = fmaxf(x[0], x[1]), lo0 = fminf(x[0], x[1]), hi1 = fmaxf(x[2], x[3]), lo1 = fminf(x[2], x[3]);
+      float y = N <= 32 ? fmaxf(hi0, hi1) : fmaxf(fminf(hi0, hi1), hi0 > hi1 ? lo0 : lo1);
+      // the lanes' values in ascending order
+#pragma unroll
+      for (int k = 2; k <= 32; k <<= 1)
+#pragma unroll
+        for (int d = k >> 1; d; d >>= 1) {
+          const float o = __shfl_xor_sync(0xffffffffu, y, d);
+          y = ((lane & d) == 0) == ((lane & k) == 0) ? fminf(y, o) : fmaxf(y, o);
+        }
+      mark = __shfl_sync(0xffffffffu, y, 32 - (N <= 32 ? N : (N + 1) / 2));
+      shift = s.score[i] - s.norm[i] - s.top[i];
     }
+    // (float32 keys, with room for what they lose: the keys proper come later)
+    const float slack = open ? 1e-6f * (fabsf(s.score[i]) + s.norm[i] + 2.f * fabsf(s.top[i]) + 1.f) : 0.f;
+    if (lane == 0) s.mark[warp] = mark > -INFINITY ? mark + shift - slack - 1e-6f * fabsf(mark) : -INFINITY;
+    __syncthreads();
+    float floor = s.mark[lane];
+#pragma unroll
+    for (int d = 16; d; d >>= 1) floor = warp_max_xor(floor, d);
+    if (s.floor.key) floor = fmaxf(floor, (float)from_ordered(s.floor.key));
+    if (!open) return;
+    const float least = floor == -INFINITY ? -3.402823466e38f : floor - shift - slack - 1e-6f * fabsf(floor);
+    unsigned ties = 0, takes = 0;                         // of this lane's logits
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      ties |= (unsigned)(x[j] == mark && x[j] > -INFINITY) << j;
+      takes |= (unsigned)(x[j] >= least && x[j] > -INFINITY) << j;
+    }
+    ties &= takes;
+    int scan = __popc(ties);
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, scan, d);
+      if (lane >= d) scan += o;
+    }
+    int before = scan - __popc(ties);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (ties >> j & 1)
+        if (before++ >= N) takes &= ~(1u << j);
+    int mine = __popc(takes), sum = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, sum, d);
+      if (lane >= d) sum += o;
+    }
+    int to = 0;
+    if (lane == 31 && sum > 0) to = atomicAdd(&s.count, sum);
+    to = __shfl_sync(0xffffffffu, to, 31) + sum - mine;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (takes >> j & 1) s.pool[to++].order = order_of(i, x[j], at + j);
   };
   // The first N of the pool stay, in order; N of them are a floor.
   auto keep_first = [&]() {
@@ -330,43 +330,63 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
     __syncthreads();
   };
   for (int u0 = 0; u0 < total; u0 += kPickThreads) {
-    // a thread's unit: its largest candidate
+    // a thread's unit: its largest candidate's key, and how far float32 may be off
     const int u = u0 + tid, i = u < total ? u / units : 0, c = u - i * units;
-    Entry mine{0, 0};
+    float top = 0.f, key = -INFINITY, off = 0.f;
+    bool there = false;
     if (u < total && s.kind[i] == 0) {
-      const float top = u0 == 0 ? own_top : part[u].x;
-      mine = Entry{ordered(key_of(s, i, top)), order_of(i, top, c * kBeamUnit)};
+      top = u0 == 0 ? own_top : part[u].x;
+      there = top > -INFINITY;
+      const float low = top - s.top[i];
+      key = s.score[i] + (low - s.norm[i]);
+      off = 1e-6f * (fabsf(s.score[i]) + fabsf(low) + s.norm[i] + fabsf(key) + 1.f);
     } else if (u < total && s.kind[i] == 1 && c == 0) {
-      mine = Entry{ordered((double)s.score[i]), order_of(i, 0.f, 0)};
+      there = true;
+      key = s.score[i];
     }
     if (u0 == 0) {  // the best units of the best groups of eight
-      Entry best = mine;
+      float best = there ? key : -INFINITY;
       int unit = u;
 #pragma unroll
       for (int d = 1; d < 8; d <<= 1) {
-        const Entry o{__shfl_xor_sync(0xffffffffu, best.key, d), __shfl_xor_sync(0xffffffffu, best.order, d)};
+        const float o = __shfl_xor_sync(0xffffffffu, best, d);
         const int other = __shfl_xor_sync(0xffffffffu, unit, d);
-        if (o.before(best)) best = o, unit = other;
+        if (o > best || (o == best && other < unit)) best = o, unit = other;
       }
       if ((tid & 7) == 0) {
         s.group[tid >> 3] = best;
         s.group_unit[tid >> 3] = unit;
       }
       __syncthreads();
-      const int groups = (min(total, kPickThreads) + 7) / 8;
-      rank_entries(groups, kFirst, s.group, [&](int place, int e) {
-        s.first[place] = s.group_unit[e];
-        atomicMax(&s.n_first, place + 1);
-      });
+      {
+        const int e = tid >> 3;
+        const float own = s.group[e];
+        int before = 0;
+#pragma unroll
+        for (int o = tid & 7; o < kPickThreads / 8; o += 8) before += s.group[o] > own || (s.group[o] == own && o < e);
+#pragma unroll
+        for (int d = 1; d < 8; d <<= 1) before += __shfl_xor_sync(0xffffffffu, before, d);
+        if ((tid & 7) == 0 && own > -INFINITY && before < kRound) {
+          s.first[before] = s.group_unit[e];
+          atomicMax(&s.n_first, before + 1);
+        }
+      }
       __syncthreads();
-      if (warp < s.n_first) look_through(s.first[warp]);
+      look_through(s.first, s.n_first);
       keep_first();
-      for (int k = 0; k < s.n_first; ++k)
-        if (s.first[k] == u) mine.key = 0;                // (done)
+      for (int k = 0; k < s.n_first; ++k) there &= s.first[k] != u;  // (done)
     }
     if (tid == 0) s.n_unit = 0;
     __syncthreads();
-    const bool look = mine.key != 0 && !s.floor.before(mine);
+    const Entry floor = s.floor;
+    bool look = there;
+    if (there && floor.key) {
+      const float f = (float)from_ordered(floor.key);
+      off += 1e-6f * fabsf(f);
+      look = key >= f - off;
+      if (look && key <= f + off)
+        look = !floor.before(Entry{ordered(s.kind[i] == 1 ? (double)s.score[i] : key_of(s, i, top)), order_of(i, top, c * kBeamUnit)});
+    }
     const unsigned some = __ballot_sync(0xffffffffu, look);
     if (some) {
       int to = 0;
@@ -376,8 +396,8 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
     }
     __syncthreads();
     const int n_unit = s.n_unit;
-    for (int r = 0; r < n_unit; r += kPickWarps) {
-      if (r + warp < n_unit) look_through(s.unit[r + warp]);
+    for (int r = 0; r < n_unit; r += kRound) {
+      look_through(s.unit + r, min(n_unit - r, kRound));
       keep_first();
     }
   }
