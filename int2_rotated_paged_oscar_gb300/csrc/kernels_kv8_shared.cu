@@ -30,21 +30,23 @@ constexpr int kSoft = 8, kConv = 8;                       // warps
 constexpr int kThreads = 32 * (kSoft + kConv + 2);
 constexpr int kRows = 128;
 constexpr int kMostPages = 2048;                          // pages of a split
-// Tensor memory, all of it (so that it begins at 0): scores, then weights, of three tiles; sums.
-constexpr uint32_t kColO = 384, kCols = 512;
-constexpr int NS = 3;
-OSCAR_HD constexpr uint32_t col_s(int s) { return 128 * s; }
+// Tensor memory, all of it (so that it begins at 0): scores, then weights, of two or three tiles; sums.  The tensor cores' additions
+// round towards zero: over thousands of tokens that would be 10^-6 of a sum and more, so for float32 outputs the sums are added up
+// in float32 proper every kFlush tokens (0.9 10^-6 of bias at 2000 tokens a split without, 0.3 with).
+constexpr uint32_t kColTotal = 256, kColO = 384, kCols = 512;
+constexpr int kFlush = 512, kMostSlots = 3;
 // A row's reference exponent follows its maximum when it is kLag behind; V scales are relative to a power of two that follows
 // the largest when it is 2^kScaleLag behind; a weight of 1 at scale 1 is 2^kBase: below 2^(kLag + kScaleLag + 1 + kBase) = 2^15.
 constexpr float kLag = 10.f;
 constexpr int kScaleLag = 1, kBase = 3;
 constexpr float kFar = 4194304.f;                         // scores (log2) whose last place counts
 
-template <int D, bool QF32>
+template <int D, bool QF32, int TERMS>
 struct Lay {
   static constexpr int QT = QF32 ? 3 : 1;                 // terms of a query
   static constexpr int NT = QF32 ? 64 : 128;              // tokens of a tile
   static constexpr int HC = NT / 2;                       // tokens of a half
+  static constexpr int NS = TERMS == 2 && !QF32 ? 2 : 3;  // tiles of scores in tensor memory
   static constexpr int kQ = kRows * D * 2, kKV = NT * D * 2;
   static constexpr int oQ = 0, oK = oQ + QT * kQ, oV = oK + 2 * kKV, oPages = oV + 2 * kKV;
   static constexpr int kSmem = oPages + kMostPages * 4 + 1024;
@@ -53,9 +55,9 @@ struct Lay {
 
 struct Shared {
   // K(i) written and S's place free; S(i) there and scales written; P(i) there and V(i) written; K read; V read and P V done
-  uint64_t qk_ready[NS], s_full[NS], pv_ready[NS], k_empty[2], v_empty[2], end;
-  float ks[NS][8], vs[NS][8];    // per group of 16 tokens (of one page): K scale, V scale relative to 2^e (2^kBase at 1)
-  int mask[NS], e[NS];           // groups that are there
+  uint64_t qk_ready[kMostSlots], s_full[kMostSlots], pv_ready[kMostSlots], k_empty[2], v_empty[2], end;
+  float ks[kMostSlots][8], vs[kMostSlots][8];    // per group of 16 tokens (of one page): K scale, V scale relative to 2^e (2^kBase at 1)
+  int mask[kMostSlots], e[kMostSlots];           // groups that are there
   float top[2][2][kRows];        // a half's largest scores, of even and odd tiles
   float l[2][kRows];             // a half's sum, at the end
   uint32_t there[kMostPages / 32];  // pages that are mapped
@@ -215,6 +217,21 @@ __device__ __forceinline__ void scale_sums(uint32_t at, float scale) {
   }
 }
 
+// total = (total + sums) scale, without a total yet sums scale.
+template <int D>
+__device__ __forceinline__ void add_sums(uint32_t total, uint32_t at, float scale, bool some) {
+#pragma unroll 1
+  for (int c = 0; c < D; c += 32) {
+    uint32_t x[32], y[32];
+    tmem_ld32_nowait(at + c, x);
+    tmem_ld32_nowait(total + c, y);
+    tmem_wait_ld();
+#pragma unroll
+    for (int j = 0; j < 32; ++j) x[j] = __float_as_uint((__uint_as_float(x[j]) + (some ? __uint_as_float(y[j]) : 0.f)) * scale);
+    tmem_st32(total + c, x);
+  }
+}
+
 // 16 bytes that no one writes while the kernel runs, read once by each SM; in the order of the code (the compiler would move a
 // plain load down to its use).
 __device__ __forceinline__ uint4 load_codes(const uint8_t* p) {
@@ -225,8 +242,10 @@ __device__ __forceinline__ uint4 load_codes(const uint8_t* p) {
 
 template <int D, int FMT, bool QF32, int TERMS>
 __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_constant__ Kv8DecodeArgs a) {
-  using L = Lay<D, QF32>;
-  constexpr int QT = L::QT, NT = L::NT, HC = L::HC, NG = HC / 16;
+  using L = Lay<D, QF32, TERMS>;
+  constexpr int QT = L::QT, NT = L::NT, HC = L::HC, NG = HC / 16, NS = L::NS, kPeriod = kFlush / NT;
+  constexpr bool kTwo = TERMS == 2;                       // sums in two parts
+  auto col_s = [](int s) -> uint32_t { return NT * s; };
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ Shared sh;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -442,11 +461,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
             l += weigh<HC, TERMS>(x, cm, f, at, ks, vs, qs, qs_lo, ref);
           else
             l += weigh_with_care<HC, TERMS>(at, ks, vs, qs, qs_lo, ref, mask);
-          if (__any_sync(0xffffffffu, alpha != 1.f) || e != e_old) {  // (the weights first: by now the sums so far are done)
+          const bool flush = kTwo && i > 0 && i % kPeriod == 0;
+          if (__any_sync(0xffffffffu, alpha != 1.f) || e != e_old || flush) {  // (the weights first: by now the sums so far are done)
             good = mbar_wait_sleep_bounded(&sh.v_empty[(i - 1) & 1], ((i - 1) >> 1) & 1, a.status);
             good = __all_sync(0xffffffffu, good);
             tc_fence_after();
-            if (good) scale_sums<D / 2>(base + kColO + half * (D / 2), alpha * exp2f((float)(e_old - e)));
+            const float scale = alpha * exp2f((float)(e_old - e));
+            const uint32_t o_at = base + kColO + half * (D / 2), total_at = base + kColTotal + half * (D / 2);
+            if (good) {
+              if (flush) {
+                add_sums<D / 2>(total_at, o_at, scale, i > kPeriod);
+              } else {
+                scale_sums<D / 2>(o_at, scale);
+                if (kTwo && i > kPeriod) scale_sums<D / 2>(total_at, scale);
+              }
+            }
           }
           tmem_wait_st();
           tc_fence_before();
@@ -598,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
 #pragma unroll
           for (int kk = 0; kk < NT / 16; ++kk)            // (a half's weights: its first terms, then its second ones)
             tc_mma_ts(kColO, col_s(s) + HC * (kk / NG) + u * (HC / 2) + 8 * (kk % NG), vd + ((kk * 2048) >> 4), kIdesc,
-                      i > 0 || u < TERMS - 1 || kk);
+                      (kTwo ? i % kPeriod : i) > 0 || u < TERMS - 1 || kk);
         tc_commit(&sh.qk_ready[s]);
         tc_commit(&sh.v_empty[b]);
       }
@@ -621,6 +650,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
     for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {  // (each half of the threads stores half of the channels)
       float v[32];
       tmem_ld32(base + kColO + c, v);
+      if (kTwo && tiles > kPeriod) {
+        float more[32];
+        tmem_ld32(base + kColTotal + c, more);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] += more[j];
+      }
       if (valid)
 #pragma unroll
         for (int j = 0; j < 32; j += 4)
@@ -637,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
 Kv8DecodeWs kv8_shared_plan(const Geom& g, int batch, int n_groups, int max_shared, int max_own, Kv8Groups* groups, int* own_splits) {
   Kv8DecodeWs w = kv8_plan(g, batch, max_own / g.P);
   *own_splits = w.max_splits;
-  // The split that takes the fewest rounds of (its units + 3, a CTA's start and end).
+  // The split that takes the fewest rounds of (its units + 5, a CTA's start and end).
   const long long tiles = ((long long)max_shared * g.P + kPrefixUnit - 1) / kPrefixUnit;
   const long long rows = (long long)batch * g.gq(), row_tiles = rows / kRows > n_groups ? rows / kRows : n_groups;
   const long long pairs = row_tiles * g.Hkv > 0 ? row_tiles * g.Hkv : 1;
@@ -648,7 +683,7 @@ Kv8DecodeWs kv8_shared_plan(const Geom& g, int batch, int n_groups, int max_shar
     const long long fit = 152 * rounds / pairs, splits = fit < all ? fit : all;
     if (splits == 0) continue;
     const long long per = (all + splits - 1) / splits;
-    const long long c = ((pairs * ((all + per - 1) / per) + 151) / 152) * (per + 3);
+    const long long c = ((pairs * ((all + per - 1) / per) + 151) / 152) * (per + 5);
     if (per <= most && (cost < 0 || c < cost)) best = per, cost = c;
   }
   groups->n = n_groups;
@@ -671,10 +706,10 @@ static int launch_prefix(const Kv8DecodeArgs& a, cudaStream_t s, bool pdl) {
     return launch_pdl(kern, grid, dim3(kThreads), smem, s, pdl, a);
   };
   if (a.out_dtype == kDtypeF32)
-    return a.q_dtype == kDtypeF32 ? go(kv8_prefix_kernel<D, FMT, true, 2>, Lay<D, true>::kSmem)
-                                  : go(kv8_prefix_kernel<D, FMT, false, 2>, Lay<D, false>::kSmem);
-  return a.q_dtype == kDtypeF32 ? go(kv8_prefix_kernel<D, FMT, true, 1>, Lay<D, true>::kSmem)
-                                : go(kv8_prefix_kernel<D, FMT, false, 1>, Lay<D, false>::kSmem);
+    return a.q_dtype == kDtypeF32 ? go(kv8_prefix_kernel<D, FMT, true, 2>, Lay<D, true, 1>::kSmem)
+                                  : go(kv8_prefix_kernel<D, FMT, false, 2>, Lay<D, false, 1>::kSmem);
+  return a.q_dtype == kDtypeF32 ? go(kv8_prefix_kernel<D, FMT, true, 1>, Lay<D, true, 1>::kSmem)
+                                : go(kv8_prefix_kernel<D, FMT, false, 1>, Lay<D, false, 1>::kSmem);
 }
 
 int launch_kv8_shared_prefix(const Kv8DecodeArgs& a, void* stream, bool pdl) {
