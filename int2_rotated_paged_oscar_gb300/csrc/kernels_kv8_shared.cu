@@ -53,13 +53,20 @@ struct Lay {
   static constexpr int kTasks = NT * D / 16 / (32 * kConv);  // 16-byte chunks of keys (and of values) a thread takes of a tile
 };
 
+// Per group of 16 tokens (of one page): K scale; V scale relative to 2^e (2^kBase at 1), its logarithm and its inverse.
+struct Scales {
+  float ks[8], vs[8], lg[8], inv[8];
+};
+
 struct Shared {
   // K(i) written and S's place free; S(i) there and scales written; P(i) there and V(i) written; K read; V read and P V done
   uint64_t qk_ready[kMostSlots], s_full[kMostSlots], pv_ready[kMostSlots], k_empty[2], v_empty[2], end;
-  float ks[kMostSlots][8], vs[kMostSlots][8];    // per group of 16 tokens (of one page): K scale, V scale relative to 2^e (2^kBase at 1)
-  int mask[kMostSlots], e[kMostSlots];           // groups that are there
+  Scales sc[kMostSlots];
+  int mask[kMostSlots], plain[kMostSlots], e[kMostSlots];  // groups that are there; all are, with V scales
   float top[2][2][kRows];        // a half's largest scores, of even and odd tiles
   float l[2][kRows];             // a half's sum, at the end
+  float down[kRows];             // what the power of two of a row's query leaves to multiply by
+  int row_req[kRows];            // a row's request, -1 for none
   uint32_t there[kMostPages / 32];  // pages that are mapped
   uint32_t tmem;
   int lo, size, shared, tile, holder, holes;
@@ -112,33 +119,43 @@ __device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
   return r;
 }
 
-// Weights of a row's scores in a tile: 2^(score - m) by the page's V scale, as TERMS f16 numbers.  The sum of the weights before
-// the V scale is returned.  A score's scale f = K scale x query scale has a rounding; what it leaves out at a page's largest
-// score goes into the page's weights where they are held to 22 bits.
-template <int HC, int TERMS>
-__device__ __forceinline__ float weigh(const uint32_t (&x)[HC], const float (&cm)[HC / 16], const float (&f)[HC / 16], uint32_t at, const float* ks,
-                                       const float* vs, float qs, float qs_lo, float ref) {
-  const uint64_t bias = pair(-ref, -ref);
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
+
+// Weights of a row's scores in a half tile, 2^(score - m) by the page's V scale, as TERMS f16 numbers; the sum of the weights before
+// the V scale is returned.  One number: the V scale is in the exponent, and out of the sum again.  Two numbers, of 22 bits: it is
+// a factor, with what the rounding of a score's scale f = K scale x query scale leaves out at the group's largest score.
+// ONE: all of the half tile's tokens are of one page.
+template <int HC, int TERMS, bool ONE>
+__device__ __forceinline__ float weigh(const uint32_t (&x)[HC], const float (&cm)[HC / 16], const float (&f)[HC / 16], uint32_t at,
+                                       const float* ks, float qs, float qs_lo, float ref) {
+  const float *vs = ks + 8, *lg = ks + 16, *inv = ks + 24;  // (of Scales)
   float total = 0.f;
 #pragma unroll
   for (int c = 0; c < HC / 32; ++c) {
     uint32_t hi[16], lo[16];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int k = 2 * c + u;
-      float g = vs[k], fix = 1.f;
+      const int k = 2 * c + u, s = ONE ? 0 : k;
+      float g = 1.f, back = 1.f, bias = -ref;
       if constexpr (TERMS == 2) {
-        fix = ex2(fminf(cm[k] * fmaf(ks[k], qs_lo, fmaf(ks[k], qs, -f[k])), 1.f));
-        g *= fix;
+        back = ex2(fminf(cm[k] * fmaf(ks[s], qs_lo, fmaf(ks[s], qs, -f[s])), 1.f));
+        g = vs[s] * back;
+      } else {
+        bias += lg[s];
+        back = inv[s];
       }
-      const uint64_t ff = pair(f[k], f[k]), gg = pair(g, g);
+      const uint64_t ff = pair(f[s], f[s]), bb = pair(bias, bias), gg = pair(g, g);
       uint64_t sum[2] = {0, 0};
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const uint64_t e = fma2(pair(x[32 * c + 16 * u + 2 * j], x[32 * c + 16 * u + 2 * j + 1]), ff, bias);
-        const uint64_t p = pair(ex2(first(e)), ex2(second(e)));
-        sum[j & 1] = add2(sum[j & 1], p);
-        const uint64_t w = mul2(p, gg);
+        const uint64_t e = fma2(pair(x[32 * c + 16 * u + 2 * j], x[32 * c + 16 * u + 2 * j + 1]), ff, bb);
+        uint64_t w = pair(ex2(first(e)), ex2(second(e)));
+        sum[j & 1] = add2(sum[j & 1], w);
+        if constexpr (TERMS == 2) w = mul2(w, gg);
         hi[8 * u + j] = pack_half2(first(w), second(w));
         if constexpr (TERMS == 2) {
           const __half2 h = *reinterpret_cast<const __half2*>(&hi[8 * u + j]);
@@ -146,7 +163,7 @@ __device__ __forceinline__ float weigh(const uint32_t (&x)[HC], const float (&cm
         }
       }
       const uint64_t both = add2(sum[0], sum[1]);
-      total = fmaf(first(both) + second(both), fix, total);
+      total = fmaf(first(both) + second(both), back, total);
     }
     tmem_st16(at + 16 * c, hi);
     if constexpr (TERMS == 2) tmem_st16(at + HC / 2 + 16 * c, lo);
@@ -154,10 +171,12 @@ __device__ __forceinline__ float weigh(const uint32_t (&x)[HC], const float (&cm
   return total;
 }
 
-// The same where some groups are not there, or some row's scores are so large (kFar) that a last place of one counts: there
-// distances are formed from the raw sums, 0 at a group's largest.  Other rows come out as from weigh, bit for bit.
+// The same where some groups are not there or have no V scale (all of a page's values 0), or some row's scores are so large (kFar)
+// that a last place of one counts: there distances are formed from the raw sums, 0 at a group's largest.  Other rows come out as
+// from weigh, bit for bit.
 template <int HC, int TERMS>
-__device__ __noinline__ float weigh_with_care(uint32_t at, const float* ks, const float* vs, float qs, float qs_lo, float ref, int mask) {
+__device__ __noinline__ float weigh_with_care(uint32_t at, const float* ks, float qs, float qs_lo, float ref, int mask) {
+  const float *vs = ks + 8, *lg = ks + 16, *inv = ks + 24;
   const bool far = fabsf(ref) >= kFar;
   float total = 0.f;
   float v[HC / 32][32];
@@ -169,32 +188,35 @@ __device__ __noinline__ float weigh_with_care(uint32_t at, const float* ks, cons
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int k = 2 * c + u;
-      const bool there = mask >> k & 1;
+      const bool there = mask >> k & 1, some = vs[k] > 0.f;
       const float f = ks[k] * qs;
-      float g = vs[k], fix = 1.f, cm = v[c][16 * u];
+      float g = 1.f, back = 1.f, more = 0.f, cm = v[c][16 * u];
 #pragma unroll
       for (int j = 1; j < 16; ++j) cm = fmaxf(cm, v[c][16 * u + j]);
       const bool apart = far && cm > -INFINITY;
       if constexpr (TERMS == 2) {
-        if (!apart && there) fix = ex2(fminf(cm * fmaf(ks[k], qs_lo, fmaf(ks[k], qs, -f)), 1.f));
-        g *= fix;
+        if (!apart && there) back = ex2(fminf(cm * fmaf(ks[k], qs_lo, fmaf(ks[k], qs, -f)), 1.f));
+        g = vs[k] * back;
+      } else if (some) {
+        more = lg[k];
+        back = inv[k];
       }
-      const float off = apart ? cm : 0.f, bias = apart ? fminf(fmaf(cm, f, -ref), kLag) : -ref;
+      const float off = apart ? cm : 0.f, bias = (apart ? fminf(fmaf(cm, f, -ref), kLag) : -ref) + more;
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         float w[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float p = there ? ex2(fmaf(v[c][16 * u + 2 * j + e] - off, f, bias)) : 0.f;
-          sum[2 * (j & 1) + e] += p;
-          w[e] = there ? p * g : 0.f;
+          w[e] = there ? ex2(fmaf(v[c][16 * u + 2 * j + e] - off, f, bias)) : 0.f;
+          sum[2 * (j & 1) + e] += w[e];
+          w[e] = there && some ? w[e] * g : 0.f;
         }
         hi[8 * u + j] = pack_half2(w[0], w[1]);
         const __half2 h = *reinterpret_cast<const __half2*>(&hi[8 * u + j]);
         lo[8 * u + j] = pack_half2(w[0] - __low2float(h), w[1] - __high2float(h));
       }
-      total = fmaf((sum[0] + sum[2]) + (sum[1] + sum[3]), fix, total);
+      total = fmaf((sum[0] + sum[2]) + (sum[1] + sum[3]), back, total);
     }
     tmem_st16(at + 16 * c, hi);
     if constexpr (TERMS == 2) tmem_st16(at + HC / 2 + 16 * c, lo);
@@ -320,17 +342,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
   const int pages = sh.holder < 0 ? 0 : min(per, sh.shared - e0);
   // the row of a softmax thread
   bool valid = false;
-  int req = 0, head = 0;
+  int req = 0;
   const int row = tid & (kRows - 1), half = warp >> 2;     // two softmax threads a row
   if (pages > 0 && warp < kSoft) {
     const int r = sh.tile * kRows + row;
     req = sh.lo + r / G;
-    head = h * G + r % G;
     if (r < sh.size * G) {
       const int n = a.seq_lens[req];
       valid = n > 0 && kv8_own_sound(a, n, sh.shared);
     }
   }
+  if (warp < kSoft / 2) sh.row_req[row] = valid ? req : -1;
   if (!__syncthreads_or(valid)) {                         // no rows, or no pages for them
     pdl_wait();
     return;
@@ -353,63 +375,73 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
       if (lane == 0) sh.there[i0 >> 5] = all;
     }
   }
-  float qs = 0.f, qs_lo = 0.f;                            // what a score's raw sum is multiplied by, but for the page's scale
   const bool live = __any_sync(0xffffffffu, valid);
-  float up = 1.f;
-  if (warp < kSoft && live) {
-    const size_t at = (size_t)req * a.q_stride + (size_t)head * D;
-    float big = 0.f;
-    if (valid)
-      for (int c = 0; c < D; c += 4) {
-        const float4 x = kv8_load4<QF32>(a.q, at + c);
-        big = fmaxf(fmaxf(big, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(x.z), fabsf(x.w)));
-      }
-    float down;
-    power_of_two(big, &up, &down);
-    constexpr double kScale = 1.4426950408889634 / (D == 128 ? 11.313708498984761 : 8.0);
-    qs = down * (float)kScale;
-    qs_lo = down * (float)(kScale - (double)(float)kScale);
-  }
-  // Half of a row's channels a thread, times up, as operands; whether f16 ones hold them
-  auto put_query = [&](bool f16) {
-    bool exact = true;
-#pragma unroll 2
-    for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 8) {
-      float x[8] = {};
-      if (valid) {
-        const size_t at = (size_t)req * a.q_stride + (size_t)head * D + c;
-        const float4 u = kv8_load4<QF32>(a.q, at), w = kv8_load4<QF32>(a.q, at + 4);
-        x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = w.x, x[5] = w.y, x[6] = w.z, x[7] = w.w;
-      }
+  // The queries as operands, eight channels a thread and D / 8 threads a row, brought near 2^14 by a power of two
+  bool exact = !QF32;                                     // keys and queries are f16 operands
+  {
+    constexpr int kLanes = D / 8, kStep = 32 * (kSoft + kConv) / kLanes, kPasses = kRows / kStep;
+    const int r0 = tid / kLanes, c = tid % kLanes * 8;
+    float4 x[kPasses][2];
+    if (warp < kSoft + kConv) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] *= up;
-#pragma unroll
-      for (int t = 0; t < QT; ++t) {
-        uint32_t w[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (f16) {
-            w[k] = pack_half2(x[2 * k], x[2 * k + 1]);
-            const __half2 h = *reinterpret_cast<const __half2*>(&w[k]);
-            exact &= __low2float(h) == x[2 * k] && __high2float(h) == x[2 * k + 1];
-          } else {
-            w[k] = pack_bf162(x[2 * k], x[2 * k + 1]);
-            x[2 * k] -= bf16_lo(w[k]);
-            x[2 * k + 1] -= bf16_hi(w[k]);
-          }
+      for (int k = 0; k < kPasses; ++k) {
+        const int r = r0 + k * kStep, its = sh.row_req[r];
+        x[k][0] = x[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (its >= 0) {
+          const size_t at = (size_t)its * a.q_stride + (size_t)(h * G + (sh.tile * kRows + r) % G) * D + c;
+          x[k][0] = kv8_load4<QF32>(a.q, at);
+          x[k][1] = kv8_load4<QF32>(a.q, at + 4);
         }
-        *reinterpret_cast<uint4*>(smem + L::oQ + t * L::kQ + sw128_offset(row, c, kRows)) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+#pragma unroll
+      for (int k = 0; k < kPasses; ++k) {
+        float4 &u = x[k][0], &w = x[k][1];
+        float big = fmaxf(fmaxf(fmaxf(fabsf(u.x), fabsf(u.y)), fmaxf(fabsf(u.z), fabsf(u.w))),
+                          fmaxf(fmaxf(fabsf(w.x), fabsf(w.y)), fmaxf(fabsf(w.z), fabsf(w.w))));
+#pragma unroll
+        for (int d = 1; d < kLanes; d <<= 1) big = warp_max_xor(big, d);
+        float up, down;
+        power_of_two(big, &up, &down);
+        if (c == 0) sh.down[r0 + k * kStep] = down;
+        u = make_float4(u.x * up, u.y * up, u.z * up, u.w * up);
+        w = make_float4(w.x * up, w.y * up, w.z * up, w.w * up);
       }
     }
-    return exact;
-  };
-  bool exact = !QF32;                                     // keys and queries are f16 operands
-  if constexpr (!QF32) exact = !__syncthreads_or(warp < kSoft && live && !put_query(true));
-  if (!exact && warp < kSoft && live) put_query(false);
+    auto put = [&](bool f16) {
+      bool all = true;
+#pragma unroll
+      for (int k = 0; k < kPasses; ++k) {
+        float y[8] = {x[k][0].x, x[k][0].y, x[k][0].z, x[k][0].w, x[k][1].x, x[k][1].y, x[k][1].z, x[k][1].w};
+#pragma unroll
+        for (int t = 0; t < QT; ++t) {
+          uint32_t w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (f16) {
+              w[j] = pack_half2(y[2 * j], y[2 * j + 1]);
+              const __half2 v = *reinterpret_cast<const __half2*>(&w[j]);
+              all &= __low2float(v) == y[2 * j] && __high2float(v) == y[2 * j + 1];
+            } else {
+              w[j] = pack_bf162(y[2 * j], y[2 * j + 1]);
+              y[2 * j] -= bf16_lo(w[j]);
+              y[2 * j + 1] -= bf16_hi(w[j]);
+            }
+          }
+          *reinterpret_cast<uint4*>(smem + L::oQ + t * L::kQ + sw128_offset(r0 + k * kStep, c, kRows)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      return all;
+    };
+    if constexpr (!QF32) exact = !__syncthreads_or(warp < kSoft + kConv && !put(true));
+    if (!exact && warp < kSoft + kConv) put(false);
+  }
   fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  constexpr double kScale = 1.4426950408889634 / (D == 128 ? 11.313708498984761 : 8.0);
+  const float down = sh.down[row], qs = down * (float)kScale;  // what a score's raw sum is multiplied by, but for the page's scale
+  const float qs_lo = down * (float)(kScale - (double)(float)kScale);
   const int tiles = (pages * P + NT - 1) / NT;
   bool good = true;
   float m = -INFINITY, l = 0.f;
@@ -426,8 +458,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
       }
       if (live) {
         const uint32_t at = base + col_s(b) + HC * half;
-        const int mask = sh.mask[b] >> (NG * half) & ((1 << NG) - 1), e = sh.e[b];
-        const float *ks = sh.ks[b] + NG * half, *vs = sh.vs[b] + NG * half;
+        const int mask = sh.mask[b] >> (NG * half) & ((1 << NG) - 1), plain = sh.plain[b], e = sh.e[b];
+        const float* ks = sh.sc[b].ks + NG * half;
         uint32_t x[HC];
 #pragma unroll
         for (int c = 0; c < HC; c += 32) tmem_ld32_nowait(at + c, *reinterpret_cast<uint32_t(*)[32]>(&x[c]));
@@ -437,12 +469,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
         tmem_wait_ld();
 #pragma unroll
         for (int k = 0; k < NG; ++k) {
-          float y[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            y[j] = fmaxf(fmaxf(__uint_as_float(x[16 * k + 4 * j]), __uint_as_float(x[16 * k + 4 * j + 1])),
-                         fmaxf(__uint_as_float(x[16 * k + 4 * j + 2]), __uint_as_float(x[16 * k + 4 * j + 3])));
-          cm[k] = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+          auto v = [&](int j) { return __uint_as_float(x[16 * k + j]); };
+          cm[k] = max3(max3(max3(v(0), v(1), v(2)), v(3), v(4)), max3(max3(v(5), v(6), v(7)), v(8), v(9)),
+                       max3(max3(v(10), v(11), v(12)), max3(v(13), v(14), v(15)), v(0)));
           if (mask >> k & 1) top = fmaxf(top, __fmul_rd(cm[k], f[k]));
         }
         // the largest of both halves: a pair of warps meets once a tile, after a wait that ran out too
@@ -457,10 +486,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
           l *= alpha;
           e_mine = e;
           const float ref = m == -INFINITY ? 0.f : m;
-          if (mask == (1 << NG) - 1 && !__any_sync(0xffffffffu, fabsf(ref) >= kFar))
-            l += weigh<HC, TERMS>(x, cm, f, at, ks, vs, qs, qs_lo, ref);
+          if (!plain || __any_sync(0xffffffffu, fabsf(ref) >= kFar))
+            l += weigh_with_care<HC, TERMS>(at, ks, qs, qs_lo, ref, mask);
+          else if (P >= HC)
+            l += weigh<HC, TERMS, true>(x, cm, f, at, ks, qs, qs_lo, ref);
           else
-            l += weigh_with_care<HC, TERMS>(at, ks, vs, qs, qs_lo, ref, mask);
+            l += weigh<HC, TERMS, false>(x, cm, f, at, ks, qs, qs_lo, ref);
           const bool flush = kTwo && i > 0 && i % kPeriod == 0;
           if (__any_sync(0xffffffffu, alpha != 1.f) || e != e_old || flush) {  // (the weights first: by now the sums so far are done)
             good = mbar_wait_sleep_bounded(&sh.v_empty[(i - 1) & 1], ((i - 1) >> 1) & 1, a.status);
@@ -595,11 +626,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
       const int e = __reduce_max_sync(0xffffffffu, some ? max((int)(now.y >> 23) - 127, -110) : -110);
       e_ref = i == 0 || e > e_ref + kScaleLag ? e : e_ref;
       if (lane < 2 * NG) {
-        sh.ks[s][lane] = some ? __uint_as_float(now.x) : 1.f;
-        sh.vs[s][lane] = some ? __uint_as_float(now.y) * pow2(kBase - e_ref) : 0.f;
+        const float g = some ? __uint_as_float(now.y) * pow2(kBase - e_ref) : 0.f;
+        sh.sc[s].ks[lane] = some ? __uint_as_float(now.x) : 1.f;
+        sh.sc[s].vs[lane] = g;
+        sh.sc[s].lg[lane] = log2f(g);
+        sh.sc[s].inv[lane] = 1.f / g;
       }
+      const bool plain = __all_sync(0xffffffffu, lane >= 2 * NG || (some && __uint_as_float(now.y) > 0.f));
       if (lane == 0) {
         sh.mask[s] = (int)mask;
+        sh.plain[s] = plain;
         sh.e[s] = e_ref;
       }
       __syncwarp();
@@ -642,12 +678,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
   good = !__syncthreads_or(!good);
   tc_fence_after();
   // ------------------------------------------------------------------ the split's partial
+  float* o_rows = reinterpret_cast<float*>(smem);         // [row][m, l, -, -, O]; the operands are done with
   if (good && warp < kSoft && live) {
-    const float sum = sh.l[0][row] + sh.l[1][row], scale = pow2(e_mine - kBase);
-    float* pp = a.part + (((size_t)req * g.Hq + head) * a.wl.max_splits + split) * (D + 4);
-    if (valid && half == 0) *reinterpret_cast<float2*>(pp) = make_float2(sum == sum ? m : INFINITY, sum);  // (a NaN must not look like no partial)
+    const float scale = pow2(e_mine - kBase);
 #pragma unroll 1
-    for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {  // (each half of the threads stores half of the channels)
+    for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {  // (each half of the threads has half of the channels)
       float v[32];
       tmem_ld32(base + kColO + c, v);
       if (kTwo && tiles > kPeriod) {
@@ -656,12 +691,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] += more[j];
       }
-      if (valid)
 #pragma unroll
-        for (int j = 0; j < 32; j += 4)
-          *reinterpret_cast<float4*>(pp + 4 + c + j) = make_float4(v[j] * scale, v[j + 1] * scale, v[j + 2] * scale, v[j + 3] * scale);
+      for (int j = 0; j < 32; j += 4)
+        *reinterpret_cast<float4*>(o_rows + row * (D + 4) + 4 + c + j) =
+            make_float4(v[j] * scale, v[j + 1] * scale, v[j + 2] * scale, v[j + 3] * scale);
     }
+    const float sum = sh.l[0][row] + sh.l[1][row];
+    if (half == 0) *reinterpret_cast<float2*>(o_rows + row * (D + 4)) = make_float2(sum == sum ? m : INFINITY, sum);  // (a NaN must not look like no partial)
   }
+  good = !__syncthreads_or(!good);
+  if (good)
+    for (int i = tid; i < kRows * (D / 4 + 1); i += kThreads) {  // 16 bytes a thread, a row's next to one another
+      const int r = i / (D / 4 + 1), c = i % (D / 4 + 1) * 4, its = sh.row_req[r];
+      if (its < 0) continue;
+      const size_t to = ((size_t)its * g.Hq + h * G + ((sh.tile * kRows + r) & (G - 1))) * a.wl.max_splits + split;
+      *reinterpret_cast<float4*>(a.part + to * (D + 4) + c) = *reinterpret_cast<const float4*>(o_rows + r * (D + 4) + c);
+    }
   __syncthreads();
   if (warp == 0) tmem_dealloc(sh.tmem, kCols);
   pdl_wait();
@@ -706,8 +751,8 @@ static int launch_prefix(const Kv8DecodeArgs& a, cudaStream_t s, bool pdl) {
     return launch_pdl(kern, grid, dim3(kThreads), smem, s, pdl, a);
   };
   if (a.out_dtype == kDtypeF32)
-    return a.q_dtype == kDtypeF32 ? go(kv8_prefix_kernel<D, FMT, true, 2>, Lay<D, true, 1>::kSmem)
-                                  : go(kv8_prefix_kernel<D, FMT, false, 2>, Lay<D, false, 1>::kSmem);
+    return a.q_dtype == kDtypeF32 ? go(kv8_prefix_kernel<D, FMT, true, 2>, Lay<D, true, 2>::kSmem)
+                                  : go(kv8_prefix_kernel<D, FMT, false, 2>, Lay<D, false, 2>::kSmem);
   return a.q_dtype == kDtypeF32 ? go(kv8_prefix_kernel<D, FMT, true, 1>, Lay<D, true, 1>::kSmem)
                                 : go(kv8_prefix_kernel<D, FMT, false, 1>, Lay<D, false, 1>::kSmem);
 }
