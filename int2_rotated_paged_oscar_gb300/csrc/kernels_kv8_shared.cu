@@ -8,8 +8,8 @@
 // (tcgen05), so it is bound by memory up to 128 rows of a kv head and by the tensor cores and the exponentials beyond.
 //
 // Roles in a CTA, around two buffers of a tile of 128 tokens (64 for float32 queries, whose three terms take the room):
-//   8 warps   codes from global memory through registers, two tiles ahead, to keys and values in shared memory, exactly.  Rows are
-//             tokens: for S the channels of a row are the contracted dimension, for O the tokens are.
+//   2 x 4     warps, keys and values: codes from global memory through registers, two tiles ahead, to operands in shared memory,
+//             exactly.  Rows are tokens: for S the channels of a row are the contracted dimension, for O the tokens are.
 //   2 warps   issue S = Q K^T and O += P V.
 //   2 x 4     warps, one half of a tile's tokens each, a thread per row: S from tensor memory, the running maximum and sum, P to
 //             tensor memory in the place of S, which holds three tiles.
@@ -50,7 +50,7 @@ struct Lay {
   static constexpr int kQ = kRows * D * 2, kKV = NT * D * 2;
   static constexpr int oQ = 0, oK = oQ + QT * kQ, oV = oK + 2 * kKV, oPages = oV + 2 * kKV;
   static constexpr int kSmem = oPages + kMostPages * 4 + 1024;
-  static constexpr int kTasks = NT * D / 16 / (32 * kConv);  // 16-byte chunks of keys (and of values) a thread takes of a tile
+  static constexpr int kTasks = NT * D / 16 / (16 * kConv);  // 16-byte chunks of keys (or of values) a thread takes of a tile
 };
 
 // Per group of 16 tokens (of one page): K scale; V scale relative to 2^e (2^kBase at 1), its logarithm and its inverse.
@@ -281,9 +281,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
   pdl_launch_dependents();
   if (tid == 0) {
     for (int b = 0; b < NS; ++b) {
-      mbar_init(&sh.qk_ready[b], kConv + 1);
+      mbar_init(&sh.qk_ready[b], kConv / 2 + 1);
       mbar_init(&sh.s_full[b], 2);
-      mbar_init(&sh.pv_ready[b], kSoft + kConv);
+      mbar_init(&sh.pv_ready[b], kSoft + kConv / 2);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sh.k_empty[b], 1);
@@ -519,30 +519,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
     sh.l[half][row] = l;
   } else if (warp < kSoft + kConv) {
     // ---------------------------------------------------------------- codes to operands
-    constexpr int T = L::kTasks, kStep = D == 128 ? 32 : 64;
-    const int ct = tid - 32 * kSoft, log_p = 31 - __clz(P);
+    constexpr int T = L::kTasks, kStep = D == 128 ? 16 : 32;
+    const bool is_v = warp >= kSoft + kConv / 2;
+    const int ct = (tid - 32 * kSoft) & (16 * kConv - 1), log_p = 31 - __clz(P);
     const Kv8Geom kg{P, D, g.Hkv};
-    const uint8_t* layer = a.pool + (size_t)a.layer * g.num_pages * kg.page_bytes() + (size_t)h * kg.block_bytes();
     // Chunk j of token t0 (+ kStep a task: the turns stay).  Eight neighbouring lanes take the four chunks of 64 channels of two
     // neighbouring tokens: their halves' first (or second) 16 bytes lie in different banks.
     const int t0 = D == 128 ? 4 * (ct >> 5) + 2 * (lane >> 4) + ((lane >> 2) & 1) : ct >> 2;
     const int j = D == 128 ? (lane & 3) + 4 * ((lane >> 3) & 1) : ct & 3;
-    auto place = [&](int turn) {                          // of the chunk in its tokens' 128-byte line, in bytes
-      return D == 128 ? (j ^ turn) * 16 : ((4 * (t0 & 1) + j) ^ turn) * 16;
-    };
-    const uint8_t *k_src = layer + place(D == 128 ? 4 * (t0 & 1) : 0), *v_src = layer + P * D + place(2 * ((t0 >> 1) & 3));
-    const uint32_t dst = (j >> 2) * NT * 128 + t0 * 128 + (((2 * (j & 3)) ^ (t0 & 7)) << 4);
+    const int turn = is_v ? 2 * ((t0 >> 1) & 3) : D == 128 ? 4 * (t0 & 1) : 0;
+    const int place = D == 128 ? j ^ turn : (4 * (t0 & 1) + j) ^ turn;  // of the chunk in its tokens' 128-byte line
+    const uint8_t* src = a.pool + (size_t)a.layer * g.num_pages * kg.page_bytes() + (size_t)h * kg.block_bytes() +
+                         (is_v ? kg.v_off() : 0) + place * 16;
+    uint8_t* dst = smem + (is_v ? L::oV : L::oK) + (j >> 2) * NT * 128 + t0 * 128 + (((2 * (j & 3)) ^ (t0 & 7)) << 4);
+    const ptrdiff_t next = (t0 & 1) ? -16 : 16;           // to the chunk's other 16 bytes
     const uint32_t nothing = FMT == kKv8Int8 ? 0x80808080u : 0u;
-    const bool holes = sh.holes;
-    uint4 kw[2][T], vw[T];
-    auto load = [&](int i, uint4 (&x)[T], const uint8_t* src) {
+    const bool holes = sh.holes, f16 = is_v || exact;
+    uint64_t *empty = is_v ? sh.v_empty : sh.k_empty, *ready = is_v ? sh.pv_ready : sh.qk_ready;
+    uint4 x[2][T];
+    auto load = [&](int i, uint4 (&x)[T]) {
 #pragma unroll
       for (int k = 0; k < T; ++k) {
         const int t = i * NT + t0 + kStep * k, e = min(t >> log_p, pages - 1);
         x[k] = load_codes(src + (size_t)page_at[e] * 128 + (t & (P - 1) & (D == 64 ? ~1 : ~0)) * D);
       }
     };
-    auto store = [&](uint8_t* to, const uint4 (&x)[T], bool f16, int i) {
+    auto store = [&](int i, uint8_t* to, const uint4 (&x)[T], bool f16) {
 #pragma unroll
       for (int k = 0; k < T; ++k) {
         uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
@@ -556,33 +558,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
           y[2 * i] = f16 ? kv8_pair<FMT, 0>(w[i]) : bf16_pair<FMT, 0>(w[i]);
           y[2 * i + 1] = f16 ? kv8_pair<FMT, 1>(w[i]) : bf16_pair<FMT, 1>(w[i]);
         }
-        *reinterpret_cast<uint4*>(to + dst + k * kStep * 128) = make_uint4(y[0], y[1], y[2], y[3]);
-        *reinterpret_cast<uint4*>(to + (dst ^ 16) + k * kStep * 128) = make_uint4(y[4], y[5], y[6], y[7]);
+        *reinterpret_cast<uint4*>(to + k * kStep * 128) = make_uint4(y[0], y[1], y[2], y[3]);
+        *reinterpret_cast<uint4*>(to + k * kStep * 128 + next) = make_uint4(y[4], y[5], y[6], y[7]);
       }
     };
-    load(0, kw[0], k_src);
-    load(0, vw, v_src);
-    load(1, kw[1], k_src);
+    load(0, x[0]);
+    load(1, x[1]);
     for (int i0 = 0, s = 0; i0 < tiles && good; i0 += 2) {
 #pragma unroll
       for (int b = 0; b < 2; ++b, s = s == NS - 1 ? 0 : s + 1) {
-        const int i = i0 + b, ph = (i >> 1) & 1;
+        const int i = i0 + b;
         if (i >= tiles) break;
-        if (i >= 2) good = mbar_wait_sleep_bounded(&sh.k_empty[b], ph ^ 1, a.status);
+        if (i >= 2) good = mbar_wait_sleep_bounded(&empty[b], ((i >> 1) & 1) ^ 1, a.status);
         good = __all_sync(0xffffffffu, good);
         if (!good) break;
-        if (exact) store(smem + L::oK + b * L::kKV, kw[b], true, i);
-        else store(smem + L::oK + b * L::kKV, kw[b], false, i);
+        if (f16) store(i, dst + b * L::kKV, x[b], true);
+        else store(i, dst + b * L::kKV, x[b], false);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.qk_ready[s]);
-        load(i + 2, kw[b], k_src);
-        if (i >= 2) good = mbar_wait_sleep_bounded(&sh.v_empty[b], ph ^ 1, a.status);
-        good = __all_sync(0xffffffffu, good);
-        if (!good) break;
-        store(smem + L::oV + b * L::kKV, vw, true, i);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.pv_ready[s]);
-        load(i + 1, vw, v_src);
+        if (lane == 0) mbar_arrive(&ready[s]);
+        load(i + 2, x[b]);
       }
     }
   } else if (warp == kSoft + kConv) {
