@@ -458,11 +458,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
       }
       if (live) {
         const uint32_t at = base + col_s(b) + HC * half;
-        const int mask = sh.mask[b] >> (NG * half) & ((1 << NG) - 1), plain = sh.plain[b], e = sh.e[b];
-        const float* ks = sh.sc[b].ks + NG * half;
         uint32_t x[HC];
 #pragma unroll
         for (int c = 0; c < HC; c += 32) tmem_ld32_nowait(at + c, *reinterpret_cast<uint32_t(*)[32]>(&x[c]));
+        const float* ks = sh.sc[b].ks + NG * half;
+        const int mask = sh.mask[b] >> (NG * half) & ((1 << NG) - 1), plain = sh.plain[b], e = sh.e[b];
         float f[NG], cm[NG], top = -INFINITY;
 #pragma unroll
         for (int k = 0; k < NG; ++k) f[k] = ks[k] * qs;
@@ -479,25 +479,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
         asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");
         top = fmaxf(top, sh.top[i & 1][half ^ 1][row]);
         if (good) {
-          const bool follow = top > m + kLag || (m == -INFINITY && top > m);
-          const float alpha = follow && i > 0 ? ex2(m - top) : 1.f;
-          const int e_old = i > 0 ? e_mine : e;
-          if (follow) m = top;
-          l *= alpha;
-          e_mine = e;
-          const float ref = m == -INFINITY ? 0.f : m;
-          if (!plain || __any_sync(0xffffffffu, fabsf(ref) >= kFar))
+          // as a rule the reference stays, and no score is so large that a last place of it counts
+          float scale = 1.f, ref = m;
+          bool care = !plain, rescale = false, flush = false;
+          if (__any_sync(0xffffffffu, top > m + kLag || !(fabsf(m) < kFar)) || e != e_mine || (kTwo && i % kPeriod == 0)) {
+            const bool follow = top > m + kLag || (m == -INFINITY && top > m);
+            const float alpha = follow && i > 0 ? ex2(m - top) : 1.f;
+            if (i == 0) e_mine = e;
+            if (follow) m = top;
+            l *= alpha;
+            scale = alpha * exp2f((float)(e_mine - e));
+            flush = kTwo && i > 0 && i % kPeriod == 0;
+            rescale = __any_sync(0xffffffffu, alpha != 1.f) || e != e_mine || flush;
+            e_mine = e;
+            ref = m == -INFINITY ? 0.f : m;
+            care |= __any_sync(0xffffffffu, fabsf(ref) >= kFar);
+          }
+          if (care)
             l += weigh_with_care<HC, TERMS>(at, ks, qs, qs_lo, ref, mask);
           else if (P >= HC)
             l += weigh<HC, TERMS, true>(x, cm, f, at, ks, qs, qs_lo, ref);
           else
             l += weigh<HC, TERMS, false>(x, cm, f, at, ks, qs, qs_lo, ref);
-          const bool flush = kTwo && i > 0 && i % kPeriod == 0;
-          if (__any_sync(0xffffffffu, alpha != 1.f) || e != e_old || flush) {  // (the weights first: by now the sums so far are done)
+          if (rescale) {                                  // (the weights first: by now the sums so far are done)
             good = mbar_wait_sleep_bounded(&sh.v_empty[(i - 1) & 1], ((i - 1) >> 1) & 1, a.status);
             good = __all_sync(0xffffffffu, good);
             tc_fence_after();
-            const float scale = alpha * exp2f((float)(e_old - e));
             const uint32_t o_at = base + kColO + half * (D / 2), total_at = base + kColTotal + half * (D / 2);
             if (good) {
               if (flush) {
