@@ -35,10 +35,10 @@ constexpr int kMostPages = 2048;                          // pages of a split
 // in float32 proper every kFlush tokens (0.9 10^-6 of bias at 2000 tokens a split without, 0.3 with).
 constexpr uint32_t kColTotal = 256, kColO = 384, kCols = 512;
 constexpr int kFlush = 512, kMostSlots = 3;
-// A row's reference exponent follows its maximum when it is kLag behind; V scales are relative to a power of two that follows
-// the largest when it is 2^kScaleLag behind; a weight of 1 at scale 1 is 2^kBase: below 2^(kLag + kScaleLag + 1 + kBase) = 2^15.
-constexpr float kLag = 10.f;
-constexpr int kScaleLag = 1, kBase = 3;
+// A row has two reference exponents, whole numbers: m of its scores s, for l, and m + d of s + log2(V scale), for O, so that what
+// counts is a page's part in the sum and a loud page that a row does not look at costs nothing.  They follow their maxima when
+// these are kLag ahead; a weight at the second one is 2^kBase, none is above 2^(kLag + kBase) = 2^15.
+constexpr float kLag = 12.f, kBase = 3.f;
 constexpr float kFar = 4194304.f;                         // scores (log2) whose last place counts
 
 template <int D, bool QF32, int TERMS>
@@ -53,17 +53,17 @@ struct Lay {
   static constexpr int kTasks = NT * D / 16 / (16 * kConv);  // 16-byte chunks of keys (or of values) a thread takes of a tile
 };
 
-// Per group of 16 tokens (of one page): K scale; V scale relative to 2^e (2^kBase at 1), its logarithm and its inverse.
+// Per group of 16 tokens (of one page): K scale, V scale and its logarithm.
 struct Scales {
-  float ks[8], vs[8], lg[8], inv[8];
+  float ks[8], vs[8], lg[8];
 };
 
 struct Shared {
   // K(i) written and S's place free; S(i) there and scales written; P(i) there and V(i) written; K read; V read and P V done
   uint64_t qk_ready[kMostSlots], s_full[kMostSlots], pv_ready[kMostSlots], k_empty[2], v_empty[2], end;
   Scales sc[kMostSlots];
-  int mask[kMostSlots], plain[kMostSlots], e[kMostSlots];  // groups that are there; all are, with V scales
-  float top[2][2][kRows];        // a half's largest scores, of even and odd tiles
+  int mask[kMostSlots], plain[kMostSlots];  // groups that are there; all are, with V scales
+  float2 top[2][2][kRows];       // a half's largest s and s + log2(V scale), of even and odd tiles
   float l[2][kRows];             // a half's sum, at the end
   float down[kRows];             // what the power of two of a row's query leaves to multiply by
   int row_req[kRows];            // a row's request, -1 for none
@@ -72,7 +72,8 @@ struct Shared {
   int lo, size, shared, tile, holder, holes;
 };
 
-__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+// 2^e of a whole number e, within float32's normal numbers; 0 below them.
+__device__ __forceinline__ float pow2(float e) { return e < -126.f ? 0.f : __uint_as_float((uint32_t)(127 + (int)fminf(e, 127.f)) << 23); }
 
 // Two neighbouring code bytes of a word as a BF16 pair, both exact: bytes 0, 1 (HALF = 0) or 2, 3.  INT8: the low seven bits
 // under the exponent of 128 are 128 + them; the top bit chooses what is taken off, 128 or 256.  E4M3: sign, exponent and mantissa
@@ -125,14 +126,15 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
   return r;
 }
 
-// Weights of a row's scores in a half tile, 2^(score - m) by the page's V scale, as TERMS f16 numbers; the sum of the weights before
-// the V scale is returned.  One number: the V scale is in the exponent, and out of the sum again.  Two numbers, of 22 bits: it is
+// Weights of a row's scores in a half tile, 2^(s - m - d + kBase) by the page's V scale, as TERMS f16 numbers; sum 2^(s - m) is
+// returned.  One number: the V scale is in the exponent, and out of the sum again.  Two numbers, of 22 bits: it is
 // a factor, with what the rounding of a score's scale f = K scale x query scale leaves out at the group's largest score.
 // ONE: all of the half tile's tokens are of one page.
 template <int HC, int TERMS, bool ONE>
 __device__ __forceinline__ float weigh(const uint32_t (&x)[HC], const float (&cm)[HC / 16], const float (&f)[HC / 16], uint32_t at,
-                                       const float* ks, float qs, float qs_lo, float ref) {
-  const float *vs = ks + 8, *lg = ks + 16, *inv = ks + 24;  // (of Scales)
+                                       const float* ks, float qs, float qs_lo, float m, float d) {
+  const float *vs = ks + 8, *lg = ks + 16;                // (of Scales)
+  const float diff = d - kBase, to_o = pow2(-diff);
   float total = 0.f;
 #pragma unroll
   for (int c = 0; c < HC / 32; ++c) {
@@ -140,13 +142,14 @@ __device__ __forceinline__ float weigh(const uint32_t (&x)[HC], const float (&cm
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int k = 2 * c + u, s = ONE ? 0 : k;
-      float g = 1.f, back = 1.f, bias = -ref;
+      float g = 1.f, back, bias;
       if constexpr (TERMS == 2) {
         back = ex2(fminf(cm[k] * fmaf(ks[s], qs_lo, fmaf(ks[s], qs, -f[s])), 1.f));
-        g = vs[s] * back;
+        g = vs[s] * to_o * back;
+        bias = -m;
       } else {
-        bias += lg[s];
-        back = inv[s];
+        bias = lg[s] - (m + diff);
+        back = ex2(diff - lg[s]);
       }
       const uint64_t ff = pair(f[s], f[s]), bb = pair(bias, bias), gg = pair(g, g);
       uint64_t sum[2] = {0, 0};
@@ -171,13 +174,16 @@ __device__ __forceinline__ float weigh(const uint32_t (&x)[HC], const float (&cm
   return total;
 }
 
-// The same where some groups are not there or have no V scale (all of a page's values 0), or some row's scores are so large (kFar)
-// that a last place of one counts: there distances are formed from the raw sums, 0 at a group's largest.  Other rows come out as
-// from weigh, bit for bit.
+// The same where some groups are not there or have no V scale (all of a page's values 0) or one too far from the others, or some
+// row's scores are so large (kFar) that a last place of one counts: there distances are formed from the raw sums, 0 at a group's
+// largest.  Other rows come out as from weigh, bit for bit.
 template <int HC, int TERMS>
-__device__ __noinline__ float weigh_with_care(uint32_t at, const float* ks, float qs, float qs_lo, float ref, int mask) {
-  const float *vs = ks + 8, *lg = ks + 16, *inv = ks + 24;
-  const bool far = fabsf(ref) >= kFar;
+__device__ __noinline__ float weigh_with_care(uint32_t at, const float* ks, float qs, float qs_lo, float m, float d, int mask) {
+  const float *vs = ks + 8, *lg = ks + 16;
+  const bool any = d > -INFINITY;                         // (else no page so far has values)
+  if (m == -INFINITY) m = 0.f;
+  const bool far = fabsf(m) >= kFar;
+  const float diff = any ? d - kBase : 0.f, to_o = pow2(-diff);
   float total = 0.f;
   float v[HC / 32][32];
 #pragma unroll
@@ -188,20 +194,23 @@ __device__ __noinline__ float weigh_with_care(uint32_t at, const float* ks, floa
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int k = 2 * c + u;
-      const bool there = mask >> k & 1, some = vs[k] > 0.f;
+      const bool there = mask >> k & 1, some = there && any && vs[k] > 0.f;
       const float f = ks[k] * qs;
-      float g = 1.f, back = 1.f, more = 0.f, cm = v[c][16 * u];
+      float cm = v[c][16 * u];
 #pragma unroll
       for (int j = 1; j < 16; ++j) cm = fmaxf(cm, v[c][16 * u + j]);
       const bool apart = far && cm > -INFINITY;
+      // weights by way of s - m: where the scores are large, or the V scale is 0 or so small that 2^(s + log2 - m - d) vanishes
+      const bool by_m = TERMS == 2 || apart || !some || diff - lg[k] > 60.f;
+      float back = 1.f, bias = -m;
       if constexpr (TERMS == 2) {
         if (!apart && there) back = ex2(fminf(cm * fmaf(ks[k], qs_lo, fmaf(ks[k], qs, -f)), 1.f));
-        g = vs[k] * back;
-      } else if (some) {
-        more = lg[k];
-        back = inv[k];
+      } else if (!by_m) {
+        bias = lg[k] - (m + diff);
+        back = ex2(diff - lg[k]);
       }
-      const float off = apart ? cm : 0.f, bias = (apart ? fminf(fmaf(cm, f, -ref), kLag) : -ref) + more;
+      if (apart) bias = fminf(fmaf(cm, f, -m), kLag);
+      const float off = apart ? cm : 0.f, g = !some ? 0.f : by_m ? fminf(vs[k] * to_o, 65504.f) * (TERMS == 2 ? back : 1.f) : 1.f;
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -210,7 +219,8 @@ __device__ __noinline__ float weigh_with_care(uint32_t at, const float* ks, floa
         for (int e = 0; e < 2; ++e) {
           w[e] = there ? ex2(fmaf(v[c][16 * u + 2 * j + e] - off, f, bias)) : 0.f;
           sum[2 * (j & 1) + e] += w[e];
-          w[e] = there && some ? w[e] * g : 0.f;
+          w[e] = some ? w[e] * g : 0.f;
+          if (apart) w[e] = fminf(w[e], 65504.f);
         }
         hi[8 * u + j] = pack_half2(w[0], w[1]);
         const __half2 h = *reinterpret_cast<const __half2*>(&hi[8 * u + j]);
@@ -444,8 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
   const float qs_lo = down * (float)(kScale - (double)(float)kScale);
   const int tiles = (pages * P + NT - 1) / NT;
   bool good = true;
-  float m = -INFINITY, l = 0.f;
-  int e_mine = 0;                                         // the sums are in units of 2^(e_mine - kBase)
+  float m = -INFINITY, d = -INFINITY, l = 0.f;            // l in units of 2^m, the sums of 2^(m + d - kBase)
   const uint32_t base = (uint32_t)(warp & 3) << 21;  // a softmax warp's 32 lanes
 
   if (warp < kSoft) {
@@ -462,8 +471,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
 #pragma unroll
         for (int c = 0; c < HC; c += 32) tmem_ld32_nowait(at + c, *reinterpret_cast<uint32_t(*)[32]>(&x[c]));
         const float* ks = sh.sc[b].ks + NG * half;
-        const int mask = sh.mask[b] >> (NG * half) & ((1 << NG) - 1), plain = sh.plain[b], e = sh.e[b];
-        float f[NG], cm[NG], top = -INFINITY;
+        const int mask = sh.mask[b] >> (NG * half) & ((1 << NG) - 1), plain = sh.plain[b];
+        float f[NG], cm[NG], top = -INFINITY, top_o = -INFINITY;
 #pragma unroll
         for (int k = 0; k < NG; ++k) f[k] = ks[k] * qs;
         tmem_wait_ld();
@@ -472,35 +481,47 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
           auto v = [&](int j) { return __uint_as_float(x[16 * k + j]); };
           cm[k] = max3(max3(max3(v(0), v(1), v(2)), v(3), v(4)), max3(max3(v(5), v(6), v(7)), v(8), v(9)),
                        max3(max3(v(10), v(11), v(12)), max3(v(13), v(14), v(15)), v(0)));
-          if (mask >> k & 1) top = fmaxf(top, __fmul_rd(cm[k], f[k]));
+          const float y = mask >> k & 1 ? __fmul_rd(cm[k], f[k]) : -INFINITY;
+          top = fmaxf(top, y);
+          top_o = fmaxf(top_o, y + ks[16 + k]);           // (+ the logarithm of the V scale)
         }
         // the largest of both halves: a pair of warps meets once a tile, after a wait that ran out too
-        sh.top[i & 1][half][row] = top;
+        sh.top[i & 1][half][row] = make_float2(top, top_o);
         asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");
-        top = fmaxf(top, sh.top[i & 1][half ^ 1][row]);
+        const float2 other = sh.top[i & 1][half ^ 1][row];
+        top = fmaxf(top, other.x);
+        top_o = fmaxf(top_o, other.y);
         if (good) {
-          // as a rule the reference stays, and no score is so large that a last place of it counts
-          float scale = 1.f, ref = m;
+          // as a rule the references stay, and no score is so large that a last place of it counts
+          float scale = 1.f;
           bool care = !plain, rescale = false, flush = false;
-          if (__any_sync(0xffffffffu, top > m + kLag || !(fabsf(m) < kFar)) || e != e_mine || (kTwo && i % kPeriod == 0)) {
-            const bool follow = top > m + kLag || (m == -INFINITY && top > m);
-            const float alpha = follow && i > 0 ? ex2(m - top) : 1.f;
-            if (i == 0) e_mine = e;
-            if (follow) m = top;
-            l *= alpha;
-            scale = alpha * exp2f((float)(e_mine - e));
+          if (__any_sync(0xffffffffu, top > m + kLag || top_o > m + d + kLag || !(fabsf(m) < kFar)) || (kTwo && i % kPeriod == 0)) {
+            if (top > m + kLag || (m == -INFINITY && top > m)) {
+              const float to = ceilf(top);
+              l = m == -INFINITY ? l : l * pow2(m - to);
+              if (fabsf(to) < kFar) d += m - to;          // (m + d stays)
+              else scale = d == -INFINITY ? 1.f : pow2(m - to);
+              m = to;
+            }
+            float d_new = ceilf(top_o - m);
+            if (!(fabsf(m) < kFar)) {                       // (differences of such scores say nothing: the largest V scale)
+              d_new = -INFINITY;
+              for (int k = 0; k < 2 * NG; ++k) d_new = fmaxf(d_new, ceilf(sh.sc[b].lg[k]));
+            }
+            if (d == -INFINITY ? d_new > d : d_new > d + (fabsf(m) < kFar ? kLag : 0.f)) {
+              scale = d == -INFINITY ? 1.f : scale * pow2(d - d_new);  // (1: there is nothing in the sums)
+              d = d_new;
+            }
             flush = kTwo && i > 0 && i % kPeriod == 0;
-            rescale = __any_sync(0xffffffffu, alpha != 1.f) || e != e_mine || flush;
-            e_mine = e;
-            ref = m == -INFINITY ? 0.f : m;
-            care |= __any_sync(0xffffffffu, fabsf(ref) >= kFar);
+            rescale = __any_sync(0xffffffffu, scale != 1.f) || flush;
+            care |= __any_sync(0xffffffffu, !(fabsf(m) < kFar));
           }
           if (care)
-            l += weigh_with_care<HC, TERMS>(at, ks, qs, qs_lo, ref, mask);
+            l += weigh_with_care<HC, TERMS>(at, ks, qs, qs_lo, m, d, mask);
           else if (P >= HC)
-            l += weigh<HC, TERMS, true>(x, cm, f, at, ks, qs, qs_lo, ref);
+            l += weigh<HC, TERMS, true>(x, cm, f, at, ks, qs, qs_lo, m, d);
           else
-            l += weigh<HC, TERMS, false>(x, cm, f, at, ks, qs, qs_lo, ref);
+            l += weigh<HC, TERMS, false>(x, cm, f, at, ks, qs, qs_lo, m, d);
           if (rescale) {                                  // (the weights first: by now the sums so far are done)
             good = mbar_wait_sleep_bounded(&sh.v_empty[(i - 1) & 1], ((i - 1) >> 1) & 1, a.status);
             good = __all_sync(0xffffffffu, good);
@@ -593,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
     // and the scales of the tile's groups of 16 tokens, a lane each, two tiles ahead
     const Kv8Geom kg{P, D, g.Hkv};
     const uint8_t* scales = a.pool + (size_t)a.layer * g.num_pages * kg.page_bytes() + (size_t)h * kg.block_bytes() + kg.scale_off();
-    int e_ref = 0;
+    float most = 0.f;
     uint2 sc[2];
     auto page_of = [&](int i) { return (i * NT + (lane & (2 * NG - 1)) * 16) >> (31 - __clz(P)); };
     auto load_scales = [&](int i, uint2& s) {
@@ -624,20 +645,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
       const int e_page = page_of(i);
       const bool some = e_page < pages && (sh.there[e_page >> 5] >> (e_page & 31) & 1);
       const unsigned mask = __ballot_sync(0xffffffffu, some && lane < 2 * NG);
-      const int e = __reduce_max_sync(0xffffffffu, some ? max((int)(now.y >> 23) - 127, -110) : -110);
-      e_ref = i == 0 || e > e_ref + kScaleLag ? e : e_ref;
+      const float v_scale = some ? __uint_as_float(now.y) : 0.f;
       if (lane < 2 * NG) {
-        const float g = some ? __uint_as_float(now.y) * pow2(kBase - e_ref) : 0.f;
         sh.sc[s].ks[lane] = some ? __uint_as_float(now.x) : 1.f;
-        sh.sc[s].vs[lane] = g;
-        sh.sc[s].lg[lane] = log2f(g);
-        sh.sc[s].inv[lane] = 1.f / g;
+        sh.sc[s].vs[lane] = v_scale;
+        sh.sc[s].lg[lane] = log2f(v_scale);
       }
-      const bool plain = __all_sync(0xffffffffu, lane >= 2 * NG || (some && __uint_as_float(now.y) > 0.f));
+      // (V scales more than 2^60 below the largest so far take the careful way, which keeps their part in the sum of weights)
+      const uint32_t bits = __float_as_uint(v_scale);
+      most = fmaxf(most, __uint_as_float(__reduce_max_sync(0xffffffffu, lane < 2 * NG ? bits : 0u)));
+      const float least = __uint_as_float(__reduce_min_sync(0xffffffffu, lane < 2 * NG ? bits : 0x7F800000u));
+      const bool plain = least > 0.f && least > most * 8.673617379884035e-19f;
       if (lane == 0) {
         sh.mask[s] = (int)mask;
         sh.plain[s] = plain;
-        sh.e[s] = e_ref;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.s_full[s]);
@@ -681,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
   // ------------------------------------------------------------------ the split's partial
   float* o_rows = reinterpret_cast<float*>(smem);         // [row][m, l, -, -, O]; the operands are done with
   if (good && warp < kSoft && live) {
-    const float scale = pow2(e_mine - kBase);
+    const float scale = d == -INFINITY ? 0.f : pow2(d - kBase);
 #pragma unroll 1
     for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {  // (each half of the threads has half of the channels)
       float v[32];

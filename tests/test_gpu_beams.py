@@ -2,9 +2,9 @@
 a prefix, the choice of the next beams, the reordering of their states, and a run of them together.
 
 Tolerances of the shared decode: the bound of a float32 evaluation (oracle.kv8.attend_bound); the shared part's weights enter
-their products as f16 numbers of a weight up to 2^3 or more for the largest: two of them (22 bits) where the output is float32, one (11 bits,
-2^-12 of the weight) where it is BF16, and no finer than f16's last place, 2^-25 / 2^3; a BF16 output is rounded once more
-(2^-8 of the value).  Selections: keys within 10^-6 of the oracle's and a float32 rounding (2^-24); tokens and parents are
+their products as f16 numbers, of weight times V scale, the largest being 2^2 or more: two of them (22 bits) where the output is float32,
+one (11 bits, 2^-12 of the weight) where it is BF16, and no finer than f16's last place, 2^-25 / 2^2 of the largest weight times
+its page's largest value; a BF16 output is rounded once more (2^-8 of the value).  Selections: keys within 10^-6 of the oracle's and a float32 rounding (2^-24); tokens and parents are
 equal unless the keys of two beams' candidates are closer than 2 10^-6.  Reordered states are equal.
 """
 import numpy as np
@@ -100,7 +100,8 @@ def within(r, out, q, qd, od, bt, lens, slots):
                 s = k @ q[b, i] / np.sqrt(r.d)
                 e = np.exp(s - s.max())
                 p = e / e.sum()
-                bound = bound + 2.0 ** (-22 if od == 0 else -12) * (p @ np.abs(v)) + 2.0 ** -28 * (e < 2.0 ** -6) @ np.abs(v) / e.sum()
+                page = np.concatenate([np.full(min(r.P, len(p) - t), np.abs(v[t:t + r.P]).max()) for t in range(0, len(p), r.P)])
+                bound = bound + 2.0 ** (-22 if od == 0 else -12) * (p @ np.abs(v)) + 2.0 ** -27 * len(p) * (p * page).max()
                 if od == 1:
                     bound = bound + (np.abs(want) + bound) * 2.0 ** -8
                 off = np.abs(got[b, i] - want)
@@ -201,6 +202,33 @@ def test_shared_magnitudes(osc, fmt, qd, loud):
         q = acts(rng, (3, 4, 64), False)
         out = shared_decode(r, q, qd, 0, [2, 1], [9, 9], bt, lens, slots)
         within(r, out, q, qd, 0, bt, lens, slots)
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("qd,od", [(0, 0), (1, 0), (1, 1), (0, 1)])
+@pytest.mark.parametrize("loud", [1e6, 1e12, 1e25])
+def test_shared_loud_pages_that_no_one_looks_at(osc, fmt, qd, od, loud):
+    """Values of any size with weights that vanish leave the digits of the others; a page of zero values counts in the sum alone."""
+    rng = np.random.default_rng(61)
+    P, d = 16, 128
+    rig, bt, slots, lens = family(osc, rng, [3], [24], [0, 5, 20], P=P, d=d, G=2, fmt=fmt)
+    with rig as r:
+        u = np.zeros((1, 2, d))
+        u[..., ::2] = 3.0
+        k, v = r.K[0][:384] * 0.3 + u, r.V[0][:384].copy()
+        far = np.zeros(384, bool)
+        far[32:64] = far[200:240] = True                    # whole pages and, at 200, the middle of them
+        k[far] -= 2 * u[0]
+        v[far] *= loud
+        v[96:112] = 0
+        r.write([k], [v], 1, [384], [0], bt[:1], slots[:1])
+        for b in (1, 2):
+            r.write([r.K[b][384:] * 0.3 + u], [r.V[b][384:]], 1, [lens[b] - 384], [384], bt[b:b + 1], slots[b:b + 1])
+        q = acts(rng, (3, 4, d), False) * 0.3
+        q[..., ::2] += 5.0                                  # scores of the loud tokens: some 150 below the others
+        out = shared_decode(r, q, qd, od, [3], [24], bt, lens, slots)
+        assert r.status() == 0
+        within(r, out, q, qd, od, bt, lens, slots)
 
 
 @pytest.mark.parametrize("fmt", [0, 1])
