@@ -11,6 +11,8 @@
 //   2 x 4     warps, keys and values: codes from global memory through registers, two tiles ahead, to operands in shared memory,
 //             exactly.  Rows are tokens: for S the channels of a row are the contracted dimension, for O the tokens are.
 //   2 warps   issue S = Q K^T and O += P V.
+//   1 warp    has the scales of a tile's groups of 16 tokens, a lane each, two tiles ahead (in the warp that issues S they held
+//             its next product back: 47 us instead of 43 for 12 ragged groups of head dim 64).
 //   2 x 4     warps, one half of a tile's tokens each, a thread per row: S from tensor memory, the running maximum and sum, P to
 //             tensor memory in the place of S, which holds three tiles.
 // BF16 queries, brought near 2^14 by a power of two, are f16 numbers but for components below 2^-31 of the largest: keys and
@@ -27,10 +29,10 @@ namespace {
 #include "tc_common.cuh"
 
 constexpr int kSoft = 8, kConv = 8;                       // warps
-constexpr int kThreads = 32 * (kSoft + kConv + 2);
+constexpr int kThreads = 32 * (kSoft + kConv + 3);
 constexpr int kRows = 128;
 constexpr int kMostPages = 2048;                          // pages of a split
-// Tensor memory, all of it (so that it begins at 0): scores, then weights, of two or three tiles; sums.  The tensor cores' additions
+// Tensor memory, all of it (so that it begins at 0): scores, then weights, of NS tiles; sums.  The tensor cores' additions
 // round towards zero: over thousands of tokens that would be 10^-6 of a sum and more, so for float32 outputs the sums are added up
 // in float32 proper every kFlush tokens (0.9 10^-6 of bias at 2000 tokens a split without, 0.3 with).
 constexpr uint32_t kColTotal = 256, kColO = 384, kCols = 512;
@@ -611,17 +613,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
     // ---------------------------------------------------------------- S = Q K^T
     const uint32_t idesc = exact ? idesc_f16_f32(kRows, NT) : idesc_bf16_f32(kRows, NT);
     const uint64_t q_desc = smem_desc_sw128(smem_u32(smem + L::oQ)), k_desc = smem_desc_sw128(smem_u32(smem + L::oK));
-    // and the scales of the tile's groups of 16 tokens, a lane each, two tiles ahead
-    const Kv8Geom kg{P, D, g.Hkv};
-    const uint8_t* scales = a.pool + (size_t)a.layer * g.num_pages * kg.page_bytes() + (size_t)h * kg.block_bytes() + kg.scale_off();
-    float most = 0.f;
-    uint2 sc[2];
-    auto page_of = [&](int i) { return (i * NT + (lane & (2 * NG - 1)) * 16) >> (31 - __clz(P)); };
-    auto load_scales = [&](int i, uint2& s) {
-      asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(s.x), "=r"(s.y) : "l"(scales + (size_t)page_at[min(page_of(i), pages - 1)] * 128));
-    };
-    load_scales(0, sc[0]);
-    load_scales(1, sc[1]);
     for (int i = 0, s = 0, ph = 0; i < tiles; ++i) {
       const int b = i & 1;
       good = mbar_wait_sleep_bounded(&sh.qk_ready[s], ph, a.status);
@@ -641,6 +632,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
         tc_commit(&sh.k_empty[b]);
       }
       __syncwarp();
+      if (++s == NS) s = 0, ph ^= 1;
+    }
+    if (lane == 0) tc_commit(&sh.end);
+  } else if (warp == kSoft + kConv + 1) {
+    // ---------------------------------------------------------------- scales
+    const Kv8Geom kg{P, D, g.Hkv};
+    const uint8_t* scales = a.pool + (size_t)a.layer * g.num_pages * kg.page_bytes() + (size_t)h * kg.block_bytes() + kg.scale_off();
+    float most = 0.f;
+    uint2 sc[2];
+    auto page_of = [&](int i) { return (i * NT + (lane & (2 * NG - 1)) * 16) >> (31 - __clz(P)); };
+    auto load_scales = [&](int i, uint2& s) {
+      asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(s.x), "=r"(s.y) : "l"(scales + (size_t)page_at[min(page_of(i), pages - 1)] * 128));
+    };
+    load_scales(0, sc[0]);
+    load_scales(1, sc[1]);
+    for (int i = 0, s = 0, ph = 0; i < tiles; ++i) {
+      const int b = i & 1;
+      good = mbar_wait_sleep_bounded(&sh.qk_ready[s], ph, a.status);
+      good = __all_sync(0xffffffffu, good);
+      if (!good) break;
       const uint2 now = b ? sc[1] : sc[0];
       const int e_page = page_of(i);
       const bool some = e_page < pages && (sh.there[e_page >> 5] >> (e_page & 31) & 1);
@@ -666,7 +677,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
       else load_scales(i + 2, sc[0]);
       if (++s == NS) s = 0, ph ^= 1;
     }
-    if (lane == 0) tc_commit(&sh.end);
   } else {
     // ---------------------------------------------------------------- O += P V
     constexpr uint32_t kIdesc = idesc_f16_f32(kRows, D) | (1u << 16);  // the second operand's contracted dimension along its rows
