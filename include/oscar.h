@@ -534,7 +534,7 @@ oscar_status oscar_kv8_sparse_decode_attn(oscar_ctx* ctx, int32_t layer, const v
  * group read once for all of its requests (samples or beams of one prompt, conversations behind one
  * system prompt).  Group i holds requests group_starts[i] .. group_starts[i + 1] - 1 of the batch, and the first
  * shared_pages[i] entries of their block-table rows are the same pages (forks of n tokens share n / P).
- * group_starts [n_groups + 1], from 0 to batch, and shared_pages [n_groups]: device int32; a group may hold one
+ * group_starts [n_groups + 1], ascending from 0 to batch, and shared_pages [n_groups]: device int32; a group may hold one
  * request or none, and share no page.  A group's shared pages are found through the row of its first request that
  * is not empty.  max_shared (pages) bounds shared_pages and max_own (tokens) what the requests hold behind them
  * (host values, they size the grids and the workspace); the other arguments as for

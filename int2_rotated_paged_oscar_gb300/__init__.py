@@ -593,7 +593,7 @@ def _logits(x, device: Optional[int], dtype: int, batch: int, beams: int, vocab:
     if x is None or isinstance(x, int):
         return x, 0
     shape, stride = tuple(x.shape), tuple(x.stride())
-    if len(shape) == 3 and (shape[0] <= 1 or shape[1] <= 1 or stride[0] == shape[1] * stride[1]):
+    if len(shape) == 3 and shape[1] == beams and (shape[0] <= 1 or shape[1] <= 1 or stride[0] == shape[1] * stride[1]):
         step = stride[1] if shape[1] > 1 else stride[0]
         shape, stride = (shape[0] * shape[1], shape[2]), (step, stride[2])
     if len(shape) != 2 or shape[0] < batch * beams or shape[1] != vocab or x.dtype is not (_torch_types or _types()).get(dtype, x.dtype) \

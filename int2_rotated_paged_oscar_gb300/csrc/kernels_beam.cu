@@ -276,11 +276,11 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
     if (s.floor.key) floor = fmaxf(floor, (float)from_ordered(s.floor.key));
     if (!open) return;
     const float least = floor == -INFINITY ? -3.402823466e38f : floor - shift - slack - 1e-6f * fabsf(floor);
-    unsigned ties = 0, takes = 0;                         // of this lane's logits
+    unsigned ties = 0, takes = 0;                         // of this lane's logits (a floor beyond float32's range, a NaN, stops none)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       ties |= (unsigned)(x[j] == mark && x[j] > -INFINITY) << j;
-      takes |= (unsigned)(x[j] >= least && x[j] > -INFINITY) << j;
+      takes |= (unsigned)(!(x[j] < least) && x[j] > -INFINITY) << j;
     }
     ties &= takes;
     int scan = __popc(ties);

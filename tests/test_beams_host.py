@@ -126,6 +126,9 @@ def test_logits_of_other_shapes_and_strides_are_refused(osc):
     assert osc._logits(on(wide.reshape(6, 40)), 0, F32, 3, 2, 40)[1] == 40
     assert osc._logits(on(wide.reshape(6, 40)), 0, F32, 2, 2, 40)[1] == 40  # some of the rows
     assert osc._logits(on(wide[:1, :1]), 0, F32, 1, 1, 40)[1] == 0
+    for batch, beams in ((1, 6), (6, 1), (2, 3), (1, 1)):                    # rows of other beams
+        with pytest.raises(osc.OscarError):
+            osc._logits(on(wide), 0, F32, batch, beams, 40)
     for bad in (wide[:, :, ::2], wide.transpose(1, 2), wide[:, :1].expand(3, 2, 40), wide[:2], torch.zeros(3, 3, 40)[:, :2],
                 wide.to(torch.bfloat16), wide.reshape(-1), torch.zeros(60).as_strided((3, 2, 40), (8, 4, 1))):
         with pytest.raises(osc.OscarError):

@@ -170,6 +170,20 @@ def test_shared_decode_equals_decode(osc, sizes, shared, G, fmt, P, d, qd, od):
         assert ((out.double() - want).abs() <= scale * (2.0 ** -7 if od == 1 else 2.0 ** -15)).all()
 
 
+@pytest.mark.parametrize("fmt,qd,od", [(0, 1, 1), (1, 1, 0)])
+def test_shared_decode_of_many_groups_on_the_same_pages(osc, fmt, qd, od):
+    """More groups than a warp has lanes, most of them empty; splits of as many pages as a CTA takes; a page of several groups."""
+    rng = np.random.default_rng(9)
+    rig, bt, slots, lens = family(osc, rng, [3], [4096], [0, 37, 5], G=2, d=64, fmt=fmt)
+    with rig as r:
+        q = acts(rng, (3, r.heads * 2, 64), False)
+        sizes = [0] * 40 + [1] + [0] * 59 + [2] + [0] * 59
+        shared = [7] * 40 + [4096] + [0] * 59 + [4090] + [4096] * 59
+        out = shared_decode(r, q, qd, od, sizes, shared, bt, lens, slots)
+        assert r.status() == 0
+        within(r, out, q, qd, od, bt, lens, slots)
+
+
 @pytest.mark.parametrize("fmt,qd,od", [(0, 1, 0), (1, 0, 0), (1, 1, 1)])
 def test_shared_requests_do_not_depend_on_their_company(osc, fmt, qd, od):
     """A request's output has the same bits wherever it lies in its group."""
@@ -556,6 +570,18 @@ def test_wide_range_of_logits(choose):
         choose.check(torch.from_numpy((rng.normal(size=(2, 3, 3000)) * scale).astype(np.float32)).cuda(), -rng.random((2, 3)), 8)
     x = rng.normal(size=(1, 2, 3000)).astype(np.float32)
     choose.check(torch.from_numpy(x + np.array([[[1000.0], [-1e5]]], np.float32)).cuda(), np.zeros((1, 2)), 8)
+
+
+def test_scores_and_logits_near_the_largest_float32(choose):
+    """score - top is below float32's range where every key is inside it."""
+    x = np.zeros((1, 2, 40), np.float32)
+    x[0, 0] = 1.9e38
+    x[0, 0, 5] = 2e38
+    choose.check(torch.from_numpy(x).cuda(), [[-2e38, -3e38]], 4)
+    choose.check(torch.from_numpy(x[:, ::-1].copy()).cuda(), [[-3e38, -2e38]], 4)
+    wide = np.zeros((1, 3, 5000), np.float32)
+    wide[0, 1], wide[0, 1, 4000:] = 1.9e38, 2e38
+    choose.check(torch.from_numpy(wide).cuda(), [[-3e38, -2e38, -3.2e38]], 64)
 
 
 def test_rising_rows_and_one_beam_that_leads(choose):
