@@ -767,7 +767,7 @@ Kv8DecodeWs kv8_shared_plan(const Geom& g, int batch, int n_groups, int max_shar
   groups->max_shared = max_shared;
   groups->max_own = max_own;
   groups->units_per_split = (int)best;
-  groups->max_tiles = (int)(rows / kRows + n_groups);
+  groups->max_tiles = (int)((rows + (long long)n_groups * (kRows - g.gq())) / kRows);  // (a group's last tile has a request's rows or more)
   groups->slots = (int)((all + best - 1) / best);
   w.max_splits += groups->slots;
   w.total = (size_t)batch * g.Hq * w.max_splits * (g.D + 4) * sizeof(float);
