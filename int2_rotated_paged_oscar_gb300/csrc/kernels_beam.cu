@@ -5,8 +5,7 @@
 // the n_out largest, the lowest i V + v first among equal ones.
 //
 // The logits are read once.  A first kernel, a warp per unit of 1024 logits, leaves the unit's maximum and sum of exponentials; it is
-// bound by memory (2 or 4 bytes and some five instructions a logit).  A second one, a CTA per item, forms the rows' normalisers and
-// looks through the best few units once more; then through those others whose largest candidate comes before the last of the
+// bound by memory and by the latency of a warp's one chain.  A second one, a CTA per item, forms the rows' normalisers and looks through the best few units once more; then through those others whose largest candidate comes before the last of the
 // n_out at hand.
 #include "beam_internal.h"
 #include "common.cuh"
@@ -51,13 +50,15 @@ __device__ __forceinline__ const void* row_of(const BeamArgs& a, long long row) 
 
 // ------------------------------------------------------------------ units
 constexpr int kUnitThreads = 256;
+constexpr float kNear = 4096.f;                            // c and its last place are below 2^13 and 2^-11
 
 template <bool BF16>
 __global__ void __launch_bounds__(kUnitThreads) beam_unit_kernel(const __grid_constant__ BeamArgs a) {
   using V = Vec<BF16>;
   constexpr int kVecs = kBeamUnit / (32 * V::N);
   const int lane = threadIdx.x & 31, units = beam_units(a.vocab);
-  const long long at = (long long)blockIdx.x * (kUnitThreads / 32) + (threadIdx.x >> 5), row = at / units;
+  const long long at = (long long)blockIdx.x * (kUnitThreads / 32) + (threadIdx.x >> 5);
+  const long long row = at >> 32 ? at / units : (uint32_t)at / (uint32_t)units;  // (a division of 64 bits takes five times as long)
   pdl_wait();
   pdl_launch_dependents();
   if (row >= (long long)a.batch * a.beams) return;
@@ -70,19 +71,36 @@ __global__ void __launch_bounds__(kUnitThreads) beam_unit_kernel(const __grid_co
 #pragma unroll
   for (int k = 0; k < kVecs; ++k) v[k].load(x, i0 + k * 32 * V::N, a.vocab, aligned);
   float m = -INFINITY;
+  if constexpr (BF16) {
+    __nv_bfloat162 t = __float2bfloat162_rn(-INFINITY);
 #pragma unroll
-  for (int k = 0; k < kVecs; ++k)
+    for (int k = 0; k < kVecs; ++k)
 #pragma unroll
-    for (int j = 0; j < V::N; ++j) m = fmaxf(m, v[k].get(j));
+      for (int j = 0; j < 4; ++j) t = __hmax2(t, *reinterpret_cast<const __nv_bfloat162*>(&v[k].w[j]));
+    m = fmaxf(__low2float(t), __high2float(t));
+  } else {
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) m = max3(max3(m, v[k].get(0), v[k].get(1)), v[k].get(2), v[k].get(3));
+  }
 #pragma unroll
   for (int d = 16; d; d >>= 1) m = warp_max_xor(m, d);
   const float ref = m == -INFINITY ? 0.f : m;
-  float s[4] = {0.f, 0.f, 0.f, 0.f};                      // (a NaN or +infinity makes a NaN of it)
+  // 2^(x log2 e - c) with c = ref log2 e rounded, and what that leaves out once, for the sum; beyond kNear it is no small number
+  const bool near = fabsf(ref) < kNear;
+  const float c = ref * kLog2e;
+  const uint64_t up = pair(kLog2e, kLog2e), off = pair(-c, -c);
+  uint64_t s[2] = {0, 0};                                 // (a NaN or +infinity makes a NaN of it)
 #pragma unroll
   for (int k = 0; k < kVecs; ++k)
 #pragma unroll
-    for (int j = 0; j < V::N; ++j) s[j & 3] += ex2((v[k].get(j) - ref) * kLog2e);
-  float sum = (s[0] + s[1]) + (s[2] + s[3]);
+    for (int j = 0; j < V::N; j += 2) {
+      const float lo = v[k].get(j), hi = v[k].get(j + 1);
+      const uint64_t y = near ? fma2(pair(lo, hi), up, off) : pair((lo - ref) * kLog2e, (hi - ref) * kLog2e);
+      s[(j >> 1) & 1] = add2(s[(j >> 1) & 1], pair(ex2(first(y)), ex2(second(y))));
+    }
+  s[0] = add2(s[0], s[1]);
+  float sum = first(s[0]) + second(s[0]);
+  if (near) sum = fmaf(sum, fmaf(-ref, kLog2e, c) * 0.6931471805599453f, sum);  // (2^r of |r| <= 2^-12, half a last place of c)
 #pragma unroll
   for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
   if (lane == 0) reinterpret_cast<float2*>(a.part)[at] = make_float2(m, sum);

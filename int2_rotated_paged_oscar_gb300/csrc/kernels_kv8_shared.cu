@@ -102,32 +102,6 @@ __device__ __forceinline__ uint64_t desc_rows(uint32_t saddr, uint32_t across) {
          (uint64_t)2 << 61;
 }
 
-__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) { return (uint64_t)hi << 32 | lo; }
-__device__ __forceinline__ uint64_t pair(float lo, float hi) { return pair(__float_as_uint(lo), __float_as_uint(hi)); }
-__device__ __forceinline__ float first(uint64_t x) { return __uint_as_float((uint32_t)x); }
-__device__ __forceinline__ float second(uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); }
-__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
-  return r;
-}
-
-__device__ __forceinline__ float max3(float x, float y, float z) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
-  return r;
-}
-
 // Weights of a row's scores in a half tile, 2^(s - m - d + kBase) by the page's V scale, as TERMS f16 numbers; sum 2^(s - m) is
 // returned.  One number: the V scale is in the exponent, and out of the sum again.  Two numbers, of 22 bits: it is
 // a factor, with what the rounding of a score's scale f = K scale x query scale leaves out at the group's largest score.
