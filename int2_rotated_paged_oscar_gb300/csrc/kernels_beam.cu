@@ -4,9 +4,12 @@
 //
 // the n_out largest, the lowest i V + v first among equal ones.
 //
-// The logits are read once.  A first kernel, a warp per unit of 1024 logits, leaves the unit's maximum and sum of exponentials; it is
-// bound by memory and by the latency of a warp's one chain.  A second one, a CTA per item, forms the rows' normalisers and looks through the best few units once more; then through those others whose largest candidate comes before the last of the
-// n_out at hand.
+// The logits are read once: a first kernel, a warp per unit of 1024 logits, leaves the unit's maximum and sum of exponentials.  It is
+// bound by memory and by the latency of a warp's one chain (32 x 8 rows of 131,072 BF16 logits: 14.6 us, 4.6 of 6.7 TB/s;
+// fewer CTAs whose warps take one unit after another, the next one's loads ahead: 19 us).  A second one, a CTA per item, forms
+// the rows' normalisers and looks through the best few units once more, 128 logits a warp with a common floor; then through those
+// others whose largest candidate comes before the last of the n_out at hand.  That is one chain of barriers, 5 to 13 us
+// (both kernels: 11 us for 8 x 4 beams of 32,768 and 25 for 32 x 8 of 131,072; 33 and 107 in the simplest form).
 #include "beam_internal.h"
 #include "common.cuh"
 

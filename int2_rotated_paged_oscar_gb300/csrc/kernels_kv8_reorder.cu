@@ -3,7 +3,9 @@
 // A beam's state is its block-table row, its length, and its BF16 tail rows in its request slot.  The first child of a beam
 // keeps the slot, so its tail does not move; each further child takes the slot of a beam without a child, and n mod P rows are
 // copied there in every layer.  Slots that are read are never written, so the copies need no order among themselves.
-// Bound by memory: layers x kv heads x 2 x (n mod P) rows of 2 d bytes, read and written once per copied child.
+// Bound by memory: layers x kv heads x 2 x (n mod P) rows of 2 d bytes, read and written once per copied child.  A CTA
+// takes runs (layer, kv head, K or V) as one range of 16-byte vectors, eight of a thread under way: 36 layers of 16 x 8 beams
+// 88 us, 22 us for 4 x 4 (147 and 23 with one run a CTA at a time).
 #include "beam_internal.h"
 #include "common.cuh"
 
