@@ -267,7 +267,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
   uint32_t* page_at = reinterpret_cast<uint32_t*>(smem + L::oPages);  // of the split's pages, in units of 128 bytes
   const Geom& g = a.g;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int h = blockIdx.y, split = blockIdx.x / a.groups.max_tiles, tile = blockIdx.x % a.groups.max_tiles;
+  // A page's heads lie together, so CTAs of the same pages follow one another, kv heads first (64 samples of 32K 134 us a call with
+  // a head's splits one after another, 131 so; 4 prompts of 8K 41.2, 39.4).
+  const int h = blockIdx.x % a.g.Hkv, at_x = blockIdx.x / a.g.Hkv, tile = at_x % a.groups.max_tiles, split = at_x / a.groups.max_tiles;
   const int G = g.gq(), P = g.P;
   // The grid before this one is the decode kernel of the same call: all that this one reads was there before it.  What it leaves
   // (for the merge, which follows this grid) is waited for at the end.
@@ -730,7 +732,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
 Kv8DecodeWs kv8_shared_plan(const Geom& g, int batch, int n_groups, int max_shared, int max_own, Kv8Groups* groups, int* own_splits) {
   Kv8DecodeWs w = kv8_plan(g, batch, max_own / g.P);
   *own_splits = w.max_splits;
-  // The split that takes the fewest rounds of (its units + 5, a CTA's start and end).
+  // The split that takes the fewest rounds of (its units + 8, a CTA's start and end: 64 samples of 32K 128 us a call in one round of
+  // 128 CTAs, 132 in two of 288, which 5 would choose).
   const long long tiles = ((long long)max_shared * g.P + kPrefixUnit - 1) / kPrefixUnit;
   const long long rows = (long long)batch * g.gq(), row_tiles = rows / kRows > n_groups ? rows / kRows : n_groups;
   const long long pairs = row_tiles * g.Hkv > 0 ? row_tiles * g.Hkv : 1;
@@ -741,14 +744,15 @@ Kv8DecodeWs kv8_shared_plan(const Geom& g, int batch, int n_groups, int max_shar
     const long long fit = 152 * rounds / pairs, splits = fit < all ? fit : all;
     if (splits == 0) continue;
     const long long per = (all + splits - 1) / splits;
-    const long long c = ((pairs * ((all + per - 1) / per) + 151) / 152) * (per + 5);
+    const long long c = ((pairs * ((all + per - 1) / per) + 151) / 152) * (per + 8);
     if (per <= most && (cost < 0 || c < cost)) best = per, cost = c;
   }
   groups->n = n_groups;
   groups->max_shared = max_shared;
   groups->max_own = max_own;
   groups->units_per_split = (int)best;
-  groups->max_tiles = (int)((rows + (long long)n_groups * (kRows - g.gq())) / kRows);  // (a group's last tile has a request's rows or more)
+  // (a group's last tile has a request's rows or more; no more tiles than requests, so a grid of 2^31 would have partials of a TB)
+  groups->max_tiles = (int)((rows + (long long)(n_groups < batch ? n_groups : batch) * (kRows - g.gq())) / kRows);
   groups->slots = (int)((all + best - 1) / best);
   w.max_splits += groups->slots;
   w.total = (size_t)batch * g.Hq * w.max_splits * (g.D + 4) * sizeof(float);
@@ -757,7 +761,7 @@ Kv8DecodeWs kv8_shared_plan(const Geom& g, int batch, int n_groups, int max_shar
 
 template <int D, int FMT>
 static int launch_prefix(const Kv8DecodeArgs& a, cudaStream_t s, bool pdl) {
-  const dim3 grid(a.groups.slots * a.groups.max_tiles, a.g.Hkv);
+  const dim3 grid(a.groups.slots * a.groups.max_tiles * a.g.Hkv);
   auto go = [&](auto kern, size_t smem) {
     const cudaError_t e = ensure_smem_limit(kern, smem);
     if (e != cudaSuccess) return (int)e;
