@@ -18,7 +18,7 @@
 //             tensor memory in the place of S, which holds two or three tiles.
 // Prefix of 130,048 tokens, 8 requests of 4 heads a kv head, INT8: 81 us (3.3 of 6.7 TB/s), of which some 7 are a CTA's start
 // and end.  Prefix of 32,768 tokens, 64 requests of 8 heads, E4M3: 90 us, 760 TFLOP/s.  A tile of 128 tokens takes some 2600 clocks
-// (1040 on the tensor cores fed without a pause, 1540 in issue slots, 1280 in shared memory's ports); without the softmax and the
+// (1040 on the tensor cores fed without a pause, 1400 in issue slots, 1280 in shared memory's ports); without the softmax and the
 // conversion it would take 1530: the handing over from role to role.  On the CUDA cores the same took 3.9 and 12.3 ms.
 //
 // BF16 queries, brought near 2^14 by a power of two, are f16 numbers but for components below 2^-31 of the largest: keys and
