@@ -78,14 +78,15 @@ __device__ __forceinline__ bool kv8_own_sound(const Kv8DecodeArgs& a, int n, int
          n <= (long long)a.g.max_pages_per_req * a.g.P;
 }
 
-// Group of request b and its shared pages, found by a whole warp; -1 where the groups do not hold it.
+// Shared pages of the group that holds request b, found by a whole warp: 0 .. max_shared, so that a page index formed from them
+// cannot wrap, or -1 where no group holds it or the group's word is another one.
 __device__ __forceinline__ int kv8_shared_of(const Kv8DecodeArgs& a, int b) {
   int c = 0;
   for (int i = threadIdx.x & 31; i < a.groups.n; i += 32) c += a.groups.starts[i] <= b;
   const int at = __reduce_add_sync(0xffffffffu, c) - 1;
   if (at < 0) return -1;
   const int lo = a.groups.starts[at], hi = a.groups.starts[at + 1], s = a.groups.shared[at];
-  return lo >= 0 && lo <= b && b < hi && hi <= a.batch ? s : -1;
+  return lo >= 0 && lo <= b && b < hi && hi <= a.batch && s >= 0 && s <= a.groups.max_shared ? s : -1;
 }
 
 // Prefix partials of a row whose group shares s pages.

@@ -347,6 +347,24 @@ def test_shared_decode_reports_bad_arguments_on_the_device(osc):
         same(out, [0, 1, 3, 4])
 
 
+@pytest.mark.parametrize("word", [0x7fffffff, 0x7fffffe0, 0x40000000, 1 << 20, -0x80000000, -2])
+def test_shared_page_counts_of_any_size_are_reported(osc, word):
+    """A count of shared pages beyond the bound, to the largest word: the group's requests get zeros, the others what they had."""
+    rng = np.random.default_rng(13)
+    sizes, shared, own = [3, 2], [6, 4], [3, 0, 17, 40, 5]
+    rig, bt, slots, lens = family(osc, rng, sizes, shared, own, P=16, d=64, G=4, fmt=0)
+    with rig as r:
+        q = acts(rng, (5, 8, 64), False)
+        kw = dict(max_shared=6, max_own=40)
+        good = shared_decode(r, q, 1, 0, sizes, shared, bt, lens, slots, **kw)
+        for at, rows, rest in ((0, [0, 1, 2], [3, 4]), (1, [3, 4], [0, 1, 2])):
+            bad = list(shared)
+            bad[at] = word
+            out = shared_decode(r, q, 1, 0, sizes, bad, bt, lens, slots, **kw)
+            assert r.status() == osc.DEV_BAD_LEN and not out[rows].any()
+            assert torch.equal(out[rest], good[rest])
+
+
 def test_shared_graphs_and_streams(osc):
     """Captured once and replayed on new inputs; two graphs with one workspace replayed in turn; two streams at once."""
     rng = np.random.default_rng(10)
