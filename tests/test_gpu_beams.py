@@ -726,6 +726,44 @@ def test_reorder_reports_bad_arguments_on_the_device(osc):
             assert np.array_equal(r.tail.float().cpu().numpy(), tail)
 
 
+def test_reorder_reports_states_that_do_not_move(osc):
+    """A length or slot out of range is reported where no row is copied too: with a parent's only child, and with the slot of an empty beam."""
+    rng = np.random.default_rng(2)
+    P = 16
+    with Rig(osc, P=P, slots=6, oracle=False) as r:
+        r.tail.copy_(torch.randn(r.tail.shape, device="cuda"))
+        bt, lens, slots = rng.integers(0, 9, (4, 5)).astype(np.int32), np.array([5, 20, 33, 32], np.int32), np.array([5, 0, 3, 2], np.int32)
+        tail = r.tail.float().cpu().numpy()
+        for parents in ([0, 1, 2, 3], [3, 2, 1, 0], [2, -1, 3, 1]):
+            got = reorder(r, parents, bt, lens, slots, 1, 4)
+            assert r.status() == 0
+            for bad in (6, -1, 1 << 30):
+                s = slots.copy()
+                s[0 if -1 in parents else 2] = bad           # (beam 0's slot goes to the empty beam)
+                got = reorder(r, parents, bt, lens, s, 1, 4)
+                assert r.status() == osc.DEV_BAD_SLOT
+                want = reorder_oracle(parents, bt, lens, s, tail.copy(), P, 1, 4)
+                assert all(np.array_equal(a, b) for a, b in zip(got, want))
+            for bad in (-3, 12 * P + 1):
+                n = lens.copy()
+                n[2] = bad
+                got = reorder(r, parents, bt, n, slots, 1, 4)
+                assert r.status() == osc.DEV_BAD_LEN
+                want = reorder_oracle(parents, bt, n, slots, tail.copy(), P, 1, 4)
+                assert all(np.array_equal(a, b) for a, b in zip(got, want))
+            assert np.array_equal(r.tail.float().cpu().numpy(), tail)
+        n, s = lens.copy(), slots.copy()                     # tails of no rows: nothing would be copied, the states are bad all the same
+        n[3], s[0] = 32, 6
+        reorder(r, [3, 3, 1, 2], bt, n, s, 1, 4)
+        assert r.status() == osc.DEV_BAD_SLOT
+        n[3], s[0] = -16, 5
+        reorder(r, [3, 3, 1, 2], bt, n, s, 1, 4)
+        assert r.status() == osc.DEV_BAD_LEN
+        n[0], n[3] = -1, 32                                  # a childless beam's length is nobody's
+        reorder(r, [3, 3, 1, 2], bt, n, s, 1, 4)
+        assert r.status() == 0 and np.array_equal(r.tail.float().cpu().numpy(), tail)
+
+
 # ------------------------------------------------------------------------------------------------ together
 @pytest.mark.parametrize("fmt,G", [(0, 4), (1, 8)])
 def test_beam_search_run(osc, fmt, G):
