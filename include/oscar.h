@@ -540,7 +540,9 @@ oscar_status oscar_kv8_sparse_decode_attn(oscar_ctx* ctx, int32_t layer, const v
  * (host values, they size the grids and the workspace); the other arguments as for
  * oscar_kv8_decode_attn.  A request of length 0 (a padded batch) gets zeros; one that no group holds, that is shorter
  * than its group's shared pages or beyond the bounds gets zeros and sets OSCAR_DEV_BAD_LEN; a page that is not
- * mapped is left out and sets OSCAR_DEV_BAD_PAGE. */
+ * mapped is left out and sets OSCAR_DEV_BAD_PAGE.  The workspace size holds for every call of at most batch requests in
+ * at most n_groups groups with the same max_shared and max_own: a program that shrinks its batch or joins groups keeps its
+ * workspace. */
 oscar_status oscar_kv8_shared_workspace_size(const oscar_config* cfg, int32_t batch, int32_t n_groups, int32_t max_shared,
                                              int32_t max_own, size_t* bytes);
 oscar_status oscar_kv8_shared_decode_attn(oscar_ctx* ctx, int32_t layer, const void* q, int64_t q_stride, int32_t q_dtype,

@@ -729,16 +729,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
 
 }  // namespace
 
-Kv8DecodeWs kv8_shared_plan(const Geom& g, int batch, int n_groups, int max_shared, int max_own, Kv8Groups* groups, int* own_splits) {
-  Kv8DecodeWs w = kv8_plan(g, batch, max_own / g.P);
-  *own_splits = w.max_splits;
-  // The split that takes the fewest rounds of (its units + 8, a CTA's start and end: 64 samples of 32K 128 us a call in one round of
-  // 128 CTAs, 132 in two of 288, which 5 would choose).
-  const long long tiles = ((long long)max_shared * g.P + kPrefixUnit - 1) / kPrefixUnit;
-  const long long rows = (long long)batch * g.gq(), row_tiles = rows / kRows > n_groups ? rows / kRows : n_groups;
+// Units of a split of prefixes of `all` units behind so many row tiles: the split that takes the fewest rounds of (its units + 8, a
+// CTA's start and end: 64 samples of 32K 128 us a call in one round of 128 CTAs, 132 in two of 288, which 5 would choose).
+static long long prefix_units(const Geom& g, long long row_tiles, long long all) {
   const long long pairs = row_tiles * g.Hkv > 0 ? row_tiles * g.Hkv : 1;
   const long long most = (long long)kMostPages * g.P / kPrefixUnit;
-  const long long all = tiles > 0 ? tiles : 1;
   long long best = most < all ? most : all, cost = -1;
   for (long long rounds = 1; rounds <= 16; ++rounds) {    // as many splits as fill that many rounds
     const long long fit = 152 * rounds / pairs, splits = fit < all ? fit : all;
@@ -747,6 +742,19 @@ Kv8DecodeWs kv8_shared_plan(const Geom& g, int batch, int n_groups, int max_shar
     const long long c = ((pairs * ((all + per - 1) / per) + 151) / 152) * (per + 8);
     if (per <= most && (cost < 0 || c < cost)) best = per, cost = c;
   }
+  return best;
+}
+
+static long long prefix_all(const Geom& g, int max_shared) {
+  const long long units = ((long long)max_shared * g.P + kPrefixUnit - 1) / kPrefixUnit;
+  return units > 0 ? units : 1;
+}
+
+Kv8DecodeWs kv8_shared_plan(const Geom& g, int batch, int n_groups, int max_shared, int max_own, Kv8Groups* groups, int* own_splits) {
+  Kv8DecodeWs w = kv8_plan(g, batch, max_own / g.P);
+  *own_splits = w.max_splits;
+  const long long rows = (long long)batch * g.gq(), all = prefix_all(g, max_shared);
+  const long long best = prefix_units(g, rows / kRows > n_groups ? rows / kRows : n_groups, all);
   groups->n = n_groups;
   groups->max_shared = max_shared;
   groups->max_own = max_own;
@@ -757,6 +765,24 @@ Kv8DecodeWs kv8_shared_plan(const Geom& g, int batch, int n_groups, int max_shar
   w.max_splits += groups->slots;
   w.total = (size_t)batch * g.Hq * w.max_splits * (g.D + 4) * sizeof(float);
   return w;
+}
+
+// The most that a plan of up to so many requests and groups takes: fewer rows are split into more parts, so the largest batch is not
+// the one with the most partials.  For b requests the row tiles are max(b G / kRows, groups), any count from `lo` to n_groups.
+size_t kv8_shared_ws_bytes(const Geom& g, int batch, int n_groups, int max_shared, int max_own) {
+  const long long all = prefix_all(g, max_shared);
+  auto slots = [&](long long row_tiles) {
+    const long long per = prefix_units(g, row_tiles, all);
+    return (all + per - 1) / per;
+  };
+  long long places = 0, next = n_groups, among = 0;       // among: the most slots of row tiles next + 1 .. n_groups
+  for (long long b = batch; b > 0; --b) {
+    const long long tiles = b * g.gq() / kRows, lo = tiles > 1 ? tiles : 1;
+    for (; next >= lo; --next) among = among > slots(next) ? among : slots(next);
+    const long long its = b * (kv8_plan(g, (int)b, max_own / g.P).max_splits + (lo <= n_groups ? among : slots(lo)));
+    places = its > places ? its : places;
+  }
+  return (size_t)places * g.Hq * (g.D + 4) * sizeof(float);
 }
 
 template <int D, int FMT>

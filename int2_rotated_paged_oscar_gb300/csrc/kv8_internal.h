@@ -129,6 +129,8 @@ struct IntPairs {
 Kv8DecodeWs kv8_plan(const Geom& g, int batch, long long max_pages);
 // the same for requests in groups: the plan of their own parts, with room for the prefixes' partials
 Kv8DecodeWs kv8_shared_plan(const Geom& g, int batch, int n_groups, int max_shared, int max_own, Kv8Groups* groups, int* own_splits);
+// bytes that serve every call of at most so many requests and groups with these bounds
+size_t kv8_shared_ws_bytes(const Geom& g, int batch, int n_groups, int max_shared, int max_own);
 size_t kv8_select_ws_bytes(const Geom& g, int batch, int max_seq);
 
 int launch_kv8_write(const Kv8WriteArgs& a, void* stream, bool pdl);

@@ -10,7 +10,6 @@ using oscar::fail;
 using oscar::Geom;
 using oscar::kMaxGrid;
 using oscar::Kv8DecodeArgs;
-using oscar::Kv8Groups;
 using oscar::LaunchScope;
 using oscar::need_kv8;
 using oscar::ReorderArgs;
@@ -38,9 +37,7 @@ oscar_status oscar_kv8_shared_workspace_size(const oscar_config* cfg, int32_t ba
   if (st != OSCAR_OK) return st;
   if (!bytes || batch < 0) return fail(OSCAR_ERR_INVALID, "bad arguments to workspace size");
   if ((st = check_groups(g, n_groups, max_shared, max_own)) != OSCAR_OK) return st;
-  Kv8Groups groups{};
-  int own = 0;
-  *bytes = oscar::kv8_shared_plan(g, batch, n_groups, max_shared, max_own, &groups, &own).total;
+  *bytes = oscar::kv8_shared_ws_bytes(g, batch, n_groups, max_shared, max_own);
   return OSCAR_OK;
 }
 

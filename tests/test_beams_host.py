@@ -69,6 +69,21 @@ def test_workspace_sizes(osc):
     assert lib.oscar_kv8_shared_workspace_size(ctypes.byref(c), 1, 1, 1, 1, None) == osc.ERR_INVALID
 
 
+@pytest.mark.parametrize("heads,G,d,P", [(8, 8, 128, 64), (2, 4, 64, 16), (8, 4, 128, 64), (1, 8, 128, 16), (8, 1, 64, 32)])
+@pytest.mark.parametrize("shared,own", [(0, 0), (1, 5), (128, 300), (512, 1024), (4096, 9000)])
+def test_a_workspace_serves_fewer_requests_and_groups(osc, heads, G, d, P, shared, own):
+    """A smaller batch is split into more parts; the size covers every smaller batch and every smaller number of groups."""
+    cfg = osc.make_config(num_layers=1, n_q_heads=heads * G, n_kv_heads=heads, head_dim=d, page_size=P, sink=0, recent=1, max_requests=4,
+                          max_pages_per_req=4096, num_pages=4)
+    size = lambda b, n: osc.oscar_kv8_shared_workspace_size(cfg, b, n, shared, own)  # noqa: E731
+    batches, groups = [*range(1, 70), 127, 128, 129, 160, 255, 256, 257, 300], [1, 2, 3, 4, 7, 12, 13, 16, 19, 20, 33, 64]
+    table = np.array([[size(b, n) for n in groups] for b in batches], dtype=np.int64)
+    assert (np.diff(table, axis=0) >= 0).all() and (np.diff(table, axis=1) >= 0).all()
+    # a place of (m, l, O) for every query head at least, in the prefix and in a request's own part
+    assert (table >= np.array(batches)[:, None] * heads * G * 2 * (d + 4) * 4).all()
+    assert size(1, 1) <= size(2, 0) <= size(2, 1)             # (no group counts as one)
+
+
 @pytest.mark.parametrize("beams", [1, 2, 7, 64])
 @pytest.mark.parametrize("vocab", [1, 1024, 1025, 50021, 131072, 1 << 24])
 def test_the_workspace_holds_two_numbers_for_every_1024_logits(osc, beams, vocab):

@@ -365,6 +365,27 @@ def test_shared_page_counts_of_any_size_are_reported(osc, word):
             assert torch.equal(out[rest], good[rest])
 
 
+def test_shared_workspace_serves_a_shrinking_batch(osc):
+    """One workspace of the largest batch's size, as requests finish and groups end: the same bits as with one of the call's own."""
+    rng = np.random.default_rng(14)
+    sizes, shared = [24, 5, 3], [300, 300, 40]
+    own = [int(x) for x in rng.integers(0, 90, 32)]
+    rig, bt, slots, lens = family(osc, rng, sizes, shared, own, P=16, d=64, G=8, fmt=0)
+    with rig as r:
+        o, q = osc, r.rows(acts(rng, (32, 16, 64), False), 1)
+        bounds = dict(max_shared=300, max_own=96)
+        size = o.oscar_kv8_shared_workspace_size(r.cfg, 32, 3, 300, 96)
+        ws = torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")
+        for left in ([24, 5, 3], [24, 5], [24], [17], [16], [9], [4], [1]):
+            B, n = sum(left), len(left)
+            want = shared_decode(r, q[:B], 1, 0, left, shared[:n], bt[:B], lens[:B], slots[:B], **bounds)
+            got = torch.full_like(want, 5.0)
+            t = dev(bt[:B])
+            o.oscar_kv8_shared_decode_attn(r.ctx, r.layer, q[:B], 1, got, 0, dev(np.concatenate([[0], np.cumsum(left)])), dev(shared[:n]),
+                                           n, 300, t, t.shape[1], dev(lens[:B]), dev(slots[:B]), B, 96, ws, size)
+            assert r.status() == 0 and torch.equal(got, want)
+
+
 def test_shared_graphs_and_streams(osc):
     """Captured once and replayed on new inputs; two graphs with one workspace replayed in turn; two streams at once."""
     rng = np.random.default_rng(10)
