@@ -49,6 +49,7 @@ constexpr int kFlush = 512, kMostSlots = 3;
 // these are kLag ahead; a weight at the second one is 2^kBase, none is above 2^(kLag + kBase) = 2^15.
 constexpr float kLag = 12.f, kBase = 3.f;
 constexpr float kFar = 4194304.f;                         // scores (log2) whose last place counts
+constexpr float kLoud = 96.f;                             // log2 of a V scale by the second reference, beyond which float32 ends
 
 template <int D, bool QF32, int TERMS>
 struct Lay {
@@ -159,61 +160,69 @@ __device__ __forceinline__ float weigh(const uint32_t (&x)[HC], const float (&cm
 
 // The same where some groups are not there or have no V scale (all of a page's values 0) or one too far from the others, or some
 // row's scores are so large (kFar) that a last place of one counts: there distances are formed from the raw sums, 0 at a group's
-// largest.  Other rows come out as from weigh, bit for bit.
+// largest.  A V scale 2^kLoud above the second reference (on a page whose weights vanish next to it) is taken by 2^kLoud less, its
+// weights by as much more.  Other rows come out as from weigh, bit for bit.  A group at a time: few registers, which the caller's
+// scores need (all 64 scores at once cost 2 us of 94 at 64 samples of 32K).
 template <int HC, int TERMS>
 __device__ __noinline__ float weigh_with_care(uint32_t at, const float* ks, float qs, float qs_lo, float m, float d, int mask) {
+  constexpr int NG = HC / 16;
   const float *vs = ks + 8, *lg = ks + 16;
-  const bool any = d > -INFINITY;                         // (else no page so far has values)
   if (m == -INFINITY) m = 0.f;
   const bool far = fabsf(m) >= kFar;
-  const float diff = any ? d - kBase : 0.f, to_o = pow2(-diff);
+  float v[16];
+  auto load = [&](int k) {                                // returns the largest
+    tmem_ld16(at + 16 * k, *reinterpret_cast<uint32_t(*)[16]>(&v));
+    float cm = v[0];
+#pragma unroll
+    for (int j = 1; j < 16; ++j) cm = fmaxf(cm, v[j]);
+    return cm;
+  };
+  const bool any = d > -INFINITY;                         // (else no page so far has values)
+  const float diff = any ? d - kBase : 0.f;
   float total = 0.f;
-  float v[HC / 32][32];
+  uint32_t lo[TERMS == 2 ? NG : 1][8];
 #pragma unroll
-  for (int c = 0; c < HC / 32; ++c) tmem_ld32(at + 32 * c, v[c]);
-#pragma unroll
-  for (int c = 0; c < HC / 32; ++c) {
-    uint32_t hi[16], lo[16];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int k = 2 * c + u;
-      const bool there = mask >> k & 1, some = there && any && vs[k] > 0.f;
-      const float f = ks[k] * qs;
-      float cm = v[c][16 * u];
-#pragma unroll
-      for (int j = 1; j < 16; ++j) cm = fmaxf(cm, v[c][16 * u + j]);
-      const bool apart = far && cm > -INFINITY;
-      // weights by way of s - m: where the scores are large, or the V scale is 0 or so small that 2^(s + log2 - m - d) vanishes
-      const bool by_m = TERMS == 2 || apart || !some || diff - lg[k] > 60.f;
-      float back = 1.f, bias = -m;
-      if constexpr (TERMS == 2) {
-        if (!apart && there) back = ex2(fminf(cm * fmaf(ks[k], qs_lo, fmaf(ks[k], qs, -f)), 1.f));
-      } else if (!by_m) {
-        bias = lg[k] - (m + diff);
-        back = ex2(diff - lg[k]);
-      }
-      if (apart) bias = fminf(fmaf(cm, f, -m), kLag);
-      const float off = apart ? cm : 0.f, g = !some ? 0.f : by_m ? fminf(vs[k] * to_o, 65504.f) * (TERMS == 2 ? back : 1.f) : 1.f;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        float w[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          w[e] = there ? ex2(fmaf(v[c][16 * u + 2 * j + e] - off, f, bias)) : 0.f;
-          sum[2 * (j & 1) + e] += w[e];
-          w[e] = some ? w[e] * g : 0.f;
-          if (apart) w[e] = fminf(w[e], 65504.f);
-        }
-        hi[8 * u + j] = pack_half2(w[0], w[1]);
-        const __half2 h = *reinterpret_cast<const __half2*>(&hi[8 * u + j]);
-        lo[8 * u + j] = pack_half2(w[0] - __low2float(h), w[1] - __high2float(h));
-      }
-      total = fmaf((sum[0] + sum[2]) + (sum[1] + sum[3]), back, total);
+  for (int k = 0; k < NG; ++k) {                          // (a group's scores are read before its weights or others' take their place)
+    const float f = ks[k] * qs, cm = load(k);
+    const bool there = mask >> k & 1, some = there && any && vs[k] > 0.f;
+    const bool apart = far && cm > -INFINITY;
+    const float off = apart ? cm : 0.f;
+    float bias = apart ? fminf(fmaf(cm, f, -m), kLag) : -m, back = 1.f, g = some ? 1.f : 0.f;
+    if (TERMS == 1 && some && diff - lg[k] <= 60.f) {
+      bias = apart ? bias + (lg[k] - diff) : lg[k] - (m + diff);
+      back = ex2(diff - lg[k]);
+    } else if (TERMS == 1) {                              // (2^(s + log2(V scale) - m - d) vanishes)
+      if (some) g = vs[k] * pow2(-diff);
+    } else {
+      if (!apart && there) back = ex2(fminf(cm * fmaf(ks[k], qs_lo, fmaf(ks[k], qs, -f)), 1.f));
+      const bool loud = some && lg[k] - diff > kLoud;
+      const float e = -diff - (loud ? kLoud : 0.f);
+      if (some) g = fminf(vs[k] * pow2(fminf(e, 126.f)) * pow2(fmaxf(e - 126.f, 0.f)), 1e36f) * back;
+      if (loud) bias += kLoud, back = 0.f;                // (such a weight is below 2^-80 of the row's largest)
     }
-    tmem_st16(at + 16 * c, hi);
-    if constexpr (TERMS == 2) tmem_st16(at + HC / 2 + 16 * c, lo);
+    uint32_t hi[8];
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float w[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        w[e] = there ? ex2(fmaf(v[2 * j + e] - off, f, bias)) : 0.f;
+        sum[2 * (j & 1) + e] += w[e];
+        w[e] = some ? w[e] * g : 0.f;
+      }
+      hi[j] = pack_half2(w[0], w[1]);
+      if constexpr (TERMS == 2) {
+        const __half2 h = *reinterpret_cast<const __half2*>(&hi[j]);
+        lo[k][j] = pack_half2(w[0] - __low2float(h), w[1] - __high2float(h));
+      }
+    }
+    total = fmaf((sum[0] + sum[2]) + (sum[1] + sum[3]), back, total);
+    tmem_st8(at + 8 * k, hi);
   }
+  if constexpr (TERMS == 2)
+#pragma unroll
+    for (int k = 0; k < NG; ++k) tmem_st8(at + HC / 2 + 8 * k, lo[k]);
   return total;
 }
 
@@ -622,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
     // ---------------------------------------------------------------- scales
     const Kv8Geom kg{P, D, g.Hkv};
     const uint8_t* scales = a.pool + (size_t)a.layer * g.num_pages * kg.page_bytes() + (size_t)h * kg.block_bytes() + kg.scale_off();
-    float most = 0.f;
+    float most = 0.f, least = INFINITY;                   // V scales so far, but for those of pages of zeros
     uint2 sc[2];
     auto page_of = [&](int i) { return (i * NT + (lane & (2 * NG - 1)) * 16) >> (31 - __clz(P)); };
     auto load_scales = [&](int i, uint2& s) {
@@ -632,24 +641,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
     load_scales(1, sc[1]);
     for (int i = 0, s = 0, ph = 0; i < tiles; ++i) {
       const int b = i & 1;
-      good = mbar_wait_sleep_bounded(&sh.qk_ready[s], ph, a.status);
-      good = __all_sync(0xffffffffu, good);
-      if (!good) break;
       const uint2 now = b ? sc[1] : sc[0];
       const int e_page = page_of(i);
       const bool some = e_page < pages && (sh.there[e_page >> 5] >> (e_page & 31) & 1);
       const unsigned mask = __ballot_sync(0xffffffffu, some && lane < 2 * NG);
-      const float v_scale = some ? __uint_as_float(now.y) : 0.f;
+      const float v_scale = some ? __uint_as_float(now.y) : 0.f, log_v = log2f(v_scale);
+      // (V scales 2^60 from others so far, or so small that 2^-d is beyond float32, take the careful way)
+      const uint32_t bits = __float_as_uint(v_scale);
+      const float high = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < 2 * NG ? bits : 0u));
+      const float low = __uint_as_float(__reduce_min_sync(0xffffffffu, lane < 2 * NG && bits ? bits : 0x7F800000u));
+      most = fmaxf(most, high);
+      least = fminf(least, low);
+      const bool all = __all_sync(0xffffffffu, lane >= 2 * NG || bits);
+      const bool plain = all && low > most * 8.673617379884035e-19f && high * 8.673617379884035e-19f < least && least > 7.888609052210118e-31f;
+      good = mbar_wait_sleep_bounded(&sh.qk_ready[s], ph, a.status);  // (the place of S and of these is free)
+      good = __all_sync(0xffffffffu, good);
+      if (!good) break;
       if (lane < 2 * NG) {
         sh.sc[s].ks[lane] = some ? __uint_as_float(now.x) : 1.f;
         sh.sc[s].vs[lane] = v_scale;
-        sh.sc[s].lg[lane] = log2f(v_scale);
+        sh.sc[s].lg[lane] = log_v;
       }
-      // (V scales more than 2^60 below the largest so far take the careful way, which keeps their part in the sum of weights)
-      const uint32_t bits = __float_as_uint(v_scale);
-      most = fmaxf(most, __uint_as_float(__reduce_max_sync(0xffffffffu, lane < 2 * NG ? bits : 0u)));
-      const float least = __uint_as_float(__reduce_min_sync(0xffffffffu, lane < 2 * NG ? bits : 0x7F800000u));
-      const bool plain = least > 0.f && least > most * 8.673617379884035e-19f;
       if (lane == 0) {
         sh.mask[s] = (int)mask;
         sh.plain[s] = plain;

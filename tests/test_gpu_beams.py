@@ -268,6 +268,55 @@ def test_shared_where_one_key_leads_by_far(osc, fmt, qd, size):
                 assert np.allclose(out[b, 2 * h:2 * h + 2], want, rtol=0, atol=np.abs(want).max() * 2.0 ** -20)
 
 
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("qd,od", [(0, 0), (1, 0), (1, 1), (0, 1)])
+@pytest.mark.parametrize("below,loud,size", [(0.3, 1e6, 1.0), (0.3, 1e10, 1.0), (0.3, 1e13, 1.0), (0.6, 1e20, 1.0), (0.6, 1e23, 1.0),
+                                             (2.0, 1e36, 1e-3), (0.9, 1e32, 1e-3), (0.9, 1e34, 1e-3), (0.9, 1e36, 1e-3)])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_shared_loud_values_of_small_weights(osc, fmt, qd, od, below, loud, size, zeros):
+    """Weights of e^-26 (below = 0.3) to e^-170 on values up to 10^39 times the others': they count for what they are, in a tile with a
+    page of zeros too, and a weight of 0 on the largest values is 0."""
+    rng = np.random.default_rng(62)
+    P, d = 16, 128
+    rig, bt, slots, lens = family(osc, rng, [3], [24], [0, 5, 20], P=P, d=d, G=2, fmt=fmt)
+    with rig as r:
+        u = np.zeros((1, 2, d))
+        u[..., ::2] = 3.0
+        k, v = r.K[0][:384] * 0.3 + u, r.V[0][:384] * size
+        far = np.zeros(384, bool)
+        far[32:64] = far[208:240] = True
+        k[far] -= below * u[0]
+        v[far] *= loud
+        if zeros:
+            v[96:112] = v[160:176] = 0
+        r.write([k], [v], 1, [384], [0], bt[:1], slots[:1])
+        for b in (1, 2):
+            r.write([r.K[b][384:] * 0.3 + u], [r.V[b][384:] * size], 1, [lens[b] - 384], [384], bt[b:b + 1], slots[b:b + 1])
+        q = acts(rng, (3, 4, d), False) * 0.3
+        q[..., ::2] += 5.0
+        within(r, r.decode(q, qd, od, bt, lens, slots), q, qd, od, bt, lens, slots)
+        out = shared_decode(r, q, qd, od, [3], [24], bt, lens, slots)
+        assert r.status() == 0
+        within(r, out, q, qd, od, bt, lens, slots)
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("qd,od", [(0, 0), (1, 0), (1, 1), (0, 1)])
+@pytest.mark.parametrize("size", [1e-34, 1e-36, 1e-37, 1e-38, 1e36])
+def test_shared_values_near_the_ends_of_float32(osc, fmt, qd, od, size):
+    rng = np.random.default_rng(63)
+    rig, bt, slots, lens = family(osc, rng, [3], [24], [0, 5, 20], P=16, d=128, G=2, fmt=fmt)
+    with rig as r:
+        r.write([r.K[0][:384]], [r.V[0][:384] * size], 1, [384], [0], bt[:1], slots[:1])
+        for b in (1, 2):
+            r.write([r.K[b][384:]], [r.V[b][384:] * size], 1, [lens[b] - 384], [384], bt[b:b + 1], slots[b:b + 1])
+        q = acts(rng, (3, 4, 128), False)
+        within(r, r.decode(q, qd, od, bt, lens, slots), q, qd, od, bt, lens, slots)
+        out = shared_decode(r, q, qd, od, [3], [24], bt, lens, slots)
+        assert r.status() == 0
+        within(r, out, q, qd, od, bt, lens, slots)
+
+
 @pytest.mark.parametrize("qd", [0, 1])
 def test_shared_decode_carries_nan_in_its_own_row(osc, qd):
     rng = np.random.default_rng(8)
