@@ -74,6 +74,7 @@ struct Shared {
   Scales sc[kMostSlots];
   int mask[kMostSlots], plain[kMostSlots];  // groups that are there; all are, with V scales
   float2 top[2][2][kRows];       // a half's largest s and s + log2(V scale), of even and odd tiles
+  float far[2][kRows];           // a half's largest s - m + log2(V scale), where scores are far from 0
   float l[2][kRows];             // a half's sum, at the end
   float down[kRows];             // what the power of two of a row's query leaves to multiply by
   int row_req[kRows];            // a row's request, -1 for none
@@ -479,10 +480,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
           top = fmaxf(top, y);
           top_o = fmaxf(top_o, y + ks[16 + k]);           // (+ the logarithm of the V scale)
         }
-        // the largest of both halves: a pair of warps meets once a tile, after a wait that ran out too
-        sh.top[i & 1][half][row] = make_float2(top, top_o);
+        // the largest of both halves: a pair of warps meets once a tile, after a wait that ran out too (a NaN: both go on without)
+        sh.top[i & 1][half][row] = make_float2(good ? top : NAN, top_o);
         asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");
         const float2 other = sh.top[i & 1][half ^ 1][row];
+        good &= other.x == other.x;
         top = fmaxf(top, other.x);
         top_o = fmaxf(top_o, other.y);
         if (good) {
@@ -493,22 +495,40 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
             if (top > m + kLag || (m == -INFINITY && top > m)) {
               const float to = ceilf(top);
               l = m == -INFINITY ? l : l * pow2(m - to);
-              if (fabsf(to) < kFar) d += m - to;          // (m + d stays)
-              else scale = d == -INFINITY ? 1.f : pow2(m - to);
+              d += m - to;                                // (m + d stays)
               m = to;
             }
             float d_new = ceilf(top_o - m);
-            if (!(fabsf(m) < kFar)) {                       // (differences of such scores say nothing: the largest V scale)
-              d_new = -INFINITY;
-              for (int k = 0; k < 2 * NG; ++k) d_new = fmaxf(d_new, ceilf(sh.sc[b].lg[k]));
+            const bool far = !(fabsf(m) < kFar);
+            if (__any_sync(0xffffffffu, far)) {
+              // Such a score plus log2(V scale) has lost the V scale: the distances by which the weights go, of both halves (the same
+              // rows, so both are here)
+              care = true;
+              float its = -INFINITY;
+#pragma unroll
+              for (int k = 0; k < NG; ++k) {
+                float most = kTwo && QF32 ? cm[k] : -INFINITY;
+                if constexpr (!kTwo || !QF32)             // (again: cm would take registers that the other forms lack)
+#pragma unroll
+                  for (int j = 0; j < 16; ++j) {
+                    float y = __uint_as_float(x[16 * k + j]);
+                    asm volatile("" : "+f"(y));
+                    most = fmaxf(most, y);
+                  }
+                const float t = m == -INFINITY ? 0.f : fminf(fmaf(most, ks[k] * qs, -m), kLag);
+                if (mask >> k & 1) its = fmaxf(its, t + ks[16 + k]);
+              }
+              sh.far[half][row] = its;
+              asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");
+              its = fmaxf(its, sh.far[half ^ 1][row]);
+              if (far) d_new = ceilf(its);
             }
-            if (d == -INFINITY ? d_new > d : d_new > d + (fabsf(m) < kFar ? kLag : 0.f)) {
-              scale = d == -INFINITY ? 1.f : scale * pow2(d - d_new);  // (1: there is nothing in the sums)
+            if (d == -INFINITY ? d_new > d : d_new > d + (far ? 0.f : kLag)) {
+              scale = d == -INFINITY ? 1.f : pow2(d - d_new);  // (1: there is nothing in the sums)
               d = d_new;
             }
             flush = kTwo && i > 0 && i % kPeriod == 0;
             rescale = __any_sync(0xffffffffu, scale != 1.f) || flush;
-            care |= __any_sync(0xffffffffu, !(fabsf(m) < kFar));
           }
           if (care)
             l += weigh_with_care<HC, TERMS>(at, ks, qs, qs_lo, m, d, mask);

@@ -268,12 +268,14 @@ def test_shared_where_one_key_leads_by_far(osc, fmt, qd, size):
                 assert np.allclose(out[b, 2 * h:2 * h + 2], want, rtol=0, atol=np.abs(want).max() * 2.0 ** -20)
 
 
+DTYPES = [(0, 0), (1, 0), (1, 1), (0, 1)]                  # of queries and outputs
+
+
 @pytest.mark.parametrize("fmt", [0, 1])
-@pytest.mark.parametrize("qd,od", [(0, 0), (1, 0), (1, 1), (0, 1)])
 @pytest.mark.parametrize("below,loud,size", [(0.3, 1e6, 1.0), (0.3, 1e10, 1.0), (0.3, 1e13, 1.0), (0.6, 1e20, 1.0), (0.6, 1e23, 1.0),
                                              (2.0, 1e36, 1e-3), (0.9, 1e32, 1e-3), (0.9, 1e34, 1e-3), (0.9, 1e36, 1e-3)])
 @pytest.mark.parametrize("zeros", [False, True])
-def test_shared_loud_values_of_small_weights(osc, fmt, qd, od, below, loud, size, zeros):
+def test_shared_loud_values_of_small_weights(osc, fmt, below, loud, size, zeros):
     """Weights of e^-26 (below = 0.3) to e^-170 on values up to 10^39 times the others': they count for what they are, in a tile with a
     page of zeros too, and a weight of 0 on the largest values is 0."""
     rng = np.random.default_rng(62)
@@ -294,16 +296,16 @@ def test_shared_loud_values_of_small_weights(osc, fmt, qd, od, below, loud, size
             r.write([r.K[b][384:] * 0.3 + u], [r.V[b][384:] * size], 1, [lens[b] - 384], [384], bt[b:b + 1], slots[b:b + 1])
         q = acts(rng, (3, 4, d), False) * 0.3
         q[..., ::2] += 5.0
-        within(r, r.decode(q, qd, od, bt, lens, slots), q, qd, od, bt, lens, slots)
-        out = shared_decode(r, q, qd, od, [3], [24], bt, lens, slots)
-        assert r.status() == 0
-        within(r, out, q, qd, od, bt, lens, slots)
+        for qd, od in DTYPES:
+            within(r, r.decode(q, qd, od, bt, lens, slots), q, qd, od, bt, lens, slots)
+            out = shared_decode(r, q, qd, od, [3], [24], bt, lens, slots)
+            assert r.status() == 0
+            within(r, out, q, qd, od, bt, lens, slots)
 
 
 @pytest.mark.parametrize("fmt", [0, 1])
-@pytest.mark.parametrize("qd,od", [(0, 0), (1, 0), (1, 1), (0, 1)])
 @pytest.mark.parametrize("size", [1e-34, 1e-36, 1e-37, 1e-38, 1e36])
-def test_shared_values_near_the_ends_of_float32(osc, fmt, qd, od, size):
+def test_shared_values_near_the_ends_of_float32(osc, fmt, size):
     rng = np.random.default_rng(63)
     rig, bt, slots, lens = family(osc, rng, [3], [24], [0, 5, 20], P=16, d=128, G=2, fmt=fmt)
     with rig as r:
@@ -311,10 +313,89 @@ def test_shared_values_near_the_ends_of_float32(osc, fmt, qd, od, size):
         for b in (1, 2):
             r.write([r.K[b][384:]], [r.V[b][384:] * size], 1, [lens[b] - 384], [384], bt[b:b + 1], slots[b:b + 1])
         q = acts(rng, (3, 4, 128), False)
-        within(r, r.decode(q, qd, od, bt, lens, slots), q, qd, od, bt, lens, slots)
-        out = shared_decode(r, q, qd, od, [3], [24], bt, lens, slots)
-        assert r.status() == 0
-        within(r, out, q, qd, od, bt, lens, slots)
+        for qd, od in DTYPES:
+            within(r, r.decode(q, qd, od, bt, lens, slots), q, qd, od, bt, lens, slots)
+            out = shared_decode(r, q, qd, od, [3], [24], bt, lens, slots)
+            assert r.status() == 0
+            within(r, out, q, qd, od, bt, lens, slots)
+
+
+# (token, its key as a share of the leading key, how loud its page's values are) of keys along the queries; the other keys' scores are of ordinary size
+FAR = {"between": [(700, 1.0, 1.0)], "at_a_sum": [(512, 1.0, 1.0)], "last": [(1595, 1.0, 1.0)], "first": [(3, 1.0, 1.0)],
+       "rises": [(100, 0.5, 1.0), (1000, 1.0, 1.0)], "halves": [(100, 1.0, 1.0), (1000, 0.5, 1.0)],
+       "ties": [(300, 1.0, 1.0), (1100, 1.0, 1.0)], "ties_in_a_tile": [(515, 1.0, 1.0), (618, 1.0, 1.0)],
+       "louder": [(300, 1.0, 1.0), (1100, 1.0, 50.0)], "quieter": [(300, 1.0, 50.0), (1100, 1.0, 1.0)],
+       "unseen_in_a_tile": [(700, 1.0, 1.0), (655, 0.0, 1e12)], "unseen_before": [(700, 1.0, 1.0), (40, 0.0, 1e12)],
+       "unseen_after": [(700, 1.0, 1.0), (1400, 0.0, 1e12)], "loud_then_quiet": [(100, 0.5, 1e12), (1000, 1.0, 1.0)],
+       "quiet_then_loud": [(100, 0.5, 1e-12), (1000, 1.0, 1.0)]}
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("size", [1e3, 1e5, 1e8, 1e15, 1e30])
+@pytest.mark.parametrize("case", list(FAR))
+def test_shared_far_scores_in_any_tile(osc, fmt, size, case):
+    """A CTA's tiles in turn, scores of ordinary size among very large ones: the output is the value of the leading key, or the mean of
+    those that lead alike, whatever the values of the pages without weight.  Off by 2^-20 of the largest.  A BF16 output's weights are
+    f16 numbers, off by half a step, 2^-11 of themselves, and their scores' exponents, unless formed from differences (scores of 2^22 in
+    log2 on), float32 numbers of the size of the score, off by 2^-24 of it: so the mean of the values v_j is off by
+    (2^-11 + ln 2 2^-24 |s|) mean |v_j|, and it is rounded once more, by 2^-8 of what it then is."""
+    rng = np.random.default_rng(71)
+    P, d, N, empty = 16, 64, 1600, 63                        # (so many groups that a split has all of the prefix)
+    sizes, shared = [3] + [0] * empty, [N // P] + [0] * empty
+    rig, bt, slots, lens = family(osc, rng, sizes, shared, [0, 5, 20], P=P, d=d, G=2, fmt=fmt)
+    with rig as r:
+        k, v = r.K[0][:N] * (0.3 / size), r.V[0][:N].copy()
+        w = np.sign(rng.normal(size=k[0].shape)) * 3.0
+        for t, u, loud in FAR[case]:
+            k[t // P * P:t // P * P + P] = 0
+            k[t] = u * w
+            v[t // P * P:t // P * P + P] *= loud
+        r.write([k], [v], 1, [N], [0], bt[:1], slots[:1])
+        for b in (1, 2):
+            r.write([r.K[b][N:] * (0.3 / size)], [r.V[b][N:]], 1, [lens[b] - N], [N], bt[b:b + 1], slots[b:b + 1])
+        q = np.repeat(w[None], 3, 0).repeat(2, 1) * size
+        lead = [t for t, u, _ in FAR[case] if u == 1.0]
+        for qd, od in DTYPES:
+            for out in (r.decode(q, qd, od, bt, lens, slots), shared_decode(r, q, qd, od, sizes, shared, bt, lens, slots)):
+                got = out.double().cpu().numpy()
+                for b in range(3):
+                    for h in range(2):
+                        v = r.ref.rows(bt[b], slots[b], lens[b], h)[1][lead]
+                        want = v.mean(0)
+                        bound = np.abs(want).max() * 2.0 ** -20
+                        if od == 1:
+                            top = 9 * d * size / np.sqrt(d) * np.log2(np.e)
+                            bound = bound + (2.0 ** -11 + np.log(2) * 2.0 ** -24 * top * (top < 2.0 ** 22)) * np.abs(v).mean(0)
+                            bound = bound + 2.0 ** -8 * (np.abs(want) + bound)
+                        assert np.all(np.abs(got[b, 2 * h:2 * h + 2] - want) <= bound), (b, h)
+            assert r.status() == 0
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("size", [1e3, 1e8, 1e30])
+@pytest.mark.parametrize("until", [16, 400, 512, 1584])
+@pytest.mark.parametrize("loud", [1.0, 1e12])
+def test_shared_far_below_first(osc, fmt, size, until, loud):
+    """Tokens whose scores are far below those of the rest come first: nothing of them is left, loud or not."""
+    rng = np.random.default_rng(72)
+    P, d, N, empty = 16, 64, 1600, 63
+    sizes, shared = [3] + [0] * empty, [N // P] + [0] * empty
+    rig, bt, slots, lens = family(osc, rng, sizes, shared, [0, 5, 20], P=P, d=d, G=2, fmt=fmt)
+    with rig as r:
+        k, v = r.K[0][:N] * (0.3 / size), r.V[0][:N].copy()
+        w = np.sign(rng.normal(size=k[0].shape)) * 3.0
+        k[:until] = -w * (0.5 + 0.5 * rng.random((until, 1, 1)))
+        v[:until] *= loud
+        r.write([k], [v], 1, [N], [0], bt[:1], slots[:1])
+        for b in (1, 2):
+            r.write([r.K[b][N:] * (0.3 / size)], [r.V[b][N:]], 1, [lens[b] - N], [N], bt[b:b + 1], slots[b:b + 1])
+        q = np.repeat(w[None], 3, 0).repeat(2, 1) * size * (1 + 0.1 * acts(rng, (3, 4, d), False))
+        rows = r.ref.rows
+        r.ref.rows = lambda *a: [x[until:] for x in rows(*a)]        # (what the other tokens give)
+        for qd, od in DTYPES:
+            out = shared_decode(r, q, qd, od, sizes, shared, bt, lens, slots)
+            assert r.status() == 0
+            within(r, out, q, qd, od, bt, lens, slots)
 
 
 @pytest.mark.parametrize("qd", [0, 1])
