@@ -571,10 +571,10 @@ oscar_status oscar_kv8_fork(oscar_ctx* ctx, const int32_t* src_bt, int32_t n, in
  * takes the slot of an old beam without a child, in ascending order of those, and unless it is empty
  * its parent's seq_lens mod P tail rows are copied there in every layer (other rows of the slab stay as they are).  So
  * an item's slots are the same ones before and after, and a beam's tail moves only if its parent has
- * several children.  All arguments are device int32 and the outputs must not overlap the inputs.  A parent out of
- * range counts as -1 and sets OSCAR_DEV_BAD_SLOT; a slot out of range that a beam keeps or takes sets OSCAR_DEV_BAD_SLOT and
- * a parent's length out of range OSCAR_DEV_BAD_LEN, whether rows would be copied or not: they are not copied, and the
- * new arrays hold the slot or length as it was.  The call can be captured into a graph: it does not touch
+ * several children.  All arguments are device int32; the outputs must overlap neither the inputs nor one another (else
+ * OSCAR_ERR_INVALID).  A parent out of range counts as -1 and sets OSCAR_DEV_BAD_SLOT; a slot out of range that a beam
+ * keeps or takes sets OSCAR_DEV_BAD_SLOT and a parent's length out of range OSCAR_DEV_BAD_LEN, whether rows would be
+ * copied or not: they are not copied, and the new arrays hold the slot or length as it was.  The call can be captured into a graph: it does not touch
  * the page allocator, whose refcounts follow with oscar_ref_pages of the parent's pages for every further child and
  * oscar_unref_pages of the pages of every beam without one, before the next page is allocated. */
 oscar_status oscar_kv8_reorder(oscar_ctx* ctx, const int32_t* parents, int32_t batch, int32_t beams, const int32_t* block_table,

@@ -17,6 +17,12 @@ inline oscar_status check_device(const oscar_ctx* ctx) {
   return OSCAR_OK;
 }
 
+// Whether two arrays of so many bytes share one (a null array holds none).
+inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + nb && y < x + na;
+}
+
 inline oscar_status need_kv8(oscar_ctx* ctx) {
   if (!ctx) return fail(OSCAR_ERR_INVALID, "context is null");
   if (!ctx->kv8_pool) return fail(OSCAR_ERR_INVALID, "no 8-bit cache is bound to the context (oscar_kv8_bind)");

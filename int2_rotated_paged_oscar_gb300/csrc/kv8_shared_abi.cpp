@@ -12,6 +12,7 @@ using oscar::kMaxGrid;
 using oscar::Kv8DecodeArgs;
 using oscar::LaunchScope;
 using oscar::need_kv8;
+using oscar::overlap;
 using oscar::ReorderArgs;
 using oscar::validate;
 
@@ -102,13 +103,13 @@ oscar_status oscar_kv8_reorder(oscar_ctx* ctx, const int32_t* parents, int32_t b
   if (batch == 0) return OSCAR_OK;
   if (!parents || !block_table || !seq_lens || !req_slot || !new_block_table || !new_seq_lens || !new_req_slot)
     return fail(OSCAR_ERR_INVALID, "null tensor argument");
-  const size_t rows = (size_t)batch * beams, table = rows * bt_stride;
-  const struct { const int32_t* p; size_t n; } in[] = {{parents, rows}, {block_table, table}, {seq_lens, rows}, {req_slot, rows}},
-                                               to[] = {{new_block_table, table}, {new_seq_lens, rows}, {new_req_slot, rows}};
-  for (const auto& o : to)
-    for (const auto& i : in)
-      if (o.p < i.p + i.n && i.p < o.p + o.n)
-        return fail(OSCAR_ERR_INVALID, "the new tables, lengths and slots must not overlap the old ones");
+  const size_t rows = 4 * (size_t)batch * beams, table = rows * bt_stride;  // bytes
+  const struct { const int32_t* p; size_t n; } of[] = {{new_block_table, table}, {new_seq_lens, rows}, {new_req_slot, rows},
+                                                       {parents, rows}, {block_table, table}, {seq_lens, rows}, {req_slot, rows}};
+  for (int o = 0; o < 3; ++o)
+    for (int i = o + 1; i < 7; ++i)
+      if (overlap(of[o].p, of[o].n, of[i].p, of[i].n))
+        return fail(OSCAR_ERR_INVALID, "the new tables, lengths and slots must overlap neither the old ones nor one another");
   ReorderArgs a{};
   a.g = ctx->g;
   a.parents = parents;

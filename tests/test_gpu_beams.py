@@ -832,6 +832,23 @@ def test_reorder_refusals(osc):
         assert o.oscar_launch_count(r.ctx) == before
 
 
+def test_reorder_outputs_over_one_another_are_refused(osc):
+    with Rig(osc) as r:
+        o = osc
+        i, room = [dev(np.zeros(24)) for _ in range(8)], dev(np.zeros(64))
+        good = (r.ctx, i[0], 2, 2, i[1], 6, i[2], i[3], room[:24], room[24:28], room[28:32])
+        before = o.oscar_launch_count(r.ctx)
+        for at, value in [(9, room[:4]), (9, room[23:27]), (10, room[12:16]), (10, room[24:28]), (10, room[27:31]), (10, room[21:25]), (8, room[8:32])]:
+            a = list(good)
+            a[at] = value
+            with pytest.raises(o.OscarError, match="overlap") as e:
+                o.oscar_kv8_reorder(*a)
+            assert e.value.status == o.ERR_INVALID
+        assert o.oscar_launch_count(r.ctx) == before
+        o.oscar_kv8_reorder(*good)                           # next to one another is fine
+        assert o.oscar_launch_count(r.ctx) == before + 1 and r.status() == 0
+
+
 @pytest.mark.parametrize("P,d", GEO)
 @pytest.mark.parametrize("batch,beams,layers", [(1, 1, 1), (1, 3, 2), (3, 4, 5), (2, 64, 1)])
 def test_reorder(osc, P, d, batch, beams, layers):
