@@ -595,7 +595,8 @@ oscar_status oscar_kv8_reorder(oscar_ctx* ctx, const int32_t* parents, int32_t b
  * leaves the beam out and sets OSCAR_DEV_BAD_VALUE.  Exponentials and their sums are float32's (the normaliser is good to
  * 10^-6): candidates of different beams whose keys differ by less may come in either order; equal rows and scores
  * are equal.  1 <= beams, n_out <= 64, vocab <= 2^24.  The context is any one with device buffers; the workspace's
- * rules are those of the 8-bit cache's calls, the outputs must not overlap the inputs. */
+ * rules are those of the 8-bit cache's calls; outputs and workspace must overlap neither the inputs nor one another
+ * (else OSCAR_ERR_INVALID). */
 oscar_status oscar_beam_select_workspace_size(int32_t batch, int32_t beams, int32_t vocab, int32_t n_out, size_t* bytes);
 oscar_status oscar_beam_select(oscar_ctx* ctx, const void* logits, int64_t row_stride, int32_t dtype, const float* scores,
                                const uint8_t* finished, int32_t pad_token, int32_t batch, int32_t beams, int32_t vocab,

@@ -1,12 +1,13 @@
 // C ABI of the choice of beams (see include/oscar.h).
 #include "beam_internal.h"
-#include "oscar_ctx.h"
+#include "kv8_checks.h"
 
 using oscar::BeamArgs;
 using oscar::check_workspace;
 using oscar::cuda_fail;
 using oscar::fail;
 using oscar::LaunchScope;
+using oscar::overlap;
 
 namespace {
 
@@ -17,11 +18,6 @@ oscar_status check_sizes(int32_t batch, int32_t beams, int32_t vocab, int32_t n_
     return fail(OSCAR_ERR_UNSUPPORTED, "batch %d, beams %d, vocab %d, n_out %d: at most 65535, %d, %d, %d", batch, beams, vocab,
                 n_out, oscar::kMaxBeams, oscar::kMaxVocab, oscar::kMaxCandidates);
   return OSCAR_OK;
-}
-
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a && b && x < y + nb && y < x + na;
 }
 
 }  // namespace
@@ -59,13 +55,17 @@ oscar_status oscar_beam_select(oscar_ctx* ctx, const void* logits, int64_t row_s
   const size_t elem = dtype == OSCAR_DTYPE_BF16 ? 2 : 4;
   if (reinterpret_cast<uintptr_t>(logits) % elem) return fail(OSCAR_ERR_INVALID, "logits must be aligned to its elements");
   const size_t rows = (size_t)batch * beams, out = 4 * (size_t)batch * n_out, read = ((rows - 1) * row_stride + vocab) * elem;
-  for (const void* o : {static_cast<const void*>(out_scores), static_cast<const void*>(out_tokens), static_cast<const void*>(out_parents)})
-    if (overlap(o, out, scores, 4 * rows) || overlap(o, out, finished, rows) || overlap(o, out, logits, read))
-      return fail(OSCAR_ERR_INVALID, "the outputs must not overlap the inputs");
   if ((st = check_workspace(workspace)) != OSCAR_OK) return st;
   BeamArgs a{};
   const size_t need = oscar::beam_ws_bytes(batch, beams, vocab);
   if (ws_bytes < need) return fail(OSCAR_ERR_INVALID, "workspace too small: %zu < %zu bytes", ws_bytes, need);
+  // what is written, then what is read
+  const struct { const void* p; size_t n; } of[] = {{out_scores, out}, {out_tokens, out}, {out_parents, out}, {workspace, need},
+                                                    {scores, 4 * rows}, {finished, rows}, {logits, read}};
+  for (int o = 0; o < 4; ++o)
+    for (int i = o + 1; i < 7; ++i)
+      if (overlap(of[o].p, of[o].n, of[i].p, of[i].n))
+        return fail(OSCAR_ERR_INVALID, "the outputs and the workspace must overlap neither the inputs nor one another");
   a.logits = logits;
   a.stride = row_stride;
   a.dtype = dtype;

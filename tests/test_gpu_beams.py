@@ -642,6 +642,28 @@ def test_choice_refusals(osc, choose):
     assert choose.status() == 0
 
 
+def test_choice_outputs_and_workspace_over_one_another_are_refused(osc, choose):
+    o, B, K, V, N = osc, 2, 3, 2000, 4
+    size = o.oscar_beam_select_workspace_size(B, K, V, N)
+    room = torch.zeros(1 << 16, dtype=torch.uint8, device="cuda")
+    at = lambda i, n, t: room[i:i + n].view(t)  # noqa: E731
+    f, i4 = torch.float32, torch.int32
+    good = [choose.ctx, at(0, 4 * B * K * V, f).view(B, K, V), 0, at(48128, 4 * B * K, f), None, 0, B, K, V, N, at(48640, 32, f), at(48672, 32, i4),
+            at(48704, 32, i4), at(48896, size, torch.uint8), size]
+    before = o.oscar_launch_count(choose.ctx)
+    for where, value in [(11, at(48704, 32, i4)), (11, at(48660, 32, i4)), (12, at(48640, 32, i4)), (10, at(48700, 32, f)), (12, at(48900, 32, i4)),
+                         (10, at(48896 + size - 4, 32, f)), (13, at(48640, size, torch.uint8)), (13, at(47872, size, torch.uint8)),
+                         (13, at(48128, size, torch.uint8)), (4, at(48640, B * K, torch.uint8)), (4, at(48896, B * K, torch.uint8))]:
+        a = list(good)
+        a[where] = value
+        with pytest.raises(o.OscarError, match="overlap") as e:
+            o.oscar_beam_select(*a)
+        assert e.value.status == o.ERR_INVALID
+    assert o.oscar_launch_count(choose.ctx) == before
+    o.oscar_beam_select(*good)                               # next to one another is fine
+    assert o.oscar_launch_count(choose.ctx) == before + 2 and choose.status() == 0
+
+
 @pytest.mark.parametrize("dtype", BOTH)
 @pytest.mark.parametrize("B,K,V,n_out", [(1, 1, 1, 1), (1, 1, 1, 4), (2, 2, 7, 4), (1, 2, 997, 2), (3, 5, 1024, 10), (2, 4, 1025, 8), (2, 3, 4097, 64),
                                          (1, 64, 333, 64), (2, 8, 32768, 16), (1, 5, 50021, 10), (1, 1, 131072, 1), (1, 4, 300001, 8)])
