@@ -530,7 +530,7 @@ oscar_status oscar_kv8_sparse_decode_attn(oscar_ctx* ctx, int32_t layer, const v
                                           const int32_t* seq_lens, const int32_t* req_slot, int32_t batch,
                                           void* workspace, size_t ws_bytes, void* stream);
 
-/* Decode attention of requests that share a prefix: what oscar_kv8_decode_attn returns, with the shared pages of a
+/* Decode attention of requests that share a prefix: what oscar_kv8_decode_attn computes, with the shared pages of a
  * group read once for all of its requests (samples or beams of one prompt, conversations behind one
  * system prompt).  Group i holds requests group_starts[i] .. group_starts[i + 1] - 1 of the batch, and the first
  * shared_pages[i] entries of their block-table rows are the same pages (forks of n tokens share n / P).
@@ -540,8 +540,12 @@ oscar_status oscar_kv8_sparse_decode_attn(oscar_ctx* ctx, int32_t layer, const v
  * (host values, they size the grids and the workspace); the other arguments as for
  * oscar_kv8_decode_attn.  A request of length 0 (a padded batch) gets zeros; one that no group holds, that is shorter
  * than its group's shared pages or beyond the bounds gets zeros and sets OSCAR_DEV_BAD_LEN; a page that is not
- * mapped is left out and sets OSCAR_DEV_BAD_PAGE.  The workspace size holds for every call of at most batch requests in
- * at most n_groups groups with the same max_shared and max_own: a program that shrinks its batch or joins groups keeps its
+ * mapped is left out and sets OSCAR_DEV_BAD_PAGE.
+ * Next to oscar_kv8_decode_attn the shared part's weights have fewer bits: 22 for float32 outputs, and for BF16 ones 11 (a
+ * weight is off by up to 2^-11 of itself, where the output's own rounding is 2^-8; some 6 to 8 % of the values come out
+ * one BF16 step apart).  A caller who wants the nearest BF16 numbers asks for float32 and rounds.
+ * The workspace size holds for every call of at most batch requests in at most n_groups groups with the same
+ * max_shared and max_own: a program whose requests finish or whose groups end keeps its
  * workspace. */
 oscar_status oscar_kv8_shared_workspace_size(const oscar_config* cfg, int32_t batch, int32_t n_groups, int32_t max_shared,
                                              int32_t max_own, size_t* bytes);
@@ -583,9 +587,10 @@ oscar_status oscar_kv8_reorder(oscar_ctx* ctx, const int32_t* parents, int32_t b
 
 /* The next beams of a beam search.  Candidate (i, v) of a batch item continues beam i with token v and has
  *     key = scores[i] + ((x_v - m) - log sum_u e^(x_u - m)),  x = logits[i], m = max x,
- * the sum of log probabilities so far.  The n_out candidates of the largest keys, in descending order and the
- * lowest i * vocab + v first among equal ones: out_scores [batch][n_out] (float32 keys), out_tokens (v) and
- * out_parents (i, as oscar_kv8_reorder takes them), both int32.
+ * the sum of log probabilities so far.  The n_out candidates of the largest keys, compared in 64 bits, in descending order; among
+ * equal keys the lowest beam comes first, within a beam the larger logit (a small difference may be lost in a large score), then the lowest
+ * token: out_scores [batch][n_out] (the keys, rounded to float32), out_tokens (v) and out_parents (i, as
+ * oscar_kv8_reorder takes them), both int32.
  *  logits: rows [batch][beams][vocab] of dtype (BF16 or F32), row_stride elements apart (0: adjacent) and aligned to
  *  their elements only (16-byte aligned rows are read fastest).  scores: [batch][beams] float32; a beam at -infinity has no
  *  candidates (beams 1 .. of a first step).  finished [batch][beams] (bytes; NULL: none): a beam that is not 0 there has one candidate,
