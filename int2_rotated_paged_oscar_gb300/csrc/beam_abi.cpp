@@ -3,6 +3,7 @@
 #include "kv8_checks.h"
 
 using oscar::BeamArgs;
+using oscar::check_device;
 using oscar::check_workspace;
 using oscar::cuda_fail;
 using oscar::fail;
@@ -38,13 +39,9 @@ oscar_status oscar_beam_select(oscar_ctx* ctx, const void* logits, int64_t row_s
                                size_t ws_bytes, void* stream) {
   if (!ctx) return fail(OSCAR_ERR_INVALID, "context is null");
   if (!ctx->d_status) return fail(OSCAR_ERR_INVALID, "context was created without device buffers");
-  int dev = 0;
-  const cudaError_t ce = cudaGetDevice(&dev);
-  if (ce != cudaSuccess) return cuda_fail(ce, "current device");
-  if (dev != ctx->device)
-    return fail(OSCAR_ERR_INVALID, "the context's buffers are on device %d, the current device is %d", ctx->device, dev);
-  oscar_status st = check_sizes(batch, beams, vocab, n_out);
+  oscar_status st = check_device(ctx);
   if (st != OSCAR_OK) return st;
+  if ((st = check_sizes(batch, beams, vocab, n_out)) != OSCAR_OK) return st;
   if (dtype != OSCAR_DTYPE_BF16 && dtype != OSCAR_DTYPE_F32) return fail(OSCAR_ERR_INVALID, "bad dtype %d of logits", dtype);
   if (row_stride == 0) row_stride = vocab;
   if (row_stride > (1LL << 40)) return fail(OSCAR_ERR_UNSUPPORTED, "row stride %lld of logits", (long long)row_stride);
