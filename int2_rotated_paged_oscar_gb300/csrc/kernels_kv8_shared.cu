@@ -727,7 +727,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
   // ------------------------------------------------------------------ the split's partial
   float* o_rows = reinterpret_cast<float*>(smem);         // [row][m, l, -, -, O]; the operands are done with
   if (good && warp < kSoft && live) {
-    const float scale = d == -INFINITY ? 0.f : pow2(d - kBase);
+    // m may lag by 2^kLag, and a sum so much larger end float32: the sum of weights is brought to [1, 2) (not where m has no place
+    // for it), O with it, by two powers of two
+    const float sum = sh.l[0][row] + sh.l[1][row];
+    const float up = fabsf(m) < kFar && sum > 0.f && sum < INFINITY ? (float)((int)(__float_as_uint(sum) >> 23) - 127) : 0.f;
+    const float to = d - kBase - up, scale = d == -INFINITY ? 0.f : pow2(fmaxf(to, -120.f)), less = pow2(fminf(to + 120.f, 0.f));
 #pragma unroll 1
     for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {  // (each half of the threads has half of the channels)
       float v[32];
@@ -741,10 +745,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
 #pragma unroll
       for (int j = 0; j < 32; j += 4)
         *reinterpret_cast<float4*>(o_rows + row * (D + 4) + 4 + c + j) =
-            make_float4(v[j] * scale, v[j + 1] * scale, v[j + 2] * scale, v[j + 3] * scale);
+            make_float4(v[j] * scale * less, v[j + 1] * scale * less, v[j + 2] * scale * less, v[j + 3] * scale * less);
     }
-    const float sum = sh.l[0][row] + sh.l[1][row];
-    if (half == 0) *reinterpret_cast<float2*>(o_rows + row * (D + 4)) = make_float2(sum == sum ? m : INFINITY, sum);  // (a NaN must not look like no partial)
+    if (half == 0)                                        // (a NaN must not look like no partial)
+      *reinterpret_cast<float2*>(o_rows + row * (D + 4)) = make_float2(sum == sum ? m + up : INFINITY, sum * pow2(-up));
   }
   good = !__syncthreads_or(!good);
   if (good)

@@ -320,6 +320,31 @@ def test_shared_values_near_the_ends_of_float32(osc, fmt, size):
             within(r, out, q, qd, od, bt, lens, slots)
 
 
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("rise", [0.05, 0.09, 0.12])
+def test_shared_large_values_while_the_reference_lags(osc, fmt, rise):
+    """Scores that rise by 4 to 10 after a split's first tiles, on values of 10^35: no sum leaves float32."""
+    rng = np.random.default_rng(64)
+    P, d, empty = 16, 128, 63                                # (so many groups that a split has all of the prefix)
+    sizes, shared = [3] + [0] * empty, [24] + [0] * empty
+    rig, bt, slots, lens = family(osc, rng, sizes, shared, [0, 5, 20], P=P, d=d, G=2, fmt=fmt)
+    with rig as r:
+        u = np.zeros((1, 2, d))
+        u[..., ::2] = 3.0
+        k, v = r.K[0][:384] * 0.1 + u, r.V[0][:384] * 1e35
+        k[128:] += rise * u
+        r.write([k], [v], 1, [384], [0], bt[:1], slots[:1])
+        for b in (1, 2):
+            r.write([r.K[b][384:] * 0.1 + u], [r.V[b][384:] * 1e35], 1, [lens[b] - 384], [384], bt[b:b + 1], slots[b:b + 1])
+        q = acts(rng, (3, 4, d), False) * 0.1
+        q[..., ::2] += 5.0
+        for qd, od in DTYPES:
+            within(r, r.decode(q, qd, od, bt, lens, slots), q, qd, od, bt, lens, slots)
+            out = shared_decode(r, q, qd, od, sizes, shared, bt, lens, slots)
+            assert r.status() == 0
+            within(r, out, q, qd, od, bt, lens, slots)
+
+
 # (token, its key as a share of the leading key, how loud its page's values are) of keys along the queries; the other keys' scores are of ordinary size
 FAR = {"between": [(700, 1.0, 1.0)], "at_a_sum": [(512, 1.0, 1.0)], "last": [(1595, 1.0, 1.0)], "first": [(3, 1.0, 1.0)],
        "rises": [(100, 0.5, 1.0), (1000, 1.0, 1.0)], "halves": [(100, 1.0, 1.0), (1000, 0.5, 1.0)],
