@@ -652,6 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
     const Kv8Geom kg{P, D, g.Hkv};
     const uint8_t* scales = a.pool + (size_t)a.layer * g.num_pages * kg.page_bytes() + (size_t)h * kg.block_bytes() + kg.scale_off();
     float most = 0.f, least = INFINITY;                   // V scales so far, but for those of pages of zeros
+    bool zeros = false;                                   // there were such
     uint2 sc[2];
     auto page_of = [&](int i) { return (i * NT + (lane & (2 * NG - 1)) * 16) >> (31 - __clz(P)); };
     auto load_scales = [&](int i, uint2& s) {
@@ -666,14 +667,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefix_kernel(const __grid_co
       const bool some = e_page < pages && (sh.there[e_page >> 5] >> (e_page & 31) & 1);
       const unsigned mask = __ballot_sync(0xffffffffu, some && lane < 2 * NG);
       const float v_scale = some ? __uint_as_float(now.y) : 0.f, log_v = log2f(v_scale);
-      // (V scales 2^60 from others so far, or so small that 2^-d is beyond float32, take the careful way)
+      // The careful way is for V scales 2^60 from others so far or so small that 2^-d is beyond float32; and, with two numbers a
+      // weight, for whatever comes after a page of zeros: where that one leads, d is as far below as the other scores are.  (Else
+      // a row's d is at least the smallest V scale so far, but for kLag.)
       const uint32_t bits = __float_as_uint(v_scale);
       const float high = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < 2 * NG ? bits : 0u));
       const float low = __uint_as_float(__reduce_min_sync(0xffffffffu, lane < 2 * NG && bits ? bits : 0x7F800000u));
       most = fmaxf(most, high);
       least = fminf(least, low);
       const bool all = __all_sync(0xffffffffu, lane >= 2 * NG || bits);
-      const bool plain = all && low > most * 8.673617379884035e-19f && high * 8.673617379884035e-19f < least && least > 7.888609052210118e-31f;
+      zeros |= __any_sync(0xffffffffu, lane < 2 * NG && some && !bits);
+      const bool plain = all && !(kTwo && zeros) && low > most * 8.673617379884035e-19f && high * 8.673617379884035e-19f < least && least > 7.888609052210118e-31f;
       good = mbar_wait_sleep_bounded(&sh.qk_ready[s], ph, a.status);  // (the place of S and of these is free)
       good = __all_sync(0xffffffffu, good);
       if (!good) break;

@@ -345,6 +345,41 @@ def test_shared_large_values_while_the_reference_lags(osc, fmt, rise):
             within(r, out, q, qd, od, bt, lens, slots)
 
 
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("below", [0.2, 0.5, 0.8, 1.0])
+@pytest.mark.parametrize("loud", [1.0, 1e14, 1e30])
+def test_shared_leading_pages_of_zeros(osc, monkeypatch, fmt, below, loud):
+    """Zero values under scores 17 to 85 above the rest, in the first tiles of a split: the rest keeps its digits, as far as
+    float32 has weights.  (Below 2^-126 it has none: that much of every value may be missing.)"""
+    bound = O.attend_bound
+
+    def flushed(q, k, v, P):
+        want, off = bound(q, k, v, P)
+        return want, off + 2.0 ** -126 * np.abs(v).sum(0)
+
+    monkeypatch.setattr(O, "attend_bound", flushed)
+    rng = np.random.default_rng(65)
+    P, d, empty = 16, 128, 63                                # (so many groups that a split has all of the prefix)
+    sizes, shared = [3] + [0] * empty, [32] + [0] * empty
+    rig, bt, slots, lens = family(osc, rng, sizes, shared, [0, 5, 20], P=P, d=d, G=2, fmt=fmt)
+    with rig as r:
+        u = np.zeros((1, 2, d))
+        u[..., ::2] = 3.0
+        k, v = r.K[0][:512] * 0.1, r.V[0][:512] * loud
+        k[:256] += below * u
+        v[:256] = 0
+        v[400:416] /= loud
+        r.write([k], [v], 1, [512], [0], bt[:1], slots[:1])
+        for b in (1, 2):
+            r.write([r.K[b][512:] * 0.1], [r.V[b][512:]], 1, [lens[b] - 512], [512], bt[b:b + 1], slots[b:b + 1])
+        q = acts(rng, (3, 4, d), False) * 0.1
+        q[..., ::2] += 5.0
+        for qd, od in DTYPES:
+            out = shared_decode(r, q, qd, od, sizes, shared, bt, lens, slots)
+            assert r.status() == 0
+            within(r, out, q, qd, od, bt, lens, slots)
+
+
 # (token, its key as a share of the leading key, how loud its page's values are) of keys along the queries; the other keys' scores are of ordinary size
 FAR = {"between": [(700, 1.0, 1.0)], "at_a_sum": [(512, 1.0, 1.0)], "last": [(1595, 1.0, 1.0)], "first": [(3, 1.0, 1.0)],
        "rises": [(100, 0.5, 1.0), (1000, 1.0, 1.0)], "halves": [(100, 1.0, 1.0), (1000, 0.5, 1.0)],
