@@ -58,14 +58,15 @@ __global__ void __launch_bounds__(kThreads) kv8_reorder_kernel(const __grid_cons
     if (tid == 0) {
       a.new_seq_lens[j] = n;
       a.new_req_slot[j] = slot;
+      // (a state is checked wherever it goes: a parent's first child hands its length and slot on without a copy)
+      const bool bad_slot = slot < 0 || slot >= g.max_req, bad_len = n < 0 || (long long)n > (long long)g.max_pages_per_req * g.P;
+      if (bad_slot || bad_len) flag_error(a.status, (bad_slot ? kDevBadSlot : 0) | (bad_len ? kDevBadLen : 0));
     }
   }
-  // (a state is checked wherever it goes: a parent's first child hands its length and slot on without a copy)
-  const int src_slot = p >= 0 ? a.req_slot[row0 + p] : slot;
-  const bool bad_slot = src_slot < 0 || src_slot >= g.max_req || slot < 0 || slot >= g.max_req;
-  const bool bad_len = n < 0 || (long long)n > (long long)g.max_pages_per_req * g.P;
-  if (blockIdx.x == 0 && tid == 0 && (bad_slot || bad_len)) flag_error(a.status, (bad_slot ? kDevBadSlot : 0) | (bad_len ? kDevBadLen : 0));
-  if (first || p < 0 || bad_slot || bad_len) return;
+  if (first || p < 0) return;
+  const int src_slot = a.req_slot[row0 + p];
+  if (src_slot < 0 || src_slot >= g.max_req || slot < 0 || slot >= g.max_req) return;
+  if (n < 0 || (long long)n > (long long)g.max_pages_per_req * g.P) return;
   const int vecs = (n % g.P) * g.D / 8;                 // 16-byte vectors of the K or V rows of one kv head
   if (vecs == 0) return;
   const size_t half = (size_t)g.P * g.D, region = (size_t)g.Hkv * 2 * half, layer = (size_t)g.max_req * region;
